@@ -287,6 +287,137 @@ SWIGLU_API int swiglu_mlp(const void* x, const void* w_gate, const void* w_up,
                           int64_t M, int64_t d, int64_t d_ff, int dtype, void* stream);
 
 /*
+ * Mixture of experts: the MLP of a model whose tokens each pass through k of
+ * E SwiGLU experts.  swiglu_linear (the router's logits), swiglu_route,
+ * swiglu_experts_up and swiglu_experts_down compute it in turn:
+ *
+ *     l = x . W_router                                   [T, E]
+ *     ids, weights = the k best experts of every token   [T, k]
+ *     h[r] = silu(x[t] . W_gate[e]) * (x[t] . W_up[e])   [T k, d_ff]
+ *     y[t] = residual[t] + sum_j weights[t, j] h[r(t, j)] . W_down[e(t, j)]
+ *
+ * r runs over the T k (token, choice) pairs sorted by expert.  Which expert
+ * has how many rows stays on the device: no call waits for the host, and every
+ * call can be captured in a CUDA graph and replayed with another routing.
+ * bf16 operands, f32 sums, fixed orders of summation, as everywhere above.
+ * None of these has a counterpart in the pages.
+ */
+enum { SWIGLU_WEIGHTS_KN = 0,     /* [K, N], N contiguous                          */
+       SWIGLU_WEIGHTS_NK = 1 };   /* [N, K], K contiguous (torch.nn.Linear.weight)  */
+enum { SWIGLU_ACT_NONE = 0, SWIGLU_ACT_RELU = 1, SWIGLU_ACT_SILU = 2,
+       SWIGLU_ACT_GELU = 3,       /* v Phi(v), by the error function               */
+       SWIGLU_ACT_GELU_TANH = 4 };/* its tanh form                                 */
+enum { SWIGLU_SCORE_SOFTMAX = 0, SWIGLU_SCORE_SIGMOID = 1 };
+enum { SWIGLU_GROUP_MAX = 0,      /* a group's value is its best candidate's       */
+       SWIGLU_GROUP_TOP2 = 1 };   /* ... the sum of its two best scores            */
+
+/*
+ * y = act(x . W + bias) + residual.
+ *
+ *     x [M, K] bf16; W bf16, [K, N] or [N, K] (layout); bias [N], bf16 or f32
+ *     (bias_dtype), or NULL; residual [M, N] in y's type, or NULL, may be y
+ *     itself; y [M, N], bf16 or f32 (out_dtype).
+ *
+ * The bias is added to the f32 sum, the activation applied to that, the
+ * residual added, and the result rounded once.  K is a multiple of 8, N any
+ * number ([K, N] weights with N no multiple of 8 are copied to padded rows in
+ * the workspace first, by a kernel of its own).  K == 0 gives
+ * act(bias) + residual.  bf16 outputs use the fast exponential;
+ * f32 outputs the accurate functions.
+ * workspace: as swiglu_up_ex, swiglu_linear_workspace_bytes(M, K, N) bytes
+ * (on the current device), or NULL for the library's own.
+ * Errors: SWIGLU_ERR_INVALID_ARG, _UNSUPPORTED (a size above 2^30),
+ * _ALIGNMENT, _WORKSPACE, _ARCH, _OOM, _CUDA.
+ */
+SWIGLU_API int swiglu_linear(const void* x, const void* w, const void* bias, const void* residual,
+                             void* y, int64_t M, int64_t K, int64_t N, int activation,
+                             int bias_dtype, int out_dtype, int layout, void* workspace,
+                             size_t workspace_bytes, void* stream);
+SWIGLU_API size_t swiglu_linear_workspace_bytes(int64_t M, int64_t K, int64_t N);
+
+/*
+ * Routing.  logits [T, E] (f32 or bf16); E <= 1024, k <= 32.
+ *
+ *     s = softmax(l) over the token's experts, or sigmoid(l), in f32
+ *     v = l without a bias (both scores grow with the logit), s + bias with
+ *         one (bias f32 [E]: a balance bias, which moves the choice only)
+ *     groups > 1: the experts are groups of E / groups neighbours (groups <=
+ *         32); only those of the topk_groups best groups are candidates, by
+ *         the group's largest v, or the sum of its two largest (with
+ *         SWIGLU_GROUP_TOP2 and no bias: of its two largest s)
+ *     ids     the k best candidates by v, best first, ties to the lowest
+ *             index                                              [T, k]
+ *     weights s of those, divided by their sum if `renormalize`, times `scale`
+ *
+ * Softmax runs over all of the token's experts, whatever the groups.  An
+ * expert whose logit is -inf or NaN, or whose v is, is masked: it is never
+ * chosen and has score 0 in the softmax.  Where fewer than k experts are
+ * candidates, the rest of the row has id -1 and weight 0.
+ *
+ * offsets, order, position (all three, or all NULL): the choices sorted by
+ * expert, as swiglu_dispatch writes them.
+ * Errors: SWIGLU_ERR_INVALID_ARG, _UNSUPPORTED, _ALIGNMENT, _ARCH, _OOM, _CUDA.
+ */
+SWIGLU_API int swiglu_route(const void* logits, const float* bias, int32_t* ids, float* weights,
+                            int32_t* offsets, int32_t* order, int32_t* position, int64_t T,
+                            int64_t E, int64_t k, int logits_dtype, int score, int64_t groups,
+                            int64_t topk_groups, int group_score, int renormalize, float scale,
+                            void* stream);
+
+/*
+ * The choices ids [T, k] sorted by expert (a stable counting sort), for ids
+ * that did not come from swiglu_route or were changed since (a padding token's
+ * set to -1, say).  Ids outside 0 ... E - 1 are dropped.
+ *
+ *     offsets  [E + 1]: expert e has the sorted rows offsets[e] ... offsets[e + 1] - 1
+ *     order    [T k]: sorted row -> t k + j; -1 past offsets[E]
+ *     position [T, k]: its inverse; -1 for a dropped choice
+ *
+ * int32 throughout.  Errors as swiglu_route.
+ */
+SWIGLU_API int swiglu_dispatch(const int32_t* ids, int32_t* offsets, int32_t* order,
+                               int32_t* position, int64_t T, int64_t k, int64_t E, void* stream);
+
+/*
+ * The experts' up projections: h[r] = silu(x[t] . W_gate[e]) * (x[t] . W_up[e])
+ * for sorted row r = (token t = order[r] / k, expert e).
+ *
+ *     x [T, d]; w_gate, w_up [E, d, d_ff] or [E, d_ff, d] (layout); h [T k, d_ff]
+ *     in sorted order, zero past offsets[E].  All bf16; d, d_ff multiples of 8.
+ *
+ * Offsets and order outside their ranges (a routing that swiglu_route or
+ * swiglu_dispatch did not write) give wrong rows, never an access outside the
+ * tensors.  workspace as swiglu_linear.  Errors as swiglu_linear.
+ */
+SWIGLU_API int swiglu_experts_up(const void* x, const void* w_gate, const void* w_up,
+                                 const int32_t* offsets, const int32_t* order, void* h, int64_t T,
+                                 int64_t k, int64_t E, int64_t d, int64_t d_ff, int layout,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+SWIGLU_API size_t swiglu_experts_up_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t d,
+                                                    int64_t d_ff);
+
+/*
+ * The experts' down projections and the weighted sum over a token's choices:
+ *
+ *     y[t] = residual[t] + sum_j weights[t, j] h[position[t, j]] . W_down[e]
+ *
+ *     h [T k, d_ff] in sorted order; w_down [E, d_ff, d] or [E, d, d_ff];
+ *     residual [T, d] or NULL, may be y itself; y [T, d].  All bf16 but
+ *     weights (f32 [T, k]).  Choices with position -1 add nothing.
+ *
+ * The products of each row, and the sum over j (ascending, from the
+ * residual), are f32; y is rounded once.  Two kernels; the rows' products
+ * stay in the workspace in between.  workspace, errors as swiglu_experts_up.
+ */
+SWIGLU_API int swiglu_experts_down(const void* h, const void* w_down, const int32_t* offsets,
+                                   const int32_t* position, const float* weights,
+                                   const void* residual, void* y, int64_t T, int64_t k, int64_t E,
+                                   int64_t d_ff, int64_t d, int layout, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+SWIGLU_API size_t swiglu_experts_down_workspace_bytes(int64_t T, int64_t k, int64_t E,
+                                                      int64_t d_ff, int64_t d);
+
+/*
  * As swiglu_up, for callers that cannot allocate device memory.  Some
  * callers may not call cudaMalloc (or any allocator) while they run this
  * operation: a host framework that invokes operators from an enqueue

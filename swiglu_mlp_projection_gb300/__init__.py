@@ -484,7 +484,13 @@ def version():
     return int(_lib.load().swiglu_version())
 
 
-__all__ = ["swiglu_up", "swiglu_down", "swiglu_mlp", "workspace_bytes",
+from .moe import (Routing, dispatch, experts_down, experts_down_workspace_bytes,  # noqa: E402
+                  experts_up, experts_up_workspace_bytes, linear, linear_workspace_bytes,
+                  route, swiglu_moe)
+
+__all__ = ["linear", "route", "dispatch", "experts_up", "experts_down", "swiglu_moe", "Routing",
+           "linear_workspace_bytes", "experts_up_workspace_bytes",
+           "experts_down_workspace_bytes", "swiglu_up", "swiglu_down", "swiglu_mlp", "workspace_bytes",
            "down_workspace_bytes", "plan", "down_plan", "split_k_slices",
            "check_device_status", "release_stream_workspace", "release_workspaces",
            "cached_workspace_bytes", "version", "SwiGLUError", "PATHS"]

@@ -23,6 +23,7 @@ STATUS_NAMES = {
 
 # Every symbol include/swiglu.h declares, with its ctypes signature.
 _i64, _vp, _int, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_flt = ctypes.c_float
 
 
 class PlanInfo(ctypes.Structure):
@@ -51,6 +52,18 @@ SIGNATURES = {
     "swiglu_pack_weights": ([_vp, _vp, _vp, _i64, _i64, _int, _vp], _int),
     "swiglu_up_packed": ([_vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _vp, _sz, _vp], _int),
     "swiglu_mlp": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp], _int),
+    "swiglu_linear": ([_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _int, _int, _vp,
+                       _sz, _vp], _int),
+    "swiglu_linear_workspace_bytes": ([_i64, _i64, _i64], _sz),
+    "swiglu_route": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _i64, _i64,
+                      _int, _int, _flt, _vp], _int),
+    "swiglu_dispatch": ([_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp], _int),
+    "swiglu_experts_up": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int, _vp,
+                           _sz, _vp], _int),
+    "swiglu_experts_up_workspace_bytes": ([_i64, _i64, _i64, _i64, _i64], _sz),
+    "swiglu_experts_down": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int,
+                             _vp, _sz, _vp], _int),
+    "swiglu_experts_down_workspace_bytes": ([_i64, _i64, _i64, _i64, _i64], _sz),
     "swiglu_down_plan": ([_i64, _i64, _i64, _int, _int, _int, ctypes.POINTER(PlanInfo)], _int),
     "swiglu_workspace_bytes": ([_i64, _i64, _i64, _int, _int], _sz),
     "swiglu_plan": ([_i64, _i64, _i64, _int, _int, _int, ctypes.POINTER(PlanInfo)], _int),

@@ -1,0 +1,849 @@
+// Grouped products on the tensor cores (bf16): every expert's rows of x times
+// that expert's weights, in one launch, and the general linear product as the
+// case of one group.
+//
+//   experts, up:    h[r]  = silu(x[t(r)] . W_gate[e]) * (x[t(r)] . W_up[e])
+//   experts, down:  z[r]  = h[r] . W_down[e]        (weighted and added up over
+//                                                    a token's choices afterwards)
+//   linear:         y[m]  = act(x[m] . W + bias) + residual[m]
+//
+// Rows r are sorted by expert; offsets[e] .. offsets[e + 1] are expert e's.
+// They are known on the device only, so the kernel plans its own work: a
+// chunk is up to n_max rows of one expert (an expert's rows are spread evenly
+// over its chunks), a unit is a chunk and a group of output columns, and the
+// grid is one CTA pair per two SMs, whatever the routing.
+//
+// Orientation: the weights are the MMA's A operand and the rows its B operand
+// (D^T = W^T x^T), because the count of rows varies from one to thousands and
+// N takes any multiple of 32, where M is 256.  A row too many costs 1/32 of a
+// step instead of a 256-row tile: 64 experts of 512 +- 150 rows would
+// waste about a quarter of 256-row tiles.
+//
+// A pair (cta_group::2) computes 256 rows of W^T times N <= 256 rows of x;
+// each CTA stages 128 weight columns and half of the x rows per 64-deep k
+// block.  SwiGLU: a CTA's 128 weight columns are 64 gate columns and the 64
+// up columns with the same indices, so a unit is 128 columns of h and gate and
+// up meet in one CTA (through shared memory, in the epilogue).  Otherwise a
+// unit is 256 adjacent output columns.
+//
+// Units run whole, round robin, as long as they fill the pairs; the units of
+// a last, partial wave are cut along K in equal shares (a share ends inside a
+// unit: its pair writes the f32 sums so far to the workspace, and the pair
+// that arrives last adds them in k order and runs the epilogue).  No output
+// depends on the order of arrival.
+#include <atomic>
+
+#include "common.cuh"
+#include "grouped.h"
+#include "internal.h"
+#include "tc_common.cuh"
+#include "tc_pair.cuh"
+
+namespace swg {
+namespace {
+
+using namespace tc;
+
+constexpr int kBK = 64;
+constexpr int kThreads = 192;
+constexpr int kEpiThreads = 128;
+constexpr uint32_t kChunkBytes = 64 * kBK * 2;    // one 64-column weight box
+constexpr uint32_t kABytes = 2 * kChunkBytes;     // a CTA's 128 weight columns
+constexpr uint32_t kRowBoxBytes = 16 * kBK * 2;   // one 16-row box of x
+constexpr uint32_t kRingBytes = 192u * 1024u;
+constexpr int kMaxStages = 12;
+constexpr uint32_t kTmemCols = 512;               // two accumulators of up to 256 columns
+constexpr int kAccCols = 256;
+constexpr int kStageCols = 132;                   // f32 staging row: 128 columns and 16 bytes
+constexpr uint32_t kStagingBytes = 32 * kStageCols * 4;
+constexpr size_t kFixedBytes = 1024 + kStagingBytes + (2 * kMaxStages + 5) * 8 + 64;
+
+struct Args {
+  const int* offsets;      // [E + 1]; null: one group of `rows` rows
+  const int* order;        // up: sorted row -> token * top_k + choice
+  int E, top_k, tokens;
+  int rows;                // rows of the sorted operand (an upper bound of offsets[E])
+  int n_kb, n_out;
+  int ncg;                 // column groups (units) per chunk
+  int n_max;               // most rows of a chunk, a multiple of 32
+  int stages;
+  uint32_t stage_bytes;
+  int kmajor;              // weights stored [n_out, K]
+  int min_kb;              // fewest k blocks of a share of a cut unit
+  void* out;
+  int out_f32;
+  const void* bias;        // linear
+  int bias_f32, act;
+  const void* resid;       // linear, in the output's type
+  float* part;
+  unsigned* counters;      // two per pair, zero on entry, left at zero
+  unsigned* status;
+  uint64_t timeout_ns;
+};
+
+// The work of a launch, from the offsets; the same in every thread.
+struct Schedule {
+  int64_t units, whole;    // units [0, whole) run whole
+  int64_t cut_iters, q;    // the others: k blocks in all, and per pair
+};
+
+struct Unit {
+  int e, col0, row0, nrows, n;   // n: nrows rounded up to a multiple of 32
+};
+
+// First row of expert e, within the rows there are (whatever the caller's
+// offsets say, no row outside them is touched).
+__device__ __forceinline__ int first_row(const Args& a, int e) {
+  if (!a.offsets) return e == 0 ? 0 : a.rows;
+  const int v = a.offsets[e];
+  return v < 0 ? 0 : v > a.rows ? a.rows : v;
+}
+
+// s_row[e], s_chunk[e]: first row and first chunk of expert e (E + 1 entries).
+__device__ void plan_chunks(const Args& a, int* s_row, int* s_chunk) {
+  for (int e = threadIdx.x; e <= a.E; e += kThreads) s_row[e] = first_row(a, e);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int base = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + (int)threadIdx.x;
+      int c = 0;
+      if (e < a.E) {
+        const int m = s_row[e + 1] - s_row[e];
+        c = m > 0 ? (m + a.n_max - 1) / a.n_max : 0;
+      }
+      int inc = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if ((int)threadIdx.x >= o) inc += v;
+      }
+      if (e < a.E) s_chunk[e] = base + inc - c;
+      base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (threadIdx.x == 0) s_chunk[a.E] = base;
+  }
+}
+
+__device__ __forceinline__ Schedule make_schedule(const Args& a, int64_t chunks, int64_t pairs) {
+  Schedule s;
+  s.units = chunks * a.ncg;
+  s.whole = s.units;
+  s.cut_iters = 0;
+  s.q = 1;
+  const int64_t rem = s.units % pairs;
+  if (rem * 4 <= pairs * 3 && rem > 0) {
+    int64_t q = (rem * a.n_kb + pairs - 1) / pairs;
+    if (q < a.min_kb) q = a.min_kb;
+    if (q < a.n_kb) {
+      s.whole = s.units - rem;
+      s.cut_iters = rem * a.n_kb;
+      s.q = q;
+    }
+  }
+  return s;
+}
+
+// The work items of one pair: whole units, then its share of the cut units.
+struct WorkIter {
+  int64_t u_next, it, it_end;
+  __device__ WorkIter(const Schedule& s, int64_t pair) : u_next(pair) {
+    it = pair * s.q < s.cut_iters ? pair * s.q : s.cut_iters;
+    it_end = (pair + 1) * s.q < s.cut_iters ? (pair + 1) * s.q : s.cut_iters;
+  }
+  __device__ bool next(const Args& a, const Schedule& s, int64_t pairs, int64_t& u, int& kb0,
+                       int& kb1) {
+    if (u_next < s.whole) {
+      u = u_next;
+      u_next += pairs;
+      kb0 = 0;
+      kb1 = a.n_kb;
+      return true;
+    }
+    if (it < it_end) {
+      const int64_t rel = it / a.n_kb;
+      const int64_t stop = (rel + 1) * a.n_kb < it_end ? (rel + 1) * a.n_kb : it_end;
+      u = s.whole + rel;
+      kb0 = (int)(it - rel * a.n_kb);
+      kb1 = (int)(stop - rel * a.n_kb);
+      it = stop;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Unit u: units run expert by expert, column group by column group, chunk by
+// chunk, so that the pairs at work share an expert's weights and rows in L2.
+template <int COLS>
+__device__ __forceinline__ Unit find_unit(const Args& a, const int* s_row, const int* s_chunk,
+                                          int64_t u) {
+  const int c = (int)(u / a.ncg);
+  int lo = 0, hi = a.E;   // s_chunk[lo] <= c < s_chunk[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s_chunk[mid] <= c) lo = mid;
+    else hi = mid;
+  }
+  const int nc = s_chunk[lo + 1] - s_chunk[lo];
+  const int l = (int)(u - (int64_t)s_chunk[lo] * a.ncg);
+  const int cg = l / nc, chunk = l - cg * nc;
+  const int m = s_row[lo + 1] - s_row[lo];
+  const int per = (m + nc - 1) / nc;
+  Unit r;
+  r.e = lo;
+  r.col0 = cg * COLS;
+  r.row0 = s_row[lo] + chunk * per;
+  int n = m - chunk * per;
+  if (n > per) n = per;
+  if (n < 0) n = 0;
+  r.nrows = n;
+  r.n = n <= 32 ? 32 : (n + 31) / 32 * 32;
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Four rows of a 2-D tensor map whose box is one row high: columns c0 .. of
+// rows r0 .. r3 land below one another (rows outside the tensor read as zero).
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int c0, const int (&r)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+      : "memory");
+}
+
+__device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity, unsigned* status,
+                                           uint64_t timeout_ns) {
+  int never = 0;
+  return mbar_wait(bar, parity, &never, status, timeout_ns);
+}
+
+// act(v).  f32 outputs use the accurate functions; bf16 outputs the fast
+// exponential and divide, whose error (about 2^-21 of the value) is far below
+// the half ulp (2^-9) of the rounding that follows.
+// tanh form: 0.5 v (1 + tanh z) = v sigma(2 z), z = sqrt(2 / pi) (v + 0.044715 v^3).
+__device__ __forceinline__ float activate(float v, int act, bool accurate) {
+  switch (act) {
+    case kActRelu: return v > 0.f ? v : (v != v ? v : 0.f);
+    case kActSilu: return accurate ? silu_accurate(v) : silu_fast(v);
+    case kActGelu: return 0.5f * v * erfcf(-0.70710678118654752f * v);
+    case kActGeluTanh: {
+      const float z2 = 1.5957691216057308f * (v + 0.044715f * v * v * v);
+      return accurate ? v / (1.0f + expf(-z2)) : __fdividef(v, 1.0f + __expf(-z2));
+    }
+    default: return v;
+  }
+}
+
+template <int MODE, bool GATHER>
+__global__ void __launch_bounds__(kThreads, 1)
+grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
+                  const __grid_constant__ CUtensorMap tm_wa,
+                  const __grid_constant__ CUtensorMap tm_wb, const Args a) {
+  constexpr int kCols = MODE == kGroupedSwiGLU ? 128 : 256;   // output columns of a unit
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  uint8_t* stages = smem_raw + pad;
+  float* staging = reinterpret_cast<float*>(stages + (size_t)a.stages * a.stage_bytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(staging) + kStagingBytes);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* tfull = empty + kMaxStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile unsigned* ticket_slot = reinterpret_cast<volatile unsigned*>(tmem_slot + 2);
+  int* s_row = reinterpret_cast<int*>(tmem_slot + 4);
+  int* s_chunk = s_row + a.E + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int64_t pair = (int64_t)(blockIdx.x >> 1);
+  const int64_t pairs = (int64_t)(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      // rank 0's stage is full once its own bytes have landed and rank 1 has
+      // relayed that its half has landed too
+      mbar_init(&full[s], rank == 0 ? 2 : 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 2 * kEpiThreads);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_wa);
+    tma_prefetch_desc(&tm_wb);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  // The set-up above overlaps the previous kernel's tail; the routing, the
+  // operands and the outputs are touched only after it has finished.
+  pdl_wait();
+  pdl_launch_dependents();
+  plan_chunks(a, s_row, s_chunk);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // both CTAs' barriers and TMEM are ready
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // The pair's MMAs address both TMEMs with one column address; if the two
+  // allocations disagree, neither CTA does any work.
+  const bool skip = ld_shared_cluster_u32(mapa_shared(smem_u32(tmem_slot), rank ^ 1u)) != tmem;
+  if (skip && threadIdx.x == 0) atomicOr(a.status, kStatusPairTmem);
+  const Schedule sch = make_schedule(a, s_chunk[a.E], pairs);
+
+  if (warp == 0) {
+    // ---------------- TMA producer (each CTA; the whole warp) ----------------
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = !skip;
+    WorkIter w(sch, pair);
+    int64_t u;
+    int kb0, kb1;
+    while (ok && w.next(a, sch, pairs, u, kb0, kb1)) {
+      const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
+      const int half = un.n >> 1;                          // this CTA's rows of x
+      const int brow = un.row0 + (int)rank * half;
+      // columns of the CTA's two weight boxes
+      const int ca = MODE == kGroupedSwiGLU ? un.col0 + 64 * (int)rank : un.col0 + 128 * (int)rank;
+      const int cb = MODE == kGroupedSwiGLU ? ca : ca + 64;
+      int src[4] = {0, 0, 0, 0};
+      if constexpr (GATHER) {
+        // lane i fetches rows 4 i .. 4 i + 3; rows past the chunk read as zero
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = 4 * lane + q;
+          int t = a.tokens;
+          if (r < half && brow + r < un.row0 + un.nrows) {
+            const int flat = a.order[brow + r];
+            t = flat / a.top_k;
+            if (flat < 0 || t >= a.tokens) t = a.tokens;
+          }
+          src[q] = t;
+        }
+      }
+      for (int kb = kb0; kb < kb1; ++kb) {
+        uint8_t* st = stages + (size_t)stage * a.stage_bytes;
+        if (lane == 0) {
+          ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.status, a.timeout_ns);
+          if (ok) mbar_arrive_expect_tx(&full[stage], kABytes + (uint32_t)half * 128u);
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        if (!ok) break;
+        if (lane == 0) {
+          if (a.kmajor) {
+            tma_load_3d(st, &tm_wa, &full[stage], kb * kBK, ca, un.e);
+            tma_load_3d(st + kChunkBytes, &tm_wb, &full[stage], kb * kBK, cb, un.e);
+          } else {
+            tma_load_3d(st, &tm_wa, &full[stage], ca, kb * kBK, un.e);
+            tma_load_3d(st + kChunkBytes, &tm_wb, &full[stage], cb, kb * kBK, un.e);
+          }
+        }
+        if constexpr (GATHER) {
+          if (4 * lane < half)
+            tma_gather4(st + kABytes + lane * 512, &tm_x, &full[stage], kb * kBK, src);
+        } else {
+          if (16 * lane < half)
+            tma_load_2d(st + kABytes + lane * kRowBoxBytes, &tm_x, &full[stage], kb * kBK,
+                        brow + 16 * lane);
+        }
+        ++issued;
+        if (++stage == a.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (issued > 0 && !ok && lane == 0) {
+      // let the loads still in flight land before the CTA can exit
+      const int64_t first = issued > a.stages ? issued - a.stages : 0;
+      for (int64_t i = first; i < issued; ++i)
+        wait_drain(&full[i % a.stages], (uint32_t)((i / a.stages) & 1), a.status, a.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1 && rank == 0) {
+    // ---------------- MMA issuer (rank 0 of the pair) ----------------
+    if (lane == 0) {
+      const uint32_t a_step = a.kmajor ? 32u : 2048u;
+      const uint32_t a_lbo = a.kmajor ? 16u : kChunkBytes;
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = !skip;
+      WorkIter w(sch, pair);
+      int64_t u;
+      int kb0, kb1;
+      while (ok && w.next(a, sch, pairs, u, kb0, kb1)) {
+        const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
+        // D format f32, A and B bf16; A (weights) MN-major for [K, n_out] weights
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
+                               ((a.kmajor ? 0u : 1u) << 15) | ((uint32_t)(un.n >> 3) << 17) |
+                               (16u << 24);
+        if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, a.status, a.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem + (uint32_t)(acc * kAccCols);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&full[stage], phase, abort_flag, a.status, a.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(stages + (size_t)stage * a.stage_bytes);
+          const uint32_t b_addr = a_addr + kABytes;
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk) {
+            const uint64_t ad = smem_desc_sw128(a_addr + kk * a_step, a_lbo, 1024u);
+            const uint64_t bd = smem_desc_sw128(b_addr + kk * 32u, 16u, 1024u);
+            mma_bf16_pair(d_tmem, ad, bd, idesc, (kb != kb0 || kk != 0) ? 1u : 0u);
+          }
+          mma_commit_pair_mc(&empty[stage], (uint16_t)0x3);
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair_mc(&tfull[acc], (uint16_t)0x3);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      mma_commit_pair(drain);
+      wait_drain(drain, 0, a.status, a.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- rank 1: tell rank 0 when this CTA's half has landed ----------------
+    if (lane == 0) {
+      const uint32_t full0 = mapa_shared(smem_u32(full), 0u);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = !skip;
+      WorkIter w(sch, pair);
+      int64_t u;
+      int kb0, kb1;
+      while (ok && w.next(a, sch, pairs, u, kb0, kb1)) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&full[stage], phase, abort_flag, a.status, a.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_remote(full0 + (uint32_t)stage * 8u);
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- epilogue: warps 2..5 (each CTA) ----------------
+    const int quarter = warp & 3;
+    const int col = quarter * 32 + lane;   // accumulator lane = weight column of this CTA
+    const int et = threadIdx.x - 64;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0u);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    WorkIter w(sch, pair);
+    int64_t u;
+    int kb0, kb1;
+    while (!skip && w.next(a, sch, pairs, u, kb0, kb1)) {
+      const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
+      if (!mbar_wait(&tfull[acc], acc_phase, abort_flag, a.status, a.timeout_ns)) break;
+      tc_fence_after();
+      const uint32_t t_acc = tmem + lane_off + (uint32_t)(acc * kAccCols);
+      const bool whole = kb0 == 0 && kb1 == a.n_kb;
+      const int nchunk = (un.nrows + 31) >> 5;
+      int64_t c0 = 0, rel = 0;
+      int nseg = 0;
+      if (!whole) {
+        // A share of a cut unit: store the sums so far, take a ticket; the
+        // last of the unit's pairs adds all the shares in k order.  A pair's
+        // slot 0 holds the share of the unit its range begins in, slot 1 that
+        // of the unit its range ends in.
+        rel = u - sch.whole;
+        c0 = rel * a.n_kb / sch.q;
+        nseg = (int)(((rel + 1) * a.n_kb - 1) / sch.q - c0 + 1);
+        const int which = pair * sch.q / a.n_kb == rel ? 0 : 1;
+        float* mine = a.part + ((pair * 2 + which) * 2 + rank) * (int64_t)(a.n_max * 128) + col;
+#pragma unroll 1
+        for (int c = 0; c < nchunk; ++c) {
+          uint32_t v[32];
+          tmem_ld_x32(t_acc + (uint32_t)(c * 32), v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c * 32 + i < un.nrows)
+              __stcg(mine + (int64_t)(c * 32 + i) * 128, __uint_as_float(v[i]));
+        }
+        tc_fence_before();
+        if (rank == 1) mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
+        else mbar_arrive(&tempty[acc]);
+        __threadfence();
+        named_bar_sync(1, kEpiThreads);
+        if (et == 0) *ticket_slot = atomicAdd(a.counters + c0 * 2 + rank, 1u);
+        named_bar_sync(1, kEpiThreads);
+        const unsigned ticket = *ticket_slot;
+        if (ticket + 1u != (unsigned)nseg) {
+          // not the last (or a counter left over by a call that gave up)
+          if (ticket >= (unsigned)nseg && et == 0) atomicOr(a.status, kStatusStaleCounter);
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
+          continue;
+        }
+        __threadfence();
+        if (et == 0) a.counters[c0 * 2 + rank] = 0u;   // left at zero for the next call
+      }
+      // this CTA's output columns, and the bias of this thread's column
+      const int cbase = MODE == kGroupedSwiGLU ? un.col0 + 64 * (int)rank
+                                               : un.col0 + 128 * (int)rank;
+      float bias = 0.f;
+      if constexpr (MODE == kGroupedLinear) {
+        if (a.bias && cbase + col < a.n_out)
+          bias = a.bias_f32 ? ((const float*)a.bias)[cbase + col]
+                            : bf16_lo(((const uint16_t*)a.bias)[cbase + col]);
+      }
+#pragma unroll 1
+      for (int c = 0; c < nchunk; ++c) {
+        uint32_t v[32];
+        if (whole) {
+          tmem_ld_x32(t_acc + (uint32_t)(c * 32), v);
+          tmem_wait_ld();
+        } else {
+          float s[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = 0.f;
+#pragma unroll 1
+          for (int sg = 0; sg < nseg; ++sg) {
+            const int64_t p = c0 + sg;
+            const int which = p * sch.q / a.n_kb == rel ? 0 : 1;
+            const float* src = a.part + ((p * 2 + which) * 2 + rank) * (int64_t)(a.n_max * 128) +
+                               (int64_t)(c * 32) * 128 + col;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c * 32 + i < un.nrows) s[i] += __ldcg(src + i * 128);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(s[i]);
+        }
+        if constexpr (MODE == kGroupedSwiGLU) {
+          // Columns 0-63 hold x.W_gate, 64-127 x.W_up of the same 64 columns
+          // of h.  The halves swap 16 rows: the gate threads finish rows 0-15
+          // of the chunk, the up threads rows 16-31.
+          const bool is_up = col >= 64;
+          const int j = col & 63;
+          float* xg = staging;              // [16][64]: gate of rows 16-31
+          float* xu = staging + 16 * 64;    // [16][64]: up of rows 0-15
+          uint16_t* hs = reinterpret_cast<uint16_t*>(staging + 2 * 16 * 64);   // [32][72]
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (is_up) xu[i * 64 + j] = __uint_as_float(v[i]);
+            else xg[i * 64 + j] = __uint_as_float(v[16 + i]);
+          }
+          named_bar_sync(1, kEpiThreads);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float g = is_up ? xg[i * 64 + j] : __uint_as_float(v[i]);
+            const float up = is_up ? __uint_as_float(v[16 + i]) : xu[i * 64 + j];
+            hs[((is_up ? 16 : 0) + i) * 72 + j] = (uint16_t)f32_to_bf16_bits(silu_fast(g) * up);
+          }
+          named_bar_sync(1, kEpiThreads);
+#pragma unroll
+          for (int it = 0; it < 2; ++it) {
+            const int g = it * kEpiThreads + et;
+            const int r = g >> 3, c8 = (g & 7) * 8;
+            if (c * 32 + r < un.nrows && cbase + c8 < a.n_out)
+              *reinterpret_cast<uint4*>((uint16_t*)a.out +
+                                        (int64_t)(un.row0 + c * 32 + r) * a.n_out + cbase + c8) =
+                  *reinterpret_cast<const uint4*>(hs + r * 72 + c8);
+          }
+        } else {
+          if (c) named_bar_sync(1, kEpiThreads);   // the previous chunk has been copied out
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float f = __uint_as_float(v[i]);
+            if constexpr (MODE == kGroupedLinear) f = activate(f + bias, a.act, a.out_f32 != 0);
+            staging[i * kStageCols + col] = f;
+          }
+          named_bar_sync(1, kEpiThreads);
+#pragma unroll
+          for (int it = 0; it < 4; ++it) {
+            const int g = it * kEpiThreads + et;
+            const int r = g >> 4, c8 = (g & 15) * 8;
+            if (c * 32 + r >= un.nrows || cbase + c8 >= a.n_out) continue;
+            const int64_t o = (int64_t)(un.row0 + c * 32 + r) * a.n_out + cbase + c8;
+            if (MODE == kGroupedLinear && (a.n_out & 7)) {
+              // rows off 16-byte boundaries: element by element
+              for (int i = 0; i < 8 && cbase + c8 + i < a.n_out; ++i) {
+                float f = staging[r * kStageCols + c8 + i];
+                if (a.out_f32) {
+                  if (a.resid) f += ((const float*)a.resid)[o + i];
+                  ((float*)a.out)[o + i] = f;
+                } else {
+                  if (a.resid) f += bf16_lo(((const uint16_t*)a.resid)[o + i]);
+                  ((uint16_t*)a.out)[o + i] = (uint16_t)f32_to_bf16_bits(f);
+                }
+              }
+              continue;
+            }
+            const float4* sp = reinterpret_cast<const float4*>(staging + r * kStageCols + c8);
+            float4 lo = sp[0], hi = sp[1];
+            if (a.out_f32) {
+              if (MODE == kGroupedLinear && a.resid) {
+                const float4 rl = *reinterpret_cast<const float4*>((const float*)a.resid + o);
+                const float4 rh = *reinterpret_cast<const float4*>((const float*)a.resid + o + 4);
+                lo.x += rl.x; lo.y += rl.y; lo.z += rl.z; lo.w += rl.w;
+                hi.x += rh.x; hi.y += rh.y; hi.z += rh.z; hi.w += rh.w;
+              }
+              float4* dst = reinterpret_cast<float4*>((float*)a.out + o);
+              dst[0] = lo;
+              dst[1] = hi;
+            } else {
+              if (MODE == kGroupedLinear && a.resid) {
+                const uint4 rr = *reinterpret_cast<const uint4*>((const uint16_t*)a.resid + o);
+                lo.x += bf16_lo(rr.x); lo.y += bf16_hi(rr.x);
+                lo.z += bf16_lo(rr.y); lo.w += bf16_hi(rr.y);
+                hi.x += bf16_lo(rr.z); hi.y += bf16_hi(rr.z);
+                hi.z += bf16_lo(rr.w); hi.w += bf16_hi(rr.w);
+              }
+              uint4 q;
+              q.x = pack_bf16x2(lo.x, lo.y);
+              q.y = pack_bf16x2(lo.z, lo.w);
+              q.z = pack_bf16x2(hi.x, hi.y);
+              q.w = pack_bf16x2(hi.z, hi.w);
+              *reinterpret_cast<uint4*>((uint16_t*)a.out + o) = q;
+            }
+          }
+        }
+      }
+      // staging is free, and every accumulator column of this buffer is read
+      named_bar_sync(1, kEpiThreads);
+      if (whole) {
+        tc_fence_before();
+        if (rank == 1) mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
+        else mbar_arrive(&tempty[acc]);
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+    if constexpr (MODE == kGroupedSwiGLU) {
+      // rows that no expert has (dropped choices) are zero
+      const int first = s_row[a.E];
+      const int per = a.n_out / 8;
+      for (int64_t r = first + (int64_t)blockIdx.x; r < a.rows; r += gridDim.x)
+        for (int c8 = et; c8 < per; c8 += kEpiThreads)
+          *reinterpret_cast<uint4*>((uint16_t*)a.out + r * a.n_out + (int64_t)c8 * 8) =
+              make_uint4(0u, 0u, 0u, 0u);
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // Neither CTA of a pair leaves (or frees its TMEM) while the other may still
+  // signal its barriers or read its shared memory.
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// y = act(bias) + residual, for products over nothing (K = 0).
+__global__ void __launch_bounds__(256)
+empty_linear_kernel(const void* bias, int bias_f32, int act, const void* resid, void* y, int out_f32,
+                    int64_t M, int64_t N) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < M * N;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t n = i % N;
+    float v = 0.f;
+    if (bias) v = bias_f32 ? ((const float*)bias)[n] : bf16_lo(((const uint16_t*)bias)[n]);
+    v = activate(v, act, out_f32 != 0);
+    if (resid) v += out_f32 ? ((const float*)resid)[i] : bf16_lo(((const uint16_t*)resid)[i]);
+    if (out_f32) ((float*)y)[i] = v;
+    else ((uint16_t*)y)[i] = (uint16_t)f32_to_bf16_bits(v);
+  }
+}
+
+// [K, N] weights whose rows are no multiple of 16 bytes, copied to rows of
+// round8(N) (zeros behind N), which TMA can read.
+__global__ void __launch_bounds__(256)
+pad_rows_kernel(const uint16_t* __restrict__ w, uint16_t* __restrict__ out, int64_t K, int64_t N,
+                int64_t Np) {
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < K * Np;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t k = i / Np, n = i - k * Np;
+    out[i] = n < N ? w[k * N + n] : (uint16_t)0;
+  }
+}
+
+size_t smem_bytes(const GroupedPlan& p, int E) {
+  return kFixedBytes + (size_t)p.stages * p.stage_bytes + (size_t)(2 * (E + 1)) * sizeof(int);
+}
+
+template <int MODE, bool GATHER>
+cudaError_t launch_mode(const CUtensorMap& mx, const CUtensorMap& ma, const CUtensorMap& mb,
+                        const Args& a, int pairs, size_t smem, cudaStream_t st) {
+  auto kern = grouped_tc_kernel<MODE, GATHER>;
+  static std::atomic<int> configured[64];   // zero: not yet set on that device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) configured[dev].store(1, std::memory_order_release);
+  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, mx, ma, mb, a);
+}
+
+}  // namespace
+
+GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, int64_t K, int64_t n_out,
+                         bool swiglu, int pairs) {
+  GroupedPlan p{};
+  // Rows per chunk.  An expert has at most `tokens` rows (a token chooses it
+  // once) and rows / E on average; chunks for twice the average keep most
+  // experts in one chunk, so that their weights are read once.
+  int64_t want = E == 1 ? rows : 2 * ((rows + E - 1) / E) + 16;
+  if (want > tokens) want = tokens;
+  if (E == 1 && want > 256) {
+    const int64_t c = (want + 255) / 256;
+    want = (want + c - 1) / c;
+  }
+  if (want > 256) want = 256;
+  p.n_max = (int)((want + 31) / 32 * 32);
+  if (p.n_max < 32) p.n_max = 32;
+  p.stage_bytes = kABytes + (uint32_t)(p.n_max / 2) * 128u;
+  p.stages = (int)(kRingBytes / p.stage_bytes);
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.pairs = pairs < 1 ? 1 : pairs;
+  p.counters_bytes = ((size_t)p.pairs * 2 * sizeof(unsigned) + 255) / 256 * 256;
+  p.part_bytes = (size_t)p.pairs * 4 * (size_t)p.n_max * 128 * sizeof(float);
+  (void)K;
+  (void)n_out;
+  (void)swiglu;
+  return p;
+}
+
+cudaError_t launch_grouped(int mode, const GroupedCall& c, const GroupedPlan& p, float* part,
+                           unsigned* counters, bool counters_clean, unsigned* status,
+                           uint64_t timeout_ns, cudaStream_t st) {
+  if (c.rows == 0 || c.n_out == 0) return cudaSuccess;
+  cudaError_t e;
+  if (c.K == 0) {
+    if (mode != kGroupedLinear)
+      return cudaMemsetAsync(c.out, 0, (size_t)c.rows * c.n_out * (c.out_f32 ? 4 : 2), st);
+    int64_t blocks = (c.rows * c.n_out + 255) / 256;
+    if (blocks > 1216) blocks = 1216;
+    empty_linear_kernel<<<(unsigned)blocks, 256, 0, st>>>(c.bias, c.bias_f32, c.act, c.resid, c.out,
+                                                         c.out_f32, c.rows, c.n_out);
+    return cudaGetLastError();
+  }
+  CUtensorMap mx, ma, mb;
+  const bool gather = mode == kGroupedSwiGLU;
+  const int64_t xrows = gather ? c.tokens : c.rows;
+  if ((e = make_tmap_bf16_2d(&mx, c.x, xrows, c.K, kBK, gather ? 1 : 16)) != cudaSuccess) return e;
+  const bool kmajor = c.wlayout == kWeightsNK;
+  const void* wa = c.wa;
+  int64_t wcols = c.n_out;
+  if (!kmajor && c.n_out % 8 != 0) {
+    if (!c.padded || mode != kGroupedLinear) return cudaErrorInvalidValue;
+    wcols = (c.n_out + 7) / 8 * 8;
+    int64_t blocks = (c.K * wcols + 255) / 256;
+    if (blocks > 1216) blocks = 1216;
+    pad_rows_kernel<<<(unsigned)blocks, 256, 0, st>>>((const uint16_t*)c.wa, (uint16_t*)c.padded,
+                                                     c.K, c.n_out, wcols);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    wa = c.padded;
+  }
+  const int64_t wr = kmajor ? c.n_out : c.K, wc = kmajor ? c.K : wcols;
+  if ((e = make_tmap_bf16_3d(&ma, wa, c.E, wr, wc, 64, 64)) != cudaSuccess) return e;
+  if (mode == kGroupedSwiGLU) {
+    if ((e = make_tmap_bf16_3d(&mb, c.wb, c.E, wr, wc, 64, 64)) != cudaSuccess) return e;
+  } else {
+    mb = ma;
+  }
+  Args a{};
+  a.offsets = c.offsets;
+  a.order = c.order;
+  a.E = (int)c.E;
+  a.top_k = (int)(c.top_k > 0 ? c.top_k : 1);
+  a.tokens = (int)c.tokens;
+  a.rows = (int)c.rows;
+  a.n_kb = (int)((c.K + kBK - 1) / kBK);
+  a.n_out = (int)c.n_out;
+  const int cols = mode == kGroupedSwiGLU ? 128 : 256;
+  a.ncg = (int)((c.n_out + cols - 1) / cols);
+  a.n_max = p.n_max;
+  a.stages = p.stages;
+  a.stage_bytes = p.stage_bytes;
+  a.kmajor = kmajor ? 1 : 0;
+  a.min_kb = 4;
+  a.out = c.out;
+  a.out_f32 = c.out_f32;
+  a.bias = c.bias;
+  a.bias_f32 = c.bias_f32;
+  a.act = c.act;
+  a.resid = c.resid;
+  a.part = part;
+  a.counters = counters;
+  a.status = status;
+  a.timeout_ns = timeout_ns;
+  if (!counters_clean &&
+      (e = cudaMemsetAsync(counters, 0, p.counters_bytes, st)) != cudaSuccess)
+    return e;
+  const size_t smem = smem_bytes(p, a.E);
+  switch (mode) {
+    case kGroupedSwiGLU: return launch_mode<kGroupedSwiGLU, true>(mx, ma, mb, a, p.pairs, smem, st);
+    case kGroupedPlain: return launch_mode<kGroupedPlain, false>(mx, ma, mb, a, p.pairs, smem, st);
+    default: return launch_mode<kGroupedLinear, false>(mx, ma, mb, a, p.pairs, smem, st);
+  }
+}
+
+}  // namespace swg

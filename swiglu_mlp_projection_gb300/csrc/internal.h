@@ -110,11 +110,30 @@ int api_fail(int status, const char* detail);
 int api_cuda_fail(cudaError_t e, const char* what);
 void api_clear_error();
 unsigned* api_status_word(int dev);   // device address of the error word
+uint64_t api_wait_timeout_ns();       // bound of every device-side wait
+int api_max_pairs(int dev);           // 2-CTA clusters of the tile kernel that fit at once
+
+
+// The workspace of one call: arrival counters and a body of partial sums,
+// 256-byte aligned: in the caller's buffer (checked), the stream's cached one,
+// a captured call's slice or a per-call allocation (`pooled`, which the caller
+// frees on the stream after its launches).
+struct Workspace {
+  unsigned* counters = nullptr;
+  char* body = nullptr;
+  bool counters_clean = false;   // the counters are zero already
+  void* pooled = nullptr;
+};
+int api_take_workspace(int dev, cudaStream_t st, void* caller, size_t caller_bytes,
+                       size_t counter_bytes, size_t body_bytes, Workspace* ws);
 constexpr int64_t kSimtMaxGridYZ = 65535;
 
 // TMA descriptor of a row-major bf16 matrix [rows, cols], 128-byte swizzle.
 cudaError_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
                               int box_cols, int box_rows, int l2_promo_bytes = 256);
+// `depth` such matrices, one after another (coordinates column, row, matrix).
+cudaError_t make_tmap_bf16_3d(CUtensorMap* map, const void* base, int64_t depth, int64_t rows,
+                              int64_t cols, int box_cols, int box_rows, int l2_promo_bytes = 256);
 
 // Skinny tensor-core path (bf16, small M): swap-AB split-K over a balanced
 // partition of (64-column block, 64-deep k block) units.

@@ -370,6 +370,73 @@ unsigned* take_graph_counters(int dev, size_t bytes) {
   return r;
 }
 
+// Where a call without a caller workspace keeps its arrival counters and its
+// `body_bytes` of partial sums:
+//   the stream's cached buffer -> counters already zero;
+//   a captured call -> its capture's slice (see GraphSlice), counters zero;
+//   else a per-call pool allocation -> counters to be cleared (a captured call
+//   takes zero ones from the graph-counter region when it can, see
+//   GraphCounters, and allocates only the rest).
+int take_workspace(int dev, cudaStream_t st, size_t counter_bytes, size_t body_bytes,
+                   bool inject_oom, Workspace* ws) {
+  int v;
+  *ws = Workspace{};
+  float* part = nullptr;
+  unsigned* counters = nullptr;
+  if (!inject_oom &&
+      (v = stream_workspace(dev, st, body_bytes, &part, &counters)) != SWIGLU_OK)
+    return v;
+  if (part) {
+    ws->counters = counters;
+    ws->counters_clean = true;
+    ws->body = (char*)part;
+    if (counter_bytes) ensure_graph_counters(dev, st);
+    return SWIGLU_OK;
+  }
+  // The calls of one capture share a slice and may need different counts of
+  // counters; the body starts behind a region as large as any of them, so that
+  // no call's sums land where a later call expects zeros.
+  const size_t slice_counters =
+      counter_bytes > kStreamCounterBytes ? counter_bytes : kStreamCounterBytes;
+  if (char* gw = inject_oom ? nullptr : graph_workspace(dev, st, slice_counters + body_bytes)) {
+    ws->counters = (unsigned*)gw;
+    ws->counters_clean = true;
+    ws->body = gw + slice_counters;
+    return SWIGLU_OK;
+  }
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (counter_bytes && !inject_oom && cudaStreamIsCapturing(st, &cs) == cudaSuccess &&
+      cs != cudaStreamCaptureStatusNone)
+    counters = take_graph_counters(dev, counter_bytes);
+  cudaGetLastError();
+  const size_t own = counters ? body_bytes : counter_bytes + body_bytes;
+  if (own > 0 && inject_oom)
+    return fail(SWIGLU_ERR_OOM, "workspace of %zu bytes: allocation failure injected "
+                "(SWIGLU_INJECT_OOM)", own);
+  if (own > 0) {
+    cudaMemPool_t pool;
+    if ((v = device_pool(dev, &pool)) != SWIGLU_OK) return v;
+    cudaError_t e = cudaMallocFromPoolAsync(&ws->pooled, own, pool, st);
+    if (e != cudaSuccess) {
+      ws->pooled = nullptr;
+      if (e == cudaErrorMemoryAllocation) {
+        cudaGetLastError();
+        return fail(SWIGLU_ERR_OOM, "workspace of %zu bytes: %s", own, cudaGetErrorString(e));
+      }
+      return cuda_fail(e, "cudaMallocFromPoolAsync");
+    }
+  }
+  if (counters) {
+    ws->counters = counters;
+    ws->counters_clean = true;
+    ws->body = (char*)ws->pooled;
+  } else {
+    ws->counters = (unsigned*)ws->pooled;
+    ws->body = (char*)ws->pooled + counter_bytes;
+  }
+  return SWIGLU_OK;
+}
+
 int elem_bytes(int dtype) { return dtype == SWIGLU_BF16 ? 2 : 4; }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -694,8 +761,7 @@ int run(const Call& c) {
 
   // Where the partial sums (and the arrival counters) live:
   //   caller workspace -> [counters][partials] inside it, counters cleared;
-  //   else the stream's cached buffer -> counters already zero;
-  //   else a per-call pool allocation -> counters cleared.
+  //   else take_workspace finds them.
   // An FP8 call keeps x's codes and row scales ahead of them: at the start
   // of a caller workspace (a documented layout), else at the start of the
   // partial-sum region.
@@ -717,54 +783,15 @@ int run(const Call& c) {
       counters = (unsigned*)((char*)c.workspace + fp8_prefix);
       part = (float*)((char*)c.workspace + fp8_prefix + counter_bytes);
     } else {
-      if (!p.inject_oom &&
-          (v = stream_workspace(dev, st, p.workspace - counter_bytes, &part, &counters)) != SWIGLU_OK)
+      Workspace ws;
+      if ((v = take_workspace(dev, st, counter_bytes, p.workspace - counter_bytes, p.inject_oom,
+                              &ws)) != SWIGLU_OK)
         return v;
-      if (part) {
-        counters_clean = true;
-        fp8_base = (char*)part;
-        part = (float*)((char*)part + fp8_prefix);
-        if (counter_bytes) ensure_graph_counters(dev, st);
-      } else if (char* gw = p.inject_oom ? nullptr : graph_workspace(dev, st, p.workspace)) {
-        // a captured call: its capture's slice (see GraphSlice), counters clean
-        counters = (unsigned*)gw;
-        counters_clean = true;
-        fp8_base = gw + counter_bytes;
-        part = (float*)(fp8_base + fp8_prefix);
-      } else {
-        // A captured call takes clean counters from the graph-counter region
-        // when it can (see GraphCounters) and allocates only the rest.
-        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-        if (counter_bytes && !p.inject_oom && cudaStreamIsCapturing(st, &cs) == cudaSuccess &&
-            cs != cudaStreamCaptureStatusNone)
-          counters = take_graph_counters(dev, counter_bytes);
-        cudaGetLastError();
-        const size_t own = counters ? p.workspace - counter_bytes : p.workspace;
-        if (own > 0 && p.inject_oom)
-          return fail(SWIGLU_ERR_OOM, "workspace of %zu bytes: allocation failure injected "
-                      "(SWIGLU_INJECT_OOM)", own);
-        if (own > 0) {
-          cudaMemPool_t pool;
-          if ((v = device_pool(dev, &pool)) != SWIGLU_OK) return v;
-          cudaError_t e = cudaMallocFromPoolAsync(&pooled, own, pool, st);
-          if (e != cudaSuccess) {
-            if (e == cudaErrorMemoryAllocation) {
-              cudaGetLastError();
-              return fail(SWIGLU_ERR_OOM, "workspace of %zu bytes: %s", own,
-                          cudaGetErrorString(e));
-            }
-            return cuda_fail(e, "cudaMallocFromPoolAsync");
-          }
-        }
-        if (counters) {
-          counters_clean = true;
-          fp8_base = (char*)pooled;
-        } else {
-          counters = (unsigned*)pooled;
-          fp8_base = (char*)pooled + counter_bytes;
-        }
-        part = (float*)(fp8_base + fp8_prefix);
-      }
+      counters = ws.counters;
+      counters_clean = ws.counters_clean;
+      pooled = ws.pooled;
+      fp8_base = ws.body;
+      part = (float*)(fp8_base + fp8_prefix);
     }
   }
 
@@ -892,6 +919,27 @@ int api_fail(int status, const char* detail) { return fail(status, "%s", detail)
 int api_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
 
 void api_clear_error() { t_err[0] = 0; }
+
+uint64_t api_wait_timeout_ns() { return wait_timeout_ns(); }
+
+int api_max_pairs(int dev) {
+  if (dev < 0 || dev >= kMaxDevices) return 0;
+  std::lock_guard<std::mutex> lk(g_mu);
+  return g_dev[dev].max_pairs;
+}
+
+int api_take_workspace(int dev, cudaStream_t st, void* caller, size_t caller_bytes,
+                       size_t counter_bytes, size_t body_bytes, Workspace* ws) {
+  if (!caller)
+    return take_workspace(dev, st, counter_bytes, body_bytes, read_tuning().inject_oom != 0, ws);
+  if (caller_bytes < counter_bytes + body_bytes || ((uintptr_t)caller & 255u))
+    return fail(SWIGLU_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)",
+                counter_bytes + body_bytes, caller_bytes);
+  *ws = Workspace{};
+  ws->counters = (unsigned*)caller;
+  ws->body = (char*)caller + counter_bytes;
+  return SWIGLU_OK;
+}
 
 unsigned* api_status_word(int dev) {
   if (dev < 0 || dev >= kMaxDevices) return nullptr;

@@ -37,10 +37,11 @@ namespace {
 // the memory at `base` has been freed and reused.
 struct TmapKey {
   const void* base;
+  int64_t depth;   // matrices, one after another (0: a 2-D map)
   int64_t rows, cols;
   int box_cols, box_rows, promo;
   bool operator==(const TmapKey& o) const {
-    return base == o.base && rows == o.rows && cols == o.cols && box_cols == o.box_cols &&
+    return base == o.base && depth == o.depth && rows == o.rows && cols == o.cols && box_cols == o.box_cols &&
            box_rows == o.box_rows && promo == o.promo;
   }
 };
@@ -56,14 +57,12 @@ std::mutex g_cache_mu;
 size_t slot_of(const TmapKey& k) {
   uint64_t h = (uint64_t)(uintptr_t)k.base * 0x9E3779B97F4A7C15ull;
   h ^= (uint64_t)k.rows * 0xC2B2AE3D27D4EB4Full + (uint64_t)k.cols;
+  h ^= (uint64_t)k.depth * 0x9FB21C651E98DF25ull;
   h ^= (uint64_t)(k.box_cols * 131 + k.box_rows * 7 + k.promo) * 0x165667B19E3779F9ull;
   return (size_t)((h >> 17) % kCacheSlots);
 }
-}  // namespace
 
-cudaError_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
-                              int box_cols, int box_rows, int l2_promo_bytes) {
-  const TmapKey key{base, rows, cols, box_cols, box_rows, l2_promo_bytes};
+cudaError_t make_tmap(CUtensorMap* map, const TmapKey& key) {
   const size_t slot = slot_of(key);
   {
     std::lock_guard<std::mutex> lk(g_cache_mu);
@@ -75,18 +74,18 @@ cudaError_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, int64_t rows, 
   std::call_once(g_once, init_encode);
   if (!g_encode) return g_init_err != cudaSuccess ? g_init_err : cudaErrorSymbolNotFound;
   // A tensor map needs every extent >= 1; callers never ask for empty maps.
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-  cuuint32_t elem_strides[2] = {1, 1};
+  cuuint64_t dims[3] = {(cuuint64_t)key.cols, (cuuint64_t)key.rows, (cuuint64_t)key.depth};
+  cuuint64_t strides[2] = {(cuuint64_t)key.cols * 2, (cuuint64_t)key.cols * 2 * (cuuint64_t)key.rows};
+  cuuint32_t box[3] = {(cuuint32_t)key.box_cols, (cuuint32_t)key.box_rows, 1};
+  cuuint32_t elem_strides[3] = {1, 1, 1};
   const CUtensorMapL2promotion promo =
-      l2_promo_bytes >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
-      : l2_promo_bytes >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
-      : l2_promo_bytes >= 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
-                             : CU_TENSOR_MAP_L2_PROMOTION_NONE;
-  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
-                        strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, promo,
+      key.promo >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+      : key.promo >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+      : key.promo >= 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                        : CU_TENSOR_MAP_L2_PROMOTION_NONE;
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, key.depth > 0 ? 3 : 2,
+                        const_cast<void*>(key.base), dims, strides, box, elem_strides,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promo,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
   std::lock_guard<std::mutex> lk(g_cache_mu);
@@ -94,6 +93,20 @@ cudaError_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, int64_t rows, 
   g_cache[slot].map = *map;
   g_cache[slot].valid = true;
   return cudaSuccess;
+}
+}  // namespace
+
+cudaError_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
+                              int box_cols, int box_rows, int l2_promo_bytes) {
+  return make_tmap(map, TmapKey{base, 0, rows, cols, box_cols, box_rows, l2_promo_bytes});
+}
+
+// `depth` such matrices one after another, a box within one of them:
+// coordinates (column, row, matrix).  Rows past a matrix's end read as zero,
+// not as the next matrix.
+cudaError_t make_tmap_bf16_3d(CUtensorMap* map, const void* base, int64_t depth, int64_t rows,
+                              int64_t cols, int box_cols, int box_rows, int l2_promo_bytes) {
+  return make_tmap(map, TmapKey{base, depth, rows, cols, box_cols, box_rows, l2_promo_bytes});
 }
 
 }  // namespace swg
