@@ -45,20 +45,37 @@ namespace {
 using namespace tc;
 
 constexpr int kBK = 64;
-constexpr int kThreads = 192;
-constexpr int kEpiThreads = 128;
+// Warps: 0 loads weights (TMA), 1 issues MMAs (rank 0) or relays (rank 1),
+// 2-9 are the epilogue (two groups of four, each covering the 128 accumulator
+// lanes), 10 and up load rows (one warp of TMA, or four of cp.async).
+constexpr int kEpiThreads = 128;                  // one epilogue group
+constexpr int kRowWarp = 10;
+constexpr int kGatherThreads = 128;
+constexpr int threads_of(bool gather) { return kRowWarp * 32 + (gather ? kGatherThreads : 32); }
 constexpr uint32_t kChunkBytes = 64 * kBK * 2;    // one 64-column weight box
 constexpr uint32_t kABytes = 2 * kChunkBytes;     // a CTA's 128 weight columns
-constexpr uint32_t kRowBoxBytes = 16 * kBK * 2;   // one 16-row box of x
 constexpr uint32_t kRingBytes = 192u * 1024u;
 constexpr int kMaxStages = 12;
 constexpr uint32_t kTmemCols = 512;               // two accumulators of up to 256 columns
 constexpr int kAccCols = 256;
-constexpr int kStageCols = 132;                   // f32 staging row: 128 columns and 16 bytes
-constexpr uint32_t kStagingBytes = 32 * kStageCols * 4;
-constexpr size_t kFixedBytes = 1024 + kStagingBytes + (2 * kMaxStages + 5) * 8 + 64;
+// An epilogue group's staging.  SwiGLU: halves of 32 rows of gate and up,
+// [16][64] f32 each, and 32 rows of h, [32][72] bf16; otherwise 16 rows of
+// f32, [16][132] (128 columns and 16 bytes, against bank conflicts).
+constexpr int kStageCols = 132, kHCols = 72;
+constexpr uint32_t kStagingBytes = 2 * 16 * 64 * 4 + 32 * kHCols * 2;
+static_assert(kStagingBytes >= 16 * kStageCols * 4, "staging too small");
+constexpr size_t kFixedBytes = 1024 + 2 * kStagingBytes + (2 * kMaxStages + 5) * 8 + 64;
+static_assert(kFixedBytes + kRingBytes + 2 * (kMaxExperts + 1) * 4 <= 232448,
+              "shared memory exceeded");
+
+// Tensor maps of the row operand with boxes of 128, 64, 32 and 16 rows.
+struct RowMaps {
+  CUtensorMap box[4];
+};
 
 struct Args {
+  const uint16_t* x;       // gathered rows: [tokens, K]
+  int K;
   const int* offsets;      // [E + 1]; null: one group of `rows` rows
   const int* order;        // up: sorted row -> token * top_k + choice
   int E, top_k, tokens;
@@ -81,10 +98,12 @@ struct Args {
   uint64_t timeout_ns;
 };
 
-// The work of a launch, from the offsets; the same in every thread.
+// The work of a launch, from the offsets; the same in every thread.  (Units
+// fit 32 bits: a unit is at least 128 columns of at least one row.)
 struct Schedule {
-  int64_t units, whole;    // units [0, whole) run whole
-  int64_t cut_iters, q;    // the others: k blocks in all, and per pair
+  uint32_t units, whole;   // units [0, whole) run whole
+  uint32_t cut_iters, q;   // the others (fewer than one per pair): k blocks in
+                           // all, and per pair
 };
 
 struct Unit {
@@ -101,7 +120,7 @@ __device__ __forceinline__ int first_row(const Args& a, int e) {
 
 // s_row[e], s_chunk[e]: first row and first chunk of expert e (E + 1 entries).
 __device__ void plan_chunks(const Args& a, int* s_row, int* s_chunk) {
-  for (int e = threadIdx.x; e <= a.E; e += kThreads) s_row[e] = first_row(a, e);
+  for (int e = threadIdx.x; e <= a.E; e += blockDim.x) s_row[e] = first_row(a, e);
   __syncthreads();
   if (threadIdx.x < 32) {
     int base = 0;
@@ -125,19 +144,20 @@ __device__ void plan_chunks(const Args& a, int* s_row, int* s_chunk) {
   }
 }
 
-__device__ __forceinline__ Schedule make_schedule(const Args& a, int64_t chunks, int64_t pairs) {
+__device__ __forceinline__ Schedule make_schedule(const Args& a, uint32_t chunks,
+                                                  uint32_t pairs) {
   Schedule s;
-  s.units = chunks * a.ncg;
+  s.units = chunks * (uint32_t)a.ncg;
   s.whole = s.units;
   s.cut_iters = 0;
   s.q = 1;
-  const int64_t rem = s.units % pairs;
+  const uint32_t rem = s.units % pairs;
   if (rem * 4 <= pairs * 3 && rem > 0) {
-    int64_t q = (rem * a.n_kb + pairs - 1) / pairs;
-    if (q < a.min_kb) q = a.min_kb;
-    if (q < a.n_kb) {
+    uint32_t q = (rem * (uint32_t)a.n_kb + pairs - 1) / pairs;
+    if (q < (uint32_t)a.min_kb) q = a.min_kb;
+    if (q < (uint32_t)a.n_kb) {
       s.whole = s.units - rem;
-      s.cut_iters = rem * a.n_kb;
+      s.cut_iters = rem * (uint32_t)a.n_kb;
       s.q = q;
     }
   }
@@ -146,12 +166,12 @@ __device__ __forceinline__ Schedule make_schedule(const Args& a, int64_t chunks,
 
 // The work items of one pair: whole units, then its share of the cut units.
 struct WorkIter {
-  int64_t u_next, it, it_end;
-  __device__ WorkIter(const Schedule& s, int64_t pair) : u_next(pair) {
+  uint32_t u_next, it, it_end;
+  __device__ WorkIter(const Schedule& s, uint32_t pair) : u_next(pair) {
     it = pair * s.q < s.cut_iters ? pair * s.q : s.cut_iters;
     it_end = (pair + 1) * s.q < s.cut_iters ? (pair + 1) * s.q : s.cut_iters;
   }
-  __device__ bool next(const Args& a, const Schedule& s, int64_t pairs, int64_t& u, int& kb0,
+  __device__ bool next(const Args& a, const Schedule& s, uint32_t pairs, uint32_t& u, int& kb0,
                        int& kb1) {
     if (u_next < s.whole) {
       u = u_next;
@@ -161,11 +181,12 @@ struct WorkIter {
       return true;
     }
     if (it < it_end) {
-      const int64_t rel = it / a.n_kb;
-      const int64_t stop = (rel + 1) * a.n_kb < it_end ? (rel + 1) * a.n_kb : it_end;
+      const uint32_t n_kb = (uint32_t)a.n_kb;
+      const uint32_t rel = it / n_kb;
+      const uint32_t stop = (rel + 1) * n_kb < it_end ? (rel + 1) * n_kb : it_end;
       u = s.whole + rel;
-      kb0 = (int)(it - rel * a.n_kb);
-      kb1 = (int)(stop - rel * a.n_kb);
+      kb0 = (int)(it - rel * n_kb);
+      kb1 = (int)(stop - rel * n_kb);
       it = stop;
       return true;
     }
@@ -177,8 +198,8 @@ struct WorkIter {
 // chunk, so that the pairs at work share an expert's weights and rows in L2.
 template <int COLS>
 __device__ __forceinline__ Unit find_unit(const Args& a, const int* s_row, const int* s_chunk,
-                                          int64_t u) {
-  const int c = (int)(u / a.ncg);
+                                          uint32_t u) {
+  const int c = (int)(u / (uint32_t)a.ncg);
   int lo = 0, hi = a.E;   // s_chunk[lo] <= c < s_chunk[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -186,7 +207,7 @@ __device__ __forceinline__ Unit find_unit(const Args& a, const int* s_row, const
     else hi = mid;
   }
   const int nc = s_chunk[lo + 1] - s_chunk[lo];
-  const int l = (int)(u - (int64_t)s_chunk[lo] * a.ncg);
+  const int l = (int)(u - (uint32_t)s_chunk[lo] * (uint32_t)a.ncg);
   const int cg = l / nc, chunk = l - cg * nc;
   const int m = s_row[lo + 1] - s_row[lo];
   const int per = (m + nc - 1) / nc;
@@ -211,15 +232,17 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// Four rows of a 2-D tensor map whose box is one row high: columns c0 .. of
-// rows r0 .. r3 land below one another (rows outside the tensor read as zero).
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                            int c0, const int (&r)[4]) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(c0), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-      : "memory");
+// 16 bytes global -> shared, asynchronously; `bytes` 0 writes zeros instead.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity, unsigned* status,
@@ -232,30 +255,106 @@ __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity, unsig
 // exponential and divide, whose error (about 2^-21 of the value) is far below
 // the half ulp (2^-9) of the rounding that follows.
 // tanh form: 0.5 v (1 + tanh z) = v sigma(2 z), z = sqrt(2 / pi) (v + 0.044715 v^3).
-__device__ __forceinline__ float activate(float v, int act, bool accurate) {
-  switch (act) {
-    case kActRelu: return v > 0.f ? v : (v != v ? v : 0.f);
-    case kActSilu: return accurate ? silu_accurate(v) : silu_fast(v);
-    case kActGelu: return 0.5f * v * erfcf(-0.70710678118654752f * v);
-    case kActGeluTanh: {
-      const float z2 = 1.5957691216057308f * (v + 0.044715f * v * v * v);
-      return accurate ? v / (1.0f + expf(-z2)) : __fdividef(v, 1.0f + __expf(-z2));
-    }
-    default: return v;
+template <int ACT, bool ACCURATE>
+__device__ __forceinline__ float activate(float v) {
+  if constexpr (ACT == kActRelu) return v > 0.f ? v : (v != v ? v : 0.f);
+  if constexpr (ACT == kActSilu) return ACCURATE ? silu_accurate(v) : silu_fast(v);
+  if constexpr (ACT == kActGelu) return 0.5f * v * erfcf(-0.70710678118654752f * v);
+  if constexpr (ACT == kActGeluTanh) {
+    const float z2 = 1.5957691216057308f * (v + 0.044715f * v * v * v);
+    return ACCURATE ? v / (1.0f + expf(-z2)) : __fdividef(v, 1.0f + __expf(-z2));
+  }
+  return v;
+}
+
+template <int ACT, bool ACCURATE, int N>
+__device__ __forceinline__ void activate_all(float* v) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = activate<ACT, ACCURATE>(v[i]);
+}
+
+template <int N>
+__device__ __forceinline__ void activate_n(float* v, int act, bool accurate) {
+  switch (act * 2 + (accurate ? 1 : 0)) {
+    case kActRelu * 2: case kActRelu * 2 + 1: activate_all<kActRelu, true, N>(v); break;
+    case kActSilu * 2: activate_all<kActSilu, false, N>(v); break;
+    case kActSilu * 2 + 1: activate_all<kActSilu, true, N>(v); break;
+    case kActGelu * 2: case kActGelu * 2 + 1: activate_all<kActGelu, true, N>(v); break;
+    case kActGeluTanh * 2: activate_all<kActGeluTanh, false, N>(v); break;
+    case kActGeluTanh * 2 + 1: activate_all<kActGeluTanh, true, N>(v); break;
+    default: break;
   }
 }
 
+// Two f32 -> packed bf16, to nearest even (`lo` in the low half).
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint16_t cvt_bf16(float v) {
+  uint16_t r;
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(v));
+  return r;
+}
+
+// Up to 8 neighbouring outputs of one row, at element `o`; `left` columns of
+// the row remain from there.
+template <int MODE>
+__device__ __forceinline__ void store_row8(const Args& a, int64_t o, int left, const float* src) {
+  if (MODE == kGroupedLinear && (a.n_out & 7)) {
+    // rows off 16-byte boundaries: element by element
+    for (int i = 0; i < 8 && i < left; ++i) {
+      float f = src[i];
+      if (a.out_f32) {
+        if (a.resid) f += ((const float*)a.resid)[o + i];
+        ((float*)a.out)[o + i] = f;
+      } else {
+        if (a.resid) f += bf16_lo(((const uint16_t*)a.resid)[o + i]);
+        ((uint16_t*)a.out)[o + i] = cvt_bf16(f);
+      }
+    }
+    return;
+  }
+  const float4* sp = reinterpret_cast<const float4*>(src);
+  float4 lo = sp[0], hi = sp[1];
+  if (a.out_f32) {
+    if (MODE == kGroupedLinear && a.resid) {
+      const float4 rl = *reinterpret_cast<const float4*>((const float*)a.resid + o);
+      const float4 rh = *reinterpret_cast<const float4*>((const float*)a.resid + o + 4);
+      lo.x += rl.x; lo.y += rl.y; lo.z += rl.z; lo.w += rl.w;
+      hi.x += rh.x; hi.y += rh.y; hi.z += rh.z; hi.w += rh.w;
+    }
+    float4* dst = reinterpret_cast<float4*>((float*)a.out + o);
+    dst[0] = lo;
+    dst[1] = hi;
+    return;
+  }
+  if (MODE == kGroupedLinear && a.resid) {
+    const uint4 rr = *reinterpret_cast<const uint4*>((const uint16_t*)a.resid + o);
+    lo.x += bf16_lo(rr.x); lo.y += bf16_hi(rr.x);
+    lo.z += bf16_lo(rr.y); lo.w += bf16_hi(rr.y);
+    hi.x += bf16_lo(rr.z); hi.y += bf16_hi(rr.z);
+    hi.z += bf16_lo(rr.w); hi.w += bf16_hi(rr.w);
+  }
+  uint4 q;
+  q.x = cvt_bf16x2(lo.x, lo.y);
+  q.y = cvt_bf16x2(lo.z, lo.w);
+  q.z = cvt_bf16x2(hi.x, hi.y);
+  q.w = cvt_bf16x2(hi.z, hi.w);
+  *reinterpret_cast<uint4*>((uint16_t*)a.out + o) = q;
+}
+
 template <int MODE, bool GATHER>
-__global__ void __launch_bounds__(kThreads, 1)
-grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
-                  const __grid_constant__ CUtensorMap tm_wa,
+__global__ void __launch_bounds__(threads_of(GATHER), 1)
+grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ CUtensorMap tm_wa,
                   const __grid_constant__ CUtensorMap tm_wb, const Args a) {
   constexpr int kCols = MODE == kGroupedSwiGLU ? 128 : 256;   // output columns of a unit
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;
-  float* staging = reinterpret_cast<float*>(stages + (size_t)a.stages * a.stage_bytes);
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(staging) + kStagingBytes);
+  uint8_t* staging_base = stages + (size_t)a.stages * a.stage_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging_base + 2 * kStagingBytes);
   uint64_t* empty = full + kMaxStages;
   uint64_t* tfull = empty + kMaxStages;
   uint64_t* tempty = tfull + 2;
@@ -268,24 +367,25 @@ grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int64_t pair = (int64_t)(blockIdx.x >> 1);
-  const int64_t pairs = (int64_t)(gridDim.x >> 1);
+  const uint32_t pair = blockIdx.x >> 1;
+  const uint32_t pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
+    // A stage is full once the weight box, this CTA's rows (one TMA arrival,
+    // or one per gathering thread) and, on rank 0, rank 1's word that its
+    // half has landed have arrived.
+    const uint32_t arrivals = 1u + (GATHER ? (uint32_t)kGatherThreads : 1u) + (rank == 0 ? 1u : 0u);
     for (int s = 0; s < a.stages; ++s) {
-      // rank 0's stage is full once its own bytes have landed and rank 1 has
-      // relayed that its half has landed too
-      mbar_init(&full[s], rank == 0 ? 2 : 1);
+      mbar_init(&full[s], arrivals);
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 2 * kEpiThreads);
+      mbar_init(&tempty[i], 2 * 2 * kEpiThreads);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_x);
     tma_prefetch_desc(&tm_wa);
     tma_prefetch_desc(&tm_wb);
   }
@@ -307,76 +407,163 @@ grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
   // allocations disagree, neither CTA does any work.
   const bool skip = ld_shared_cluster_u32(mapa_shared(smem_u32(tmem_slot), rank ^ 1u)) != tmem;
   if (skip && threadIdx.x == 0) atomicOr(a.status, kStatusPairTmem);
-  const Schedule sch = make_schedule(a, s_chunk[a.E], pairs);
+  const Schedule sch = make_schedule(a, (uint32_t)s_chunk[a.E], pairs);
 
   if (warp == 0) {
-    // ---------------- TMA producer (each CTA; the whole warp) ----------------
-    int stage = 0;
-    uint32_t phase = 0;
-    int64_t issued = 0;
-    bool ok = !skip;
-    WorkIter w(sch, pair);
-    int64_t u;
-    int kb0, kb1;
-    while (ok && w.next(a, sch, pairs, u, kb0, kb1)) {
-      const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
-      const int half = un.n >> 1;                          // this CTA's rows of x
-      const int brow = un.row0 + (int)rank * half;
-      // columns of the CTA's two weight boxes
-      const int ca = MODE == kGroupedSwiGLU ? un.col0 + 64 * (int)rank : un.col0 + 128 * (int)rank;
-      const int cb = MODE == kGroupedSwiGLU ? ca : ca + 64;
-      int src[4] = {0, 0, 0, 0};
-      if constexpr (GATHER) {
-        // lane i fetches rows 4 i .. 4 i + 3; rows past the chunk read as zero
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int r = 4 * lane + q;
-          int t = a.tokens;
-          if (r < half && brow + r < un.row0 + un.nrows) {
-            const int flat = a.order[brow + r];
-            t = flat / a.top_k;
-            if (flat < 0 || t >= a.tokens) t = a.tokens;
+    // ---------------- weights (TMA, one thread of each CTA) ----------------
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int64_t issued = 0;
+      bool ok = !skip;
+      WorkIter w(sch, pair);
+      uint32_t u;
+      int kb0, kb1;
+      while (ok && w.next(a, sch, pairs, u, kb0, kb1)) {
+        const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
+        // columns of the CTA's two weight boxes
+        const int ca = un.col0 + (MODE == kGroupedSwiGLU ? 64 : 128) * (int)rank;
+        const int cb = MODE == kGroupedSwiGLU ? ca : ca + 64;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.status, a.timeout_ns)) {
+            ok = false;
+            break;
           }
-          src[q] = t;
-        }
-      }
-      for (int kb = kb0; kb < kb1; ++kb) {
-        uint8_t* st = stages + (size_t)stage * a.stage_bytes;
-        if (lane == 0) {
-          ok = mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.status, a.timeout_ns);
-          if (ok) mbar_arrive_expect_tx(&full[stage], kABytes + (uint32_t)half * 128u);
-        }
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-        if (!ok) break;
-        if (lane == 0) {
+          uint8_t* st = stages + (size_t)stage * a.stage_bytes;
+          mbar_arrive_expect_tx(&full[stage], kABytes);
           if (a.kmajor) {
             tma_load_3d(st, &tm_wa, &full[stage], kb * kBK, ca, un.e);
-            tma_load_3d(st + kChunkBytes, &tm_wb, &full[stage], kb * kBK, cb, un.e);
+            // (one 128-column box where the columns are neighbours)
+            if constexpr (MODE == kGroupedSwiGLU)
+              tma_load_3d(st + kChunkBytes, &tm_wb, &full[stage], kb * kBK, cb, un.e);
           } else {
             tma_load_3d(st, &tm_wa, &full[stage], ca, kb * kBK, un.e);
             tma_load_3d(st + kChunkBytes, &tm_wb, &full[stage], cb, kb * kBK, un.e);
           }
-        }
-        if constexpr (GATHER) {
-          if (4 * lane < half)
-            tma_gather4(st + kABytes + lane * 512, &tm_x, &full[stage], kb * kBK, src);
-        } else {
-          if (16 * lane < half)
-            tma_load_2d(st + kABytes + lane * kRowBoxBytes, &tm_x, &full[stage], kb * kBK,
-                        brow + 16 * lane);
-        }
-        ++issued;
-        if (++stage == a.stages) {
-          stage = 0;
-          phase ^= 1u;
+          ++issued;
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
+      if (issued > 0 && !ok) {
+        // let the loads still in flight land before the CTA can exit
+        const int64_t first = issued > a.stages ? issued - a.stages : 0;
+        for (int64_t i = first; i < issued; ++i)
+          wait_drain(&full[i % a.stages], (uint32_t)((i / a.stages) & 1), a.status, a.timeout_ns);
+      }
     }
-    if (issued > 0 && !ok && lane == 0) {
-      // let the loads still in flight land before the CTA can exit
-      const int64_t first = issued > a.stages ? issued - a.stages : 0;
-      for (int64_t i = first; i < issued; ++i)
-        wait_drain(&full[i % a.stages], (uint32_t)((i / a.stages) & 1), a.status, a.timeout_ns);
+    __syncwarp();
+  } else if (warp >= kRowWarp) {
+    // ---------------- rows of x ----------------
+    if constexpr (GATHER) {
+      // Rows gathered through `order`: 128 threads copy 16 bytes each, 16 rows
+      // at a time, into the 128-byte-swizzled layout (16-byte chunk c of row r
+      // at chunk c ^ (r & 7)).  A stage's copies are waited for kLag stages
+      // later, made visible to the MMAs (which read through the async proxy)
+      // and announced.
+      constexpr int kLag = 3;
+      const int gt = threadIdx.x - kRowWarp * 32;
+      const int c16 = gt & 7, r16 = gt >> 3;
+      const uint32_t dst0 = kABytes + (uint32_t)r16 * 128u + (uint32_t)((c16 ^ (r16 & 7)) * 16);
+      int stage = 0, ready = 0, pending = 0;
+      uint32_t phase = 0;
+      bool ok = !skip;
+      WorkIter w(sch, pair);
+      uint32_t u;
+      int kb0, kb1;
+      while (ok && w.next(a, sch, pairs, u, kb0, kb1)) {
+        const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
+        const int half = un.n >> 1;
+        const int brow = un.row0 + (int)rank * half;
+        const int nb = half >> 4;
+        // this thread's rows (null: past the chunk, zeros)
+        const uint16_t* src[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          src[j] = nullptr;
+          const int r = brow + j * 16 + r16;
+          if (j < nb && r < un.row0 + un.nrows) {
+            const int flat = a.order[r];
+            const int t = flat / a.top_k;
+            if (flat >= 0 && t < a.tokens) src[j] = a.x + (int64_t)t * a.K;
+          }
+        }
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.status, a.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = smem_u32(stages + (size_t)stage * a.stage_bytes) + dst0;
+          const int k = kb * kBK + c16 * 8;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < nb) {
+              const bool in = src[j] != nullptr && k < a.K;
+              cp_async_16(dst + j * 2048, in ? src[j] + k : a.x, in ? 16u : 0u);
+            }
+          cp_async_commit();
+          if (++pending > kLag) {
+            cp_async_wait<kLag>();
+            fence_async_smem();
+            mbar_arrive(&full[ready]);
+            if (++ready == a.stages) ready = 0;
+            --pending;
+          }
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      cp_async_wait<0>();
+      fence_async_smem();
+      for (; pending > 0; --pending) {
+        mbar_arrive(&full[ready]);
+        if (++ready == a.stages) ready = 0;
+      }
+    } else if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int64_t issued = 0;
+      bool ok = !skip;
+      WorkIter w(sch, pair);
+      uint32_t u;
+      int kb0, kb1;
+      while (ok && w.next(a, sch, pairs, u, kb0, kb1)) {
+        const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
+        const int half = un.n >> 1;
+        const int brow = un.row0 + (int)rank * half;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.status, a.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sb = stages + (size_t)stage * a.stage_bytes + kABytes;
+          mbar_arrive_expect_tx(&full[stage], (uint32_t)half * 128u);
+          // boxes of 128, 64, 32 and 16 rows, as the bits of `half` ask
+          int r = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int n = 128 >> b;
+            if (half & n) {
+              tma_load_2d(sb + r * 128, &tm_x.box[b], &full[stage], kb * kBK, brow + r);
+              r += n;
+            }
+          }
+          ++issued;
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (issued > 0 && !ok) {
+        const int64_t first = issued > a.stages ? issued - a.stages : 0;
+        for (int64_t i = first; i < issued; ++i)
+          wait_drain(&full[i % a.stages], (uint32_t)((i / a.stages) & 1), a.status, a.timeout_ns);
+      }
     }
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
@@ -390,7 +577,7 @@ grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
       uint32_t acc_phase = 0;
       bool ok = !skip;
       WorkIter w(sch, pair);
-      int64_t u;
+      uint32_t u;
       int kb0, kb1;
       while (ok && w.next(a, sch, pairs, u, kb0, kb1)) {
         const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
@@ -443,7 +630,7 @@ grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
       uint32_t phase = 0;
       bool ok = !skip;
       WorkIter w(sch, pair);
-      int64_t u;
+      uint32_t u;
       int kb0, kb1;
       while (ok && w.next(a, sch, pairs, u, kb0, kb1)) {
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -461,16 +648,21 @@ grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
     }
     __syncwarp();
   } else {
-    // ---------------- epilogue: warps 2..5 (each CTA) ----------------
+    // ---------------- epilogue: warps 2..9 (each CTA) ----------------
+    // Two groups of four warps; group g takes the chunks of 32 rows c = g, g + 2, ...
+    const int grp = (warp - 2) >> 2;
     const int quarter = warp & 3;
     const int col = quarter * 32 + lane;   // accumulator lane = weight column of this CTA
-    const int et = threadIdx.x - 64;
+    const int et = (warp - 2 - 4 * grp) * 32 + lane;
+    const uint32_t gbar = 1u + (uint32_t)grp;
+    constexpr uint32_t kBothBar = 3;
+    float* staging = reinterpret_cast<float*>(staging_base + grp * kStagingBytes);
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0u);
     int acc = 0;
     uint32_t acc_phase = 0;
     WorkIter w(sch, pair);
-    int64_t u;
+    uint32_t u;
     int kb0, kb1;
     while (!skip && w.next(a, sch, pairs, u, kb0, kb1)) {
       const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
@@ -479,20 +671,20 @@ grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
       const uint32_t t_acc = tmem + lane_off + (uint32_t)(acc * kAccCols);
       const bool whole = kb0 == 0 && kb1 == a.n_kb;
       const int nchunk = (un.nrows + 31) >> 5;
-      int64_t c0 = 0, rel = 0;
-      int nseg = 0;
+      uint32_t c0 = 0, rel = 0, nseg = 0;
       if (!whole) {
         // A share of a cut unit: store the sums so far, take a ticket; the
         // last of the unit's pairs adds all the shares in k order.  A pair's
         // slot 0 holds the share of the unit its range begins in, slot 1 that
         // of the unit its range ends in.
+        const uint32_t n_kb = (uint32_t)a.n_kb;
         rel = u - sch.whole;
-        c0 = rel * a.n_kb / sch.q;
-        nseg = (int)(((rel + 1) * a.n_kb - 1) / sch.q - c0 + 1);
-        const int which = pair * sch.q / a.n_kb == rel ? 0 : 1;
+        c0 = rel * n_kb / sch.q;
+        nseg = ((rel + 1) * n_kb - 1) / sch.q - c0 + 1;
+        const uint32_t which = pair * sch.q / n_kb == rel ? 0 : 1;
         float* mine = a.part + ((pair * 2 + which) * 2 + rank) * (int64_t)(a.n_max * 128) + col;
 #pragma unroll 1
-        for (int c = 0; c < nchunk; ++c) {
+        for (int c = grp; c < nchunk; c += 2) {
           uint32_t v[32];
           tmem_ld_x32(t_acc + (uint32_t)(c * 32), v);
           tmem_wait_ld();
@@ -505,13 +697,13 @@ grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
         if (rank == 1) mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
         else mbar_arrive(&tempty[acc]);
         __threadfence();
-        named_bar_sync(1, kEpiThreads);
-        if (et == 0) *ticket_slot = atomicAdd(a.counters + c0 * 2 + rank, 1u);
-        named_bar_sync(1, kEpiThreads);
+        named_bar_sync(kBothBar, 2 * kEpiThreads);
+        if (grp == 0 && et == 0) *ticket_slot = atomicAdd(a.counters + c0 * 2 + rank, 1u);
+        named_bar_sync(kBothBar, 2 * kEpiThreads);
         const unsigned ticket = *ticket_slot;
-        if (ticket + 1u != (unsigned)nseg) {
+        if (ticket + 1u != nseg) {
           // not the last (or a counter left over by a call that gave up)
-          if (ticket >= (unsigned)nseg && et == 0) atomicOr(a.status, kStatusStaleCounter);
+          if (ticket >= nseg && grp == 0 && et == 0) atomicOr(a.status, kStatusStaleCounter);
           if (++acc == 2) {
             acc = 0;
             acc_phase ^= 1u;
@@ -519,11 +711,10 @@ grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
           continue;
         }
         __threadfence();
-        if (et == 0) a.counters[c0 * 2 + rank] = 0u;   // left at zero for the next call
+        if (grp == 0 && et == 0) a.counters[c0 * 2 + rank] = 0u;   // left at zero for the next call
       }
       // this CTA's output columns, and the bias of this thread's column
-      const int cbase = MODE == kGroupedSwiGLU ? un.col0 + 64 * (int)rank
-                                               : un.col0 + 128 * (int)rank;
+      const int cbase = un.col0 + (MODE == kGroupedSwiGLU ? 64 : 128) * (int)rank;
       float bias = 0.f;
       if constexpr (MODE == kGroupedLinear) {
         if (a.bias && cbase + col < a.n_out)
@@ -531,27 +722,25 @@ grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
                             : bf16_lo(((const uint16_t*)a.bias)[cbase + col]);
       }
 #pragma unroll 1
-      for (int c = 0; c < nchunk; ++c) {
-        uint32_t v[32];
+      for (int c = grp; c < nchunk; c += 2) {
+        float v[32];
         if (whole) {
-          tmem_ld_x32(t_acc + (uint32_t)(c * 32), v);
+          uint32_t* vu = reinterpret_cast<uint32_t*>(v);
+          tmem_ld_x32(t_acc + (uint32_t)(c * 32), vu);
           tmem_wait_ld();
         } else {
-          float s[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = 0.f;
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
 #pragma unroll 1
-          for (int sg = 0; sg < nseg; ++sg) {
-            const int64_t p = c0 + sg;
-            const int which = p * sch.q / a.n_kb == rel ? 0 : 1;
+          for (uint32_t sg = 0; sg < nseg; ++sg) {
+            const uint32_t p = c0 + sg;
+            const uint32_t which = p * sch.q / (uint32_t)a.n_kb == rel ? 0 : 1;
             const float* src = a.part + ((p * 2 + which) * 2 + rank) * (int64_t)(a.n_max * 128) +
                                (int64_t)(c * 32) * 128 + col;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (c * 32 + i < un.nrows) s[i] += __ldcg(src + i * 128);
+              if (c * 32 + i < un.nrows) v[i] += __ldcg(src + i * 128);
           }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(s[i]);
         }
         if constexpr (MODE == kGroupedSwiGLU) {
           // Columns 0-63 hold x.W_gate, 64-127 x.W_up of the same 64 columns
@@ -559,22 +748,21 @@ grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
           // of the chunk, the up threads rows 16-31.
           const bool is_up = col >= 64;
           const int j = col & 63;
-          float* xg = staging;              // [16][64]: gate of rows 16-31
-          float* xu = staging + 16 * 64;    // [16][64]: up of rows 0-15
-          uint16_t* hs = reinterpret_cast<uint16_t*>(staging + 2 * 16 * 64);   // [32][72]
+          float* give = staging + (is_up ? 16 * 64 : 0) + j;   // gate: [0], up: [1]
+          const float* take = staging + (is_up ? 0 : 16 * 64) + j;
+          uint16_t* hs = reinterpret_cast<uint16_t*>(staging + 2 * 16 * 64);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) give[i * 64] = is_up ? v[i] : v[16 + i];
+          named_bar_sync(gbar, kEpiThreads);
+          uint16_t* hrow = hs + (is_up ? 16 * kHCols : 0) + j;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (is_up) xu[i * 64 + j] = __uint_as_float(v[i]);
-            else xg[i * 64 + j] = __uint_as_float(v[16 + i]);
+            const float other = take[i * 64];
+            const float g = is_up ? other : v[i];
+            const float up = is_up ? v[16 + i] : other;
+            hrow[i * kHCols] = cvt_bf16(silu_fast(g) * up);
           }
-          named_bar_sync(1, kEpiThreads);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float g = is_up ? xg[i * 64 + j] : __uint_as_float(v[i]);
-            const float up = is_up ? __uint_as_float(v[16 + i]) : xu[i * 64 + j];
-            hs[((is_up ? 16 : 0) + i) * 72 + j] = (uint16_t)f32_to_bf16_bits(silu_fast(g) * up);
-          }
-          named_bar_sync(1, kEpiThreads);
+          named_bar_sync(gbar, kEpiThreads);
 #pragma unroll
           for (int it = 0; it < 2; ++it) {
             const int g = it * kEpiThreads + et;
@@ -582,69 +770,37 @@ grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
             if (c * 32 + r < un.nrows && cbase + c8 < a.n_out)
               *reinterpret_cast<uint4*>((uint16_t*)a.out +
                                         (int64_t)(un.row0 + c * 32 + r) * a.n_out + cbase + c8) =
-                  *reinterpret_cast<const uint4*>(hs + r * 72 + c8);
+                  *reinterpret_cast<const uint4*>(hs + r * kHCols + c8);
           }
         } else {
-          if (c) named_bar_sync(1, kEpiThreads);   // the previous chunk has been copied out
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float f = __uint_as_float(v[i]);
-            if constexpr (MODE == kGroupedLinear) f = activate(f + bias, a.act, a.out_f32 != 0);
-            staging[i * kStageCols + col] = f;
-          }
-          named_bar_sync(1, kEpiThreads);
-#pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const int g = it * kEpiThreads + et;
-            const int r = g >> 4, c8 = (g & 15) * 8;
-            if (c * 32 + r >= un.nrows || cbase + c8 >= a.n_out) continue;
-            const int64_t o = (int64_t)(un.row0 + c * 32 + r) * a.n_out + cbase + c8;
-            if (MODE == kGroupedLinear && (a.n_out & 7)) {
-              // rows off 16-byte boundaries: element by element
-              for (int i = 0; i < 8 && cbase + c8 + i < a.n_out; ++i) {
-                float f = staging[r * kStageCols + c8 + i];
-                if (a.out_f32) {
-                  if (a.resid) f += ((const float*)a.resid)[o + i];
-                  ((float*)a.out)[o + i] = f;
-                } else {
-                  if (a.resid) f += bf16_lo(((const uint16_t*)a.resid)[o + i]);
-                  ((uint16_t*)a.out)[o + i] = (uint16_t)f32_to_bf16_bits(f);
-                }
-              }
-              continue;
+          for (int hp = 0; hp < 2; ++hp) {   // 16 rows at a time
+            if (hp) {
+              if (c * 32 + 16 >= un.nrows) break;
+              named_bar_sync(gbar, kEpiThreads);   // rows 0-15 have been copied out
             }
-            const float4* sp = reinterpret_cast<const float4*>(staging + r * kStageCols + c8);
-            float4 lo = sp[0], hi = sp[1];
-            if (a.out_f32) {
-              if (MODE == kGroupedLinear && a.resid) {
-                const float4 rl = *reinterpret_cast<const float4*>((const float*)a.resid + o);
-                const float4 rh = *reinterpret_cast<const float4*>((const float*)a.resid + o + 4);
-                lo.x += rl.x; lo.y += rl.y; lo.z += rl.z; lo.w += rl.w;
-                hi.x += rh.x; hi.y += rh.y; hi.z += rh.z; hi.w += rh.w;
-              }
-              float4* dst = reinterpret_cast<float4*>((float*)a.out + o);
-              dst[0] = lo;
-              dst[1] = hi;
-            } else {
-              if (MODE == kGroupedLinear && a.resid) {
-                const uint4 rr = *reinterpret_cast<const uint4*>((const uint16_t*)a.resid + o);
-                lo.x += bf16_lo(rr.x); lo.y += bf16_hi(rr.x);
-                lo.z += bf16_lo(rr.y); lo.w += bf16_hi(rr.y);
-                hi.x += bf16_lo(rr.z); hi.y += bf16_hi(rr.z);
-                hi.z += bf16_lo(rr.w); hi.w += bf16_hi(rr.w);
-              }
-              uint4 q;
-              q.x = pack_bf16x2(lo.x, lo.y);
-              q.y = pack_bf16x2(lo.z, lo.w);
-              q.z = pack_bf16x2(hi.x, hi.y);
-              q.w = pack_bf16x2(hi.z, hi.w);
-              *reinterpret_cast<uint4*>((uint16_t*)a.out + o) = q;
+            if constexpr (MODE == kGroupedLinear) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[hp * 16 + i] += bias;
+              activate_n<16>(v + hp * 16, a.act, a.out_f32 != 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) staging[i * kStageCols + col] = v[hp * 16 + i];
+            named_bar_sync(gbar, kEpiThreads);
+#pragma unroll
+            for (int it = 0; it < 2; ++it) {
+              const int g = it * kEpiThreads + et;
+              const int r = g >> 4, c8 = (g & 15) * 8;
+              const int row = c * 32 + hp * 16 + r;
+              if (row >= un.nrows || cbase + c8 >= a.n_out) continue;
+              store_row8<MODE>(a, (int64_t)(un.row0 + row) * a.n_out + cbase + c8,
+                               a.n_out - cbase - c8, staging + r * kStageCols + c8);
             }
           }
+          named_bar_sync(gbar, kEpiThreads);   // staging is free
         }
       }
-      // staging is free, and every accumulator column of this buffer is read
-      named_bar_sync(1, kEpiThreads);
+      // every accumulator column of this buffer is read
       if (whole) {
         tc_fence_before();
         if (rank == 1) mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
@@ -659,7 +815,7 @@ grouped_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
       // rows that no expert has (dropped choices) are zero
       const int first = s_row[a.E];
       const int per = a.n_out / 8;
-      for (int64_t r = first + (int64_t)blockIdx.x; r < a.rows; r += gridDim.x)
+      for (int64_t r = first + (int64_t)(blockIdx.x * 2 + grp); r < a.rows; r += 2 * gridDim.x)
         for (int c8 = et; c8 < per; c8 += kEpiThreads)
           *reinterpret_cast<uint4*>((uint16_t*)a.out + r * a.n_out + (int64_t)c8 * 8) =
               make_uint4(0u, 0u, 0u, 0u);
@@ -687,7 +843,7 @@ empty_linear_kernel(const void* bias, int bias_f32, int act, const void* resid, 
     const int64_t n = i % N;
     float v = 0.f;
     if (bias) v = bias_f32 ? ((const float*)bias)[n] : bf16_lo(((const uint16_t*)bias)[n]);
-    v = activate(v, act, out_f32 != 0);
+    activate_n<1>(&v, act, out_f32 != 0);
     if (resid) v += out_f32 ? ((const float*)resid)[i] : bf16_lo(((const uint16_t*)resid)[i]);
     if (out_f32) ((float*)y)[i] = v;
     else ((uint16_t*)y)[i] = (uint16_t)f32_to_bf16_bits(v);
@@ -713,7 +869,7 @@ size_t smem_bytes(const GroupedPlan& p, int E) {
 }
 
 template <int MODE, bool GATHER>
-cudaError_t launch_mode(const CUtensorMap& mx, const CUtensorMap& ma, const CUtensorMap& mb,
+cudaError_t launch_mode(const RowMaps& mx, const CUtensorMap& ma, const CUtensorMap& mb,
                         const Args& a, int pairs, size_t smem, cudaStream_t st) {
   auto kern = grouped_tc_kernel<MODE, GATHER>;
   static std::atomic<int> configured[64];   // zero: not yet set on that device
@@ -734,7 +890,7 @@ cudaError_t launch_mode(const CUtensorMap& mx, const CUtensorMap& ma, const CUte
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads_of(GATHER));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
@@ -785,10 +941,13 @@ cudaError_t launch_grouped(int mode, const GroupedCall& c, const GroupedPlan& p,
                                                          c.out_f32, c.rows, c.n_out);
     return cudaGetLastError();
   }
-  CUtensorMap mx, ma, mb;
+  RowMaps mx{};
+  CUtensorMap ma, mb;
   const bool gather = mode == kGroupedSwiGLU;
-  const int64_t xrows = gather ? c.tokens : c.rows;
-  if ((e = make_tmap_bf16_2d(&mx, c.x, xrows, c.K, kBK, gather ? 1 : 16)) != cudaSuccess) return e;
+  if (!gather)
+    for (int b = 0; b < 4; ++b)
+      if ((e = make_tmap_bf16_2d(&mx.box[b], c.x, c.rows, c.K, kBK, 128 >> b)) != cudaSuccess)
+        return e;
   const bool kmajor = c.wlayout == kWeightsNK;
   const void* wa = c.wa;
   int64_t wcols = c.n_out;
@@ -803,13 +962,15 @@ cudaError_t launch_grouped(int mode, const GroupedCall& c, const GroupedPlan& p,
     wa = c.padded;
   }
   const int64_t wr = kmajor ? c.n_out : c.K, wc = kmajor ? c.K : wcols;
-  if ((e = make_tmap_bf16_3d(&ma, wa, c.E, wr, wc, 64, 64)) != cudaSuccess) return e;
+  if ((e = make_tmap_bf16_3d(&ma, wa, c.E, wr, wc, 64, kmajor && !gather ? 128 : 64)) != cudaSuccess) return e;
   if (mode == kGroupedSwiGLU) {
     if ((e = make_tmap_bf16_3d(&mb, c.wb, c.E, wr, wc, 64, 64)) != cudaSuccess) return e;
   } else {
     mb = ma;
   }
   Args a{};
+  a.x = (const uint16_t*)c.x;
+  a.K = (int)c.K;
   a.offsets = c.offsets;
   a.order = c.order;
   a.E = (int)c.E;
