@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kVec = 8;   // columns per thread
+constexpr int kBatch = 4; // choices whose loads are in flight together
 
 __global__ void __launch_bounds__(kThreads)
 combine_kernel(const float* __restrict__ z, const int* __restrict__ position,
@@ -36,16 +37,33 @@ combine_kernel(const float* __restrict__ z, const int* __restrict__ position,
 #pragma unroll
       for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
     }
-    for (int j = 0; j < k; ++j) {
-      const int p = position[t * k + j];
-      if (p < 0 || p >= rows) continue;
-      const float w = weights[t * k + j];
-      const float4* src = reinterpret_cast<const float4*>(z + (int64_t)p * d + c);
-      const float4 a = __ldcs(src), b = __ldcs(src + 1);
-      acc[0] = fmaf(w, a.x, acc[0]); acc[1] = fmaf(w, a.y, acc[1]);
-      acc[2] = fmaf(w, a.z, acc[2]); acc[3] = fmaf(w, a.w, acc[3]);
-      acc[4] = fmaf(w, b.x, acc[4]); acc[5] = fmaf(w, b.y, acc[5]);
-      acc[6] = fmaf(w, b.z, acc[6]); acc[7] = fmaf(w, b.w, acc[7]);
+    // four choices at a time: their rows' loads are in flight together
+    for (int j0 = 0; j0 < k; j0 += kBatch) {
+      float w[kBatch];
+      float4 a[kBatch], b[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        int p = -1;
+        if (j0 + i < k) {
+          p = position[t * k + j0 + i];
+          w[i] = weights[t * k + j0 + i];
+        }
+        a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p < 0 || p >= rows) {
+          w[i] = 0.f;   // no term (whatever its weight)
+        } else {
+          const float4* src = reinterpret_cast<const float4*>(z + (int64_t)p * d + c);
+          a[i] = __ldcs(src);
+          b[i] = __ldcs(src + 1);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        acc[0] = fmaf(w[i], a[i].x, acc[0]); acc[1] = fmaf(w[i], a[i].y, acc[1]);
+        acc[2] = fmaf(w[i], a[i].z, acc[2]); acc[3] = fmaf(w[i], a[i].w, acc[3]);
+        acc[4] = fmaf(w[i], b[i].x, acc[4]); acc[5] = fmaf(w[i], b[i].y, acc[5]);
+        acc[6] = fmaf(w[i], b[i].z, acc[6]); acc[7] = fmaf(w[i], b[i].w, acc[7]);
+      }
     }
     uint4 o;
     o.x = pack_bf16x2(acc[0], acc[1]);

@@ -121,11 +121,11 @@ int free_workspace(const Workspace& ws, cudaStream_t st) {
 }
 
 GroupedPlan plan_up(int64_t T, int64_t k, int64_t E, int64_t d, int64_t d_ff, int pairs) {
-  return plan_grouped(T * k, T, E, d, d_ff, true, pairs);
+  return plan_grouped(T * k, T, E, d, d_ff, true, pairs, read_tuning());
 }
 
 GroupedPlan plan_down(int64_t T, int64_t k, int64_t E, int64_t d_ff, int64_t d, int pairs) {
-  return plan_grouped(T * k, T, E, d_ff, d, false, pairs);
+  return plan_grouped(T * k, T, E, d_ff, d, false, pairs, read_tuning());
 }
 
 // Room for [K, N] weights with padded rows (launch_grouped), where N asks for it.
@@ -146,7 +146,7 @@ size_t swiglu_linear_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (check_product(M, K, N, "K", "N", true) != SWIGLU_OK) return 0;
   Device dv;
   if (get_device(&dv) != SWIGLU_OK) return 0;
-  const GroupedPlan p = plan_grouped(M, M, 1, K, N, false, dv.pairs);
+  const GroupedPlan p = plan_grouped(M, M, 1, K, N, false, dv.pairs, read_tuning());
   api_clear_error();
   return p.counters_bytes + round256(p.part_bytes) + padded_bytes(K, N);
 }
@@ -178,7 +178,7 @@ int swiglu_linear(const void* x, const void* w, const void* bias, const void* re
     api_clear_error();
     return SWIGLU_OK;
   }
-  const GroupedPlan p = plan_grouped(M, M, 1, K, N, false, dv.pairs);
+  const GroupedPlan p = plan_grouped(M, M, 1, K, N, false, dv.pairs, read_tuning());
   GroupedCall c{};
   c.x = x;
   c.wa = w;

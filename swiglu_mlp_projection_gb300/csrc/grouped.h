@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "internal.h"
+
 namespace swg {
 
 // The grouped kernel's epilogues.
@@ -24,12 +26,15 @@ struct GroupedPlan {
   int n_max;             // most rows of a chunk (a multiple of 32, at most 256)
   int stages;            // shared-memory ring
   uint32_t stage_bytes;
+  int min_kb;            // fewest k blocks of a share of a cut unit
+  int prefetch_kb;       // linear: k blocks of weights asked into L2 per CTA before the
+                         // previous kernel has ended
   size_t counters_bytes, part_bytes;
 };
 
 // rows: rows of the sorted operand; tokens: most rows that one expert can have.
 GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, int64_t K, int64_t n_out,
-                         bool swiglu, int pairs);
+                         bool swiglu, int pairs, const Tuning& tn);
 
 struct GroupedCall {
   const void* x;           // [tokens, K] (SwiGLU) or [rows, K]

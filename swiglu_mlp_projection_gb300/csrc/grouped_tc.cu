@@ -86,6 +86,7 @@ struct Args {
   int stages;
   uint32_t stage_bytes;
   int kmajor;              // weights stored [n_out, K]
+  int prefetch_kb;         // linear: k blocks whose weights are asked into L2 early
   int min_kb;              // fewest k blocks of a share of a cut unit
   void* out;
   int out_f32;
@@ -232,18 +233,25 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// The same box into L2 only (a hint).
+__device__ __forceinline__ void tma_prefetch_l2_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   (uint64_t)map),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
 // 16 bytes global -> shared, asynchronously; `bytes` 0 writes zeros instead.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
+// This thread's arrival on `bar` once its cp.async so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity, unsigned* status,
                                            uint64_t timeout_ns) {
@@ -298,6 +306,69 @@ __device__ __forceinline__ uint16_t cvt_bf16(float v) {
   return r;
 }
 
+// L2 prefetch of the weights of this CTA's first k blocks (linear).
+template <int COLS>
+__device__ void prefetch_weights(const Args& a, const CUtensorMap& tm_w, const int* s_row,
+                                 const int* s_chunk, uint32_t pair, uint32_t pairs, uint32_t rank) {
+  const Schedule sch = make_schedule(a, (uint32_t)s_chunk[a.E], pairs);
+  WorkIter w(sch, pair);
+  uint32_t u;
+  int kb0, kb1, left = a.prefetch_kb;
+  while (left > 0 && w.next(a, sch, pairs, u, kb0, kb1)) {
+    const Unit un = find_unit<COLS>(a, s_row, s_chunk, u);
+    const int ca = un.col0 + 128 * (int)rank;
+    for (int kb = kb0; kb < kb1 && left > 0; ++kb, --left) {
+      if (a.kmajor) {
+        tma_prefetch_l2_3d(&tm_w, kb * kBK, ca, un.e);
+      } else {
+        tma_prefetch_l2_3d(&tm_w, ca, kb * kBK, un.e);
+        tma_prefetch_l2_3d(&tm_w, ca + 64, kb * kBK, un.e);
+      }
+    }
+  }
+}
+
+// The f32 sums of a share of a cut unit: two slots per pair, one copy per
+// rank, each [32-row chunk][4-row group][column][4 rows], so that a warp moves
+// 512 contiguous bytes at a time.
+__device__ __forceinline__ int64_t part_stride(const Args& a) { return (int64_t)a.n_max * 128 * 4; }
+__device__ __forceinline__ float* part_slot(const Args& a, uint32_t pair, uint32_t which,
+                                            uint32_t rank) {
+  return a.part + (int64_t)pair * part_stride(a) + (int64_t)(which * 2 + rank) * (a.n_max * 128);
+}
+
+// v[0 .. 4 NQ) = the sum of `nseg` shares, in order: the first one's, then
+// those of the pairs after it.  NS shares are loaded at a time, because a
+// share costs an L2 round trip, not its bytes.  `rows` of the chunk are used.
+template <int NQ, int NS>
+__device__ __forceinline__ void add_shares(float* v, const float* first, const float* rest,
+                                           int64_t stride, int nseg, int rows) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 1
+  for (int s0 = 0; s0 < nseg; s0 += NS) {
+    float4 t[NS][NQ];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const float* src = s0 + s == 0 ? first : rest + (int64_t)(s0 + s - 1) * stride;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+        t[s][q] = s0 + s < nseg && 4 * q < rows
+                      ? __ldcg(reinterpret_cast<const float4*>(src + q * 512))
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        v[4 * q] += t[s][q].x;
+        v[4 * q + 1] += t[s][q].y;
+        v[4 * q + 2] += t[s][q].z;
+        v[4 * q + 3] += t[s][q].w;
+      }
+  }
+}
+
 // Up to 8 neighbouring outputs of one row, at element `o`; `left` columns of
 // the row remain from there.
 template <int MODE>
@@ -350,6 +421,7 @@ __global__ void __launch_bounds__(threads_of(GATHER), 1)
 grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ CUtensorMap tm_wa,
                   const __grid_constant__ CUtensorMap tm_wb, const Args a) {
   constexpr int kCols = MODE == kGroupedSwiGLU ? 128 : 256;   // output columns of a unit
+  constexpr int kPrefetchWarp = 2;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;
@@ -393,15 +465,26 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
-  // The set-up above overlaps the previous kernel's tail; the routing, the
-  // operands and the outputs are touched only after it has finished.
-  pdl_wait();
-  pdl_launch_dependents();
-  plan_chunks(a, s_row, s_chunk);
+  // Without a routing the work is known at once: the first weights are asked
+  // into L2 while the previous kernel ends.
+  if (!a.offsets) {
+    plan_chunks(a, s_row, s_chunk);
+    __syncthreads();
+    if (a.prefetch_kb > 0 && warp == kPrefetchWarp && lane == 0)
+      prefetch_weights<kCols>(a, tm_wa, s_row, s_chunk, pair, pairs, rank);
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // both CTAs' barriers and TMEM are ready
   tc_fence_after();
+  // All of the above overlaps the previous kernel's tail; the routing, the
+  // operands and the outputs are touched only after it has finished.
+  pdl_wait();
+  pdl_launch_dependents();
+  if (a.offsets) {
+    plan_chunks(a, s_row, s_chunk);
+    __syncthreads();
+  }
   const uint32_t tmem = *tmem_slot;
   // The pair's MMAs address both TMEMs with one column address; if the two
   // allocations disagree, neither CTA does any work.
@@ -460,14 +543,14 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
     if constexpr (GATHER) {
       // Rows gathered through `order`: 128 threads copy 16 bytes each, 16 rows
       // at a time, into the 128-byte-swizzled layout (16-byte chunk c of row r
-      // at chunk c ^ (r & 7)).  A stage's copies are waited for kLag stages
-      // later, made visible to the MMAs (which read through the async proxy)
-      // and announced.
-      constexpr int kLag = 3;
+      // at chunk c ^ (r & 7)).  Each thread's arrival on the stage's barrier
+      // follows its copies by itself; whoever waits for the stage fences the
+      // generic proxy, which wrote the rows, against the async proxy, through
+      // which the MMAs read them.
       const int gt = threadIdx.x - kRowWarp * 32;
       const int c16 = gt & 7, r16 = gt >> 3;
       const uint32_t dst0 = kABytes + (uint32_t)r16 * 128u + (uint32_t)((c16 ^ (r16 & 7)) * 16);
-      int stage = 0, ready = 0, pending = 0;
+      int stage = 0;
       uint32_t phase = 0;
       bool ok = !skip;
       WorkIter w(sch, pair);
@@ -503,26 +586,14 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
               const bool in = src[j] != nullptr && k < a.K;
               cp_async_16(dst + j * 2048, in ? src[j] + k : a.x, in ? 16u : 0u);
             }
-          cp_async_commit();
-          if (++pending > kLag) {
-            cp_async_wait<kLag>();
-            fence_async_smem();
-            mbar_arrive(&full[ready]);
-            if (++ready == a.stages) ready = 0;
-            --pending;
-          }
+          cp_async_arrive(&full[stage]);
           if (++stage == a.stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      cp_async_wait<0>();
-      fence_async_smem();
-      for (; pending > 0; --pending) {
-        mbar_arrive(&full[ready]);
-        if (++ready == a.stages) ready = 0;
-      }
+      cp_async_wait_all();   // nothing is in flight when the CTA ends
     } else if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
@@ -596,6 +667,7 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
             ok = false;
             break;
           }
+          if constexpr (GATHER) fence_async_smem();
           tc_fence_after();
           const uint32_t a_addr = smem_u32(stages + (size_t)stage * a.stage_bytes);
           const uint32_t b_addr = a_addr + kABytes;
@@ -638,6 +710,7 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
             ok = false;
             break;
           }
+          if constexpr (GATHER) fence_async_smem();
           mbar_arrive_remote(full0 + (uint32_t)stage * 8u);
           if (++stage == a.stages) {
             stage = 0;
@@ -682,16 +755,18 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
         c0 = rel * n_kb / sch.q;
         nseg = ((rel + 1) * n_kb - 1) / sch.q - c0 + 1;
         const uint32_t which = pair * sch.q / n_kb == rel ? 0 : 1;
-        float* mine = a.part + ((pair * 2 + which) * 2 + rank) * (int64_t)(a.n_max * 128) + col;
+        float* mine = part_slot(a, pair, which, rank) + col * 4;
 #pragma unroll 1
         for (int c = grp; c < nchunk; c += 2) {
           uint32_t v[32];
           tmem_ld_x32(t_acc + (uint32_t)(c * 32), v);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c * 32 + i < un.nrows)
-              __stcg(mine + (int64_t)(c * 32 + i) * 128, __uint_as_float(v[i]));
+          for (int i = 0; i < 8; ++i)
+            if (c * 32 + 4 * i < un.nrows)
+              __stcg(reinterpret_cast<float4*>(mine + (c * 8 + i) * 512),
+                     make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                 __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
         }
         tc_fence_before();
         if (rank == 1) mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
@@ -729,18 +804,13 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
           tmem_ld_x32(t_acc + (uint32_t)(c * 32), vu);
           tmem_wait_ld();
         } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
-#pragma unroll 1
-          for (uint32_t sg = 0; sg < nseg; ++sg) {
-            const uint32_t p = c0 + sg;
-            const uint32_t which = p * sch.q / (uint32_t)a.n_kb == rel ? 0 : 1;
-            const float* src = a.part + ((p * 2 + which) * 2 + rank) * (int64_t)(a.n_max * 128) +
-                               (int64_t)(c * 32) * 128 + col;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c * 32 + i < un.nrows) v[i] += __ldcg(src + i * 128);
-          }
+          const uint32_t which = c0 * sch.q / (uint32_t)a.n_kb == rel ? 0 : 1;
+          const float* first = part_slot(a, c0, which, rank) + c * 4096 + col * 4;
+          const float* rest = part_slot(a, c0 + 1, 0, rank) + c * 4096 + col * 4;
+          if (un.nrows - c * 32 <= 8)
+            add_shares<2, 8>(v, first, rest, part_stride(a), (int)nseg, un.nrows - c * 32);
+          else
+            add_shares<8, 2>(v, first, rest, part_stride(a), (int)nseg, un.nrows - c * 32);
         }
         if constexpr (MODE == kGroupedSwiGLU) {
           // Columns 0-63 hold x.W_gate, 64-127 x.W_up of the same 64 columns
@@ -901,7 +971,7 @@ cudaError_t launch_mode(const RowMaps& mx, const CUtensorMap& ma, const CUtensor
 }  // namespace
 
 GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, int64_t K, int64_t n_out,
-                         bool swiglu, int pairs) {
+                         bool swiglu, int pairs, const Tuning& tn) {
   GroupedPlan p{};
   // Rows per chunk.  An expert has at most `tokens` rows (a token chooses it
   // once) and rows / E on average; chunks for twice the average keep most
@@ -913,6 +983,7 @@ GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, int64_t K, int
     want = (want + c - 1) / c;
   }
   if (want > 256) want = 256;
+  if (tn.gr_rows > 0) want = tn.gr_rows < 256 ? tn.gr_rows : 256;
   p.n_max = (int)((want + 31) / 32 * 32);
   if (p.n_max < 32) p.n_max = 32;
   p.stage_bytes = kABytes + (uint32_t)(p.n_max / 2) * 128u;
@@ -921,6 +992,8 @@ GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, int64_t K, int
   p.pairs = pairs < 1 ? 1 : pairs;
   p.counters_bytes = ((size_t)p.pairs * 2 * sizeof(unsigned) + 255) / 256 * 256;
   p.part_bytes = (size_t)p.pairs * 4 * (size_t)p.n_max * 128 * sizeof(float);
+  p.min_kb = tn.gr_min_kb > 0 ? tn.gr_min_kb : 4;
+  p.prefetch_kb = tn.gr_prefetch >= 0 ? tn.gr_prefetch : (E == 1 && p.n_max <= 64 ? 32 : 0);
   (void)K;
   (void)n_out;
   (void)swiglu;
@@ -985,7 +1058,8 @@ cudaError_t launch_grouped(int mode, const GroupedCall& c, const GroupedPlan& p,
   a.stages = p.stages;
   a.stage_bytes = p.stage_bytes;
   a.kmajor = kmajor ? 1 : 0;
-  a.min_kb = 4;
+  a.min_kb = p.min_kb;
+  a.prefetch_kb = c.offsets ? 0 : p.prefetch_kb;
   a.out = c.out;
   a.out_f32 = c.out_f32;
   a.bias = c.bias;

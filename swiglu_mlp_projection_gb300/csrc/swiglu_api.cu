@@ -518,6 +518,9 @@ Tuning read_tuning() {
                           {"SK_SPLIT", &t.sk_split},
                           {"SK_KB", &t.sk_kb},
                           {"SIMT_CLUSTER", &t.simt_cluster},
+                          {"GR_ROWS", &t.gr_rows},
+                          {"GR_MIN_KB", &t.gr_min_kb},
+                          {"GR_PREFETCH", &t.gr_prefetch},
                           {"INJECT_OOM", &t.inject_oom}};
     for (const Knob& k : knobs)
       if (strlen(k.key) == n && strncmp(k.key, name, n) == 0) *k.dst = v;
