@@ -3,10 +3,13 @@
 //
 //   y[t] = residual[t] + sum_j weights[t, j] z[position[t, j]]
 //
-// j ascending, in f32, rounded once.  Bound by memory: each z row is read
-// once (16-byte loads, a warp covers consecutive columns), y written once.
+// j ascending, in f32, rounded once.  A row of z whose unit of the product was
+// cut along K is the sum of that unit's shares, in k order.  Bound by memory:
+// each z row is read once (16-byte loads, a warp covers consecutive columns),
+// y written once.
 #include "common.cuh"
 #include "grouped.h"
+#include "grouped_plan.cuh"
 #include "tc_common.cuh"
 
 namespace swg {
@@ -16,12 +19,44 @@ constexpr int kThreads = 128;
 constexpr int kVec = 8;   // columns per thread
 constexpr int kBatch = 4; // choices whose loads are in flight together
 
+// Columns c .. c + 7 of sorted row p, if its unit was cut.
+__device__ __forceinline__ bool cut_row(const Work& w, const Schedule& sch, const int* s_row,
+                                        const int* s_chunk, int p, int c, float4* lo, float4* hi) {
+  int a = 0, b = w.E;   // s_row[a] <= p < s_row[b]
+  while (b - a > 1) {
+    const int mid = (a + b) >> 1;
+    if (s_row[mid] <= p) a = mid;
+    else b = mid;
+  }
+  const int m = s_row[a + 1] - s_row[a], nc = s_chunk[a + 1] - s_chunk[a];
+  if (nc < 1 || p < s_row[a]) return false;
+  const int per = (m + nc - 1) / nc;
+  const int chunk = (p - s_row[a]) / per;
+  const uint32_t u = (uint32_t)s_chunk[a] * (uint32_t)w.ncg + (uint32_t)((c >> 8) * nc + chunk);
+  if (u < sch.whole || u >= sch.units || chunk >= nc) return false;
+  float v[8];
+  add_row_shares(w, shares_of(w, sch, u - sch.whole), (uint32_t)((c >> 7) & 1),
+                 (p - s_row[a] - chunk * per) * 128 + (c & 127), v);
+  *lo = make_float4(v[0], v[1], v[2], v[3]);
+  *hi = make_float4(v[4], v[5], v[6], v[7]);
+  return true;
+}
+
+template <bool CUT>
 __global__ void __launch_bounds__(kThreads)
-combine_kernel(const float* __restrict__ z, const int* __restrict__ position,
-               const float* __restrict__ weights, const uint16_t* resid, uint16_t* y, int64_t T,
-               int k, int64_t rows, int64_t d) {
+combine_kernel(const float* __restrict__ z, const __grid_constant__ Work w, uint32_t pairs,
+               const int* __restrict__ position, const float* __restrict__ weights,
+               const uint16_t* resid, uint16_t* y, int64_t T, int k, int64_t rows, int64_t d) {
+  extern __shared__ int s_row[];   // [E + 1] first rows, then [E + 1] first chunks
   tc::pdl_wait();
   tc::pdl_launch_dependents();
+  Schedule sch{0, 0, 0, 1};
+  int* s_chunk = s_row + w.E + 1;
+  if (CUT) {
+    plan_chunks(w, s_row, s_chunk);
+    __syncthreads();
+    sch = make_schedule(w, (uint32_t)s_chunk[w.E], pairs);
+  }
   const int64_t per = d / kVec;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < T * per;
        i += (int64_t)gridDim.x * kThreads) {
@@ -39,18 +74,20 @@ combine_kernel(const float* __restrict__ z, const int* __restrict__ position,
     }
     // four choices at a time: their rows' loads are in flight together
     for (int j0 = 0; j0 < k; j0 += kBatch) {
-      float w[kBatch];
+      float wt[kBatch];
       float4 a[kBatch], b[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         int p = -1;
         if (j0 + i < k) {
           p = position[t * k + j0 + i];
-          w[i] = weights[t * k + j0 + i];
+          wt[i] = weights[t * k + j0 + i];
         }
         a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (p < 0 || p >= rows) {
-          w[i] = 0.f;   // no term (whatever its weight)
+          wt[i] = 0.f;   // no term (whatever its weight)
+        } else if (CUT && sch.cut_iters > 0 && cut_row(w, sch, s_row, s_chunk, p, (int)c, &a[i], &b[i])) {
+          // (the sums of the shares)
         } else {
           const float4* src = reinterpret_cast<const float4*>(z + (int64_t)p * d + c);
           a[i] = __ldcs(src);
@@ -59,10 +96,10 @@ combine_kernel(const float* __restrict__ z, const int* __restrict__ position,
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        acc[0] = fmaf(w[i], a[i].x, acc[0]); acc[1] = fmaf(w[i], a[i].y, acc[1]);
-        acc[2] = fmaf(w[i], a[i].z, acc[2]); acc[3] = fmaf(w[i], a[i].w, acc[3]);
-        acc[4] = fmaf(w[i], b[i].x, acc[4]); acc[5] = fmaf(w[i], b[i].y, acc[5]);
-        acc[6] = fmaf(w[i], b[i].z, acc[6]); acc[7] = fmaf(w[i], b[i].w, acc[7]);
+        acc[0] = fmaf(wt[i], a[i].x, acc[0]); acc[1] = fmaf(wt[i], a[i].y, acc[1]);
+        acc[2] = fmaf(wt[i], a[i].z, acc[2]); acc[3] = fmaf(wt[i], a[i].w, acc[3]);
+        acc[4] = fmaf(wt[i], b[i].x, acc[4]); acc[5] = fmaf(wt[i], b[i].y, acc[5]);
+        acc[6] = fmaf(wt[i], b[i].z, acc[6]); acc[7] = fmaf(wt[i], b[i].w, acc[7]);
       }
     }
     uint4 o;
@@ -76,9 +113,9 @@ combine_kernel(const float* __restrict__ z, const int* __restrict__ position,
 
 }  // namespace
 
-cudaError_t launch_combine(const float* z, const int* position, const float* weights,
-                           const void* residual, void* y, int64_t T, int64_t k, int64_t rows,
-                           int64_t d, int num_sms, cudaStream_t st) {
+cudaError_t launch_combine(const float* z, const Work* w, int pairs, const int* position,
+                           const float* weights, const void* residual, void* y, int64_t T,
+                           int64_t k, int64_t rows, int64_t d, int num_sms, cudaStream_t st) {
   if (T == 0 || d == 0) return cudaSuccess;
   int64_t blocks = (T * (d / kVec) + kThreads - 1) / kThreads;
   const int64_t most = (int64_t)num_sms * 16;
@@ -92,8 +129,13 @@ cudaError_t launch_combine(const float* z, const int* position, const float* wei
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel, z, position, weights, (const uint16_t*)residual,
-                            (uint16_t*)y, T, (int)k, rows, d);
+  if (z && w->cut) {
+    cfg.dynamicSmemBytes = (size_t)(2 * (w->E + 1)) * sizeof(int);
+    return cudaLaunchKernelEx(&cfg, combine_kernel<true>, z, *w, (uint32_t)pairs, position, weights,
+                              (const uint16_t*)residual, (uint16_t*)y, T, (int)k, rows, d);
+  }
+  return cudaLaunchKernelEx(&cfg, combine_kernel<false>, z, *w, (uint32_t)pairs, position, weights,
+                            (const uint16_t*)residual, (uint16_t*)y, T, (int)k, rows, d);
 }
 
 }  // namespace swg

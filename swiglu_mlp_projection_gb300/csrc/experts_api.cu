@@ -4,6 +4,7 @@
 #include <stdio.h>
 
 #include "grouped.h"
+#include "grouped_plan.cuh"
 #include "internal.h"
 #include "swiglu.h"
 
@@ -204,20 +205,13 @@ int swiglu_linear(const void* x, const void* w, const void* bias, const void* re
   return SWIGLU_OK;
 }
 
-static int enqueue_dispatch(const Device& dv, const int32_t* ids, int32_t* offsets, int32_t* order,
-                            int32_t* position, int64_t R, int64_t E, cudaStream_t st) {
-  const size_t scratch = dispatch_scratch_bytes(R, E);
-  Workspace ws;
-  int v;
-  if (scratch &&
-      (v = api_take_workspace(dv.dev, st, nullptr, 0, 0, round256(scratch), &ws)) != SWIGLU_OK)
-    return v;
-  cudaError_t e = launch_dispatch(ids, offsets, order, position, R, E, (int*)ws.body, st);
-  if (e != cudaSuccess) {
-    if (ws.pooled) cudaFreeAsync(ws.pooled, st);
-    return api_cuda_fail(e, "kernel launch");
-  }
-  return free_workspace(ws, st);
+// The sort's scratch.
+static int sort_workspace(const Device& dv, size_t scratch, Workspace* ws, SortCall* s,
+                          cudaStream_t st) {
+  if (!scratch) return SWIGLU_OK;
+  int v = api_take_workspace(dv.dev, st, nullptr, 0, 0, round256(scratch), ws);
+  if (v == SWIGLU_OK) s->scratch = (int*)ws->body;
+  return v;
 }
 
 int swiglu_dispatch(const int32_t* ids, int32_t* offsets, int32_t* order, int32_t* position,
@@ -235,8 +229,14 @@ int swiglu_dispatch(const int32_t* ids, int32_t* offsets, int32_t* order, int32_
   }
   Device dv;
   if ((v = get_device(&dv)) != SWIGLU_OK) return v;
-  if ((v = enqueue_dispatch(dv, ids, offsets, order, position, T * k, E, (cudaStream_t)stream)) != SWIGLU_OK)
-    return v;
+  const cudaStream_t st = (cudaStream_t)stream;
+  Workspace ws;
+  SortCall sort{offsets, order, position, nullptr};
+  if ((v = sort_workspace(dv, dispatch_scratch_bytes(T * k, E, dv.num_sms), &ws, &sort, st)) != SWIGLU_OK) return v;
+  const cudaError_t e = launch_dispatch(ids, sort, T * k, E, dv.num_sms, st);
+  v = free_workspace(ws, st);
+  if (e != cudaSuccess) return api_cuda_fail(e, "kernel launch");
+  if (v != SWIGLU_OK) return v;
   api_clear_error();
   return SWIGLU_OK;
 }
@@ -274,15 +274,20 @@ int swiglu_route(const void* logits, const float* bias, int32_t* ids, float* wei
   Device dv;
   if ((v = get_device(&dv)) != SWIGLU_OK) return v;
   const cudaStream_t st = (cudaStream_t)stream;
-  if (T > 0 && k > 0) {
-    RouteCall c{logits, logits_dtype == SWIGLU_F32, bias, ids, weights, T, E, k,
-                score == SWIGLU_SCORE_SIGMOID, (int)groups, (int)topk_groups,
-                group_score == SWIGLU_GROUP_TOP2, renormalize != 0, scale};
-    const cudaError_t e = launch_route(c, dv.num_sms, st);
-    if (e != cudaSuccess) return api_cuda_fail(e, "kernel launch");
+  if (!sort && (T == 0 || k == 0)) {
+    api_clear_error();
+    return SWIGLU_OK;
   }
-  if (sort && (v = enqueue_dispatch(dv, ids, offsets, order, position, T * k, E, st)) != SWIGLU_OK)
-    return v;
+  const RouteCall c{logits, logits_dtype == SWIGLU_F32, bias, ids, weights, T, E, k,
+                    score == SWIGLU_SCORE_SIGMOID, (int)groups, (int)topk_groups,
+                    group_score == SWIGLU_GROUP_TOP2, renormalize != 0, scale};
+  Workspace ws;
+  SortCall sc{offsets, order, position, nullptr};
+  if (sort && (v = sort_workspace(dv, route_scratch_bytes(T, E, dv.num_sms), &ws, &sc, st)) != SWIGLU_OK) return v;
+  const cudaError_t e = launch_route(c, sort ? &sc : nullptr, dv.num_sms, st);
+  v = free_workspace(ws, st);
+  if (e != cudaSuccess) return api_cuda_fail(e, "kernel launch");
+  if (v != SWIGLU_OK) return v;
   api_clear_error();
   return SWIGLU_OK;
 }
@@ -378,6 +383,8 @@ int swiglu_experts_down(const void* h, const void* w_down, const int32_t* offset
   const cudaStream_t st = (cudaStream_t)stream;
   Workspace ws;
   const float* z = nullptr;
+  Work work{};
+  int pairs = 0;
   if (rows > 0 && d_ff > 0) {
     GroupedCall c{};
     c.x = h;
@@ -396,10 +403,12 @@ int swiglu_experts_down(const void* h, const void* w_down, const int32_t* offset
                          st)) != SWIGLU_OK)
       return v;
     z = (const float*)(ws.body + round256(p.part_bytes));
+    fill_work(&work, kGroupedPlain, c, p, (float*)ws.body);
+    pairs = p.pairs;
   }
   // (a product over nothing: y = residual, or 0)
-  const cudaError_t e = launch_combine(z, position, weights, residual, y, T, z ? k : 0, rows, d,
-                                       dv.num_sms, st);
+  const cudaError_t e = launch_combine(z, &work, pairs, position, weights, residual, y, T,
+                                       z ? k : 0, rows, d, dv.num_sms, st);
   v = free_workspace(ws, st);
   if (e != cudaSuccess) return api_cuda_fail(e, "kernel launch");
   if (v != SWIGLU_OK) return v;

@@ -26,6 +26,7 @@ struct GroupedPlan {
   int n_max;             // most rows of a chunk (a multiple of 32, at most 256)
   int stages;            // shared-memory ring
   uint32_t stage_bytes;
+  int cut;               // whether units of a partial wave are cut along K
   int min_kb;            // fewest k blocks of a share of a cut unit
   int prefetch_kb;       // linear: k blocks of weights asked into L2 per CTA before the
                          // previous kernel has ended
@@ -57,11 +58,16 @@ cudaError_t launch_grouped(int mode, const GroupedCall& c, const GroupedPlan& p,
                            unsigned* counters, bool counters_clean, unsigned* status,
                            uint64_t timeout_ns, cudaStream_t st);
 
+struct Work;   // grouped_plan.cuh
+void fill_work(Work* w, int mode, const GroupedCall& c, const GroupedPlan& p, float* part);
+
 // y[t] = residual[t] + sum_j weights[t, j] z[position[t, j]], j ascending, in
-// f32, rounded once (bf16).  position -1: no term.
-cudaError_t launch_combine(const float* z, const int* position, const float* weights,
-                           const void* residual, void* y, int64_t T, int64_t k, int64_t rows,
-                           int64_t d, int num_sms, cudaStream_t st);
+// f32, rounded once (bf16).  position -1: no term.  `w`: the grouped product
+// that wrote z (row r of a cut unit is in its shares instead); z null: no term
+// at all.
+cudaError_t launch_combine(const float* z, const Work* w, int pairs, const int* position,
+                           const float* weights, const void* residual, void* y, int64_t T,
+                           int64_t k, int64_t rows, int64_t d, int num_sms, cudaStream_t st);
 
 struct RouteCall {
   const void* logits;
@@ -73,11 +79,19 @@ struct RouteCall {
   int sigmoid, groups, topk_groups, group_top2, renormalize;
   float scale;
 };
-cudaError_t launch_route(const RouteCall& c, int num_sms, cudaStream_t st);
 
 // Counting sort of the R = T k choices by expert, stable.
-size_t dispatch_scratch_bytes(int64_t R, int64_t E);
-cudaError_t launch_dispatch(const int* ids, int* offsets, int* order, int* position, int64_t R,
-                            int64_t E, int* scratch, cudaStream_t st);
+struct SortCall {
+  int* offsets;
+  int* order;
+  int* position;
+  int* scratch;        // dispatch_scratch_bytes or route_scratch_bytes
+};
+size_t dispatch_scratch_bytes(int64_t R, int64_t E, int num_sms);
+size_t route_scratch_bytes(int64_t T, int64_t E, int num_sms);
+cudaError_t launch_dispatch(const int* ids, const SortCall& s, int64_t R, int64_t E, int num_sms,
+                            cudaStream_t st);
+// sort: null, or where the sorted choices go.
+cudaError_t launch_route(const RouteCall& c, const SortCall* sort, int num_sms, cudaStream_t st);
 
 }  // namespace swg

@@ -35,6 +35,7 @@
 
 #include "common.cuh"
 #include "grouped.h"
+#include "grouped_plan.cuh"
 #include "internal.h"
 #include "tc_common.cuh"
 #include "tc_pair.cuh"
@@ -73,97 +74,24 @@ struct RowMaps {
   CUtensorMap box[4];
 };
 
-struct Args {
+struct Args : Work {
   const uint16_t* x;       // gathered rows: [tokens, K]
   int K;
-  const int* offsets;      // [E + 1]; null: one group of `rows` rows
   const int* order;        // up: sorted row -> token * top_k + choice
-  int E, top_k, tokens;
-  int rows;                // rows of the sorted operand (an upper bound of offsets[E])
-  int n_kb, n_out;
-  int ncg;                 // column groups (units) per chunk
-  int n_max;               // most rows of a chunk, a multiple of 32
+  int top_k, tokens;
   int stages;
   uint32_t stage_bytes;
   int kmajor;              // weights stored [n_out, K]
   int prefetch_kb;         // linear: k blocks whose weights are asked into L2 early
-  int min_kb;              // fewest k blocks of a share of a cut unit
   void* out;
   int out_f32;
   const void* bias;        // linear
   int bias_f32, act;
   const void* resid;       // linear, in the output's type
-  float* part;
-  unsigned* counters;      // two per pair, zero on entry, left at zero
+  unsigned* counters;      // up: two per pair, zero on entry, left at zero
   unsigned* status;
   uint64_t timeout_ns;
 };
-
-// The work of a launch, from the offsets; the same in every thread.  (Units
-// fit 32 bits: a unit is at least 128 columns of at least one row.)
-struct Schedule {
-  uint32_t units, whole;   // units [0, whole) run whole
-  uint32_t cut_iters, q;   // the others (fewer than one per pair): k blocks in
-                           // all, and per pair
-};
-
-struct Unit {
-  int e, col0, row0, nrows, n;   // n: nrows rounded up to a multiple of 32
-};
-
-// First row of expert e, within the rows there are (whatever the caller's
-// offsets say, no row outside them is touched).
-__device__ __forceinline__ int first_row(const Args& a, int e) {
-  if (!a.offsets) return e == 0 ? 0 : a.rows;
-  const int v = a.offsets[e];
-  return v < 0 ? 0 : v > a.rows ? a.rows : v;
-}
-
-// s_row[e], s_chunk[e]: first row and first chunk of expert e (E + 1 entries).
-__device__ void plan_chunks(const Args& a, int* s_row, int* s_chunk) {
-  for (int e = threadIdx.x; e <= a.E; e += blockDim.x) s_row[e] = first_row(a, e);
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    int base = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + (int)threadIdx.x;
-      int c = 0;
-      if (e < a.E) {
-        const int m = s_row[e + 1] - s_row[e];
-        c = m > 0 ? (m + a.n_max - 1) / a.n_max : 0;
-      }
-      int inc = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if ((int)threadIdx.x >= o) inc += v;
-      }
-      if (e < a.E) s_chunk[e] = base + inc - c;
-      base += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (threadIdx.x == 0) s_chunk[a.E] = base;
-  }
-}
-
-__device__ __forceinline__ Schedule make_schedule(const Args& a, uint32_t chunks,
-                                                  uint32_t pairs) {
-  Schedule s;
-  s.units = chunks * (uint32_t)a.ncg;
-  s.whole = s.units;
-  s.cut_iters = 0;
-  s.q = 1;
-  const uint32_t rem = s.units % pairs;
-  if (rem * 4 <= pairs * 3 && rem > 0) {
-    uint32_t q = (rem * (uint32_t)a.n_kb + pairs - 1) / pairs;
-    if (q < (uint32_t)a.min_kb) q = a.min_kb;
-    if (q < (uint32_t)a.n_kb) {
-      s.whole = s.units - rem;
-      s.cut_iters = rem * (uint32_t)a.n_kb;
-      s.q = q;
-    }
-  }
-  return s;
-}
 
 // The work items of one pair: whole units, then its share of the cut units.
 struct WorkIter {
@@ -194,35 +122,6 @@ struct WorkIter {
     return false;
   }
 };
-
-// Unit u: units run expert by expert, column group by column group, chunk by
-// chunk, so that the pairs at work share an expert's weights and rows in L2.
-template <int COLS>
-__device__ __forceinline__ Unit find_unit(const Args& a, const int* s_row, const int* s_chunk,
-                                          uint32_t u) {
-  const int c = (int)(u / (uint32_t)a.ncg);
-  int lo = 0, hi = a.E;   // s_chunk[lo] <= c < s_chunk[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s_chunk[mid] <= c) lo = mid;
-    else hi = mid;
-  }
-  const int nc = s_chunk[lo + 1] - s_chunk[lo];
-  const int l = (int)(u - (uint32_t)s_chunk[lo] * (uint32_t)a.ncg);
-  const int cg = l / nc, chunk = l - cg * nc;
-  const int m = s_row[lo + 1] - s_row[lo];
-  const int per = (m + nc - 1) / nc;
-  Unit r;
-  r.e = lo;
-  r.col0 = cg * COLS;
-  r.row0 = s_row[lo] + chunk * per;
-  int n = m - chunk * per;
-  if (n > per) n = per;
-  if (n < 0) n = 0;
-  r.nrows = n;
-  r.n = n <= 32 ? 32 : (n + 31) / 32 * 32;
-  return r;
-}
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int c0, int c1, int c2) {
@@ -313,9 +212,9 @@ __device__ void prefetch_weights(const Args& a, const CUtensorMap& tm_w, const i
   const Schedule sch = make_schedule(a, (uint32_t)s_chunk[a.E], pairs);
   WorkIter w(sch, pair);
   uint32_t u;
-  int kb0, kb1, left = a.prefetch_kb;
+  int kb0, kb1, left = a.prefetch_kb, e_at = 0;
   while (left > 0 && w.next(a, sch, pairs, u, kb0, kb1)) {
-    const Unit un = find_unit<COLS>(a, s_row, s_chunk, u);
+    const Unit un = find_unit<COLS>(a, s_row, s_chunk, u, e_at);
     const int ca = un.col0 + 128 * (int)rank;
     for (int kb = kb0; kb < kb1 && left > 0; ++kb, --left) {
       if (a.kmajor) {
@@ -326,15 +225,6 @@ __device__ void prefetch_weights(const Args& a, const CUtensorMap& tm_w, const i
       }
     }
   }
-}
-
-// The f32 sums of a share of a cut unit: two slots per pair, one copy per
-// rank, each [32-row chunk][4-row group][column][4 rows], so that a warp moves
-// 512 contiguous bytes at a time.
-__device__ __forceinline__ int64_t part_stride(const Args& a) { return (int64_t)a.n_max * 128 * 4; }
-__device__ __forceinline__ float* part_slot(const Args& a, uint32_t pair, uint32_t which,
-                                            uint32_t rank) {
-  return a.part + (int64_t)pair * part_stride(a) + (int64_t)(which * 2 + rank) * (a.n_max * 128);
 }
 
 // v[0 .. 4 NQ) = the sum of `nseg` shares, in order: the first one's, then
@@ -465,18 +355,16 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
-  // Without a routing the work is known at once: the first weights are asked
-  // into L2 while the previous kernel ends.
-  if (!a.offsets) {
-    plan_chunks(a, s_row, s_chunk);
-    __syncthreads();
-    if (a.prefetch_kb > 0 && warp == kPrefetchWarp && lane == 0)
-      prefetch_weights<kCols>(a, tm_wa, s_row, s_chunk, pair, pairs, rank);
-  }
+  // Without a routing the work is known at once.
+  if (!a.offsets) plan_chunks(a, s_row, s_chunk);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();   // both CTAs' barriers and TMEM are ready
   tc_fence_after();
+  // ... and the first weights are asked into L2 while the previous kernel ends
+  // (by a warp that nothing waits for: issuing blocks while the TMA unit is busy)
+  if (!a.offsets && a.prefetch_kb > 0 && warp == kPrefetchWarp && lane == 0)
+    prefetch_weights<kCols>(a, tm_wa, s_row, s_chunk, pair, pairs, rank);
   // All of the above overlaps the previous kernel's tail; the routing, the
   // operands and the outputs are touched only after it has finished.
   pdl_wait();
@@ -501,9 +389,9 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
       bool ok = !skip;
       WorkIter w(sch, pair);
       uint32_t u;
-      int kb0, kb1;
+      int kb0, kb1, e_at = 0;
       while (ok && w.next(a, sch, pairs, u, kb0, kb1)) {
-        const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
+        const Unit un = find_unit<kCols>(a, s_row, s_chunk, u, e_at);
         // columns of the CTA's two weight boxes
         const int ca = un.col0 + (MODE == kGroupedSwiGLU ? 64 : 128) * (int)rank;
         const int cb = MODE == kGroupedSwiGLU ? ca : ca + 64;
@@ -555,24 +443,35 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
       bool ok = !skip;
       WorkIter w(sch, pair);
       uint32_t u;
-      int kb0, kb1;
-      while (ok && w.next(a, sch, pairs, u, kb0, kb1)) {
-        const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
-        const int half = un.n >> 1;
-        const int brow = un.row0 + (int)rank * half;
-        const int nb = half >> 4;
-        // this thread's rows (null: past the chunk, zeros)
+      int kb0, kb1, e_at = 0;
+      // The next unit's entries of `order` are fetched a unit ahead.
+      int half = 0, next_half = 0, next0 = 0, next1 = 0;
+      int flat[8];   // -1: past the chunk, zeros
+      auto fetch = [&]() -> bool {
+        if (!w.next(a, sch, pairs, u, next0, next1)) return false;
+        const Unit un = find_unit<kCols>(a, s_row, s_chunk, u, e_at);
+        next_half = un.n >> 1;
+        const int r0 = un.row0 + (int)rank * next_half + r16;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = r0 + j * 16;
+          flat[j] = j * 16 < next_half && r < un.row0 + un.nrows ? a.order[r] : -1;
+        }
+        return true;
+      };
+      bool more = ok && fetch();
+      while (ok && more) {
         const uint16_t* src[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          src[j] = nullptr;
-          const int r = brow + j * 16 + r16;
-          if (j < nb && r < un.row0 + un.nrows) {
-            const int flat = a.order[r];
-            const int t = flat / a.top_k;
-            if (flat >= 0 && t < a.tokens) src[j] = a.x + (int64_t)t * a.K;
-          }
+          const uint32_t t = (uint32_t)flat[j] / (uint32_t)a.top_k;
+          src[j] = flat[j] >= 0 && t < (uint32_t)a.tokens ? a.x + (int64_t)t * a.K : nullptr;
         }
+        half = next_half;
+        kb0 = next0;
+        kb1 = next1;
+        const int nb = half >> 4;
+        more = fetch();
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.status, a.timeout_ns)) {
             ok = false;
@@ -601,9 +500,9 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
       bool ok = !skip;
       WorkIter w(sch, pair);
       uint32_t u;
-      int kb0, kb1;
+      int kb0, kb1, e_at = 0;
       while (ok && w.next(a, sch, pairs, u, kb0, kb1)) {
-        const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
+        const Unit un = find_unit<kCols>(a, s_row, s_chunk, u, e_at);
         const int half = un.n >> 1;
         const int brow = un.row0 + (int)rank * half;
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -649,9 +548,9 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
       bool ok = !skip;
       WorkIter w(sch, pair);
       uint32_t u;
-      int kb0, kb1;
+      int kb0, kb1, e_at = 0;
       while (ok && w.next(a, sch, pairs, u, kb0, kb1)) {
-        const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
+        const Unit un = find_unit<kCols>(a, s_row, s_chunk, u, e_at);
         // D format f32, A and B bf16; A (weights) MN-major for [K, n_out] weights
         const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) |
                                ((a.kmajor ? 0u : 1u) << 15) | ((uint32_t)(un.n >> 3) << 17) |
@@ -736,57 +635,69 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
     uint32_t acc_phase = 0;
     WorkIter w(sch, pair);
     uint32_t u;
-    int kb0, kb1;
+    int kb0, kb1, e_at = 0;
     while (!skip && w.next(a, sch, pairs, u, kb0, kb1)) {
-      const Unit un = find_unit<kCols>(a, s_row, s_chunk, u);
+      const Unit un = find_unit<kCols>(a, s_row, s_chunk, u, e_at);
       if (!mbar_wait(&tfull[acc], acc_phase, abort_flag, a.status, a.timeout_ns)) break;
       tc_fence_after();
       const uint32_t t_acc = tmem + lane_off + (uint32_t)(acc * kAccCols);
       const bool whole = kb0 == 0 && kb1 == a.n_kb;
       const int nchunk = (un.nrows + 31) >> 5;
-      uint32_t c0 = 0, rel = 0, nseg = 0;
+      Shares sh{0, 0, 0};
       if (!whole) {
-        // A share of a cut unit: store the sums so far, take a ticket; the
-        // last of the unit's pairs adds all the shares in k order.  A pair's
-        // slot 0 holds the share of the unit its range begins in, slot 1 that
-        // of the unit its range ends in.
-        const uint32_t n_kb = (uint32_t)a.n_kb;
-        rel = u - sch.whole;
-        c0 = rel * n_kb / sch.q;
-        nseg = ((rel + 1) * n_kb - 1) / sch.q - c0 + 1;
-        const uint32_t which = pair * sch.q / n_kb == rel ? 0 : 1;
-        float* mine = part_slot(a, pair, which, rank) + col * 4;
+        // A share of a cut unit: store the sums so far.  A second kernel adds
+        // them up; for the up projection, the last of the unit's pairs to take
+        // a ticket does.
+        const uint32_t rel = u - sch.whole;
+        const uint32_t slot = pair * sch.q / (uint32_t)a.n_kb == rel ? 0 : 1;
+        float* mine = part_slot(a, pair, slot, rank);
 #pragma unroll 1
         for (int c = grp; c < nchunk; c += 2) {
           uint32_t v[32];
           tmem_ld_x32(t_acc + (uint32_t)(c * 32), v);
           tmem_wait_ld();
+          if constexpr (MODE == kGroupedSwiGLU) {
+            // [32-row chunk][4-row group][column][4 rows]
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (c * 32 + 4 * i < un.nrows)
-              __stcg(reinterpret_cast<float4*>(mine + (c * 8 + i) * 512),
-                     make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                 __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+            for (int i = 0; i < 8; ++i)
+              if (c * 32 + 4 * i < un.nrows)
+                __stcg(reinterpret_cast<float4*>(mine + col * 4 + (c * 8 + i) * 512),
+                       make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                   __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+          } else {
+            // [row][column]
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c * 32 + i < un.nrows) __stcg(mine + (c * 32 + i) * 128 + col, __uint_as_float(v[i]));
+          }
         }
         tc_fence_before();
         if (rank == 1) mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
         else mbar_arrive(&tempty[acc]);
-        __threadfence();
-        named_bar_sync(kBothBar, 2 * kEpiThreads);
-        if (grp == 0 && et == 0) *ticket_slot = atomicAdd(a.counters + c0 * 2 + rank, 1u);
-        named_bar_sync(kBothBar, 2 * kEpiThreads);
-        const unsigned ticket = *ticket_slot;
-        if (ticket + 1u != nseg) {
-          // not the last (or a counter left over by a call that gave up)
-          if (ticket >= nseg && grp == 0 && et == 0) atomicOr(a.status, kStatusStaleCounter);
+        bool last = false;
+        if constexpr (MODE == kGroupedSwiGLU) {
+          sh = shares_of(a, sch, rel);
+          __threadfence();
+          named_bar_sync(kBothBar, 2 * kEpiThreads);
+          unsigned* counter = a.counters + sh.first * 2 + rank;
+          if (grp == 0 && et == 0) *ticket_slot = atomicAdd(counter, 1u);
+          named_bar_sync(kBothBar, 2 * kEpiThreads);
+          const unsigned ticket = *ticket_slot;
+          last = ticket + 1u == sh.count;
+          // (a counter left over by a call that gave up)
+          if (ticket >= sh.count && grp == 0 && et == 0) atomicOr(a.status, kStatusStaleCounter);
+          if (last) {
+            __threadfence();
+            if (grp == 0 && et == 0) *counter = 0u;   // left at zero for the next call
+          }
+        }
+        if (!last) {
           if (++acc == 2) {
             acc = 0;
             acc_phase ^= 1u;
           }
           continue;
         }
-        __threadfence();
-        if (grp == 0 && et == 0) a.counters[c0 * 2 + rank] = 0u;   // left at zero for the next call
       }
       // this CTA's output columns, and the bias of this thread's column
       const int cbase = un.col0 + (MODE == kGroupedSwiGLU ? 64 : 128) * (int)rank;
@@ -803,14 +714,13 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
           uint32_t* vu = reinterpret_cast<uint32_t*>(v);
           tmem_ld_x32(t_acc + (uint32_t)(c * 32), vu);
           tmem_wait_ld();
-        } else {
-          const uint32_t which = c0 * sch.q / (uint32_t)a.n_kb == rel ? 0 : 1;
-          const float* first = part_slot(a, c0, which, rank) + c * 4096 + col * 4;
-          const float* rest = part_slot(a, c0 + 1, 0, rank) + c * 4096 + col * 4;
+        } else if constexpr (MODE == kGroupedSwiGLU) {
+          const float* first = part_slot(a, sh.first, sh.slot, rank) + c * 4096 + col * 4;
+          const float* rest = part_slot(a, sh.first + 1, 0, rank) + c * 4096 + col * 4;
           if (un.nrows - c * 32 <= 8)
-            add_shares<2, 8>(v, first, rest, part_stride(a), (int)nseg, un.nrows - c * 32);
+            add_shares<2, 8>(v, first, rest, part_stride(a), (int)sh.count, un.nrows - c * 32);
           else
-            add_shares<8, 2>(v, first, rest, part_stride(a), (int)nseg, un.nrows - c * 32);
+            add_shares<8, 2>(v, first, rest, part_stride(a), (int)sh.count, un.nrows - c * 32);
         }
         if constexpr (MODE == kGroupedSwiGLU) {
           // Columns 0-63 hold x.W_gate, 64-127 x.W_up of the same 64 columns
@@ -904,6 +814,40 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
   }
 }
 
+// The cut units of a linear product: y = act(sum of the shares + bias) +
+// residual, eight columns of one row per thread, the shares in k order.
+// Bound by L2 latency: a share is one round trip, so four are loaded at a time.
+constexpr int kJoinThreads = 128;
+
+__global__ void __launch_bounds__(kJoinThreads)
+linear_join_kernel(const __grid_constant__ Args a, int chunks, const Schedule sch) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const uint32_t i = blockIdx.x * kJoinThreads + threadIdx.x;
+  const uint32_t per = (uint32_t)a.n_max * 32u;
+  const uint32_t rel = i / per;
+  if (rel >= sch.units - sch.whole) return;
+  const uint32_t rem = i - rel * per;
+  const int r = (int)(rem >> 5), o = (int)(rem & 31);
+  const uint32_t u = sch.whole + rel;
+  const int cg = (int)(u / (uint32_t)chunks), chunk = (int)(u - (uint32_t)cg * (uint32_t)chunks);
+  int row0, nrows;
+  chunk_rows(a.rows, chunks, chunk, &row0, &nrows);
+  const int c = cg * 256 + o * 8;
+  if (r >= nrows || c >= a.n_out) return;
+  const Shares sh = shares_of(a, sch, rel);
+  float v[8];
+  add_row_shares(a, sh, (uint32_t)(o >> 4), r * 128 + (o & 15) * 8, v);
+  if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c + j < a.n_out)
+        v[j] += a.bias_f32 ? ((const float*)a.bias)[c + j] : bf16_lo(((const uint16_t*)a.bias)[c + j]);
+  }
+  activate_n<8>(v, a.act, a.out_f32 != 0);
+  store_row8<kGroupedLinear>(a, (int64_t)(row0 + r) * a.n_out + c, a.n_out - c, v);
+}
+
 // y = act(bias) + residual, for products over nothing (K = 0).
 __global__ void __launch_bounds__(256)
 empty_linear_kernel(const void* bias, int bias_f32, int act, const void* resid, void* y, int out_f32,
@@ -992,12 +936,26 @@ GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, int64_t K, int
   p.pairs = pairs < 1 ? 1 : pairs;
   p.counters_bytes = ((size_t)p.pairs * 2 * sizeof(unsigned) + 255) / 256 * 256;
   p.part_bytes = (size_t)p.pairs * 4 * (size_t)p.n_max * 128 * sizeof(float);
-  p.min_kb = tn.gr_min_kb > 0 ? tn.gr_min_kb : 4;
+  p.min_kb = tn.gr_min_kb > 0 ? tn.gr_min_kb : 16;
+  p.cut = tn.gr_cut >= 0 ? tn.gr_cut : (!swiglu || p.n_max <= 64);
   p.prefetch_kb = tn.gr_prefetch >= 0 ? tn.gr_prefetch : (E == 1 && p.n_max <= 64 ? 32 : 0);
   (void)K;
   (void)n_out;
-  (void)swiglu;
   return p;
+}
+
+void fill_work(Work* w, int mode, const GroupedCall& c, const GroupedPlan& p, float* part) {
+  const int cols = mode == kGroupedSwiGLU ? 128 : 256;
+  w->offsets = c.offsets;
+  w->E = (int)c.E;
+  w->rows = (int)c.rows;
+  w->n_kb = (int)((c.K + kBK - 1) / kBK);
+  w->n_out = (int)c.n_out;
+  w->ncg = (int)((c.n_out + cols - 1) / cols);
+  w->n_max = p.n_max;
+  w->cut = p.cut;
+  w->min_kb = p.min_kb;
+  w->part = part;
 }
 
 cudaError_t launch_grouped(int mode, const GroupedCall& c, const GroupedPlan& p, float* part,
@@ -1044,21 +1002,13 @@ cudaError_t launch_grouped(int mode, const GroupedCall& c, const GroupedPlan& p,
   Args a{};
   a.x = (const uint16_t*)c.x;
   a.K = (int)c.K;
-  a.offsets = c.offsets;
   a.order = c.order;
-  a.E = (int)c.E;
   a.top_k = (int)(c.top_k > 0 ? c.top_k : 1);
   a.tokens = (int)c.tokens;
-  a.rows = (int)c.rows;
-  a.n_kb = (int)((c.K + kBK - 1) / kBK);
-  a.n_out = (int)c.n_out;
-  const int cols = mode == kGroupedSwiGLU ? 128 : 256;
-  a.ncg = (int)((c.n_out + cols - 1) / cols);
-  a.n_max = p.n_max;
+  fill_work(&a, mode, c, p, part);
   a.stages = p.stages;
   a.stage_bytes = p.stage_bytes;
   a.kmajor = kmajor ? 1 : 0;
-  a.min_kb = p.min_kb;
   a.prefetch_kb = c.offsets ? 0 : p.prefetch_kb;
   a.out = c.out;
   a.out_f32 = c.out_f32;
@@ -1066,19 +1016,35 @@ cudaError_t launch_grouped(int mode, const GroupedCall& c, const GroupedPlan& p,
   a.bias_f32 = c.bias_f32;
   a.act = c.act;
   a.resid = c.resid;
-  a.part = part;
   a.counters = counters;
   a.status = status;
   a.timeout_ns = timeout_ns;
-  if (!counters_clean &&
+  if (mode == kGroupedSwiGLU && p.cut && !counters_clean &&
       (e = cudaMemsetAsync(counters, 0, p.counters_bytes, st)) != cudaSuccess)
     return e;
   const size_t smem = smem_bytes(p, a.E);
   switch (mode) {
     case kGroupedSwiGLU: return launch_mode<kGroupedSwiGLU, true>(mx, ma, mb, a, p.pairs, smem, st);
     case kGroupedPlain: return launch_mode<kGroupedPlain, false>(mx, ma, mb, a, p.pairs, smem, st);
-    default: return launch_mode<kGroupedLinear, false>(mx, ma, mb, a, p.pairs, smem, st);
+    default: break;
   }
+  if ((e = launch_mode<kGroupedLinear, false>(mx, ma, mb, a, p.pairs, smem, st)) != cudaSuccess)
+    return e;
+  // cut units: a second kernel adds their shares
+  const uint32_t chunks = (uint32_t)((c.rows + p.n_max - 1) / p.n_max);
+  const Schedule sch = make_schedule(a, chunks, (uint32_t)p.pairs);
+  const uint32_t cut = sch.units - sch.whole;
+  if (cut == 0) return cudaSuccess;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((int64_t)cut * p.n_max * 32 + kJoinThreads - 1) / kJoinThreads));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear_join_kernel, a, (int)chunks, sch);
 }
 
 }  // namespace swg

@@ -18,9 +18,9 @@
 namespace swg {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kRouteThreads = 512;      // also the sort's
+constexpr int kWarps = kRouteThreads / 32;
 
 // Order-preserving map of f32 to unsigned; -inf and NaN map to 0, which no
 // other value does.  (-0 maps to +0: they tie.)
@@ -49,208 +49,257 @@ struct RouteArgs {
   float* weights;
   int64_t T;
   int E, k, sigmoid, groups, topk_groups, group_top2, renormalize, logits_f32;
+  int vec;   // rows of logits start on 16-byte boundaries
   float scale;
 };
 
-// One warp per token; lane l holds experts l VPL .. l VPL + VPL - 1, so the
-// lowest lane with the largest key holds the lowest index.
+// The sorted choices' outputs and scratch.
+struct SortArgs {
+  const int* ids;
+  int* offsets;
+  int* order;
+  int* position;
+  int64_t R;       // choices
+  int64_t seg;     // choices per block
+  int E;
+  int* counts;     // [E][blocks]: how many choices of its segment each block found
+};
+
+// VPL values of row t, experts lane VPL ..; -inf past E and for NaN.
 template <int VPL>
-__global__ void __launch_bounds__(kThreads)
-route_kernel(const RouteArgs a) {
-  extern __shared__ float s_mem[];   // groups: per warp E candidate values, then the groups' keys
-  tc::pdl_wait();
-  tc::pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int E = a.E;
-  for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < a.T; t += (int64_t)gridDim.x * kWarps) {
-    float l[VPL], s[VPL];
-    unsigned key[VPL];
-    float m = -INFINITY;
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, int lane, float* l) {
+  const int e0 = lane * VPL;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane * VPL + i;
-      l[i] = -INFINITY;
-      if (e < E) {
-        const float v = a.logits_f32 ? ((const float*)a.logits)[t * E + e]
-                                     : bf16_lo(((const uint16_t*)a.logits)[t * E + e]);
-        if (v > -INFINITY) l[i] = v;   // NaN counts as -inf
-      }
-      m = fmaxf(m, l[i]);
-    }
-    if (a.sigmoid) {
+  for (int i = 0; i < VPL; ++i) l[i] = -INFINITY;
+  if (a.logits_f32) {
+    const float* src = (const float*)a.logits + t * a.E + e0;
+    if (VPL >= 4 && a.vec) {   // E is a multiple of 4
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) s[i] = 1.0f / (1.0f + expf(-l[i]));
+      for (int i = 0; i < VPL; i += 4)
+        if (e0 + i < a.E) {
+          const float4 q = __ldg(reinterpret_cast<const float4*>(src + i));
+          l[i] = q.x;
+          if constexpr (VPL >= 4) { l[i + 1] = q.y; l[i + 2] = q.z; l[i + 3] = q.w; }
+        }
     } else {
-      m = warp_max(m);
-      float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        // (an infinite logit has exp(inf - inf) = 1)
-        s[i] = l[i] > -INFINITY ? (l[i] == m ? 1.0f : expf(l[i] - m)) : 0.f;
-        sum += s[i];
-      }
-      sum = warp_sum(sum);
-      if (sum > 0.f) {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) s[i] = s[i] / sum;
-      }
+      for (int i = 0; i < VPL; ++i)
+        if (e0 + i < a.E) l[i] = __ldg(src + i);
     }
-    float v[VPL];
+  } else {
+    const uint16_t* src = (const uint16_t*)a.logits + t * a.E + e0;
+    if (VPL >= 8 && a.vec) {   // E is a multiple of 8
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane * VPL + i;
-      v[i] = l[i];
-      if (a.bias && e < E && l[i] > -INFINITY) v[i] = s[i] + a.bias[e];
-      key[i] = sort_key(v[i]);
-    }
-    if (a.groups > 1) {
-      // the groups' values: the largest candidate, or the sum of the two largest
-      float* vals = s_mem + warp * (E + 32);
-      unsigned* gk = reinterpret_cast<unsigned*>(vals + E);
-      const bool scores = a.group_top2 && !a.bias;   // the top-two sum is of scores
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane * VPL + i;
-        if (e < E) vals[e] = key[i] ? (scores ? s[i] : v[i]) : -INFINITY;
-      }
-      __syncwarp();
-      const int size = E / a.groups;
-      unsigned mine = 0u;
-      if (lane < a.groups) {
-        float b0 = -INFINITY, b1 = -INFINITY;
-        for (int q = 0; q < size; ++q) {
-          int i = q + lane;   // start apart: other banks
-          if (i >= size) i %= size;
-          const float x = vals[lane * size + i];
-          if (x > b0) {
-            b1 = b0;
-            b0 = x;
-          } else if (x > b1) {
-            b1 = x;
+      for (int i = 0; i < VPL; i += 8)
+        if (e0 + i < a.E) {
+          const uint4 q = __ldg(reinterpret_cast<const uint4*>(src + i));
+          if constexpr (VPL >= 8) {
+            l[i] = bf16_lo(q.x); l[i + 1] = bf16_hi(q.x);
+            l[i + 2] = bf16_lo(q.y); l[i + 3] = bf16_hi(q.y);
+            l[i + 4] = bf16_lo(q.z); l[i + 5] = bf16_hi(q.z);
+            l[i + 6] = bf16_lo(q.w); l[i + 7] = bf16_hi(q.w);
           }
         }
-        mine = sort_key(a.group_top2 && b1 > -INFINITY ? b0 + b1 : b0);
-      }
-      gk[lane] = mine;
-      __syncwarp();
-      int better = 0;
-      for (int g = 0; g < a.groups; ++g) {
-        const unsigned o = gk[g];
-        better += (o > mine || (o == mine && g < lane)) ? 1 : 0;
-      }
-      const unsigned kept = __ballot_sync(kAll, lane < a.groups && better < a.topk_groups);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane * VPL + i;
-        if (e >= E || !((kept >> (e / size)) & 1u)) key[i] = 0u;
-      }
-    }
-    // k times the best that is left; lane j keeps choice j
-    int my_id = -1;
-    float my_w = 0.f, total = 0.f;
-    for (int j = 0; j < a.k; ++j) {
-      unsigned best = 0u;
-      int bi = 0;
+    } else {
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (key[i] > best) {
-          best = key[i];
-          bi = i;
-        }
-      const unsigned top = __reduce_max_sync(kAll, best);
-      if (top == 0u) break;
-      const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
-      float sv = 0.f;
+        if (e0 + i < a.E) l[i] = bf16_lo(__ldg(src + i));
+    }
+  }
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i == bi) {
-          sv = s[i];
-          if (lane == owner) key[i] = 0u;
-        }
-      const int id = __shfl_sync(kAll, lane * VPL + bi, owner);
-      const float w = __shfl_sync(kAll, sv, owner);
-      total += w;
-      if (lane == j) {
-        my_id = id;
-        my_w = w;
+  for (int i = 0; i < VPL; ++i) l[i] = l[i] > -INFINITY ? l[i] : -INFINITY;   // NaN: -inf
+}
+
+// Larger and second of the pairs (b0, b1) and (c0, c1), each in order.
+__device__ __forceinline__ void merge_two(float& b0, float& b1, float c0, float c1) {
+  b1 = fmaxf(fminf(b0, c0), fmaxf(b1, c1));
+  b0 = fmaxf(b0, c0);
+}
+
+// Keys of the experts outside the kept groups become 0.  cand: the values a
+// group is ranked by, -inf for experts that cannot be chosen.
+template <int VPL>
+__device__ __forceinline__ void limit_groups(const RouteArgs& a, int lane, const float* cand,
+                                             unsigned* key, float* vals) {
+  const int size = a.E / a.groups;
+  unsigned mine = 0u;   // lane g: group g's key
+  const int lpg = size / VPL;   // lanes per group, where groups are whole lanes
+  const bool aligned = lpg * VPL == size && lpg > 0 && (lpg & (lpg - 1)) == 0;
+  if (aligned) {
+    float b0 = -INFINITY, b1 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) merge_two(b0, b1, cand[i], -INFINITY);
+    for (int o = 1; o < lpg; o <<= 1) {
+      const float c0 = __shfl_xor_sync(kAll, b0, o), c1 = __shfl_xor_sync(kAll, b1, o);
+      merge_two(b0, b1, c0, c1);
+    }
+    const unsigned k = sort_key(a.group_top2 && b1 > -INFINITY ? b0 + b1 : b0);
+    // lane g takes group g's key (the lanes of a group hold the same one)
+    const int from = lane * lpg;
+    mine = __shfl_sync(kAll, k, from & 31);
+    if (lane >= a.groups) mine = 0u;
+  } else {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane * VPL + i < a.E) vals[lane * VPL + i] = cand[i];
+    __syncwarp();
+    if (lane < a.groups) {
+      float b0 = -INFINITY, b1 = -INFINITY;
+      for (int q = 0; q < size; ++q) {
+        int i = q + lane;   // start apart: other banks
+        if (i >= size) i %= size;
+        merge_two(b0, b1, vals[lane * size + i], -INFINITY);
       }
+      mine = sort_key(a.group_top2 && b1 > -INFINITY ? b0 + b1 : b0);
     }
-    if (a.renormalize && total > 0.f) my_w = my_w / total;
-    if (lane < a.k) {
-      a.ids[t * a.k + lane] = my_id;
-      a.weights[t * a.k + lane] = my_w * a.scale;
-    }
+  }
+  int better = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const unsigned o = __shfl_sync(kAll, mine, g);
+    better += (o > mine || (o == mine && g < lane)) ? 1 : 0;
+  }
+  const unsigned kept = __ballot_sync(kAll, lane < a.groups && better < a.topk_groups);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane * VPL + i;
+    if (e >= a.E || !((kept >> (e / size)) & 1u)) key[i] = 0u;
   }
 }
 
-constexpr int kSortThreads = 256;
-constexpr int kSortWarps = kSortThreads / 32;
-
-// Counts of each block's segment of the choices: hist [blocks][E].
-__global__ void __launch_bounds__(kSortThreads)
-hist_kernel(const int* __restrict__ ids, int* __restrict__ hist, int64_t R, int E, int64_t seg) {
-  extern __shared__ int s_cnt[];
-  tc::pdl_wait();
-  tc::pdl_launch_dependents();
-  for (int e = threadIdx.x; e < E; e += kSortThreads) s_cnt[e] = 0;
-  __syncthreads();
-  const int64_t r0 = (int64_t)blockIdx.x * seg, r1 = r0 + seg < R ? r0 + seg : R;
-  for (int64_t r = r0 + threadIdx.x; r < r1; r += kSortThreads) {
-    const int e = ids[r];
-    if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
+// One warp, one token.  Lane l holds experts l VPL .. l VPL + VPL - 1, so the
+// lowest lane with the largest key holds the lowest index.  vals: E floats of
+// shared memory of the warp's own.  Lane j < k returns choice j.
+template <int VPL>
+__device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, int lane, float* vals,
+                                           float* weight) {
+  float l[VPL], s[VPL];
+  unsigned key[VPL];
+  load_logits<VPL>(a, t, lane, l);
+  if (a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) s[i] = 1.0f / (1.0f + expf(-l[i]));
+  } else {
+    float m = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) m = fmaxf(m, l[i]);
+    m = warp_max(m);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      // (an infinite logit has exp(inf - inf) = 1)
+      s[i] = l[i] > -INFINITY ? (l[i] == m ? 1.0f : expf(l[i] - m)) : 0.f;
+      sum += s[i];
+    }
+    sum = warp_sum(sum);
+    if (sum > 0.f) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) s[i] = s[i] / sum;
+    }
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kSortThreads) hist[(int64_t)blockIdx.x * E + e] = s_cnt[e];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane * VPL + i;
+    if (a.bias && e < a.E && l[i] > -INFINITY) l[i] = s[i] + __ldg(a.bias + e);
+    key[i] = sort_key(l[i]);
+  }
+  if (a.groups > 1) {
+    float cand[VPL];
+    const bool scores = a.group_top2 && !a.bias;   // the top-two sum is of scores
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) cand[i] = key[i] ? (scores ? s[i] : l[i]) : -INFINITY;
+    limit_groups<VPL>(a, lane, cand, key, vals);
+  }
+  // the scores, for the lanes that end up with a choice
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (lane * VPL + i < a.E) vals[lane * VPL + i] = s[i];
+  __syncwarp();
+  // k times the best that is left; lane j keeps choice j
+  int my_id = -1;
+  for (int j = 0; j < a.k; ++j) {
+    unsigned best = key[0];
+    int bi = 0;
+#pragma unroll
+    for (int i = 1; i < VPL; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        bi = i;
+      }
+    const unsigned top = __reduce_max_sync(kAll, best);
+    if (top == 0u) break;
+    const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
+    const int id = owner * VPL + __shfl_sync(kAll, bi, owner);
+    if (lane == j) my_id = id;
+    if (lane == owner) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (i == bi) key[i] = 0u;
+    }
+  }
+  float w = my_id >= 0 ? vals[my_id] : 0.f;
+  if (a.renormalize) {
+    const float total = warp_sum(w);
+    if (total > 0.f) w = w / total;
+  }
+  *weight = w * a.scale;
+  return my_id;
 }
 
-// Stable scatter of one block's segment.  Each warp has a contiguous part of
-// it: the warps' counts give every (warp, expert) its first place, and a warp
-// places 32 choices at a time, equal ones in lane order.
-__global__ void __launch_bounds__(kSortThreads)
-scatter_kernel(const int* __restrict__ ids, const int* __restrict__ hist, int* __restrict__ offsets,
-               int* __restrict__ order, int* __restrict__ position, int64_t R, int E, int64_t seg) {
-  extern __shared__ int s_place[];   // [warps][E] counts, then places; then [E] totals
-  int* s_tot = s_place + kSortWarps * E;
-  tc::pdl_wait();
-  tc::pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int nb = gridDim.x;
-  for (int i = threadIdx.x; i < kSortWarps * E; i += kSortThreads) s_place[i] = 0;
+// Stable scatter of the choices of this block's segment.  Each warp has a
+// contiguous part of them: offsets, the earlier blocks' counts and the earlier
+// warps' give every (warp, expert) its first place, and a warp places 32
+// choices at a time, equal ones in lane order.  Shared memory: s_place
+// [kWarps][E], s_tot [E + 1], s_before [E].
+__device__ void scatter_block(const SortArgs& a, const int* ids, int* s_place) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
+  const int nb = (int)gridDim.x, blk = (int)blockIdx.x;
+  int* s_tot = s_place + kWarps * E;
+  int* s_before = s_tot + E + 1;
+  const int64_t r0 = (int64_t)blk * a.seg < a.R ? (int64_t)blk * a.seg : a.R;
+  const int64_t r1 = r0 + a.seg < a.R ? r0 + a.seg : a.R;
+  for (int i = threadIdx.x; i < kWarps * E; i += kRouteThreads) s_place[i] = 0;
   __syncthreads();
-  const int64_t r0 = (int64_t)blockIdx.x * seg, r1 = r0 + seg < R ? r0 + seg : R;
-  const int64_t part = (seg + kSortWarps - 1) / kSortWarps;
+  int64_t part = (r1 - r0 + kWarps - 1) / kWarps;
+  part = (part + 31) / 32 * 32;
   const int64_t w0 = r0 + warp * part;
   const int64_t w1 = w0 + part < r1 ? w0 + part : r1;
   for (int64_t r = w0 + lane; r < w1; r += 32) {
     const int e = ids[r];
     if (e >= 0 && e < E) atomicAdd(&s_place[warp * E + e], 1);
   }
-  __syncthreads();
-  // per expert: all blocks' total, and what the blocks before this one hold
-  for (int e = threadIdx.x; e < E; e += kSortThreads) {
-    int before = 0, all = 0;
-    if (hist) {
-      for (int b = 0; b < nb; ++b) {
-        const int c = hist[(int64_t)b * E + e];
-        if (b < (int)blockIdx.x) before += c;
+  if (nb > 1) {
+    // a warp per expert: all blocks' counts, and those of the blocks before
+#pragma unroll 4
+    for (int e = warp; e < E; e += kWarps) {
+      int all = 0, before = 0;
+      for (int b = lane; b < nb; b += 32) {
+        const int c = __ldcg(a.counts + (int64_t)e * nb + b);
         all += c;
+        if (b < blk) before += c;
       }
-    } else {
-      for (int w = 0; w < kSortWarps; ++w) all += s_place[w * E + e];
+      all = __reduce_add_sync(kAll, all);
+      before = __reduce_add_sync(kAll, before);
+      if (lane == 0) {
+        s_tot[e] = all;
+        s_before[e] = before;
+      }
     }
-    int run = before;
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int c = s_place[w * E + e];
-      s_place[w * E + e] = run;
-      run += c;
+    __syncthreads();
+  } else {
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+      int all = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) all += s_place[w * E + e];
+      s_tot[e] = all;
+      s_before[e] = 0;
     }
-    s_tot[e] = all;
+    __syncthreads();
   }
-  __syncthreads();
   // exclusive prefix of the totals: the experts' offsets
   if (warp == 0) {
-    int base = 0;
+    int sum = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
       const int c = e < E ? s_tot[e] : 0;
@@ -260,17 +309,26 @@ scatter_kernel(const int* __restrict__ ids, const int* __restrict__ hist, int* _
         const int v = __shfl_up_sync(kAll, inc, o);
         if (lane >= o) inc += v;
       }
-      if (e < E) s_tot[e] = base + inc - c;
-      base += __shfl_sync(kAll, inc, 31);
+      if (e < E) s_tot[e] = sum + inc - c;
+      sum += __shfl_sync(kAll, inc, 31);
     }
-    if (lane == 0) s_tot[E] = base;
+    if (lane == 0) s_tot[E] = sum;
   }
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int e = threadIdx.x; e <= E; e += kSortThreads) offsets[e] = s_tot[e];
-  const int valid = s_tot[E];
-  for (int64_t base = w0; base < w1; base += 32) {
-    const int64_t r = base + lane;
+  for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+    int run = s_tot[e] + s_before[e];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int c = s_place[w * E + e];
+      s_place[w * E + e] = run;
+      run += c;
+    }
+  }
+  if (blk == 0)
+    for (int e = threadIdx.x; e <= E; e += kRouteThreads) a.offsets[e] = s_tot[e];
+  __syncthreads();
+  for (int64_t b = w0; b < w1; b += 32) {
+    const int64_t r = b + lane;
     int e = -1;
     if (r < w1) {
       e = ids[r];
@@ -279,19 +337,87 @@ scatter_kernel(const int* __restrict__ ids, const int* __restrict__ hist, int* _
     const unsigned same = __match_any_sync(kAll, e);
     const int rank = __popc(same & ((1u << lane) - 1u));
     int place = -1;
-    if (e >= 0) place = s_tot[e] + s_place[warp * E + e] + rank;
+    if (e >= 0) place = s_place[warp * E + e] + rank;
     __syncwarp();
     if (e >= 0 && rank == 0) s_place[warp * E + e] += __popc(same);
     __syncwarp();
     if (r < w1) {
-      position[r] = place;
-      if (place >= 0) order[place] = (int)r;
+      a.position[r] = place;
+      if (place >= 0) a.order[place] = (int)r;
     }
   }
   // places that no choice takes
-  for (int64_t r = (int64_t)valid + (int64_t)blockIdx.x * kSortThreads + threadIdx.x; r < R;
-       r += (int64_t)nb * kSortThreads)
-    order[r] = -1;
+  for (int64_t r = (int64_t)s_tot[E] + (int64_t)blk * kRouteThreads + threadIdx.x; r < a.R;
+       r += (int64_t)nb * kRouteThreads)
+    a.order[r] = -1;
+}
+
+enum SortMode : int { kNoSort = 0, kSortHere = 1, kCount = 2 };
+
+// Routing.  kSortHere: one block, which also sorts its choices.  kCount: block
+// b has a contiguous range of tokens and leaves its experts' counts for the
+// scatter kernel.
+template <int VPL, int SORT>
+__global__ void __launch_bounds__(kRouteThreads)
+route_kernel(const RouteArgs a, const SortArgs so) {
+  extern __shared__ int s_mem[];
+  // scores of the warps' tokens; afterwards (kSortHere) the sort's counts
+  float* vals = reinterpret_cast<float*>(s_mem) + (threadIdx.x >> 5) * a.E;
+  int* s_cnt = s_mem + kWarps * a.E;   // [E + 1]
+  tc::pdl_wait();
+  tc::pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if constexpr (SORT == kCount) {
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) s_cnt[e] = 0;
+    __syncthreads();
+  }
+  const int64_t per = (a.T + gridDim.x - 1) / gridDim.x;
+  const int64_t t0 = (int64_t)blockIdx.x * per;
+  const int64_t t1 = t0 + per < a.T ? t0 + per : a.T;
+  for (int64_t t = t0 + warp; t < t1; t += kWarps) {
+    float w;
+    const int id = route_token<VPL>(a, t, lane, vals, &w);
+    if (lane < a.k) {
+      a.ids[t * a.k + lane] = id;
+      a.weights[t * a.k + lane] = w;
+      if (SORT == kCount && id >= 0) atomicAdd(&s_cnt[id], 1);
+    }
+  }
+  if constexpr (SORT == kSortHere) {
+    __syncthreads();
+    scatter_block(so, a.ids, s_mem);
+  }
+  if constexpr (SORT == kCount) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads)
+      so.counts[(int64_t)e * gridDim.x + blockIdx.x] = s_cnt[e];
+  }
+}
+
+// Counts of each block's segment of given choices.
+__global__ void __launch_bounds__(kRouteThreads)
+count_kernel(const SortArgs a) {
+  extern __shared__ int s_mem[];
+  tc::pdl_wait();
+  tc::pdl_launch_dependents();
+  for (int e = threadIdx.x; e < a.E; e += kRouteThreads) s_mem[e] = 0;
+  __syncthreads();
+  const int64_t r0 = (int64_t)blockIdx.x * a.seg, r1 = r0 + a.seg < a.R ? r0 + a.seg : a.R;
+  for (int64_t r = r0 + threadIdx.x; r < r1; r += kRouteThreads) {
+    const int e = a.ids[r];
+    if (e >= 0 && e < a.E) atomicAdd(&s_mem[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kRouteThreads)
+    a.counts[(int64_t)e * gridDim.x + blockIdx.x] = s_mem[e];
+}
+
+__global__ void __launch_bounds__(kRouteThreads)
+scatter_kernel(const SortArgs a) {
+  extern __shared__ int s_mem[];
+  tc::pdl_wait();
+  tc::pdl_launch_dependents();
+  scatter_block(a, a.ids, s_mem);
 }
 
 template <typename... P, typename... A>
@@ -310,17 +436,60 @@ cudaError_t launch_pdl(void (*kern)(P...), unsigned grid, unsigned block, size_t
   return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 
-// Choices per block of the sort.
-int64_t sort_segment(int64_t R) {
-  int64_t seg = 2048;
-  while ((R + seg - 1) / seg > 128) seg *= 2;
-  return seg;
+size_t sort_smem(int64_t E) { return (size_t)((kWarps + 2) * E + 1) * sizeof(int); }
+
+// Blocks of a sort of R choices: one up to 2048 of them, else up to one per SM.
+int64_t sort_blocks(int64_t R, int num_sms) {
+  if (R <= 2048) return 1;
+  const int64_t nb = (R + 511) / 512;
+  return nb < num_sms ? nb : num_sms;
+}
+
+// Tokens that one block routes and sorts by itself (one launch).
+constexpr int64_t kOneBlockTokens = 64;
+
+// Blocks of the routing: a warp per token, up to one block per SM.
+int64_t route_blocks(int64_t T, int num_sms) {
+  const int64_t nb = (T + kWarps - 1) / kWarps;
+  return nb < 1 ? 1 : nb < num_sms ? nb : num_sms;
+}
+
+// (18 ints per expert of shared memory: above 48 KB from 683 experts on)
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <int VPL>
+cudaError_t launch_route_vpl(const RouteArgs& a, const SortArgs& so, int mode, unsigned grid,
+                             cudaStream_t st) {
+  const size_t smem = sort_smem(a.E);
+  cudaError_t e;
+  if (mode == kSortHere) {
+    if ((e = allow_smem(route_kernel<VPL, kSortHere>, smem)) != cudaSuccess) return e;
+    return launch_pdl(route_kernel<VPL, kSortHere>, 1, kRouteThreads, smem, st, a, so);
+  }
+  if (mode == kCount) {
+    if ((e = allow_smem(route_kernel<VPL, kCount>, smem)) != cudaSuccess) return e;
+    return launch_pdl(route_kernel<VPL, kCount>, grid, kRouteThreads, smem, st, a, so);
+  }
+  if ((e = allow_smem(route_kernel<VPL, kNoSort>, smem)) != cudaSuccess) return e;
+  return launch_pdl(route_kernel<VPL, kNoSort>, grid, kRouteThreads, smem, st, a, so);
 }
 
 }  // namespace
 
-cudaError_t launch_route(const RouteCall& c, int num_sms, cudaStream_t st) {
-  if (c.T == 0) return cudaSuccess;
+size_t dispatch_scratch_bytes(int64_t R, int64_t E, int num_sms) {
+  const int64_t nb = sort_blocks(R, num_sms);
+  return nb > 1 ? (size_t)nb * E * sizeof(int) : 0;
+}
+
+size_t route_scratch_bytes(int64_t T, int64_t E, int num_sms) {
+  return T > kOneBlockTokens ? (size_t)route_blocks(T, num_sms) * E * sizeof(int) : 0;
+}
+
+cudaError_t launch_route(const RouteCall& c, const SortCall* sort, int num_sms, cudaStream_t st) {
   RouteArgs a;
   a.logits = c.logits;
   a.bias = c.bias;
@@ -335,37 +504,40 @@ cudaError_t launch_route(const RouteCall& c, int num_sms, cudaStream_t st) {
   a.group_top2 = c.group_top2;
   a.renormalize = c.renormalize;
   a.logits_f32 = c.logits_f32;
+  a.vec = ((uintptr_t)c.logits & 15u) == 0 && c.E % (c.logits_f32 ? 4 : 8) == 0;
   a.scale = c.scale;
-  int64_t blocks = (c.T + kWarps - 1) / kWarps;
-  if (blocks > (int64_t)num_sms * 16) blocks = (int64_t)num_sms * 16;
-  const size_t smem = c.groups > 1 ? (size_t)kWarps * (c.E + 32) * sizeof(float) : 0;
-  const unsigned g = (unsigned)blocks;
-  if (c.E <= 32) return launch_pdl(route_kernel<1>, g, kThreads, smem, st, a);
-  if (c.E <= 64) return launch_pdl(route_kernel<2>, g, kThreads, smem, st, a);
-  if (c.E <= 128) return launch_pdl(route_kernel<4>, g, kThreads, smem, st, a);
-  if (c.E <= 256) return launch_pdl(route_kernel<8>, g, kThreads, smem, st, a);
-  if (c.E <= 512) return launch_pdl(route_kernel<16>, g, kThreads, smem, st, a);
-  return launch_pdl(route_kernel<32>, g, kThreads, smem, st, a);
+  SortArgs so{};
+  int mode = kNoSort;
+  const int64_t nb = route_blocks(c.T, num_sms);
+  if (sort) {
+    // (kCount: the sort's segments are the routing's ranges of tokens)
+    mode = c.T <= kOneBlockTokens ? kSortHere : kCount;
+    so = SortArgs{c.ids, sort->offsets, sort->order, sort->position, c.T * c.k,
+                  mode == kCount ? (c.T + nb - 1) / nb * c.k : c.T * c.k, (int)c.E, sort->scratch};
+  }
+  const unsigned g = (unsigned)nb;
+  cudaError_t e = c.E <= 32    ? launch_route_vpl<1>(a, so, mode, g, st)
+                  : c.E <= 64  ? launch_route_vpl<2>(a, so, mode, g, st)
+                  : c.E <= 128 ? launch_route_vpl<4>(a, so, mode, g, st)
+                  : c.E <= 256 ? launch_route_vpl<8>(a, so, mode, g, st)
+                  : c.E <= 512 ? launch_route_vpl<16>(a, so, mode, g, st)
+                               : launch_route_vpl<32>(a, so, mode, g, st);
+  if (e != cudaSuccess || mode != kCount) return e;
+  if ((e = allow_smem(scatter_kernel, sort_smem(c.E))) != cudaSuccess) return e;
+  return launch_pdl(scatter_kernel, g, kRouteThreads, sort_smem(c.E), st, so);
 }
 
-size_t dispatch_scratch_bytes(int64_t R, int64_t E) {
-  const int64_t nb = (R + sort_segment(R) - 1) / sort_segment(R);
-  return nb > 1 ? (size_t)nb * E * sizeof(int) : 0;
-}
-
-cudaError_t launch_dispatch(const int* ids, int* offsets, int* order, int* position, int64_t R,
-                            int64_t E, int* scratch, cudaStream_t st) {
-  const int64_t seg = sort_segment(R);
-  int64_t nb = (R + seg - 1) / seg;
-  if (nb < 1) nb = 1;
-  const size_t smem = (size_t)(kSortWarps * E + E + 1) * sizeof(int);   // 36 KB at E = 1024
+cudaError_t launch_dispatch(const int* ids, const SortCall& s, int64_t R, int64_t E, int num_sms,
+                            cudaStream_t st) {
+  const int64_t nb = sort_blocks(R, num_sms);
+  SortArgs so{ids, s.offsets, s.order, s.position, R, (R + nb - 1) / nb, (int)E, s.scratch};
+  cudaError_t e;
   if (nb > 1) {
-    cudaError_t e = launch_pdl(hist_kernel, (unsigned)nb, kSortThreads, (size_t)E * sizeof(int), st,
-                               ids, scratch, R, (int)E, seg);
+    e = launch_pdl(count_kernel, (unsigned)nb, kRouteThreads, (size_t)(E + 1) * sizeof(int), st, so);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(scatter_kernel, (unsigned)nb, kSortThreads, smem, st, ids,
-                    nb > 1 ? scratch : (int*)nullptr, offsets, order, position, R, (int)E, seg);
+  if ((e = allow_smem(scatter_kernel, sort_smem(E))) != cudaSuccess) return e;
+  return launch_pdl(scatter_kernel, (unsigned)nb, kRouteThreads, sort_smem(E), st, so);
 }
 
 }  // namespace swg

@@ -520,6 +520,7 @@ Tuning read_tuning() {
                           {"SIMT_CLUSTER", &t.simt_cluster},
                           {"GR_ROWS", &t.gr_rows},
                           {"GR_MIN_KB", &t.gr_min_kb},
+                          {"GR_CUT", &t.gr_cut},
                           {"GR_PREFETCH", &t.gr_prefetch},
                           {"INJECT_OOM", &t.inject_oom}};
     for (const Knob& k : knobs)
