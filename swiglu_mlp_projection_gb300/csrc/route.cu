@@ -19,8 +19,14 @@ namespace swg {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kRouteThreads = 512;      // also the sort's
-constexpr int kWarps = kRouteThreads / 32;
+// Threads per block of the routing and of the sort.  Up to 256 experts a token
+// takes 64 registers per thread, so that 32 warps fit on an SM; above that the
+// scores alone take 16 or 32 registers, and 16 warps fit.
+constexpr int block_threads(int64_t E) { return E <= 256 ? 1024 : 512; }
+constexpr int vpl_threads(int vpl) { return vpl <= 8 ? 1024 : 512; }
+// A block that routes a few tokens and sorts them by itself: its latency is
+// that of its barriers and of clearing the warps' counts.
+constexpr int kFewThreads = 256;
 
 // Order-preserving map of f32 to unsigned; -inf and NaN map to 0, which no
 // other value does.  (-0 maps to +0: they tie.)
@@ -62,7 +68,7 @@ struct SortArgs {
   int64_t R;       // choices
   int64_t seg;     // choices per block
   int E;
-  int* counts;     // [E][blocks]: how many choices of its segment each block found
+  int* counts;     // [blocks][E]: how many choices of its segment each block found
 };
 
 // VPL values of row t, experts lane VPL ..; -inf past E and for NaN.
@@ -125,6 +131,7 @@ __device__ __forceinline__ void limit_groups(const RouteArgs& a, int lane, const
   unsigned mine = 0u;   // lane g: group g's key
   const int lpg = size / VPL;   // lanes per group, where groups are whole lanes
   const bool aligned = lpg * VPL == size && lpg > 0 && (lpg & (lpg - 1)) == 0;
+  const int own = aligned ? lane / lpg : 0;   // this lane's group
   if (aligned) {
     float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
@@ -160,10 +167,17 @@ __device__ __forceinline__ void limit_groups(const RouteArgs& a, int lane, const
     better += (o > mine || (o == mine && g < lane)) ? 1 : 0;
   }
   const unsigned kept = __ballot_sync(kAll, lane < a.groups && better < a.topk_groups);
+  if (aligned) {
+    if (own >= a.groups || !((kept >> own) & 1u)) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane * VPL + i;
-    if (e >= a.E || !((kept >> (e / size)) & 1u)) key[i] = 0u;
+      for (int i = 0; i < VPL; ++i) key[i] = 0u;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane * VPL + i;
+      if (e >= a.E || !((kept >> (e / size)) & 1u)) key[i] = 0u;
+    }
   }
 }
 
@@ -171,14 +185,14 @@ __device__ __forceinline__ void limit_groups(const RouteArgs& a, int lane, const
 // lowest lane with the largest key holds the lowest index.  vals: E floats of
 // shared memory of the warp's own.  Lane j < k returns choice j.
 template <int VPL>
-__device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, int lane, float* vals,
-                                           float* weight) {
+__device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, int lane,
+                                           const float* bias, float* vals, float* weight) {
   float l[VPL], s[VPL];
   unsigned key[VPL];
   load_logits<VPL>(a, t, lane, l);
   if (a.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) s[i] = 1.0f / (1.0f + expf(-l[i]));
+    for (int i = 0; i < VPL; ++i) s[i] = __frcp_rn(1.0f + expf(-l[i]));
   } else {
     float m = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -198,8 +212,7 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, int la
   }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int e = lane * VPL + i;
-    if (a.bias && e < a.E && l[i] > -INFINITY) l[i] = s[i] + __ldg(a.bias + e);
+    if (a.bias && l[i] > -INFINITY) l[i] = s[i] + bias[i];
     key[i] = sort_key(l[i]);
   }
   if (a.groups > 1) {
@@ -211,31 +224,38 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, int la
   }
   // the scores, for the lanes that end up with a choice
   __syncwarp();
+  if constexpr (VPL >= 4) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    if (lane * VPL + i < a.E) vals[lane * VPL + i] = s[i];
+    for (int i = 0; i < VPL; i += 4)
+      *reinterpret_cast<float4*>(vals + lane * VPL + i) =
+          make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) vals[lane * VPL + i] = s[i];
+  }
   __syncwarp();
   // k times the best that is left; lane j keeps choice j
   int my_id = -1;
   for (int j = 0; j < a.k; ++j) {
     unsigned best = key[0];
-    int bi = 0;
 #pragma unroll
-    for (int i = 1; i < VPL; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        bi = i;
-      }
+    for (int i = 1; i < VPL; ++i) best = max(best, key[i]);
     const unsigned top = __reduce_max_sync(kAll, best);
     if (top == 0u) break;
     const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
-    const int id = owner * VPL + __shfl_sync(kAll, bi, owner);
-    if (lane == j) my_id = id;
+    int bi = 0;
     if (lane == owner) {
+      bool open = true;
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (i == bi) key[i] = 0u;
+        if (open && key[i] == top) {
+          key[i] = 0u;
+          bi = i;
+          open = false;
+        }
     }
+    const int id = owner * VPL + __shfl_sync(kAll, bi, owner);
+    if (lane == j) my_id = id;
   }
   float w = my_id >= 0 ? vals[my_id] : 0.f;
   if (a.renormalize) {
@@ -250,8 +270,10 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, int la
 // contiguous part of them: offsets, the earlier blocks' counts and the earlier
 // warps' give every (warp, expert) its first place, and a warp places 32
 // choices at a time, equal ones in lane order.  Shared memory: s_place
-// [kWarps][E], s_tot [E + 1], s_before [E].
+// [warps][E], s_tot [E + 1], s_before [E].
+template <int THREADS>
 __device__ void scatter_block(const SortArgs& a, const int* ids, int* s_place) {
+  constexpr int kWarps = THREADS / 32, kRouteThreads = THREADS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = a.E;
   const int nb = (int)gridDim.x, blk = (int)blockIdx.x;
   int* s_tot = s_place + kWarps * E;
@@ -269,21 +291,28 @@ __device__ void scatter_block(const SortArgs& a, const int* ids, int* s_place) {
     if (e >= 0 && e < E) atomicAdd(&s_place[warp * E + e], 1);
   }
   if (nb > 1) {
-    // a warp per expert: all blocks' counts, and those of the blocks before
-#pragma unroll 4
-    for (int e = warp; e < E; e += kWarps) {
+    // All blocks' counts, and those of the blocks before: `parts` threads per
+    // expert, each over a range of blocks, 16 loads at a time.
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) s_tot[e] = s_before[e] = 0;
+    __syncthreads();
+    const int parts = E < kRouteThreads ? kRouteThreads / E : 1;
+    const int span = (nb + parts - 1) / parts;
+    for (int i = threadIdx.x; i < parts * E; i += kRouteThreads) {
+      const int p = i / E, e = i - p * E;
+      const int b0 = p * span, b1 = b0 + span < nb ? b0 + span : nb;
       int all = 0, before = 0;
-      for (int b = lane; b < nb; b += 32) {
-        const int c = __ldcg(a.counts + (int64_t)e * nb + b);
-        all += c;
-        if (b < blk) before += c;
+      for (int b = b0; b < b1; b += 16) {
+        int c[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) c[q] = b + q < b1 ? __ldcg(a.counts + (int64_t)(b + q) * E + e) : 0;
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          all += c[q];
+          if (b + q < blk) before += c[q];
+        }
       }
-      all = __reduce_add_sync(kAll, all);
-      before = __reduce_add_sync(kAll, before);
-      if (lane == 0) {
-        s_tot[e] = all;
-        s_before[e] = before;
-      }
+      if (all) atomicAdd(&s_tot[e], all);
+      if (before) atomicAdd(&s_before[e], before);
     }
     __syncthreads();
   } else {
@@ -357,13 +386,18 @@ enum SortMode : int { kNoSort = 0, kSortHere = 1, kCount = 2 };
 // Routing.  kSortHere: one block, which also sorts its choices.  kCount: block
 // b has a contiguous range of tokens and leaves its experts' counts for the
 // scatter kernel.
+constexpr int route_threads(int vpl, int sort) {
+  return sort == kSortHere ? kFewThreads : vpl_threads(vpl);
+}
+
 template <int VPL, int SORT>
-__global__ void __launch_bounds__(kRouteThreads)
+__global__ void __launch_bounds__(route_threads(VPL, SORT), 1)
 route_kernel(const RouteArgs a, const SortArgs so) {
-  extern __shared__ int s_mem[];
-  // scores of the warps' tokens; afterwards (kSortHere) the sort's counts
-  float* vals = reinterpret_cast<float*>(s_mem) + (threadIdx.x >> 5) * a.E;
-  int* s_cnt = s_mem + kWarps * a.E;   // [E + 1]
+  constexpr int kRouteThreads = route_threads(VPL, SORT), kWarps = kRouteThreads / 32;
+  extern __shared__ __align__(16) int s_mem[];
+  // scores of the warps' tokens (32 VPL each); afterwards (kSortHere) the sort's
+  float* vals = reinterpret_cast<float*>(s_mem) + (threadIdx.x >> 5) * (32 * VPL);
+  int* s_cnt = s_mem + kWarps * 32 * VPL;   // [E]
   tc::pdl_wait();
   tc::pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -374,9 +408,13 @@ route_kernel(const RouteArgs a, const SortArgs so) {
   const int64_t per = (a.T + gridDim.x - 1) / gridDim.x;
   const int64_t t0 = (int64_t)blockIdx.x * per;
   const int64_t t1 = t0 + per < a.T ? t0 + per : a.T;
+  float bias[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    bias[i] = a.bias && lane * VPL + i < a.E ? a.bias[lane * VPL + i] : 0.f;
   for (int64_t t = t0 + warp; t < t1; t += kWarps) {
     float w;
-    const int id = route_token<VPL>(a, t, lane, vals, &w);
+    const int id = route_token<VPL>(a, t, lane, bias, vals, &w);
     if (lane < a.k) {
       a.ids[t * a.k + lane] = id;
       a.weights[t * a.k + lane] = w;
@@ -385,18 +423,20 @@ route_kernel(const RouteArgs a, const SortArgs so) {
   }
   if constexpr (SORT == kSortHere) {
     __syncthreads();
-    scatter_block(so, a.ids, s_mem);
+    scatter_block<kRouteThreads>(so, a.ids, s_mem);
   }
   if constexpr (SORT == kCount) {
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += kRouteThreads)
-      so.counts[(int64_t)e * gridDim.x + blockIdx.x] = s_cnt[e];
+      so.counts[(int64_t)blockIdx.x * a.E + e] = s_cnt[e];
   }
 }
 
 // Counts of each block's segment of given choices.
-__global__ void __launch_bounds__(kRouteThreads)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1)
 count_kernel(const SortArgs a) {
+  constexpr int kRouteThreads = THREADS;
   extern __shared__ int s_mem[];
   tc::pdl_wait();
   tc::pdl_launch_dependents();
@@ -409,15 +449,16 @@ count_kernel(const SortArgs a) {
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.E; e += kRouteThreads)
-    a.counts[(int64_t)e * gridDim.x + blockIdx.x] = s_mem[e];
+    a.counts[(int64_t)blockIdx.x * a.E + e] = s_mem[e];
 }
 
-__global__ void __launch_bounds__(kRouteThreads)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1)
 scatter_kernel(const SortArgs a) {
   extern __shared__ int s_mem[];
   tc::pdl_wait();
   tc::pdl_launch_dependents();
-  scatter_block(a, a.ids, s_mem);
+  scatter_block<THREADS>(a, a.ids, s_mem);
 }
 
 template <typename... P, typename... A>
@@ -436,7 +477,9 @@ cudaError_t launch_pdl(void (*kern)(P...), unsigned grid, unsigned block, size_t
   return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 
-size_t sort_smem(int64_t E) { return (size_t)((kWarps + 2) * E + 1) * sizeof(int); }
+size_t sort_smem(int64_t E) {
+  return (size_t)((block_threads(E) / 32 + 2) * E + 1) * sizeof(int);
+}
 
 // Blocks of a sort of R choices: one up to 2048 of them, else up to one per SM.
 int64_t sort_blocks(int64_t R, int num_sms) {
@@ -446,15 +489,15 @@ int64_t sort_blocks(int64_t R, int num_sms) {
 }
 
 // Tokens that one block routes and sorts by itself (one launch).
-constexpr int64_t kOneBlockTokens = 64;
+constexpr int64_t kOneBlockTokens = 16;
 
-// Blocks of the routing: a warp per token, up to one block per SM.
+// Blocks of the routing: 16 tokens or more each, up to one block per SM.
 int64_t route_blocks(int64_t T, int num_sms) {
-  const int64_t nb = (T + kWarps - 1) / kWarps;
+  const int64_t nb = (T + 15) / 16;
   return nb < 1 ? 1 : nb < num_sms ? nb : num_sms;
 }
 
-// (18 ints per expert of shared memory: above 48 KB from 683 experts on)
+// (up to 74 KB at 1024 experts)
 template <typename K>
 cudaError_t allow_smem(K kern, size_t bytes) {
   if (bytes <= 48 * 1024) return cudaSuccess;
@@ -464,18 +507,34 @@ cudaError_t allow_smem(K kern, size_t bytes) {
 template <int VPL>
 cudaError_t launch_route_vpl(const RouteArgs& a, const SortArgs& so, int mode, unsigned grid,
                              cudaStream_t st) {
-  const size_t smem = sort_smem(a.E);
+  constexpr int threads = vpl_threads(VPL);
+  // the warps' scores and the block's counts, or the sort's
+  size_t smem = (size_t)(threads * VPL + a.E) * sizeof(int);
+  if (smem < sort_smem(a.E)) smem = sort_smem(a.E);
   cudaError_t e;
   if (mode == kSortHere) {
     if ((e = allow_smem(route_kernel<VPL, kSortHere>, smem)) != cudaSuccess) return e;
-    return launch_pdl(route_kernel<VPL, kSortHere>, 1, kRouteThreads, smem, st, a, so);
+    return launch_pdl(route_kernel<VPL, kSortHere>, 1, kFewThreads, smem, st, a, so);
   }
   if (mode == kCount) {
     if ((e = allow_smem(route_kernel<VPL, kCount>, smem)) != cudaSuccess) return e;
-    return launch_pdl(route_kernel<VPL, kCount>, grid, kRouteThreads, smem, st, a, so);
+    return launch_pdl(route_kernel<VPL, kCount>, grid, threads, smem, st, a, so);
   }
   if ((e = allow_smem(route_kernel<VPL, kNoSort>, smem)) != cudaSuccess) return e;
-  return launch_pdl(route_kernel<VPL, kNoSort>, grid, kRouteThreads, smem, st, a, so);
+  return launch_pdl(route_kernel<VPL, kNoSort>, grid, threads, smem, st, a, so);
+}
+
+template <int THREADS>
+cudaError_t launch_scatter(const SortArgs& so, unsigned grid, cudaStream_t st) {
+  const size_t smem = sort_smem(so.E);
+  cudaError_t e = allow_smem(scatter_kernel<THREADS>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(scatter_kernel<THREADS>, grid, THREADS, smem, st, so);
+}
+
+cudaError_t launch_scatter(const SortArgs& so, unsigned grid, cudaStream_t st) {
+  return block_threads(so.E) == 1024 ? launch_scatter<1024>(so, grid, st)
+                                     : launch_scatter<512>(so, grid, st);
 }
 
 }  // namespace
@@ -523,8 +582,7 @@ cudaError_t launch_route(const RouteCall& c, const SortCall* sort, int num_sms, 
                   : c.E <= 512 ? launch_route_vpl<16>(a, so, mode, g, st)
                                : launch_route_vpl<32>(a, so, mode, g, st);
   if (e != cudaSuccess || mode != kCount) return e;
-  if ((e = allow_smem(scatter_kernel, sort_smem(c.E))) != cudaSuccess) return e;
-  return launch_pdl(scatter_kernel, g, kRouteThreads, sort_smem(c.E), st, so);
+  return launch_scatter(so, g, st);
 }
 
 cudaError_t launch_dispatch(const int* ids, const SortCall& s, int64_t R, int64_t E, int num_sms,
@@ -533,11 +591,10 @@ cudaError_t launch_dispatch(const int* ids, const SortCall& s, int64_t R, int64_
   SortArgs so{ids, s.offsets, s.order, s.position, R, (R + nb - 1) / nb, (int)E, s.scratch};
   cudaError_t e;
   if (nb > 1) {
-    e = launch_pdl(count_kernel, (unsigned)nb, kRouteThreads, (size_t)(E + 1) * sizeof(int), st, so);
+    e = launch_pdl(count_kernel<512>, (unsigned)nb, 512, (size_t)E * sizeof(int), st, so);
     if (e != cudaSuccess) return e;
   }
-  if ((e = allow_smem(scatter_kernel, sort_smem(E))) != cudaSuccess) return e;
-  return launch_pdl(scatter_kernel, (unsigned)nb, kRouteThreads, sort_smem(E), st, so);
+  return launch_scatter(so, (unsigned)nb, st);
 }
 
 }  // namespace swg

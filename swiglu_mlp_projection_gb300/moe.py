@@ -9,58 +9,62 @@ calls are asynchronous on torch's current stream (or ``stream``).
 import collections
 
 from . import _lib
-from . import _call, _check_cuda, _raw_stream
+from . import _call, _raw_stream, _torch
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 SCORES = {"softmax": 0, "sigmoid": 1}
 GROUP_SCORES = {"max": 0, "top2": 1}
 LAYOUTS = {"kn": 0, "nk": 1}
 
-Routing = collections.namedtuple("Routing", "ids weights offsets order position")
-Routing.__doc__ = """Where each token goes: ids [T, k] int32 (-1: no expert), weights [T, k]
-float32, and the (token, choice) pairs sorted by expert: offsets [E + 1],
-order [T k], position [T, k], int32 (``route`` and ``dispatch`` write them)."""
+
+
+class Routing(collections.namedtuple("Routing", "ids weights offsets order position")):
+    """Where each token goes: ids [T, k] int32 (-1: no expert), weights [T, k]
+    float32, and the (token, choice) pairs sorted by expert: offsets [E + 1],
+    order [T k], position [T, k], int32 (``route`` and ``dispatch`` write them)."""
+
+    _checked = None   # (device, T, k, E, addresses), once its tensors have been checked
 
 
 def _code(table, value, what):
-    try:
-        return table[value]
-    except (KeyError, TypeError):
-        raise ValueError("%s must be one of %s" % (what, sorted(table))) from None
+    code = table.get(value) if isinstance(value, str) else None
+    if code is None:
+        raise ValueError("%s must be one of %s" % (what, sorted(table)))
+    return code
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _check(t, name, index, dtype=None):
+    """A contiguous tensor on CUDA device `index` (of `dtype`); its address."""
+    if t.get_device() != index:
+        raise ValueError("%s must be a CUDA tensor on the first argument's device" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    return t.data_ptr()
 
 
-def _workspace(workspace):
+def _first(t, name, dtype=None):
+    """The CUDA device of the first argument; checks it as the others."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    _check(t, name, index, dtype)
+    return index
+
+
+def _workspace(workspace, index):
     if workspace is None:
         return None, 0
-    _check_cuda(workspace=workspace)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return _check(workspace, "workspace", index), workspace.numel() * workspace.element_size()
 
 
-def _same_device(index, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != index:
-            raise ValueError("%s must be on the same device as the first argument" % name)
-
-
-def _bf16(**tensors):
-    import torch
-    for name, t in tensors.items():
-        if t is not None and t.dtype != torch.bfloat16:
-            raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))
-
-
-def _out(out, shape, dtype, like):
-    import torch
+def _out(torch, out, shape, dtype, index, device):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _check_cuda(out=out)
-    _same_device(like.get_device(), out=out)
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype:
-        raise ValueError("out must be a contiguous %s tensor of %s" % (tuple(shape), dtype))
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(out, "out", index)
+    if out.shape != shape or out.dtype is not dtype:
+        raise ValueError("out must be a contiguous %s tensor of %s" % (shape, dtype))
     return out
 
 
@@ -74,35 +78,38 @@ def linear(x, w, bias=None, residual=None, activation="none", out=None, out_dtyp
     function), "gelu_tanh".  The result [M, N] is ``out_dtype`` (bfloat16, the
     default, or float32); residual has its type and may be ``out``.
     """
-    import torch
-    _check_cuda(x=x, w=w, bias=bias, residual=residual)
-    _bf16(x=x, w=w)
+    torch = _torch()
+    bf16 = torch.bfloat16
+    index = _first(x, "x", bf16)
+    pw = _check(w, "w", index, bf16)
     lay = _code(LAYOUTS, layout, "layout")
     act = _code(ACTIVATIONS, activation, "activation")
     if x.dim() != 2 or w.dim() != 2 or w.shape[lay] != x.shape[1]:
         raise ValueError("expected x [M, K] and w [K, N] (kn) or [N, K] (nk)")
     M, K = x.shape
     N = w.shape[1 - lay]
-    index = x.get_device()
-    _same_device(index, w=w, bias=bias, residual=residual)
     if out_dtype is None:
-        out_dtype = torch.bfloat16 if out is None else out.dtype
-    if out_dtype not in (torch.bfloat16, torch.float32):
+        out_dtype = bf16 if out is None else out.dtype
+    if out_dtype is not bf16 and out_dtype is not torch.float32:
         raise TypeError("out_dtype must be bfloat16 or float32")
-    bias_code = _lib.BF16
+    pb, bias_code = None, _lib.BF16
     if bias is not None:
-        if bias.shape != (N,):
+        pb = _check(bias, "bias", index)
+        if bias.dim() != 1 or bias.shape[0] != N:
             raise ValueError("bias must be [N] = [%d]" % N)
-        if bias.dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError("bias must be bfloat16 or float32")
-        bias_code = _lib.BF16 if bias.dtype == torch.bfloat16 else _lib.F32
-    if residual is not None and (residual.shape != (M, N) or residual.dtype != out_dtype):
-        raise ValueError("residual must be [M, N] of the result's dtype")
-    out = _out(out, (M, N), out_dtype, x)
-    ws, nws = _workspace(workspace)
-    _call(index, _lib.load().swiglu_linear, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual),
-          out.data_ptr(), M, K, N, act, bias_code,
-          _lib.BF16 if out_dtype == torch.bfloat16 else _lib.F32, lay, ws, nws,
+        if bias.dtype is not bf16:
+            bias_code = _lib.F32
+            if bias.dtype is not torch.float32:
+                raise TypeError("bias must be bfloat16 or float32")
+    pr = None
+    if residual is not None:
+        pr = _check(residual, "residual", index)
+        if residual.shape != (M, N) or residual.dtype is not out_dtype:
+            raise ValueError("residual must be [M, N] of the result's dtype")
+    out = _out(torch, out, (M, N), out_dtype, index, x.device)
+    ws, nws = _workspace(workspace, index)
+    _call(index, _lib.load().swiglu_linear, x.data_ptr(), pw, pb, pr, out.data_ptr(), M, K, N, act,
+          bias_code, _lib.BF16 if out_dtype is bf16 else _lib.F32, lay, ws, nws,
           stream.cuda_stream if stream is not None else _raw_stream(index))
     return out
 
@@ -118,83 +125,86 @@ def route(logits, k, score="softmax", bias=None, groups=1, topk_groups=None, gro
     best).  Ties go to the lowest index.  Experts whose logit is -inf or NaN are
     masked; missing choices are id -1 with weight 0.
     """
-    import torch
-    _check_cuda(logits=logits, bias=bias)
+    torch = _torch()
+    index = _first(logits, "logits")
     if logits.dim() != 2:
         raise ValueError("expected logits [T, E]")
-    if logits.dtype == torch.float32:
-        dt = _lib.F32
-    elif logits.dtype == torch.bfloat16:
+    f32 = torch.float32
+    dt = _lib.F32
+    if logits.dtype is not f32:
         dt = _lib.BF16
-    else:
-        raise TypeError("logits must be float32 or bfloat16, got %s" % logits.dtype)
+        if logits.dtype is not torch.bfloat16:
+            raise TypeError("logits must be float32 or bfloat16, got %s" % logits.dtype)
     T, E = logits.shape
-    index = logits.get_device()
+    pb = None
     if bias is not None:
-        _same_device(index, bias=bias)
-        if bias.shape != (E,) or bias.dtype != torch.float32:
+        pb = _check(bias, "bias", index)
+        if bias.dim() != 1 or bias.shape[0] != E or bias.dtype is not f32:
             raise ValueError("bias must be a float32 [E] = [%d] tensor" % E)
     sc = _code(SCORES, score, "score")
     gs = _code(GROUP_SCORES, group_score, "group_score")
-    if topk_groups is None:
-        topk_groups = groups
-    dev = logits.device
     if k < 0:
         raise ValueError("k must not be negative")
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    order = torch.empty(T * k, dtype=torch.int32, device=dev)
-    position = torch.empty((T, k), dtype=torch.int32, device=dev)
-    _call(index, _lib.load().swiglu_route, logits.data_ptr(), _ptr(bias), ids.data_ptr(),
+    dev, i32 = logits.device, torch.int32
+    ids = torch.empty((T, k), dtype=i32, device=dev)
+    weights = torch.empty((T, k), dtype=f32, device=dev)
+    offsets = torch.empty((E + 1,), dtype=i32, device=dev)
+    order = torch.empty((T * k,), dtype=i32, device=dev)
+    position = torch.empty((T, k), dtype=i32, device=dev)
+    _call(index, _lib.load().swiglu_route, logits.data_ptr(), pb, ids.data_ptr(),
           weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), position.data_ptr(), T, E, k,
-          dt, sc, groups, topk_groups, gs, 1 if renormalize else 0, float(scale),
+          dt, sc, groups, groups if topk_groups is None else topk_groups, gs,
+          1 if renormalize else 0, scale,
           stream.cuda_stream if stream is not None else _raw_stream(index))
-    return Routing(ids, weights, offsets, order, position)
+    r = Routing(ids, weights, offsets, order, position)
+    r._checked = (index, T, k, E, offsets.data_ptr(), order.data_ptr(), position.data_ptr(),
+                  weights.data_ptr())
+    return r
 
 
 def dispatch(ids, n_experts, weights=None, stream=None):
     """A Routing from chosen experts ids [T, k] (int32; values outside
     0 ... n_experts - 1 are dropped) and their weights [T, k] (float32)."""
-    import torch
-    _check_cuda(ids=ids, weights=weights)
-    if ids.dim() != 2 or ids.dtype != torch.int32:
+    torch = _torch()
+    index = _first(ids, "ids")
+    if ids.dim() != 2 or ids.dtype is not torch.int32:
         raise ValueError("expected int32 ids [T, k]")
     T, k = ids.shape
-    index = ids.get_device()
     if weights is not None:
-        _same_device(index, weights=weights)
-        if weights.shape != ids.shape or weights.dtype != torch.float32:
+        _check(weights, "weights", index)
+        if weights.shape != ids.shape or weights.dtype is not torch.float32:
             raise ValueError("weights must be float32 of ids' shape")
-    dev = ids.device
-    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
-    order = torch.empty(T * k, dtype=torch.int32, device=dev)
-    position = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if n_experts < 1:
+        raise ValueError("n_experts must be positive")
+    dev, i32 = ids.device, torch.int32
+    offsets = torch.empty((n_experts + 1,), dtype=i32, device=dev)
+    order = torch.empty((T * k,), dtype=i32, device=dev)
+    position = torch.empty((T, k), dtype=i32, device=dev)
     _call(index, _lib.load().swiglu_dispatch, ids.data_ptr(), offsets.data_ptr(), order.data_ptr(),
           position.data_ptr(), T, k, n_experts,
           stream.cuda_stream if stream is not None else _raw_stream(index))
     return Routing(ids, weights, offsets, order, position)
 
 
-def _check_routing(routing, T, E, index, weights):
-    import torch
-    T2, k = routing.position.shape
-    if T2 != T:
-        raise ValueError("the routing is of %d tokens, not %d" % (T2, T))
-    if routing.offsets.shape != (E + 1,) or routing.order.shape != (T * k,):
-        raise ValueError("the routing is not one of %d experts" % E)
-    for name in ("offsets", "order", "position"):
-        if getattr(routing, name).dtype != torch.int32:
-            raise TypeError("routing.%s must be int32" % name)
-    _check_cuda(offsets=routing.offsets, order=routing.order, position=routing.position)
-    _same_device(index, offsets=routing.offsets, order=routing.order, position=routing.position)
-    if weights:
-        w = routing.weights
-        if w is None or w.shape != (T, k) or w.dtype != torch.float32:
-            raise ValueError("the routing needs float32 weights [T, k]")
-        _check_cuda(weights=w)
-        _same_device(index, weights=w)
-    return k
+def _check_routing(torch, r):
+    """(device, T, k, E, addresses of offsets, order, position, weights), checked
+    once per Routing: its tensors cannot be exchanged."""
+    i32, position = torch.int32, r.position
+    index = _first(position, "routing.position", i32)
+    if position.dim() != 2 or r.offsets.dim() != 1 or r.offsets.shape[0] < 2:
+        raise ValueError("expected position [T, k] and offsets [E + 1] in the routing")
+    T, k = position.shape
+    po = _check(r.offsets, "routing.offsets", index, i32)
+    pr = _check(r.order, "routing.order", index, i32)
+    if r.order.shape != (T * k,):
+        raise ValueError("expected order [T k] = [%d] in the routing" % (T * k))
+    pw = None
+    if r.weights is not None:
+        pw = _check(r.weights, "routing.weights", index, torch.float32)
+        if r.weights.shape != (T, k):
+            raise ValueError("expected weights [T, k] in the routing")
+    r._checked = (index, T, k, r.offsets.shape[0] - 1, po, pr, position.data_ptr(), pw)
+    return r._checked
 
 
 def experts_up(x, w_gate, w_up, routing, out=None, layout="kn", workspace=None, stream=None):
@@ -204,23 +214,26 @@ def experts_up(x, w_gate, w_up, routing, out=None, layout="kn", workspace=None, 
     x [T, d]; w_gate, w_up [E, d, d_ff] ("kn") or [E, d_ff, d] ("nk"); all
     contiguous bfloat16.  Rows of dropped choices (at the end) are zero.
     """
-    import torch
-    _check_cuda(x=x, w_gate=w_gate, w_up=w_up)
-    _bf16(x=x, w_gate=w_gate, w_up=w_up)
+    torch = _torch()
+    bf16 = torch.bfloat16
+    index = _first(x, "x", bf16)
+    pg = _check(w_gate, "w_gate", index, bf16)
+    pu = _check(w_up, "w_up", index, bf16)
     lay = _code(LAYOUTS, layout, "layout")
     if x.dim() != 2 or w_gate.dim() != 3 or w_up.shape != w_gate.shape \
             or w_gate.shape[1 + lay] != x.shape[1]:
         raise ValueError("expected x [T, d] and w_gate, w_up [E, d, d_ff] or [E, d_ff, d]")
     T, d = x.shape
     E, d_ff = w_gate.shape[0], w_gate.shape[2 - lay]
-    index = x.get_device()
-    _same_device(index, w_gate=w_gate, w_up=w_up)
-    k = _check_routing(routing, T, E, index, False)
-    out = _out(out, (T * k, d_ff), torch.bfloat16, x)
-    ws, nws = _workspace(workspace)
-    _call(index, _lib.load().swiglu_experts_up, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
-          routing.offsets.data_ptr(), routing.order.data_ptr(), out.data_ptr(), T, k, E, d, d_ff,
-          lay, ws, nws, stream.cuda_stream if stream is not None else _raw_stream(index))
+    rdev, rT, k, rE, po, pr, _, _ = routing._checked or _check_routing(torch, routing)
+    if rT != T or rE != E or rdev != index:
+        raise ValueError("the routing is of %d tokens and %d experts on device %d, not %d, %d, %d"
+                         % (rT, rE, rdev, T, E, index))
+    out = _out(torch, out, (T * k, d_ff), bf16, index, x.device)
+    ws, nws = _workspace(workspace, index)
+    _call(index, _lib.load().swiglu_experts_up, x.data_ptr(), pg, pu, po, pr, out.data_ptr(), T, k,
+          E, d, d_ff, lay, ws, nws,
+          stream.cuda_stream if stream is not None else _raw_stream(index))
     return out
 
 
@@ -232,27 +245,32 @@ def experts_down(h, w_down, routing, residual=None, out=None, layout="kn", works
     [E, d, d_ff] ("nk"); residual [T, d] (may be ``out``) or None; all
     contiguous bfloat16.  Returns y [T, d].
     """
-    import torch
-    _check_cuda(h=h, w_down=w_down, residual=residual)
-    _bf16(h=h, w_down=w_down, residual=residual)
+    torch = _torch()
+    bf16 = torch.bfloat16
+    index = _first(h, "h", bf16)
+    pw = _check(w_down, "w_down", index, bf16)
     lay = _code(LAYOUTS, layout, "layout")
     if h.dim() != 2 or w_down.dim() != 3 or w_down.shape[1 + lay] != h.shape[1]:
         raise ValueError("expected h [T k, d_ff] and w_down [E, d_ff, d] or [E, d, d_ff]")
     d_ff = h.shape[1]
     E, d = w_down.shape[0], w_down.shape[2 - lay]
-    index = h.get_device()
-    _same_device(index, w_down=w_down, residual=residual)
-    T = routing.position.shape[0]
-    k = _check_routing(routing, T, E, index, True)
+    rdev, T, k, rE, po, _, pp, pt = routing._checked or _check_routing(torch, routing)
+    if rE != E or rdev != index:
+        raise ValueError("the routing is of %d experts on device %d, not %d, %d"
+                         % (rE, rdev, E, index))
+    if pt is None and T * k > 0:
+        raise ValueError("the routing needs weights")
     if h.shape[0] != T * k:
         raise ValueError("h has %d rows, the routing %d" % (h.shape[0], T * k))
-    if residual is not None and residual.shape != (T, d):
-        raise ValueError("residual must be [T, d] = [%d, %d]" % (T, d))
-    out = _out(out, (T, d), torch.bfloat16, h)
-    ws, nws = _workspace(workspace)
-    _call(index, _lib.load().swiglu_experts_down, h.data_ptr(), w_down.data_ptr(),
-          routing.offsets.data_ptr(), routing.position.data_ptr(), routing.weights.data_ptr(),
-          _ptr(residual), out.data_ptr(), T, k, E, d_ff, d, lay, ws, nws,
+    pr = None
+    if residual is not None:
+        pr = _check(residual, "residual", index, bf16)
+        if residual.shape != (T, d):
+            raise ValueError("residual must be [T, d] = [%d, %d]" % (T, d))
+    out = _out(torch, out, (T, d), bf16, index, h.device)
+    ws, nws = _workspace(workspace, index)
+    _call(index, _lib.load().swiglu_experts_down, h.data_ptr(), pw, po, pp, pt, pr, out.data_ptr(),
+          T, k, E, d_ff, d, lay, ws, nws,
           stream.cuda_stream if stream is not None else _raw_stream(index))
     return out
 
@@ -266,7 +284,7 @@ def swiglu_moe(x, w_router, w_gate, w_up, w_down, k, router_bias=None, residual=
     ("kn"; each with its last two dimensions exchanged for "nk"); router_bias
     [E] is added to the logits.  Returns (y [T, d], the Routing).
     """
-    import torch
+    torch = _torch()
     logits = linear(x, w_router, bias=router_bias, out_dtype=torch.float32, layout=layout,
                     stream=stream)
     r = route(logits, k, stream=stream, **routing)
