@@ -35,7 +35,7 @@ __device__ __forceinline__ bool cut_row(const Work& w, const Schedule& sch, cons
   const uint32_t u = (uint32_t)s_chunk[a] * (uint32_t)w.ncg + (uint32_t)((c >> 8) * nc + chunk);
   if (u < sch.whole || u >= sch.units || chunk >= nc) return false;
   float v[8];
-  add_row_shares(w, shares_of(w, sch, u - sch.whole), (uint32_t)((c >> 7) & 1),
+  add_row_shares<4>(w, shares_of(w, sch, u - sch.whole), (uint32_t)((c >> 7) & 1),
                  (p - s_row[a] - chunk * per) * 128 + (c & 127), v);
   *lo = make_float4(v[0], v[1], v[2], v[3]);
   *hi = make_float4(v[4], v[5], v[6], v[7]);
@@ -44,18 +44,21 @@ __device__ __forceinline__ bool cut_row(const Work& w, const Schedule& sch, cons
 
 template <bool CUT>
 __global__ void __launch_bounds__(kThreads)
-combine_kernel(const float* __restrict__ z, const __grid_constant__ Work w, uint32_t pairs,
-               const int* __restrict__ position, const float* __restrict__ weights,
+combine_kernel(const float* __restrict__ z, const __grid_constant__ Work w, const int* __restrict__ position, const float* __restrict__ weights,
                const uint16_t* resid, uint16_t* y, int64_t T, int k, int64_t rows, int64_t d) {
   extern __shared__ int s_row[];   // [E + 1] first rows, then [E + 1] first chunks
   tc::pdl_wait();
   tc::pdl_launch_dependents();
+  // (the plan is read only where the product says that it cut units)
   Schedule sch{0, 0, 0, 1};
   int* s_chunk = s_row + w.E + 1;
   if (CUT) {
-    plan_chunks(w, s_row, s_chunk);
-    __syncthreads();
-    sch = make_schedule(w, (uint32_t)s_chunk[w.E], pairs);
+    const uint4 q = __ldcg(w.sched);
+    sch = Schedule{q.x, q.y, q.z, q.w};
+    if (sch.cut_iters > 0) {
+      plan_chunks(w, s_row, s_chunk);
+      __syncthreads();
+    }
   }
   const int64_t per = d / kVec;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < T * per;
@@ -113,7 +116,7 @@ combine_kernel(const float* __restrict__ z, const __grid_constant__ Work w, uint
 
 }  // namespace
 
-cudaError_t launch_combine(const float* z, const Work* w, int pairs, const int* position,
+cudaError_t launch_combine(const float* z, const Work* w, const int* position,
                            const float* weights, const void* residual, void* y, int64_t T,
                            int64_t k, int64_t rows, int64_t d, int num_sms, cudaStream_t st) {
   if (T == 0 || d == 0) return cudaSuccess;
@@ -131,10 +134,10 @@ cudaError_t launch_combine(const float* z, const Work* w, int pairs, const int* 
   cfg.numAttrs = 1;
   if (z && w->cut) {
     cfg.dynamicSmemBytes = (size_t)(2 * (w->E + 1)) * sizeof(int);
-    return cudaLaunchKernelEx(&cfg, combine_kernel<true>, z, *w, (uint32_t)pairs, position, weights,
+    return cudaLaunchKernelEx(&cfg, combine_kernel<true>, z, *w, position, weights,
                               (const uint16_t*)residual, (uint16_t*)y, T, (int)k, rows, d);
   }
-  return cudaLaunchKernelEx(&cfg, combine_kernel<false>, z, *w, (uint32_t)pairs, position, weights,
+  return cudaLaunchKernelEx(&cfg, combine_kernel<false>, z, *w, position, weights,
                             (const uint16_t*)residual, (uint16_t*)y, T, (int)k, rows, d);
 }
 

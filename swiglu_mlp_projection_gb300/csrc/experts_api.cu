@@ -84,6 +84,9 @@ int wlayout_of(int layout) { return layout == SWIGLU_WEIGHTS_NK ? kWeightsNK : k
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
+// The shares of cut units, and 256 bytes for the schedule.
+size_t part_region(const GroupedPlan& p) { return round256(p.part_bytes) + 256; }
+
 struct Device {
   int dev = 0, num_sms = 0, pairs = 0;
 };
@@ -100,11 +103,11 @@ int get_device(Device* d) {
 // projection, or padded weights) follow the partial sums.  The caller frees ws.pooled.
 int run_grouped(int mode, GroupedCall c, const GroupedPlan& p, const Device& dv, void* workspace,
                 size_t ws_bytes, size_t extra, Workspace* ws, cudaStream_t st) {
-  const size_t body = round256(p.part_bytes) + extra;
+  const size_t body = part_region(p) + extra;
   int v = api_take_workspace(dv.dev, st, workspace, ws_bytes, p.counters_bytes, body, ws);
   if (v != SWIGLU_OK) return v;
-  if (extra && mode == kGroupedPlain) c.out = ws->body + round256(p.part_bytes);
-  else if (extra) c.padded = ws->body + round256(p.part_bytes);
+  if (extra && mode == kGroupedPlain) c.out = ws->body + part_region(p);
+  else if (extra) c.padded = ws->body + part_region(p);
   cudaError_t e = launch_grouped(mode, c, p, (float*)ws->body, ws->counters, ws->counters_clean,
                                  api_status_word(dv.dev), api_wait_timeout_ns(), st);
   if (e != cudaSuccess) {
@@ -149,7 +152,7 @@ size_t swiglu_linear_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (get_device(&dv) != SWIGLU_OK) return 0;
   const GroupedPlan p = plan_grouped(M, M, 1, K, N, false, dv.pairs, read_tuning());
   api_clear_error();
-  return p.counters_bytes + round256(p.part_bytes) + padded_bytes(K, N);
+  return p.counters_bytes + part_region(p) + padded_bytes(K, N);
 }
 
 int swiglu_linear(const void* x, const void* w, const void* bias, const void* residual, void* y,
@@ -298,7 +301,7 @@ static size_t experts_workspace(int64_t T, int64_t k, int64_t E, int64_t K, int6
   if (get_device(&dv) != SWIGLU_OK) return 0;
   const GroupedPlan p = up ? plan_up(T, k, E, K, N, dv.pairs) : plan_down(T, k, E, K, N, dv.pairs);
   api_clear_error();
-  return p.counters_bytes + round256(p.part_bytes) + (up ? 0 : z_bytes(T * k, N));
+  return p.counters_bytes + part_region(p) + (up ? 0 : z_bytes(T * k, N));
 }
 
 size_t swiglu_experts_up_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t d, int64_t d_ff) {
@@ -384,7 +387,6 @@ int swiglu_experts_down(const void* h, const void* w_down, const int32_t* offset
   Workspace ws;
   const float* z = nullptr;
   Work work{};
-  int pairs = 0;
   if (rows > 0 && d_ff > 0) {
     GroupedCall c{};
     c.x = h;
@@ -402,12 +404,11 @@ int swiglu_experts_down(const void* h, const void* w_down, const int32_t* offset
     if ((v = run_grouped(kGroupedPlain, c, p, dv, workspace, workspace_bytes, z_bytes(rows, d), &ws,
                          st)) != SWIGLU_OK)
       return v;
-    z = (const float*)(ws.body + round256(p.part_bytes));
+    z = (const float*)(ws.body + part_region(p));
     fill_work(&work, kGroupedPlain, c, p, (float*)ws.body);
-    pairs = p.pairs;
   }
   // (a product over nothing: y = residual, or 0)
-  const cudaError_t e = launch_combine(z, &work, pairs, position, weights, residual, y, T,
+  const cudaError_t e = launch_combine(z, &work, position, weights, residual, y, T,
                                        z ? k : 0, rows, d, dv.num_sms, st);
   v = free_workspace(ws, st);
   if (e != cudaSuccess) return api_cuda_fail(e, "kernel launch");

@@ -65,7 +65,7 @@ void fill_work(Work* w, int mode, const GroupedCall& c, const GroupedPlan& p, fl
 // f32, rounded once (bf16).  position -1: no term.  `w`: the grouped product
 // that wrote z (row r of a cut unit is in its shares instead); z null: no term
 // at all.
-cudaError_t launch_combine(const float* z, const Work* w, int pairs, const int* position,
+cudaError_t launch_combine(const float* z, const Work* w, const int* position,
                            const float* weights, const void* residual, void* y, int64_t T,
                            int64_t k, int64_t rows, int64_t d, int num_sms, cudaStream_t st);
 

@@ -19,6 +19,7 @@ struct Work {
   int cut;                 // whether units of a partial wave are cut along K
   int min_kb;              // fewest k blocks of a share of a cut unit
   float* part;             // shares of cut units
+  uint4* sched;            // the product's schedule (Schedule), for the kernel after it
 };
 
 // The work of a launch, from the offsets; the same in every thread.  (Units
@@ -77,7 +78,8 @@ __device__ __forceinline__ float* part_slot(const Work& w, uint32_t pair, uint32
 }
 
 // v[0 .. 8) = the sums of the shares at element `at` (row-major [row][128]),
-// in k order.  Four shares are loaded at a time: each is an L2 round trip.
+// in k order.  NS shares are loaded at a time: each is an L2 round trip.
+template <int NS>
 __device__ __forceinline__ void add_row_shares(const Work& w, const Shares& sh, uint32_t rank,
                                                int at, float* v) {
   const float* first = part_slot(w, sh.first, sh.slot, rank) + at;
@@ -85,10 +87,10 @@ __device__ __forceinline__ void add_row_shares(const Work& w, const Shares& sh, 
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = 0.f;
 #pragma unroll 1
-  for (uint32_t s0 = 0; s0 < sh.count; s0 += 4) {
-    float4 lo[4], hi[4];
+  for (uint32_t s0 = 0; s0 < sh.count; s0 += NS) {
+    float4 lo[NS], hi[NS];
 #pragma unroll
-    for (uint32_t s = 0; s < 4; ++s) {
+    for (uint32_t s = 0; s < NS; ++s) {
       lo[s] = hi[s] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (s0 + s < sh.count) {
         const float* src = s0 + s == 0 ? first : rest + (int64_t)(s0 + s - 1) * part_stride(w);
@@ -97,7 +99,7 @@ __device__ __forceinline__ void add_row_shares(const Work& w, const Shares& sh, 
       }
     }
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < NS; ++s) {
       v[0] += lo[s].x; v[1] += lo[s].y; v[2] += lo[s].z; v[3] += lo[s].w;
       v[4] += hi[s].x; v[5] += hi[s].y; v[6] += hi[s].z; v[7] += hi[s].w;
     }

@@ -82,6 +82,7 @@ struct Args : Work {
   int stages;
   uint32_t stage_bytes;
   int kmajor;              // weights stored [n_out, K]
+  int joined;              // linear: a kernel that adds up shares follows
   int prefetch_kb;         // linear: k blocks whose weights are asked into L2 early
   void* out;
   int out_f32;
@@ -368,7 +369,11 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
   // All of the above overlaps the previous kernel's tail; the routing, the
   // operands and the outputs are touched only after it has finished.
   pdl_wait();
-  pdl_launch_dependents();
+  // The next kernel may be placed at once, except where it adds up this one's
+  // results: its small blocks would all be placed on the few SMs that finish
+  // first (see the weights' thread).
+  const bool late = MODE == kGroupedPlain || (MODE == kGroupedLinear && a.joined);
+  if (!late) pdl_launch_dependents();
   if (a.offsets) {
     plan_chunks(a, s_row, s_chunk);
     __syncthreads();
@@ -379,6 +384,8 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
   const bool skip = ld_shared_cluster_u32(mapa_shared(smem_u32(tmem_slot), rank ^ 1u)) != tmem;
   if (skip && threadIdx.x == 0) atomicOr(a.status, kStatusPairTmem);
   const Schedule sch = make_schedule(a, (uint32_t)s_chunk[a.E], pairs);
+  if (MODE == kGroupedPlain && blockIdx.x == 0 && threadIdx.x == 32)
+    *a.sched = make_uint4(sch.units, sch.whole, sch.cut_iters, sch.q);
 
   if (warp == 0) {
     // ---------------- weights (TMA, one thread of each CTA) ----------------
@@ -418,6 +425,10 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
           }
         }
       }
+      // Every CTA is within a ring of its end by now, so the blocks of the
+      // kernel that adds up find most SMs free.  (Decode linear, K = 14336,
+      // N = 4096: JOINFIG.)
+      if (late) pdl_launch_dependents();
       if (issued > 0 && !ok) {
         // let the loads still in flight land before the CTA can exit
         const int64_t first = issued > a.stages ? issued - a.stages : 0;
@@ -643,6 +654,7 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
       const uint32_t t_acc = tmem + lane_off + (uint32_t)(acc * kAccCols);
       const bool whole = kb0 == 0 && kb1 == a.n_kb;
       const int nchunk = (un.nrows + 31) >> 5;
+      const int cbase = un.col0 + (MODE == kGroupedSwiGLU ? 64 : 128) * (int)rank;   // output columns
       Shares sh{0, 0, 0};
       if (!whole) {
         // A share of a cut unit: store the sums so far.  A second kernel adds
@@ -668,7 +680,7 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
             // [row][column]
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (c * 32 + i < un.nrows) __stcg(mine + (c * 32 + i) * 128 + col, __uint_as_float(v[i]));
+              if (c * 32 + i < un.nrows && cbase + col < a.n_out) __stcg(mine + (c * 32 + i) * 128 + col, __uint_as_float(v[i]));
           }
         }
         tc_fence_before();
@@ -699,8 +711,7 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
           continue;
         }
       }
-      // this CTA's output columns, and the bias of this thread's column
-      const int cbase = un.col0 + (MODE == kGroupedSwiGLU ? 64 : 128) * (int)rank;
+      // the bias of this thread's column
       float bias = 0.f;
       if constexpr (MODE == kGroupedLinear) {
         if (a.bias && cbase + col < a.n_out)
@@ -816,7 +827,7 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
 
 // The cut units of a linear product: y = act(sum of the shares + bias) +
 // residual, eight columns of one row per thread, the shares in k order.
-// Bound by L2 latency: a share is one round trip, so four are loaded at a time.
+// Bound by L2 latency: a share is one round trip, so eight are loaded at a time.
 constexpr int kJoinThreads = 128;
 
 __global__ void __launch_bounds__(kJoinThreads)
@@ -824,26 +835,30 @@ linear_join_kernel(const __grid_constant__ Args a, int chunks, const Schedule sc
   pdl_wait();
   pdl_launch_dependents();
   const uint32_t i = blockIdx.x * kJoinThreads + threadIdx.x;
-  const uint32_t per = (uint32_t)a.n_max * 32u;
+  int row0, nrows;
+  chunk_rows(a.rows, chunks, 0, &row0, &nrows);   // the first chunk has the most rows
+  const uint32_t per = (uint32_t)nrows * 32u;
   const uint32_t rel = i / per;
   if (rel >= sch.units - sch.whole) return;
   const uint32_t rem = i - rel * per;
   const int r = (int)(rem >> 5), o = (int)(rem & 31);
   const uint32_t u = sch.whole + rel;
   const int cg = (int)(u / (uint32_t)chunks), chunk = (int)(u - (uint32_t)cg * (uint32_t)chunks);
-  int row0, nrows;
   chunk_rows(a.rows, chunks, chunk, &row0, &nrows);
   const int c = cg * 256 + o * 8;
   if (r >= nrows || c >= a.n_out) return;
+  float bias[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    bias[j] = 0.f;
+    if (a.bias && c + j < a.n_out)
+      bias[j] = a.bias_f32 ? ((const float*)a.bias)[c + j] : bf16_lo(((const uint16_t*)a.bias)[c + j]);
+  }
   const Shares sh = shares_of(a, sch, rel);
   float v[8];
-  add_row_shares(a, sh, (uint32_t)(o >> 4), r * 128 + (o & 15) * 8, v);
-  if (a.bias) {
+  add_row_shares<8>(a, sh, (uint32_t)(o >> 4), r * 128 + (o & 15) * 8, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c + j < a.n_out)
-        v[j] += a.bias_f32 ? ((const float*)a.bias)[c + j] : bf16_lo(((const uint16_t*)a.bias)[c + j]);
-  }
+  for (int j = 0; j < 8; ++j) v[j] += bias[j];
   activate_n<8>(v, a.act, a.out_f32 != 0);
   store_row8<kGroupedLinear>(a, (int64_t)(row0 + r) * a.n_out + c, a.n_out - c, v);
 }
@@ -935,6 +950,7 @@ GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, int64_t K, int
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.pairs = pairs < 1 ? 1 : pairs;
   p.counters_bytes = ((size_t)p.pairs * 2 * sizeof(unsigned) + 255) / 256 * 256;
+  // (256 bytes behind the shares: the schedule)
   p.part_bytes = (size_t)p.pairs * 4 * (size_t)p.n_max * 128 * sizeof(float);
   p.min_kb = tn.gr_min_kb > 0 ? tn.gr_min_kb : 16;
   p.cut = tn.gr_cut >= 0 ? tn.gr_cut : (!swiglu || p.n_max <= 64);
@@ -956,6 +972,7 @@ void fill_work(Work* w, int mode, const GroupedCall& c, const GroupedPlan& p, fl
   w->cut = p.cut;
   w->min_kb = p.min_kb;
   w->part = part;
+  w->sched = (uint4*)((char*)part + p.part_bytes);
 }
 
 cudaError_t launch_grouped(int mode, const GroupedCall& c, const GroupedPlan& p, float* part,
@@ -1028,18 +1045,20 @@ cudaError_t launch_grouped(int mode, const GroupedCall& c, const GroupedPlan& p,
     case kGroupedPlain: return launch_mode<kGroupedPlain, false>(mx, ma, mb, a, p.pairs, smem, st);
     default: break;
   }
-  if ((e = launch_mode<kGroupedLinear, false>(mx, ma, mb, a, p.pairs, smem, st)) != cudaSuccess)
-    return e;
   // cut units: a second kernel adds their shares
   const uint32_t chunks = (uint32_t)((c.rows + p.n_max - 1) / p.n_max);
   const Schedule sch = make_schedule(a, chunks, (uint32_t)p.pairs);
   const uint32_t cut = sch.units - sch.whole;
+  a.joined = cut > 0;
+  if ((e = launch_mode<kGroupedLinear, false>(mx, ma, mb, a, p.pairs, smem, st)) != cudaSuccess)
+    return e;
   if (cut == 0) return cudaSuccess;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(((int64_t)cut * p.n_max * 32 + kJoinThreads - 1) / kJoinThreads));
+  const int64_t most = (c.rows + chunks - 1) / chunks;   // rows of a chunk
+  cfg.gridDim = dim3((unsigned)((cut * most * 32 + kJoinThreads - 1) / kJoinThreads));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cfg.attrs = attr;
