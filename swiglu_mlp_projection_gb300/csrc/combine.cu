@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kVec = 8;   // columns per thread
-constexpr int kBatch = 4; // choices whose loads are in flight together
+constexpr int kBatch = 8; // choices whose loads are in flight together
 
 // Columns c .. c + 7 of sorted row p, if its unit was cut.
 __device__ __forceinline__ bool cut_row(const Work& w, const Schedule& sch, const int* s_row,
@@ -44,7 +44,8 @@ __device__ __forceinline__ bool cut_row(const Work& w, const Schedule& sch, cons
 
 template <bool CUT>
 __global__ void __launch_bounds__(kThreads)
-combine_kernel(const float* __restrict__ z, const __grid_constant__ Work w, const int* __restrict__ position, const float* __restrict__ weights,
+combine_kernel(const float* __restrict__ z, const __grid_constant__ Work w,
+               const int* __restrict__ position, const float* __restrict__ weights,
                const uint16_t* resid, uint16_t* y, int64_t T, int k, int64_t rows, int64_t d) {
   extern __shared__ int s_row[];   // [E + 1] first rows, then [E + 1] first chunks
   tc::pdl_wait();
@@ -64,38 +65,47 @@ combine_kernel(const float* __restrict__ z, const __grid_constant__ Work w, cons
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < T * per;
        i += (int64_t)gridDim.x * kThreads) {
     const int64_t t = i / per, c = (i - t * per) * kVec;
+    // (the residual is used only after the first rows' loads are under way)
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
+    if (resid) r = *reinterpret_cast<const uint4*>(resid + t * d + c);
     float acc[kVec];
-    if (resid) {
-      const uint4 r = *reinterpret_cast<const uint4*>(resid + t * d + c);
-      acc[0] = bf16_lo(r.x); acc[1] = bf16_hi(r.x);
-      acc[2] = bf16_lo(r.y); acc[3] = bf16_hi(r.y);
-      acc[4] = bf16_lo(r.z); acc[5] = bf16_hi(r.z);
-      acc[6] = bf16_lo(r.w); acc[7] = bf16_hi(r.w);
-    } else {
+    int p[kBatch];
+    float wt[kBatch];
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
+    for (int i = 0; i < kBatch; ++i) {
+      p[i] = i < k ? position[t * k + i] : -1;
+      wt[i] = i < k ? weights[t * k + i] : 0.f;
     }
-    // four choices at a time: their rows' loads are in flight together
-    for (int j0 = 0; j0 < k; j0 += kBatch) {
-      float wt[kBatch];
+    // several choices at a time: their rows' loads are in flight together
+    for (int j0 = 0; j0 == 0 || j0 < k; j0 += kBatch) {
       float4 a[kBatch], b[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        int p = -1;
-        if (j0 + i < k) {
-          p = position[t * k + j0 + i];
-          wt[i] = weights[t * k + j0 + i];
-        }
         a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p < 0 || p >= rows) {
+        if (p[i] < 0 || p[i] >= rows) {
           wt[i] = 0.f;   // no term (whatever its weight)
-        } else if (CUT && sch.cut_iters > 0 && cut_row(w, sch, s_row, s_chunk, p, (int)c, &a[i], &b[i])) {
+        } else if (CUT && sch.cut_iters > 0 &&
+                   cut_row(w, sch, s_row, s_chunk, p[i], (int)c, &a[i], &b[i])) {
           // (the sums of the shares)
         } else {
-          const float4* src = reinterpret_cast<const float4*>(z + (int64_t)p * d + c);
+          const float4* src = reinterpret_cast<const float4*>(z + (int64_t)p[i] * d + c);
           a[i] = __ldcs(src);
           b[i] = __ldcs(src + 1);
         }
+      }
+      int pn[kBatch];
+      float wn[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {   // the next choices
+        const int j = j0 + kBatch + i;
+        pn[i] = j < k ? position[t * k + j] : -1;
+        wn[i] = j < k ? weights[t * k + j] : 0.f;
+      }
+      if (j0 == 0) {
+        acc[0] = bf16_lo(r.x); acc[1] = bf16_hi(r.x);
+        acc[2] = bf16_lo(r.y); acc[3] = bf16_hi(r.y);
+        acc[4] = bf16_lo(r.z); acc[5] = bf16_hi(r.z);
+        acc[6] = bf16_lo(r.w); acc[7] = bf16_hi(r.w);
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
@@ -103,6 +113,8 @@ combine_kernel(const float* __restrict__ z, const __grid_constant__ Work w, cons
         acc[2] = fmaf(wt[i], a[i].z, acc[2]); acc[3] = fmaf(wt[i], a[i].w, acc[3]);
         acc[4] = fmaf(wt[i], b[i].x, acc[4]); acc[5] = fmaf(wt[i], b[i].y, acc[5]);
         acc[6] = fmaf(wt[i], b[i].z, acc[6]); acc[7] = fmaf(wt[i], b[i].w, acc[7]);
+        p[i] = pn[i];
+        wt[i] = wn[i];
       }
     }
     uint4 o;

@@ -260,50 +260,72 @@ __device__ __forceinline__ void add_shares(float* v, const float* first, const f
   }
 }
 
-// Up to 8 neighbouring outputs of one row, at element `o`; `left` columns of
-// the row remain from there.
+// The residual at eight neighbouring outputs (element `o`, `left` columns of the
+// row remain from there), as it lies in memory.
+struct Residual8 {
+  uint4 lo, hi;
+};
+
+__device__ __forceinline__ Residual8 load_residual8(const Args& a, int64_t o, int left) {
+  Residual8 r;
+  r.lo = r.hi = make_uint4(0u, 0u, 0u, 0u);
+  if (!a.resid) return r;
+  if (a.n_out & 7) {   // rows off 16-byte boundaries: element by element
+    uint32_t q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      q[i] = 0u;
+      if (i < left)
+        q[i] = a.out_f32 ? ((const uint32_t*)a.resid)[o + i] : (uint32_t)((const uint16_t*)a.resid)[o + i];
+    }
+    if (a.out_f32) {
+      r.lo = make_uint4(q[0], q[1], q[2], q[3]);
+      r.hi = make_uint4(q[4], q[5], q[6], q[7]);
+    } else {
+      r.lo = make_uint4(q[0] | q[1] << 16, q[2] | q[3] << 16, q[4] | q[5] << 16, q[6] | q[7] << 16);
+    }
+  } else if (a.out_f32) {
+    const uint4* p = reinterpret_cast<const uint4*>((const float*)a.resid + o);
+    r.lo = p[0];
+    r.hi = p[1];
+  } else {
+    r.lo = *reinterpret_cast<const uint4*>((const uint16_t*)a.resid + o);
+  }
+  return r;
+}
+
+// v + residual, rounded to the output type, to eight neighbouring outputs.
 template <int MODE>
-__device__ __forceinline__ void store_row8(const Args& a, int64_t o, int left, const float* src) {
-  if (MODE == kGroupedLinear && (a.n_out & 7)) {
-    // rows off 16-byte boundaries: element by element
-    for (int i = 0; i < 8 && i < left; ++i) {
-      float f = src[i];
-      if (a.out_f32) {
-        if (a.resid) f += ((const float*)a.resid)[o + i];
-        ((float*)a.out)[o + i] = f;
-      } else {
-        if (a.resid) f += bf16_lo(((const uint16_t*)a.resid)[o + i]);
-        ((uint16_t*)a.out)[o + i] = cvt_bf16(f);
+__device__ __forceinline__ void store_row8(const Args& a, int64_t o, int left, float* v,
+                                           const Residual8& r) {
+  if constexpr (MODE == kGroupedLinear) {
+    if (a.resid) {
+      const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] += a.out_f32 ? __uint_as_float(w[i]) : (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+    }
+    if (a.n_out & 7) {   // rows off 16-byte boundaries: element by element
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i >= left) break;
+        if (a.out_f32) ((float*)a.out)[o + i] = v[i];
+        else ((uint16_t*)a.out)[o + i] = cvt_bf16(v[i]);
       }
+      return;
     }
-    return;
   }
-  const float4* sp = reinterpret_cast<const float4*>(src);
-  float4 lo = sp[0], hi = sp[1];
   if (a.out_f32) {
-    if (MODE == kGroupedLinear && a.resid) {
-      const float4 rl = *reinterpret_cast<const float4*>((const float*)a.resid + o);
-      const float4 rh = *reinterpret_cast<const float4*>((const float*)a.resid + o + 4);
-      lo.x += rl.x; lo.y += rl.y; lo.z += rl.z; lo.w += rl.w;
-      hi.x += rh.x; hi.y += rh.y; hi.z += rh.z; hi.w += rh.w;
-    }
     float4* dst = reinterpret_cast<float4*>((float*)a.out + o);
-    dst[0] = lo;
-    dst[1] = hi;
+    dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+    dst[1] = make_float4(v[4], v[5], v[6], v[7]);
     return;
-  }
-  if (MODE == kGroupedLinear && a.resid) {
-    const uint4 rr = *reinterpret_cast<const uint4*>((const uint16_t*)a.resid + o);
-    lo.x += bf16_lo(rr.x); lo.y += bf16_hi(rr.x);
-    lo.z += bf16_lo(rr.y); lo.w += bf16_hi(rr.y);
-    hi.x += bf16_lo(rr.z); hi.y += bf16_hi(rr.z);
-    hi.z += bf16_lo(rr.w); hi.w += bf16_hi(rr.w);
   }
   uint4 q;
-  q.x = cvt_bf16x2(lo.x, lo.y);
-  q.y = cvt_bf16x2(lo.z, lo.w);
-  q.z = cvt_bf16x2(hi.x, hi.y);
-  q.w = cvt_bf16x2(hi.z, hi.w);
+  q.x = cvt_bf16x2(v[0], v[1]);
+  q.y = cvt_bf16x2(v[2], v[3]);
+  q.z = cvt_bf16x2(v[4], v[5]);
+  q.w = cvt_bf16x2(v[6], v[7]);
   *reinterpret_cast<uint4*>((uint16_t*)a.out + o) = q;
 }
 
@@ -784,8 +806,14 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
               const int r = g >> 4, c8 = (g & 15) * 8;
               const int row = c * 32 + hp * 16 + r;
               if (row >= un.nrows || cbase + c8 >= a.n_out) continue;
-              store_row8<MODE>(a, (int64_t)(un.row0 + row) * a.n_out + cbase + c8,
-                               a.n_out - cbase - c8, staging + r * kStageCols + c8);
+              const int64_t o = (int64_t)(un.row0 + row) * a.n_out + cbase + c8;
+              const int left = a.n_out - cbase - c8;
+              Residual8 rs{};
+              if constexpr (MODE == kGroupedLinear) rs = load_residual8(a, o, left);
+              const float4* sp = reinterpret_cast<const float4*>(staging + r * kStageCols + c8);
+              const float4 lo = sp[0], hi = sp[1];
+              float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+              store_row8<MODE>(a, o, left, f, rs);
             }
           }
           named_bar_sync(gbar, kEpiThreads);   // staging is free
@@ -847,20 +875,24 @@ linear_join_kernel(const __grid_constant__ Args a, int chunks, const Schedule sc
   chunk_rows(a.rows, chunks, chunk, &row0, &nrows);
   const int c = cg * 256 + o * 8;
   if (r >= nrows || c >= a.n_out) return;
-  float bias[8];
+  // (bias and residual are used only after the shares' loads are under way)
+  const int64_t out = (int64_t)(row0 + r) * a.n_out + c;
+  const int left = a.n_out - c;
+  const Residual8 rs = load_residual8(a, out, left);
+  uint32_t bias[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    bias[j] = 0.f;
-    if (a.bias && c + j < a.n_out)
-      bias[j] = a.bias_f32 ? ((const float*)a.bias)[c + j] : bf16_lo(((const uint16_t*)a.bias)[c + j]);
+    bias[j] = 0u;
+    if (a.bias && j < left)
+      bias[j] = a.bias_f32 ? ((const uint32_t*)a.bias)[c + j] : (uint32_t)((const uint16_t*)a.bias)[c + j] << 16;
   }
   const Shares sh = shares_of(a, sch, rel);
   float v[8];
   add_row_shares<8>(a, sh, (uint32_t)(o >> 4), r * 128 + (o & 15) * 8, v);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] += bias[j];
+  for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(bias[j]);
   activate_n<8>(v, a.act, a.out_f32 != 0);
-  store_row8<kGroupedLinear>(a, (int64_t)(row0 + r) * a.n_out + c, a.n_out - c, v);
+  store_row8<kGroupedLinear>(a, out, left, v, rs);
 }
 
 // y = act(bias) + residual, for products over nothing (K = 0).
