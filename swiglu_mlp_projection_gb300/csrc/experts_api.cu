@@ -124,12 +124,8 @@ int free_workspace(const Workspace& ws, cudaStream_t st) {
   return e == cudaSuccess ? SWIGLU_OK : api_cuda_fail(e, "cudaFreeAsync(workspace)");
 }
 
-GroupedPlan plan_up(int64_t T, int64_t k, int64_t E, int64_t d, int64_t d_ff, int pairs) {
-  return plan_grouped(T * k, T, E, d, d_ff, true, pairs, read_tuning());
-}
-
-GroupedPlan plan_down(int64_t T, int64_t k, int64_t E, int64_t d_ff, int64_t d, int pairs) {
-  return plan_grouped(T * k, T, E, d_ff, d, false, pairs, read_tuning());
+GroupedPlan plan_experts(int64_t T, int64_t k, int64_t E, bool up, int pairs) {
+  return plan_grouped(T * k, T, E, up, pairs, read_tuning());
 }
 
 // Room for [K, N] weights with padded rows (launch_grouped), where N asks for it.
@@ -150,7 +146,7 @@ size_t swiglu_linear_workspace_bytes(int64_t M, int64_t K, int64_t N) {
   if (check_product(M, K, N, "K", "N", true) != SWIGLU_OK) return 0;
   Device dv;
   if (get_device(&dv) != SWIGLU_OK) return 0;
-  const GroupedPlan p = plan_grouped(M, M, 1, K, N, false, dv.pairs, read_tuning());
+  const GroupedPlan p = plan_grouped(M, M, 1, false, dv.pairs, read_tuning());
   api_clear_error();
   return p.counters_bytes + part_region(p) + padded_bytes(K, N);
 }
@@ -182,7 +178,7 @@ int swiglu_linear(const void* x, const void* w, const void* bias, const void* re
     api_clear_error();
     return SWIGLU_OK;
   }
-  const GroupedPlan p = plan_grouped(M, M, 1, K, N, false, dv.pairs, read_tuning());
+  const GroupedPlan p = plan_grouped(M, M, 1, false, dv.pairs, read_tuning());
   GroupedCall c{};
   c.x = x;
   c.wa = w;
@@ -299,7 +295,7 @@ static size_t experts_workspace(int64_t T, int64_t k, int64_t E, int64_t K, int6
   if (check_product(0, K, N, "d", "d_ff") != SWIGLU_OK || check_routing(T, k, E) != SWIGLU_OK) return 0;
   Device dv;
   if (get_device(&dv) != SWIGLU_OK) return 0;
-  const GroupedPlan p = up ? plan_up(T, k, E, K, N, dv.pairs) : plan_down(T, k, E, K, N, dv.pairs);
+  const GroupedPlan p = plan_experts(T, k, E, up, dv.pairs);
   api_clear_error();
   return p.counters_bytes + part_region(p) + (up ? 0 : z_bytes(T * k, N));
 }
@@ -350,7 +346,7 @@ int swiglu_experts_up(const void* x, const void* w_gate, const void* w_up, const
   c.wlayout = wlayout_of(layout);
   const cudaStream_t st = (cudaStream_t)stream;
   Workspace ws;
-  if ((v = run_grouped(kGroupedSwiGLU, c, plan_up(T, k, E, d, d_ff, dv.pairs), dv, workspace,
+  if ((v = run_grouped(kGroupedSwiGLU, c, plan_experts(T, k, E, true, dv.pairs), dv, workspace,
                        workspace_bytes, 0, &ws, st)) != SWIGLU_OK)
     return v;
   if ((v = free_workspace(ws, st)) != SWIGLU_OK) return v;
@@ -400,7 +396,7 @@ int swiglu_experts_down(const void* h, const void* w_down, const int32_t* offset
     c.K = d_ff;
     c.n_out = d;
     c.wlayout = wlayout_of(layout);
-    const GroupedPlan p = plan_down(T, k, E, d_ff, d, dv.pairs);
+    const GroupedPlan p = plan_experts(T, k, E, false, dv.pairs);
     if ((v = run_grouped(kGroupedPlain, c, p, dv, workspace, workspace_bytes, z_bytes(rows, d), &ws,
                          st)) != SWIGLU_OK)
       return v;

@@ -34,8 +34,8 @@ struct GroupedPlan {
 };
 
 // rows: rows of the sorted operand; tokens: most rows that one expert can have.
-GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, int64_t K, int64_t n_out,
-                         bool swiglu, int pairs, const Tuning& tn);
+GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, bool swiglu, int pairs,
+                         const Tuning& tn);
 
 struct GroupedCall {
   const void* x;           // [tokens, K] (SwiGLU) or [rows, K]

@@ -55,6 +55,36 @@ __host__ __device__ inline Schedule make_schedule(const Work& w, uint32_t chunks
   return s;
 }
 
+// The work items of one pair: whole units, then its share of the cut units.
+struct WorkIter {
+  uint32_t u_next, it, it_end;
+  __host__ __device__ WorkIter(const Schedule& s, uint32_t pair) : u_next(pair) {
+    it = pair * s.q < s.cut_iters ? pair * s.q : s.cut_iters;
+    it_end = (pair + 1) * s.q < s.cut_iters ? (pair + 1) * s.q : s.cut_iters;
+  }
+  __host__ __device__ bool next(const Work& a, const Schedule& s, uint32_t pairs, uint32_t& u, int& kb0,
+                       int& kb1) {
+    if (u_next < s.whole) {
+      u = u_next;
+      u_next += pairs;
+      kb0 = 0;
+      kb1 = a.n_kb;
+      return true;
+    }
+    if (it < it_end) {
+      const uint32_t n_kb = (uint32_t)a.n_kb;
+      const uint32_t rel = it / n_kb;
+      const uint32_t stop = (rel + 1) * n_kb < it_end ? (rel + 1) * n_kb : it_end;
+      u = s.whole + rel;
+      kb0 = (int)(it - rel * n_kb);
+      kb1 = (int)(stop - rel * n_kb);
+      it = stop;
+      return true;
+    }
+    return false;
+  }
+};
+
 // A cut unit's shares: those of pairs first .. first + count - 1, in k order.
 // A pair has two slots: slot 0 for the unit its range begins in, slot 1 for
 // the unit its range ends in (only the first pair's share can be in slot 1).

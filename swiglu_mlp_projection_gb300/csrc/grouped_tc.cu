@@ -15,9 +15,9 @@
 //
 // Orientation: the weights are the MMA's A operand and the rows its B operand
 // (D^T = W^T x^T), because the count of rows varies from one to thousands and
-// N takes any multiple of 32, where M is 256.  A row too many costs 1/32 of a
-// step instead of a 256-row tile: 64 experts of 512 +- 150 rows would
-// waste about a quarter of 256-row tiles.
+// N takes any multiple of 32, where M is 256.  64 experts of 512 +- 150 rows
+// would leave about a quarter of 256-row tiles empty; chunks of up to 256 rows,
+// rounded to 32, leave 6 %.
 //
 // A pair (cta_group::2) computes 256 rows of W^T times N <= 256 rows of x;
 // each CTA stages 128 weight columns and half of the x rows per 64-deep k
@@ -27,10 +27,27 @@
 // unit is 256 adjacent output columns.
 //
 // Units run whole, round robin, as long as they fill the pairs; the units of
-// a last, partial wave are cut along K in equal shares (a share ends inside a
-// unit: its pair writes the f32 sums so far to the workspace, and the pair
-// that arrives last adds them in k order and runs the epilogue).  No output
-// depends on the order of arrival.
+// a last, partial wave are cut along K in equal shares (grouped_plan.cuh).  A
+// pair whose share ends inside a unit writes the f32 sums so far to the
+// workspace.  A second kernel adds the shares in k order: linear_join_kernel,
+// or the weighted sum that follows the down projection anyway.  (In the kernel
+// itself, the last pair to arrive would read all of them alone: 13 us of the
+// router logits' 31 at M = 4096, K = 4096, N = 64, where the join takes 4.)
+// Only the up projection's short units (at most 64 rows) are joined by the last
+// pair, where the shares are small and a second kernel would cost as much; its
+// longer ones are not cut.  No output depends on an order of arrival.
+//
+// What bounds it, on a GB300 (6785 GB/s copy, 1878 TFLOP/s bf16):
+//   few rows: HBM.  8 experts of d = 4096, d_ff = 14336, 32 tokens: 264 us for
+//   1.88 GB (7.1 TB/s).  8 of 64 experts of d = 2048, d_ff = 1024 (67 MB, one
+//   token): 16.3 us, 10 of them streaming, the rest the chain from the previous
+//   kernel's end through offsets, order, rows and the first stages;
+//   many rows: the MMAs, once operands arrive at 32 KB per CTA and k block:
+//   one group, 4096 rows, d = 4096, d_ff = 14336 476 us (2020 TFLOP/s); 64
+//   experts of 512 rows on average 190 us (1450 TFLOP/s: 11 % of the MMA
+//   columns are chunks short of 256 rows, the last wave is half empty); 8
+//   experts, K = 14336: 640 us (1500 TFLOP/s), bound by operand delivery (the
+//   loads alone take 0.36 us per k block there, 0.24 at K = 4096).
 #include <atomic>
 
 #include "common.cuh"
@@ -48,7 +65,10 @@ using namespace tc;
 constexpr int kBK = 64;
 // Warps: 0 loads weights (TMA), 1 issues MMAs (rank 0) or relays (rank 1),
 // 2-9 are the epilogue (two groups of four, each covering the 128 accumulator
-// lanes), 10 and up load rows (one warp of TMA, or four of cp.async).
+// lanes), 10 and up load rows (one warp of TMA, or four of cp.async).  One warp
+// issuing both operands in 16-row boxes took 419 us where this takes 250
+// (M = 4096, K = 4096, N = 14336), and four-row TMA gathers 741 us where
+// cp.async takes 190 (64 experts' up projection of 4096 tokens).
 constexpr int kEpiThreads = 128;                  // one epilogue group
 constexpr int kRowWarp = 10;
 constexpr int kGatherThreads = 128;
@@ -92,36 +112,6 @@ struct Args : Work {
   unsigned* counters;      // up: two per pair, zero on entry, left at zero
   unsigned* status;
   uint64_t timeout_ns;
-};
-
-// The work items of one pair: whole units, then its share of the cut units.
-struct WorkIter {
-  uint32_t u_next, it, it_end;
-  __device__ WorkIter(const Schedule& s, uint32_t pair) : u_next(pair) {
-    it = pair * s.q < s.cut_iters ? pair * s.q : s.cut_iters;
-    it_end = (pair + 1) * s.q < s.cut_iters ? (pair + 1) * s.q : s.cut_iters;
-  }
-  __device__ bool next(const Args& a, const Schedule& s, uint32_t pairs, uint32_t& u, int& kb0,
-                       int& kb1) {
-    if (u_next < s.whole) {
-      u = u_next;
-      u_next += pairs;
-      kb0 = 0;
-      kb1 = a.n_kb;
-      return true;
-    }
-    if (it < it_end) {
-      const uint32_t n_kb = (uint32_t)a.n_kb;
-      const uint32_t rel = it / n_kb;
-      const uint32_t stop = (rel + 1) * n_kb < it_end ? (rel + 1) * n_kb : it_end;
-      u = s.whole + rel;
-      kb0 = (int)(it - rel * n_kb);
-      kb1 = (int)(stop - rel * n_kb);
-      it = stop;
-      return true;
-    }
-    return false;
-  }
 };
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
@@ -517,8 +507,9 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
         }
       }
       // Every CTA is within a ring of its end by now, so the blocks of the
-      // kernel that adds up find most SMs free.  (Decode linear, K = 14336,
-      // N = 4096: JOINFIG.)
+      // kernel that adds up find most SMs free.  (Decode linear, M = 8,
+      // K = 14336, N = 4096: 26.6 us per call, 28.7 with its 32 joining blocks
+      // placed at once, on the two SMs that have no work.)
       if (late) pdl_launch_dependents();
       if (issued > 0 && !ok) {
         // let the loads still in flight land before the CTA can exit
@@ -1041,12 +1032,16 @@ cudaError_t launch_mode(const RowMaps& mx, const CUtensorMap& ma, const CUtensor
 
 }  // namespace
 
-GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, int64_t K, int64_t n_out,
-                         bool swiglu, int pairs, const Tuning& tn) {
+GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, bool swiglu, int pairs,
+                         const Tuning& tn) {
   GroupedPlan p{};
-  // Rows per chunk.  An expert has at most `tokens` rows (a token chooses it
-  // once) and rows / E on average; chunks for twice the average keep most
-  // experts in one chunk, so that their weights are read once.
+  // Rows per chunk.  An expert has rows / E rows on average, and no more than
+  // `tokens` where a token chooses it once; chunks for twice the average keep
+  // most experts in one chunk, so that their weights are read once.  Longer
+  // chunks cost ring stages (10 at 32 rows, 6 at 192 and above), shorter ones
+  // repeat the weights: 333 tokens over 8 experts (d_ff = 4864, d = 896) take
+  // 24.3 us in chunks of up to 192 rows, 24.7 of 128, 30.0 of 64; the router
+  // logits of 4096 rows 15.0 us in chunks of 256, 18.5 of 128, 24.6 of 64.
   int64_t want = E == 1 ? rows : 2 * ((rows + E - 1) / E) + 16;
   if (want > tokens) want = tokens;
   if (E == 1 && want > 256) {
@@ -1064,11 +1059,17 @@ GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, int64_t K, int
   p.counters_bytes = ((size_t)p.pairs * 2 * sizeof(unsigned) + 255) / 256 * 256;
   // (256 bytes behind the shares: the schedule)
   p.part_bytes = (size_t)p.pairs * 4 * (size_t)p.n_max * 128 * sizeof(float);
+  // Shares of 16 k blocks or more: shorter ones only add shares to read (router
+  // logits: 15.0 us at 16, 15.8 at 4 and 8, 18.4 at 32).
   p.min_kb = tn.gr_min_kb > 0 ? tn.gr_min_kb : 16;
+  // Cutting: 24.3 against 34.9 us for the 333 tokens above, 24 against 73 us for
+  // the decode linear below; the up projection of 4096 tokens over 64 experts
+  // 233 us uncut, 238 cut (joined by the last pair).
   p.cut = tn.gr_cut >= 0 ? tn.gr_cut : (!swiglu || p.n_max <= 64);
+  // L2 prefetch before the dependency wait: 512 KB of weights per CTA (decode
+  // linear, M = 8, K = 14336, N = 4096: 24.2 us with 32 k blocks, 25.8 with 16,
+  // 26.3 with none, 27.3 with 64).  Many rows hide it.
   p.prefetch_kb = tn.gr_prefetch >= 0 ? tn.gr_prefetch : (E == 1 && p.n_max <= 64 ? 32 : 0);
-  (void)K;
-  (void)n_out;
   return p;
 }
 

@@ -1347,6 +1347,6 @@ const char* swiglu_status_string(int status) {
 
 const char* swiglu_last_error_string(void) { return t_err; }
 
-int swiglu_version(void) { return 200; }
+int swiglu_version(void) { return 300; }
 
 }  // extern "C"
