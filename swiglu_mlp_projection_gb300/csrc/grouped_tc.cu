@@ -75,12 +75,14 @@ constexpr int kGatherThreads = 128;
 constexpr int threads_of(bool gather) { return kRowWarp * 32 + (gather ? kGatherThreads : 32); }
 constexpr uint32_t kChunkBytes = 64 * kBK * 2;    // one 64-column weight box
 constexpr uint32_t kABytes = 2 * kChunkBytes;     // a CTA's 128 weight columns
+// 10 stages at 32 rows per chunk, 6 at 192 and above.  (8 experts' decode up
+// projection, 32 tokens: 269 us with 10 or 9 stages, 276 with 7, 287 with 5.)
 constexpr uint32_t kRingBytes = 192u * 1024u;
 constexpr int kMaxStages = 12;
 constexpr uint32_t kTmemCols = 512;               // two accumulators of up to 256 columns
 constexpr int kAccCols = 256;
 // An epilogue group's staging.  SwiGLU: halves of 32 rows of gate and up,
-// [16][64] f32 each, and 32 rows of h, [32][72] bf16; otherwise 16 rows of
+// [16][64] f32 each, and 32 rows of h, [32][72] bf16; linear: 16 rows of
 // f32, [16][132] (128 columns and 16 bytes, against bank conflicts).
 constexpr int kStageCols = 132, kHCols = 72;
 constexpr uint32_t kStagingBytes = 2 * 16 * 64 * 4 + 32 * kHCols * 2;
@@ -354,25 +356,22 @@ __device__ __forceinline__ Residual8 load_residual8(const Args& a, int64_t o, in
 }
 
 // v + residual, rounded to the output type, to eight neighbouring outputs.
-template <int MODE>
 __device__ __forceinline__ void store_row8(const Args& a, int64_t o, int left, float* v,
                                            const Residual8& r) {
-  if constexpr (MODE == kGroupedLinear) {
-    if (a.resid) {
-      const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+  if (a.resid) {
+    const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] += a.out_f32 ? __uint_as_float(w[i]) : (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-    }
-    if (a.n_out & 7) {   // rows off 16-byte boundaries: element by element
+    for (int i = 0; i < 8; ++i)
+      v[i] += a.out_f32 ? __uint_as_float(w[i]) : (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+  }
+  if (a.n_out & 7) {   // rows off 16-byte boundaries: element by element
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i >= left) break;
-        if (a.out_f32) ((float*)a.out)[o + i] = v[i];
-        else ((uint16_t*)a.out)[o + i] = cvt_bf16(v[i]);
-      }
-      return;
+    for (int i = 0; i < 8; ++i) {
+      if (i >= left) break;
+      if (a.out_f32) ((float*)a.out)[o + i] = v[i];
+      else ((uint16_t*)a.out)[o + i] = cvt_bf16(v[i]);
     }
+    return;
   }
   if (a.out_f32) {
     float4* dst = reinterpret_cast<float4*>((float*)a.out + o);
@@ -856,6 +855,15 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
                                         (int64_t)(un.row0 + c * 32 + r) * a.n_out + cbase + c8) =
                   *reinterpret_cast<const uint4*>(hs + r * kHCols + c8);
           }
+        } else if constexpr (MODE == kGroupedPlain) {
+          // one column, 32 rows: a warp's stores cover 32 neighbouring columns
+          // (128 bytes; staged through shared memory 2 % slower)
+          if (cbase + col < a.n_out) {
+            float* dst = (float*)a.out + (int64_t)(un.row0 + c * 32) * a.n_out + cbase + col;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c * 32 + i < un.nrows) dst[(int64_t)i * a.n_out] = v[i];
+          }
         } else {
 #pragma unroll
           for (int hp = 0; hp < 2; ++hp) {   // 16 rows at a time
@@ -863,11 +871,9 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
               if (c * 32 + 16 >= un.nrows) break;
               named_bar_sync(gbar, kEpiThreads);   // rows 0-15 have been copied out
             }
-            if constexpr (MODE == kGroupedLinear) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[hp * 16 + i] += bias;
-              activate_n<16>(v + hp * 16, a.act, a.out_f32 != 0);
-            }
+            for (int i = 0; i < 16; ++i) v[hp * 16 + i] += bias;
+            activate_n<16>(v + hp * 16, a.act, a.out_f32 != 0);
 #pragma unroll
             for (int i = 0; i < 16; ++i) staging[i * kStageCols + col] = v[hp * 16 + i];
             named_bar_sync(gbar, kEpiThreads);
@@ -879,12 +885,11 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
               if (row >= un.nrows || cbase + c8 >= a.n_out) continue;
               const int64_t o = (int64_t)(un.row0 + row) * a.n_out + cbase + c8;
               const int left = a.n_out - cbase - c8;
-              Residual8 rs{};
-              if constexpr (MODE == kGroupedLinear) rs = load_residual8(a, o, left);
+              const Residual8 rs = load_residual8(a, o, left);
               const float4* sp = reinterpret_cast<const float4*>(staging + r * kStageCols + c8);
               const float4 lo = sp[0], hi = sp[1];
               float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-              store_row8<MODE>(a, o, left, f, rs);
+              store_row8(a, o, left, f, rs);
             }
           }
           named_bar_sync(gbar, kEpiThreads);   // staging is free
@@ -963,7 +968,7 @@ linear_join_kernel(const __grid_constant__ Args a, int chunks, const Schedule sc
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(bias[j]);
   activate_n<8>(v, a.act, a.out_f32 != 0);
-  store_row8<kGroupedLinear>(a, out, left, v, rs);
+  store_row8(a, out, left, v, rs);
 }
 
 // y = act(bias) + residual, for products over nothing (K = 0).
