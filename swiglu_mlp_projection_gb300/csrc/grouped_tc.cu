@@ -1110,9 +1110,11 @@ cudaError_t launch_grouped(int mode, const GroupedCall& c, const GroupedPlan& p,
   RowMaps mx{};
   CUtensorMap ma, mb;
   const bool gather = mode == kGroupedSwiGLU;
+  // (a CTA loads at most n_max / 2 rows at a time: larger boxes are never used)
   if (!gather)
     for (int b = 0; b < 4; ++b)
-      if ((e = make_tmap_bf16_2d(&mx.box[b], c.x, c.rows, c.K, kBK, 128 >> b)) != cudaSuccess)
+      if ((128 >> b) <= p.n_max / 2 &&
+          (e = make_tmap_bf16_2d(&mx.box[b], c.x, c.rows, c.K, kBK, 128 >> b)) != cudaSuccess)
         return e;
   const bool kmajor = c.wlayout == kWeightsNK;
   const void* wa = c.wa;
