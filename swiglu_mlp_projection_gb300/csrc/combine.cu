@@ -144,7 +144,7 @@ cudaError_t launch_combine(const float* z, const Work* w, const int* position,
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (z && w->cut) {
+  if (z && w->shares) {
     cfg.dynamicSmemBytes = (size_t)(2 * (w->E + 1)) * sizeof(int);
     return cudaLaunchKernelEx(&cfg, combine_kernel<true>, z, *w, position, weights,
                               (const uint16_t*)residual, (uint16_t*)y, T, (int)k, rows, d);

@@ -27,6 +27,7 @@ struct GroupedPlan {
   int stages;            // shared-memory ring
   uint32_t stage_bytes;
   int cut;               // whether units of a partial wave are cut along K
+  int self_join;         // the last pair of a cut unit adds up its shares
   int min_kb;            // fewest k blocks of a share of a cut unit
   int prefetch_kb;       // linear: k blocks of weights asked into L2 per CTA before the
                          // previous kernel has ended

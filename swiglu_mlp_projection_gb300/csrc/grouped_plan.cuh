@@ -17,6 +17,7 @@ struct Work {
   int ncg;                 // column groups (units) per chunk
   int n_max;               // most rows of a chunk, a multiple of 32
   int cut;                 // whether units of a partial wave are cut along K
+  int shares;              // cut units' shares are left for the kernel after the product
   int min_kb;              // fewest k blocks of a share of a cut unit
   float* part;             // shares of cut units
   uint4* sched;            // the product's schedule (Schedule), for the kernel after it

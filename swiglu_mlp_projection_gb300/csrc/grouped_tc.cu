@@ -105,6 +105,7 @@ struct Args : Work {
   uint32_t stage_bytes;
   int kmajor;              // weights stored [n_out, K]
   int joined;              // linear: a kernel that adds up shares follows
+  int self_join;           // the last pair of a cut unit adds up its shares
   int prefetch_kb;         // linear: k blocks whose weights are asked into L2 early
   void* out;
   int out_f32;
@@ -750,8 +751,8 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
       Shares sh{0, 0, 0};
       if (!whole) {
         // A share of a cut unit: store the sums so far.  A second kernel adds
-        // them up; for the up projection, the last of the unit's pairs to take
-        // a ticket does.
+        // them up or, in short chunks (self_join), the last of the unit's pairs
+        // to take a ticket does.
         const uint32_t rel = u - sch.whole;
         const uint32_t slot = pair * sch.q / (uint32_t)a.n_kb == rel ? 0 : 1;
         float* mine = part_slot(a, pair, slot, rank);
@@ -760,7 +761,7 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
           uint32_t v[32];
           tmem_ld_x32(t_acc + (uint32_t)(c * 32), v);
           tmem_wait_ld();
-          if constexpr (MODE == kGroupedSwiGLU) {
+          if (MODE == kGroupedSwiGLU || a.self_join) {
             // [32-row chunk][4-row group][column][4 rows]
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -779,7 +780,7 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
         if (rank == 1) mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
         else mbar_arrive(&tempty[acc]);
         bool last = false;
-        if constexpr (MODE == kGroupedSwiGLU) {
+        if (MODE == kGroupedSwiGLU || a.self_join) {
           sh = shares_of(a, sch, rel);
           __threadfence();
           named_bar_sync(kBothBar, 2 * kEpiThreads);
@@ -817,7 +818,7 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
           uint32_t* vu = reinterpret_cast<uint32_t*>(v);
           tmem_ld_x32(t_acc + (uint32_t)(c * 32), vu);
           tmem_wait_ld();
-        } else if constexpr (MODE == kGroupedSwiGLU) {
+        } else {
           const float* first = part_slot(a, sh.first, sh.slot, rank) + c * 4096 + col * 4;
           const float* rest = part_slot(a, sh.first + 1, 0, rank) + c * 4096 + col * 4;
           if (un.nrows - c * 32 <= 8)
@@ -1070,11 +1071,15 @@ GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, bool swiglu, i
   // Cutting: 24.3 against 34.9 us for the 333 tokens above, 24 against 73 us for
   // the decode linear below; the up projection of 4096 tokens over 64 experts
   // 233 us uncut, 238 cut (joined by the last pair).
+  // Joined by the last pair up to 32 rows, by the next kernel above: decode
+  // linear, K = 14336, N = 4096: M = 8 22.7 against 24.3 us, M = 64 29.7 against
+  // 28.7; 333 tokens over 8 experts 31 against 24.3.
+  p.self_join = swiglu || (tn.gr_self >= 0 ? tn.gr_self : p.n_max <= 32);
   p.cut = tn.gr_cut >= 0 ? tn.gr_cut : (!swiglu || p.n_max <= 64);
-  // L2 prefetch before the dependency wait: 512 KB of weights per CTA (decode
-  // linear, M = 8, K = 14336, N = 4096: 24.2 us with 32 k blocks, 25.8 with 16,
-  // 26.3 with none, 27.3 with 64).  Many rows hide it.
-  p.prefetch_kb = tn.gr_prefetch >= 0 ? tn.gr_prefetch : (E == 1 && p.n_max <= 64 ? 32 : 0);
+  // L2 prefetch before the dependency wait: 384 KB of weights per CTA (decode
+  // linear, M = 8, K = 14336, N = 4096: 22.4 us with 24 k blocks, 23.1 with 16,
+  // 22.8 with 32, 24.5 with none, 24.8 with 64).  Many rows hide it.
+  p.prefetch_kb = tn.gr_prefetch >= 0 ? tn.gr_prefetch : (E == 1 && p.n_max <= 64 ? 24 : 0);
   return p;
 }
 
@@ -1088,6 +1093,7 @@ void fill_work(Work* w, int mode, const GroupedCall& c, const GroupedPlan& p, fl
   w->ncg = (int)((c.n_out + cols - 1) / cols);
   w->n_max = p.n_max;
   w->cut = p.cut;
+  w->shares = p.cut && !p.self_join;
   w->min_kb = p.min_kb;
   w->part = part;
   w->sched = (uint4*)((char*)part + p.part_bytes);
@@ -1156,7 +1162,8 @@ cudaError_t launch_grouped(int mode, const GroupedCall& c, const GroupedPlan& p,
   a.counters = counters;
   a.status = status;
   a.timeout_ns = timeout_ns;
-  if (mode == kGroupedSwiGLU && p.cut && !counters_clean &&
+  a.self_join = p.self_join;
+  if (p.self_join && p.cut && !counters_clean &&
       (e = cudaMemsetAsync(counters, 0, p.counters_bytes, st)) != cudaSuccess)
     return e;
   const size_t smem = smem_bytes(p, a.E);
@@ -1169,10 +1176,10 @@ cudaError_t launch_grouped(int mode, const GroupedCall& c, const GroupedPlan& p,
   const uint32_t chunks = (uint32_t)((c.rows + p.n_max - 1) / p.n_max);
   const Schedule sch = make_schedule(a, chunks, (uint32_t)p.pairs);
   const uint32_t cut = sch.units - sch.whole;
-  a.joined = cut > 0;
+  a.joined = cut > 0 && !p.self_join;
   if ((e = launch_mode<kGroupedLinear, false>(mx, ma, mb, a, p.pairs, smem, st)) != cudaSuccess)
     return e;
-  if (cut == 0) return cudaSuccess;
+  if (!a.joined) return cudaSuccess;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -30,7 +30,7 @@ struct SimtPlan {
 // SWIGLU_SK_SPLIT, SWIGLU_SK_KB, SWIGLU_TILE_PAIR, SWIGLU_TILE_SK, SWIGLU_TILE_SK_SPLIT,
 // SWIGLU_TILE_SEQ, SWIGLU_TILE_BAND, SWIGLU_SIMT_FUSED, SWIGLU_SIMT_CLUSTER,
 // SWIGLU_GR_ROWS, SWIGLU_GR_MIN_KB, SWIGLU_GR_CUT,
-// SWIGLU_GR_PREFETCH, SWIGLU_INJECT_OOM), read in one pass over the environment for every planned
+// SWIGLU_GR_SELF, SWIGLU_GR_PREFETCH, SWIGLU_INJECT_OOM), read in one pass over the environment for every planned
 // call, so a process may change them between calls.  -1: not set (the
 // measured default applies).
 struct Tuning {
@@ -46,6 +46,7 @@ struct Tuning {
   int gr_rows = -1;        // grouped products: rows per chunk (a multiple of 32)
   int gr_min_kb = -1;      // ... fewest k blocks of a share of a cut unit
   int gr_cut = -1;         // ... cut the units of a partial wave along K (0, 1)
+  int gr_self = -1;        // ... the last pair of a cut unit adds up its shares (0, 1)
   int gr_prefetch = -1;    // ... k blocks of weights prefetched into L2 (linear)
   // Test hook (SWIGLU_INJECT_OOM=1): every workspace the library would take
   // from its pool or its per-stream cache fails to allocate, so the call

@@ -521,6 +521,7 @@ Tuning read_tuning() {
                           {"GR_ROWS", &t.gr_rows},
                           {"GR_MIN_KB", &t.gr_min_kb},
                           {"GR_CUT", &t.gr_cut},
+                          {"GR_SELF", &t.gr_self},
                           {"GR_PREFETCH", &t.gr_prefetch},
                           {"INJECT_OOM", &t.inject_oom}};
     for (const Knob& k : knobs)
