@@ -181,6 +181,27 @@ __device__ __forceinline__ void limit_groups(const RouteArgs& a, int lane, const
   }
 }
 
+// The two largest keys that are not used, and where they are (0: none).
+template <int VPL>
+__device__ __forceinline__ void two_best(const unsigned* key, unsigned used, unsigned& best,
+                                         unsigned& second, int& bi, int& si) {
+  best = second = 0u;
+  bi = si = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const unsigned q = (used >> i) & 1u ? 0u : key[i];
+    if (q > best) {
+      second = best;
+      si = bi;
+      best = q;
+      bi = i;
+    } else if (q > second) {
+      second = q;
+      si = i;
+    }
+  }
+}
+
 // One warp, one token.  Lane l holds experts l VPL .. l VPL + VPL - 1, so the
 // lowest lane with the largest key holds the lowest index.  vals: E floats of
 // shared memory of the warp's own.  Lane j < k returns choice j.
@@ -234,28 +255,34 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, int la
     for (int i = 0; i < VPL; ++i) vals[lane * VPL + i] = s[i];
   }
   __syncwarp();
-  // k times the best that is left; lane j keeps choice j
+  // k times the best that is left; lane j keeps choice j.  A lane knows its two
+  // best (the first of equal ones first) and looks through its values again only
+  // when both have been chosen: few lanes hold three of a token's choices.
+  unsigned best = 0u, second = 0u, used = 0u;
+  int bi = 0, si = 0, have = 2;
+  two_best<VPL>(key, used, best, second, bi, si);
   int my_id = -1;
   for (int j = 0; j < a.k; ++j) {
-    unsigned best = key[0];
-#pragma unroll
-    for (int i = 1; i < VPL; ++i) best = max(best, key[i]);
     const unsigned top = __reduce_max_sync(kAll, best);
     if (top == 0u) break;
     const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
-    int bi = 0;
-    if (lane == owner) {
-      bool open = true;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (open && key[i] == top) {
-          key[i] = 0u;
-          bi = i;
-          open = false;
-        }
-    }
     const int id = owner * VPL + __shfl_sync(kAll, bi, owner);
     if (lane == j) my_id = id;
+    const bool mine = lane == owner;
+    if (mine) {
+      used |= 1u << bi;
+      best = second;
+      bi = si;
+      --have;
+    }
+    if (VPL > 2 && __any_sync(kAll, mine && have == 0)) {
+      if (mine) {
+        two_best<VPL>(key, used, best, second, bi, si);
+        have = 2;
+      }
+    } else if (mine) {
+      second = 0u;
+    }
   }
   float w = my_id >= 0 ? vals[my_id] : 0.f;
   if (a.renormalize) {
