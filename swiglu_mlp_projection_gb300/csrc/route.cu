@@ -313,13 +313,21 @@ __device__ void scatter_block(const SortArgs& a, const int* ids, int* s_place) {
   part = (part + 31) / 32 * 32;
   const int64_t w0 = r0 + warp * part;
   const int64_t w1 = w0 + part < r1 ? w0 + part : r1;
-  for (int64_t r = w0 + lane; r < w1; r += 32) {
-    const int e = ids[r];
-    if (e >= 0 && e < E) atomicAdd(&s_place[warp * E + e], 1);
-  }
+  // (the first 32 choices are loaded here and counted further down, with other
+  // loads under way)
+  const int e_first = w0 + lane < w1 ? ids[w0 + lane] : -1;
+  auto count_own = [&]() {
+    if (e_first >= 0 && e_first < E) atomicAdd(&s_place[warp * E + e_first], 1);
+    for (int64_t r = w0 + lane + 32; r < w1; r += 32) {
+      const int e = ids[r];
+      if (e >= 0 && e < E) atomicAdd(&s_place[warp * E + e], 1);
+    }
+  };
   if (nb > 1) {
     // All blocks' counts, and those of the blocks before: `parts` threads per
-    // expert, each over a range of blocks, 16 loads at a time.
+    // expert, each over a range of blocks, kBatch loads at a time (an L2 round
+    // trip each).
+    constexpr int kBatch = 20;
     for (int e = threadIdx.x; e < E; e += kRouteThreads) s_tot[e] = s_before[e] = 0;
     __syncthreads();
     const int parts = E < kRouteThreads ? kRouteThreads / E : 1;
@@ -328,12 +336,12 @@ __device__ void scatter_block(const SortArgs& a, const int* ids, int* s_place) {
       const int p = i / E, e = i - p * E;
       const int b0 = p * span, b1 = b0 + span < nb ? b0 + span : nb;
       int all = 0, before = 0;
-      for (int b = b0; b < b1; b += 16) {
-        int c[16];
+      for (int b = b0; b < b1; b += kBatch) {
+        int c[kBatch];
 #pragma unroll
-        for (int q = 0; q < 16; ++q) c[q] = b + q < b1 ? __ldcg(a.counts + (int64_t)(b + q) * E + e) : 0;
+        for (int q = 0; q < kBatch; ++q) c[q] = b + q < b1 ? __ldcg(a.counts + (int64_t)(b + q) * E + e) : 0;
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
+        for (int q = 0; q < kBatch; ++q) {
           all += c[q];
           if (b + q < blk) before += c[q];
         }
@@ -341,8 +349,10 @@ __device__ void scatter_block(const SortArgs& a, const int* ids, int* s_place) {
       if (all) atomicAdd(&s_tot[e], all);
       if (before) atomicAdd(&s_before[e], before);
     }
+    count_own();
     __syncthreads();
   } else {
+    count_own();
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += kRouteThreads) {
       int all = 0;
