@@ -29,13 +29,12 @@
 // Units run whole, round robin, as long as they fill the pairs; the units of
 // a last, partial wave are cut along K in equal shares (grouped_plan.cuh).  A
 // pair whose share ends inside a unit writes the f32 sums so far to the
-// workspace.  A second kernel adds the shares in k order: linear_join_kernel,
-// or the weighted sum that follows the down projection anyway.  (In the kernel
-// itself, the last pair to arrive would read all of them alone: 13 us of the
-// router logits' 31 at M = 4096, K = 4096, N = 64, where the join takes 4.)
-// Only the up projection's short units (at most 64 rows) are joined by the last
-// pair, where the shares are small and a second kernel would cost as much; its
-// longer ones are not cut.  No output depends on an order of arrival.
+// workspace.  They are added in k order: in short chunks (32 rows; 64 in the up
+// projection) by the last pair to arrive, where they are few, and otherwise by
+// a second kernel, linear_join_kernel or the weighted sum that follows the down
+// projection anyway.  (The last pair alone took 13 of the router logits' 31 us
+// at M = 4096, K = 4096, N = 64; the join takes 4.)  The up projection's longer
+// chunks are not cut.  No output depends on an order of arrival.
 //
 // What bounds it, on a GB300 (6785 GB/s copy, 1878 TFLOP/s bf16):
 //   few rows: HBM.  8 experts of d = 4096, d_ff = 14336, 32 tokens: 264 us for
@@ -112,7 +111,7 @@ struct Args : Work {
   const void* bias;        // linear
   int bias_f32, act;
   const void* resid;       // linear, in the output's type
-  unsigned* counters;      // up: two per pair, zero on entry, left at zero
+  unsigned* counters;      // self_join: two per pair, zero on entry, left at zero
   unsigned* status;
   uint64_t timeout_ns;
 };
@@ -1066,7 +1065,8 @@ GroupedPlan plan_grouped(int64_t rows, int64_t tokens, int64_t E, bool swiglu, i
   // (256 bytes behind the shares: the schedule)
   p.part_bytes = (size_t)p.pairs * 4 * (size_t)p.n_max * 128 * sizeof(float);
   // Shares of 16 k blocks or more: shorter ones only add shares to read (router
-  // logits: 15.0 us at 16, 15.8 at 4 and 8, 18.4 at 32).
+  // logits: 15.0 us at 16, 15.8 at 4 and 8, 18.4 at 32).  make_schedule takes 8
+  // where few pairs would have work.
   p.min_kb = tn.gr_min_kb > 0 ? tn.gr_min_kb : 16;
   // Cutting: 24.3 against 34.9 us for the 333 tokens above, 24 against 73 us for
   // the decode linear below; the up projection of 4096 tokens over 64 experts
