@@ -181,25 +181,27 @@ __device__ __forceinline__ void limit_groups(const RouteArgs& a, int lane, const
   }
 }
 
-// The two largest keys that are not used, and where they are (0: none).
+// A lane's three largest keys that are not used (0: none), the first of equal
+// ones first, and where they are.
+struct Best {
+  unsigned key[3];
+  int at[3];
+};
 template <int VPL>
-__device__ __forceinline__ void two_best(const unsigned* key, unsigned used, unsigned& best,
-                                         unsigned& second, int& bi, int& si) {
-  best = second = 0u;
-  bi = si = 0;
+__device__ __forceinline__ Best three_best(const unsigned* key, unsigned used) {
+  Best b{};
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const unsigned q = (used >> i) & 1u ? 0u : key[i];
-    if (q > best) {
-      second = best;
-      si = bi;
-      best = q;
-      bi = i;
-    } else if (q > second) {
-      second = q;
-      si = i;
-    }
+    const bool p0 = q > b.key[0], p1 = q > b.key[1], p2 = q > b.key[2];
+    b.key[2] = p1 ? b.key[1] : p2 ? q : b.key[2];
+    b.at[2] = p1 ? b.at[1] : p2 ? i : b.at[2];
+    b.key[1] = p0 ? b.key[0] : p1 ? q : b.key[1];
+    b.at[1] = p0 ? b.at[0] : p1 ? i : b.at[1];
+    b.key[0] = p0 ? q : b.key[0];
+    b.at[0] = p0 ? i : b.at[0];
   }
+  return b;
 }
 
 // One warp, one token.  Lane l holds experts l VPL .. l VPL + VPL - 1, so the
@@ -255,33 +257,34 @@ __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t, int la
     for (int i = 0; i < VPL; ++i) vals[lane * VPL + i] = s[i];
   }
   __syncwarp();
-  // k times the best that is left; lane j keeps choice j.  A lane knows its two
-  // best (the first of equal ones first) and looks through its values again only
-  // when both have been chosen: few lanes hold three of a token's choices.
-  unsigned best = 0u, second = 0u, used = 0u;
-  int bi = 0, si = 0, have = 2;
-  two_best<VPL>(key, used, best, second, bi, si);
+  // k times the best that is left; lane j keeps choice j.  A lane knows its
+  // three best and looks through its values again only when all of them have
+  // been chosen: few lanes hold four of a token's choices.
+  unsigned used = 0u;
+  int have = 3;
+  Best b = three_best<VPL>(key, used);
   int my_id = -1;
   for (int j = 0; j < a.k; ++j) {
-    const unsigned top = __reduce_max_sync(kAll, best);
+    const unsigned top = __reduce_max_sync(kAll, b.key[0]);
     if (top == 0u) break;
-    const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
-    const int id = owner * VPL + __shfl_sync(kAll, bi, owner);
+    const int owner = __ffs(__ballot_sync(kAll, b.key[0] == top)) - 1;
+    const int id = owner * VPL + __shfl_sync(kAll, b.at[0], owner);
     if (lane == j) my_id = id;
     const bool mine = lane == owner;
     if (mine) {
-      used |= 1u << bi;
-      best = second;
-      bi = si;
+      used |= 1u << b.at[0];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        b.key[i] = b.key[i + 1];
+        b.at[i] = b.at[i + 1];
+      }
       --have;
     }
-    if (VPL > 2 && __any_sync(kAll, mine && have == 0)) {
-      if (mine) {
-        two_best<VPL>(key, used, best, second, bi, si);
-        have = 2;
+    if (VPL > 3 && __any_sync(kAll, have == 0)) {
+      if (have == 0) {
+        b = three_best<VPL>(key, used);
+        have = 3;
       }
-    } else if (mine) {
-      second = 0u;
     }
   }
   float w = my_id >= 0 ? vals[my_id] : 0.f;
