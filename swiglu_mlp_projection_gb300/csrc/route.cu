@@ -68,8 +68,9 @@ struct SortArgs {
   int64_t R;       // choices
   int64_t seg;     // choices per block
   int E;
-  int* counts;     // [blocks][E]: how many choices of its segment each block found
+  int* counts;     // [blocks][count_stride(E)]: choices of its segment each block found
 };
+__host__ __device__ constexpr int count_stride(int E) { return (E + 3) / 4 * 4; }
 
 // VPL values of row t, experts lane VPL ..; -inf past E and for NaN.
 template <int VPL>
@@ -328,29 +329,41 @@ __device__ void scatter_block(const SortArgs& a, const int* ids, int* s_place) {
   };
   if (nb > 1) {
     // All blocks' counts, and those of the blocks before: `parts` threads per
-    // expert, each over a range of blocks, kBatch loads at a time (an L2 round
-    // trip each).
-    constexpr int kBatch = 20;
+    // four experts, each over a range of blocks, kBatch loads at a time (an L2
+    // round trip each).
+    constexpr int kBatch = 10;
     for (int e = threadIdx.x; e < E; e += kRouteThreads) s_tot[e] = s_before[e] = 0;
     __syncthreads();
-    const int parts = E < kRouteThreads ? kRouteThreads / E : 1;
+    const int stride = count_stride(E), quads = stride / 4;
+    const int parts = quads < kRouteThreads ? kRouteThreads / quads : 1;
     const int span = (nb + parts - 1) / parts;
-    for (int i = threadIdx.x; i < parts * E; i += kRouteThreads) {
-      const int p = i / E, e = i - p * E;
+    for (int i = threadIdx.x; i < parts * quads; i += kRouteThreads) {
+      const int p = i / quads, e = (i - p * quads) * 4;
       const int b0 = p * span, b1 = b0 + span < nb ? b0 + span : nb;
-      int all = 0, before = 0;
+      int4 all = make_int4(0, 0, 0, 0), before = all;
       for (int b = b0; b < b1; b += kBatch) {
-        int c[kBatch];
+        int4 c[kBatch];
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) c[q] = b + q < b1 ? __ldcg(a.counts + (int64_t)(b + q) * E + e) : 0;
+        for (int q = 0; q < kBatch; ++q)
+          c[q] = b + q < b1
+                     ? __ldcg(reinterpret_cast<const int4*>(a.counts + (int64_t)(b + q) * stride + e))
+                     : make_int4(0, 0, 0, 0);
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-          all += c[q];
-          if (b + q < blk) before += c[q];
+          all.x += c[q].x; all.y += c[q].y; all.z += c[q].z; all.w += c[q].w;
+          if (b + q < blk) {
+            before.x += c[q].x; before.y += c[q].y; before.z += c[q].z; before.w += c[q].w;
+          }
         }
       }
-      if (all) atomicAdd(&s_tot[e], all);
-      if (before) atomicAdd(&s_before[e], before);
+      const int va[4] = {all.x, all.y, all.z, all.w};
+      const int vb[4] = {before.x, before.y, before.z, before.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // (what pads a row of counts is 0 and adds nothing)
+        if (va[j]) atomicAdd(&s_tot[e + j], va[j]);
+        if (vb[j]) atomicAdd(&s_before[e + j], vb[j]);
+      }
     }
     count_own();
     __syncthreads();
@@ -366,22 +379,26 @@ __device__ void scatter_block(const SortArgs& a, const int* ids, int* s_place) {
     }
     __syncthreads();
   }
-  // exclusive prefix of the totals: the experts' offsets
+  // exclusive prefix of the totals: the experts' offsets (a lane has
+  // consecutive experts, so that one scan of the warp does)
   if (warp == 0) {
-    int sum = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane;
-      const int c = e < E ? s_tot[e] : 0;
-      int inc = c;
+    const int per = (E + 31) / 32, e0 = lane * per;
+    const int e1 = e0 + per < E ? e0 + per : E;
+    int own = 0;
+    for (int e = e0; e < e1; ++e) own += s_tot[e];
+    int inc = own;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kAll, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (e < E) s_tot[e] = sum + inc - c;
-      sum += __shfl_sync(kAll, inc, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, inc, o);
+      if (lane >= o) inc += v;
     }
-    if (lane == 0) s_tot[E] = sum;
+    if (lane == 31) s_tot[E] = inc;
+    int run = inc - own;
+    for (int e = e0; e < e1; ++e) {
+      const int c = s_tot[e];
+      s_tot[e] = run;
+      run += c;
+    }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kRouteThreads) {
@@ -467,8 +484,9 @@ route_kernel(const RouteArgs a, const SortArgs so) {
   }
   if constexpr (SORT == kCount) {
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kRouteThreads)
-      so.counts[(int64_t)blockIdx.x * a.E + e] = s_cnt[e];
+    const int stride = count_stride(a.E);
+    for (int e = threadIdx.x; e < stride; e += kRouteThreads)
+      so.counts[(int64_t)blockIdx.x * stride + e] = e < a.E ? s_cnt[e] : 0;
   }
 }
 
@@ -488,8 +506,9 @@ count_kernel(const SortArgs a) {
     if (e >= 0 && e < a.E) atomicAdd(&s_mem[e], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kRouteThreads)
-    a.counts[(int64_t)blockIdx.x * a.E + e] = s_mem[e];
+  const int stride = count_stride(a.E);
+  for (int e = threadIdx.x; e < stride; e += kRouteThreads)
+    a.counts[(int64_t)blockIdx.x * stride + e] = e < a.E ? s_mem[e] : 0;
 }
 
 template <int THREADS>
@@ -582,11 +601,11 @@ cudaError_t launch_scatter(const SortArgs& so, unsigned grid, cudaStream_t st) {
 
 size_t dispatch_scratch_bytes(int64_t R, int64_t E, int num_sms) {
   const int64_t nb = sort_blocks(R, num_sms);
-  return nb > 1 ? (size_t)nb * E * sizeof(int) : 0;
+  return nb > 1 ? (size_t)nb * count_stride((int)E) * sizeof(int) : 0;
 }
 
 size_t route_scratch_bytes(int64_t T, int64_t E, int num_sms) {
-  return T > kOneBlockTokens ? (size_t)route_blocks(T, num_sms) * E * sizeof(int) : 0;
+  return T > kOneBlockTokens ? (size_t)route_blocks(T, num_sms) * count_stride((int)E) * sizeof(int) : 0;
 }
 
 cudaError_t launch_route(const RouteCall& c, const SortCall* sort, int num_sms, cudaStream_t st) {
