@@ -22,10 +22,9 @@
 //
 // What bounds it, on a GB300 (in a graph): 16384 tokens, E = 256, k = 8,
 // sigmoid, bias, 4 of 8 groups: 25.9 us, where the 18.9 MB would take 2.8.
-// route_kernel issues 1020 warp instructions per token, about a fifth of them
-// the scores' exponentials and reciprocals, and keeps the issue slots 67 % busy;
-// the scatter's chain (counts, offsets, places) is L2 latency.  5001 tokens,
-// E = 60: 8.6 us, latency of the two kernels.  One token: 3.5 us, launch.
+// route_kernel issues 1020 warp instructions per token and keeps the issue slots
+// 67 % busy; the scatter's chain (counts, offsets, places) is L2 latency.  5001
+// tokens, E = 60: 8.6 us, latency of the two kernels.  One token: 3.6 us, launch.
 // Reading the next token's row ahead (prefetch) changed nothing: 26.0 us.
 #include "common.cuh"
 #include "grouped.h"
