@@ -125,6 +125,21 @@ def test_groups_and_bias(cuda_lib, T, E, k, groups, topk_groups, bias, group_sco
     check(randn(T, E, E), k, score, b, groups, topk_groups, group_score)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(256, 8), (512, 16), (1024, 32), (128, 5)])
+def test_neighbours_chosen(cuda_lib, E, k, score):
+    # all of a token's choices are neighbouring experts, in falling, rising and
+    # equal order, at the start, at the end and across the middle
+    l = randn(9, E, E, scale=0.1)
+    fall = torch.linspace(6, 5, k, device=DEV)
+    for row, at in ((0, 0), (3, E - k), (6, E // 2 - k // 2)):
+        l[row, at:at + k] = fall
+        l[row + 1, at:at + k] = fall.flip(0)
+        l[row + 2, at:at + k] = 5.0
+    check(l, k, score)
+    check(l, k, score, torch.zeros(E, device=DEV))
+
+
 def test_masks(cuda_lib):
     inf = math.inf
     l = randn(64, 40, 1)
