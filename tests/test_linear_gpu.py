@@ -73,6 +73,19 @@ def test_sizes(cuda_lib, M, K, N, layout):
 
 
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K,N", [(1, 2048, 64), (100, 2056, 64), (256, 4096, 128),
+                                   (1025, 2040, 40), (700, 6000, 264)])
+def test_few_outputs_of_long_sums(cuda_lib, M, K, N, out_dtype):
+    # few units, cut along K in short shares; whole and ragged last blocks of K
+    x, w, b, r = make(M, K, N, "nk", torch.float32, True, out_dtype, seed=K)
+    for _ in range(2):
+        y = swg.linear(x, w, bias=b, residual=r, activation="gelu", out_dtype=out_dtype,
+                       layout="nk")
+        check(y, x, w, b, r, "gelu", "nk")
+    swg.check_device_status()
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("bias,residual", [(None, False), (torch.float32, True),
                                            (torch.bfloat16, False)])
