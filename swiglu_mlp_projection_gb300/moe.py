@@ -17,13 +17,12 @@ GROUP_SCORES = {"max": 0, "top2": 1}
 LAYOUTS = {"kn": 0, "nk": 1}
 
 
-
 class Routing(collections.namedtuple("Routing", "ids weights offsets order position")):
     """Where each token goes: ids [T, k] int32 (-1: no expert), weights [T, k]
     float32, and the (token, choice) pairs sorted by expert: offsets [E + 1],
     order [T k], position [T, k], int32 (``route`` and ``dispatch`` write them)."""
 
-    _checked = None   # (device, T, k, E, addresses), once its tensors have been checked
+    __slots__ = ()   # its tensors and nothing else: copies and pickles stand for themselves
 
 
 def _code(table, value, what):
@@ -156,10 +155,7 @@ def route(logits, k, score="softmax", bias=None, groups=1, topk_groups=None, gro
           dt, sc, groups, groups if topk_groups is None else topk_groups, gs,
           1 if renormalize else 0, scale,
           stream.cuda_stream if stream is not None else _raw_stream(index))
-    r = Routing(ids, weights, offsets, order, position)
-    r._checked = (index, T, k, E, offsets.data_ptr(), order.data_ptr(), position.data_ptr(),
-                  weights.data_ptr())
-    return r
+    return Routing(ids, weights, offsets, order, position)
 
 
 def dispatch(ids, n_experts, weights=None, stream=None):
@@ -188,7 +184,7 @@ def dispatch(ids, n_experts, weights=None, stream=None):
 
 def _check_routing(torch, r):
     """(device, T, k, E, addresses of offsets, order, position, weights), checked
-    once per Routing: its tensors cannot be exchanged."""
+    in every call: a tensor's storage and sizes can change between two calls."""
     i32, position = torch.int32, r.position
     index = _first(position, "routing.position", i32)
     if position.dim() != 2 or r.offsets.dim() != 1 or r.offsets.shape[0] < 2:
@@ -203,8 +199,7 @@ def _check_routing(torch, r):
         pw = _check(r.weights, "routing.weights", index, torch.float32)
         if r.weights.shape != (T, k):
             raise ValueError("expected weights [T, k] in the routing")
-    r._checked = (index, T, k, r.offsets.shape[0] - 1, po, pr, position.data_ptr(), pw)
-    return r._checked
+    return index, T, k, r.offsets.shape[0] - 1, po, pr, position.data_ptr(), pw
 
 
 def experts_up(x, w_gate, w_up, routing, out=None, layout="kn", workspace=None, stream=None):
@@ -225,7 +220,7 @@ def experts_up(x, w_gate, w_up, routing, out=None, layout="kn", workspace=None, 
         raise ValueError("expected x [T, d] and w_gate, w_up [E, d, d_ff] or [E, d_ff, d]")
     T, d = x.shape
     E, d_ff = w_gate.shape[0], w_gate.shape[2 - lay]
-    rdev, rT, k, rE, po, pr, _, _ = routing._checked or _check_routing(torch, routing)
+    rdev, rT, k, rE, po, pr, _, _ = _check_routing(torch, routing)
     if rT != T or rE != E or rdev != index:
         raise ValueError("the routing is of %d tokens and %d experts on device %d, not %d, %d, %d"
                          % (rT, rE, rdev, T, E, index))
@@ -254,7 +249,7 @@ def experts_down(h, w_down, routing, residual=None, out=None, layout="kn", works
         raise ValueError("expected h [T k, d_ff] and w_down [E, d_ff, d] or [E, d, d_ff]")
     d_ff = h.shape[1]
     E, d = w_down.shape[0], w_down.shape[2 - lay]
-    rdev, T, k, rE, po, _, pp, pt = routing._checked or _check_routing(torch, routing)
+    rdev, T, k, rE, po, _, pp, pt = _check_routing(torch, routing)
     if rE != E or rdev != index:
         raise ValueError("the routing is of %d experts on device %d, not %d, %d"
                          % (rE, rdev, E, index))
