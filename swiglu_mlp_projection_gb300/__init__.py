@@ -62,6 +62,20 @@ def _current_device():
     return _CUR_DEVICE() if _CUR_DEVICE is not None else torch.cuda.current_device()
 
 
+def _empty(torch, shape, dtype, device, stream):
+    """A tensor for kernels on `stream` (None: the current one) to write.  It
+    comes from that stream's memory: the current stream's may still be in use
+    by work that `stream` does not wait for, and goes to that stream's next
+    tensor as soon as this one is dropped."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    # (the caller's current stream may read it when it is dropped)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def swiglu_up(x, w_gate, w_up, out=None, path="auto", workspace=None, stream=None,
               layout="kn"):
     """h = silu(x @ w_gate) * (x @ w_up) on x's CUDA device.

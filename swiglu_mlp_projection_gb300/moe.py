@@ -4,12 +4,14 @@
 them in turn.
 
 As the rest of the binding, these only marshal torch tensors into the C ABI;
-calls are asynchronous on torch's current stream (or ``stream``).
+calls are asynchronous on torch's current stream (or ``stream``).  What a call
+with a ``stream`` allocates belongs to that stream, as under
+``torch.cuda.stream(stream)``; its inputs have to be ready there.
 """
 import collections
 
 from . import _lib
-from . import _call, _raw_stream, _torch
+from . import _call, _empty, _raw_stream, _torch
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -58,9 +60,9 @@ def _workspace(workspace, index):
     return _check(workspace, "workspace", index), workspace.numel() * workspace.element_size()
 
 
-def _out(torch, out, shape, dtype, index, device):
+def _out(torch, out, shape, dtype, index, device, stream):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(torch, shape, dtype, device, stream)
     _check(out, "out", index)
     if out.shape != shape or out.dtype is not dtype:
         raise ValueError("out must be a contiguous %s tensor of %s" % (shape, dtype))
@@ -105,7 +107,7 @@ def linear(x, w, bias=None, residual=None, activation="none", out=None, out_dtyp
         pr = _check(residual, "residual", index)
         if residual.shape != (M, N) or residual.dtype is not out_dtype:
             raise ValueError("residual must be [M, N] of the result's dtype")
-    out = _out(torch, out, (M, N), out_dtype, index, x.device)
+    out = _out(torch, out, (M, N), out_dtype, index, x.device, stream)
     ws, nws = _workspace(workspace, index)
     _call(index, _lib.load().swiglu_linear, x.data_ptr(), pw, pb, pr, out.data_ptr(), M, K, N, act,
           bias_code, _lib.BF16 if out_dtype is bf16 else _lib.F32, lay, ws, nws,
@@ -145,11 +147,11 @@ def route(logits, k, score="softmax", bias=None, groups=1, topk_groups=None, gro
     if k < 0:
         raise ValueError("k must not be negative")
     dev, i32 = logits.device, torch.int32
-    ids = torch.empty((T, k), dtype=i32, device=dev)
-    weights = torch.empty((T, k), dtype=f32, device=dev)
-    offsets = torch.empty((E + 1,), dtype=i32, device=dev)
-    order = torch.empty((T * k,), dtype=i32, device=dev)
-    position = torch.empty((T, k), dtype=i32, device=dev)
+    ids = _empty(torch, (T, k), i32, dev, stream)
+    weights = _empty(torch, (T, k), f32, dev, stream)
+    offsets = _empty(torch, (E + 1,), i32, dev, stream)
+    order = _empty(torch, (T * k,), i32, dev, stream)
+    position = _empty(torch, (T, k), i32, dev, stream)
     _call(index, _lib.load().swiglu_route, logits.data_ptr(), pb, ids.data_ptr(),
           weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), position.data_ptr(), T, E, k,
           dt, sc, groups, groups if topk_groups is None else topk_groups, gs,
@@ -173,9 +175,9 @@ def dispatch(ids, n_experts, weights=None, stream=None):
     if n_experts < 1:
         raise ValueError("n_experts must be positive")
     dev, i32 = ids.device, torch.int32
-    offsets = torch.empty((n_experts + 1,), dtype=i32, device=dev)
-    order = torch.empty((T * k,), dtype=i32, device=dev)
-    position = torch.empty((T, k), dtype=i32, device=dev)
+    offsets = _empty(torch, (n_experts + 1,), i32, dev, stream)
+    order = _empty(torch, (T * k,), i32, dev, stream)
+    position = _empty(torch, (T, k), i32, dev, stream)
     _call(index, _lib.load().swiglu_dispatch, ids.data_ptr(), offsets.data_ptr(), order.data_ptr(),
           position.data_ptr(), T, k, n_experts,
           stream.cuda_stream if stream is not None else _raw_stream(index))
@@ -224,7 +226,7 @@ def experts_up(x, w_gate, w_up, routing, out=None, layout="kn", workspace=None, 
     if rT != T or rE != E or rdev != index:
         raise ValueError("the routing is of %d tokens and %d experts on device %d, not %d, %d, %d"
                          % (rT, rE, rdev, T, E, index))
-    out = _out(torch, out, (T * k, d_ff), bf16, index, x.device)
+    out = _out(torch, out, (T * k, d_ff), bf16, index, x.device, stream)
     ws, nws = _workspace(workspace, index)
     _call(index, _lib.load().swiglu_experts_up, x.data_ptr(), pg, pu, po, pr, out.data_ptr(), T, k,
           E, d, d_ff, lay, ws, nws,
@@ -262,7 +264,7 @@ def experts_down(h, w_down, routing, residual=None, out=None, layout="kn", works
         pr = _check(residual, "residual", index, bf16)
         if residual.shape != (T, d):
             raise ValueError("residual must be [T, d] = [%d, %d]" % (T, d))
-    out = _out(torch, out, (T, d), bf16, index, h.device)
+    out = _out(torch, out, (T, d), bf16, index, h.device, stream)
     ws, nws = _workspace(workspace, index)
     _call(index, _lib.load().swiglu_experts_down, h.data_ptr(), pw, po, pp, pt, pr, out.data_ptr(),
           T, k, E, d_ff, d, lay, ws, nws,
