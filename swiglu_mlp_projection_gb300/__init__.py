@@ -108,7 +108,7 @@ def swiglu_up(x, w_gate, w_up, out=None, path="auto", workspace=None, stream=Non
     if w_gate.dtype != x.dtype or w_up.dtype != x.dtype:
         raise TypeError("x, w_gate and w_up must share one dtype")
     if out is None:
-        out = torch.empty((M, d_ff), dtype=x.dtype, device=x.device)
+        out = _empty(torch, (M, d_ff), x.dtype, x.device, stream)
     elif out.shape != (M, d_ff) or out.dtype != x.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous [M, d_ff] tensor of x's dtype")
     st = stream.cuda_stream if stream is not None else _raw_stream(index)
@@ -163,7 +163,7 @@ def pack_weights(w_gate, w_up, out=None, stream=None):
     d, d_ff = w_gate.shape
     width = 128 * ((d_ff + 63) // 64)
     if out is None:
-        out = torch.empty((d, width), dtype=w_gate.dtype, device=w_gate.device)
+        out = _empty(torch, (d, width), w_gate.dtype, w_gate.device, stream)
     elif out.shape != (d, width) or out.dtype != w_gate.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous [d, %d] tensor of the weights' dtype" % width)
     index = w_gate.device.index
@@ -191,7 +191,7 @@ def swiglu_up_packed(x, w_packed, d_ff, out=None, path="auto", workspace=None, s
         raise TypeError("x and w_packed must share one dtype")
     M, d = x.shape
     if out is None:
-        out = torch.empty((M, d_ff), dtype=x.dtype, device=x.device)
+        out = _empty(torch, (M, d_ff), x.dtype, x.device, stream)
     elif out.shape != (M, d_ff) or out.dtype != x.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous [M, d_ff] tensor of x's dtype")
     index = x.device.index
@@ -227,10 +227,10 @@ def quantize_weights_fp8(w_gate, w_up, stream=None):
         raise ValueError("expected w_gate and w_up of one shape [d, d_ff]")
     d, d_ff = w_gate.shape
     dev = w_gate.device
-    w8g = torch.empty((d_ff, d), dtype=torch.uint8, device=dev)
-    w8u = torch.empty((d_ff, d), dtype=torch.uint8, device=dev)
-    sg = torch.empty(d_ff, dtype=torch.float32, device=dev)
-    su = torch.empty(d_ff, dtype=torch.float32, device=dev)
+    w8g = _empty(torch, (d_ff, d), torch.uint8, dev, stream)
+    w8u = _empty(torch, (d_ff, d), torch.uint8, dev, stream)
+    sg = _empty(torch, d_ff, torch.float32, dev, stream)
+    su = _empty(torch, d_ff, torch.float32, dev, stream)
     st = stream.cuda_stream if stream is not None else _raw_stream(dev.index)
     if _LIB is None:
         _LIB = _lib.load()
@@ -257,8 +257,8 @@ def quantize_weight_fp8(w, stream=None):
     if w.dtype != torch.bfloat16 or w.dim() != 2:
         raise ValueError("expected a bfloat16 matrix [K, N]")
     K, N = w.shape
-    w8 = torch.empty((N, K), dtype=torch.uint8, device=w.device)
-    s = torch.empty(N, dtype=torch.float32, device=w.device)
+    w8 = _empty(torch, (N, K), torch.uint8, w.device, stream)
+    s = _empty(torch, N, torch.float32, w.device, stream)
     st = stream.cuda_stream if stream is not None else _raw_stream(w.device.index)
     if _LIB is None:
         _LIB = _lib.load()
@@ -280,7 +280,7 @@ def swiglu_down_fp8(h, w, residual=None, out=None, path="auto", workspace=None, 
     if residual is not None and (residual.shape != (M, d) or residual.dtype != h.dtype):
         raise ValueError("residual must be a bfloat16 [M, d] tensor")
     if out is None:
-        out = torch.empty((M, d), dtype=h.dtype, device=h.device)
+        out = _empty(torch, (M, d), h.dtype, h.device, stream)
     elif out.shape != (M, d) or out.dtype != h.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous bfloat16 [M, d] tensor")
     index = h.device.index
@@ -315,7 +315,7 @@ def swiglu_up_fp8(x, w, out=None, path="auto", workspace=None, stream=None):
         raise ValueError("expected bfloat16 x [M, %d]" % w.d)
     M = x.shape[0]
     if out is None:
-        out = torch.empty((M, w.d_ff), dtype=x.dtype, device=x.device)
+        out = _empty(torch, (M, w.d_ff), x.dtype, x.device, stream)
     elif out.shape != (M, w.d_ff) or out.dtype != x.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous bfloat16 [M, d_ff] tensor")
     index = x.device.index
@@ -365,7 +365,7 @@ def swiglu_down(h, w_down, residual=None, out=None, path="auto", workspace=None,
     if residual is not None and residual.shape != (M, d):
         raise ValueError("residual must be [M, d]")
     if out is None:
-        out = torch.empty((M, d), dtype=h.dtype, device=h.device)
+        out = _empty(torch, (M, d), h.dtype, h.device, stream)
     elif out.shape != (M, d) or out.dtype != h.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous [M, d] tensor of h's dtype")
     index = h.device.index
@@ -403,9 +403,9 @@ def swiglu_mlp(x, w_gate, w_up, w_down, residual=None, h=None, out=None, stream=
         raise ValueError("expected x [M, d], w_gate/w_up [d, d_ff], w_down [d_ff, d]")
     dt = _dtype_code(x)
     if h is None:
-        h = torch.empty((M, d_ff), dtype=x.dtype, device=x.device)
+        h = _empty(torch, (M, d_ff), x.dtype, x.device, stream)
     if out is None:
-        out = torch.empty((M, d), dtype=x.dtype, device=x.device)
+        out = _empty(torch, (M, d), x.dtype, x.device, stream)
     index = x.device.index
     st = stream.cuda_stream if stream is not None else _raw_stream(index)
     if _LIB is None:

@@ -154,3 +154,42 @@ def test_results_in_a_graph_on_a_forked_stream(cuda_lib):
         torch.cuda.synchronize()
         assert torch.equal(y, want)
     swg.check_device_status()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("op", ["up", "packed", "down", "mlp", "fp8", "quantize"])
+def test_dense_results_are_not_the_current_streams_memory(cuda_lib, op):
+    # The current stream is held back before its last write to tensors that are
+    # then dropped: a call on another stream does not get their memory.
+    import swiglu_mlp_projection_gb300 as swg
+    dev = torch.device("cuda", 0)
+    g = torch.Generator(device=dev).manual_seed(2)
+
+    def normal(*shape):
+        return (torch.randn(*shape, generator=g, device=dev) * 0.1).to(BF)
+    M, d, f = 40, 256, 520
+    x, wg, wu, wd = normal(M, d), normal(d, f), normal(d, f), normal(f, d)
+    h = normal(M, f)
+    wp = swg.pack_weights(wg, wu)
+    w8 = swg.quantize_weights_fp8(wg, wu)
+    call = {"up": lambda s: (swg.swiglu_up(x, wg, wu, stream=s),),
+            "packed": lambda s: (swg.swiglu_up_packed(x, wp, f, stream=s),),
+            "down": lambda s: (swg.swiglu_down(h, wd, residual=x, stream=s),),
+            "mlp": lambda s: swg.swiglu_mlp(x, wg, wu, wd, stream=s),
+            "fp8": lambda s: (swg.swiglu_up_fp8(x, w8, stream=s),),
+            "quantize": lambda s: tuple(vars(swg.quantize_weights_fp8(wg, wu, stream=s))[n]
+                                        for n in ("w8_gate", "w8_up", "s_gate", "s_up"))}[op]
+    side = torch.cuda.Stream(dev)
+    want = call(None)
+    call(side)
+    torch.cuda.synchronize()
+    busy = [torch.empty_like(t) for t in want for _ in range(3)]
+    torch.cuda._sleep(20_000_000)
+    for t in busy:
+        t.fill_(77)
+    del busy, t
+    got = call(side)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    swg.check_device_status()
