@@ -26,6 +26,9 @@
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  Calls only
  *     enqueue work; they return before it runs.  Faults inside enqueued work
  *     surface at the caller's next synchronisation, as for any CUDA library.
+ *   - Calls may come from several host threads, on one stream too: a call that
+ *     uses the library's workspace enqueues its kernels without another such
+ *     call's in between.  A workspace of the caller's serves one call at a time.
  *   - Argument validation is synchronous and enqueues nothing on failure.
  *   - The return value is a swiglu_status; swiglu_last_error_string() gives a
  *     human-readable detail for the calling thread's last failure.

@@ -99,6 +99,12 @@ int get_device(Device* d) {
   return SWIGLU_OK;
 }
 
+// For a call without a workspace of its own: until it returns, no other
+// thread's call on the stream comes between its kernels.
+std::unique_lock<std::mutex> lock_calls(const Device& dv, cudaStream_t st, const void* workspace) {
+  return workspace ? std::unique_lock<std::mutex>() : api_lock_enqueue(dv.dev, st);
+}
+
 // One grouped product with its workspace; `extra` bytes (z of the down
 // projection, or padded weights) follow the partial sums.  The caller frees ws.pooled.
 int run_grouped(int mode, GroupedCall c, const GroupedPlan& p, const Device& dv, void* workspace,
@@ -195,6 +201,7 @@ int swiglu_linear(const void* x, const void* w, const void* bias, const void* re
   c.n_out = N;
   c.wlayout = wlayout_of(layout);
   const cudaStream_t st = (cudaStream_t)stream;
+  const std::unique_lock<std::mutex> lock = lock_calls(dv, st, workspace);
   Workspace ws;
   if ((v = run_grouped(kGroupedLinear, c, p, dv, workspace, workspace_bytes,
                        layout == SWIGLU_WEIGHTS_KN && K > 0 ? padded_bytes(K, N) : 0, &ws, st)) != SWIGLU_OK)
@@ -229,6 +236,7 @@ int swiglu_dispatch(const int32_t* ids, int32_t* offsets, int32_t* order, int32_
   Device dv;
   if ((v = get_device(&dv)) != SWIGLU_OK) return v;
   const cudaStream_t st = (cudaStream_t)stream;
+  const std::unique_lock<std::mutex> lock = lock_calls(dv, st, nullptr);
   Workspace ws;
   SortCall sort{offsets, order, position, nullptr};
   if ((v = sort_workspace(dv, dispatch_scratch_bytes(T * k, E, dv.num_sms), &ws, &sort, st)) != SWIGLU_OK) return v;
@@ -280,6 +288,7 @@ int swiglu_route(const void* logits, const float* bias, int32_t* ids, float* wei
   const RouteCall c{logits, logits_dtype == SWIGLU_F32, bias, ids, weights, T, E, k,
                     score == SWIGLU_SCORE_SIGMOID, (int)groups, (int)topk_groups,
                     group_score == SWIGLU_GROUP_TOP2, renormalize != 0, scale};
+  const std::unique_lock<std::mutex> lock = lock_calls(dv, st, nullptr);
   Workspace ws;
   SortCall sc{offsets, order, position, nullptr};
   if (sort && (v = sort_workspace(dv, route_scratch_bytes(T, E, dv.num_sms), &ws, &sc, st)) != SWIGLU_OK) return v;
@@ -345,6 +354,7 @@ int swiglu_experts_up(const void* x, const void* w_gate, const void* w_up, const
   c.n_out = d_ff;
   c.wlayout = wlayout_of(layout);
   const cudaStream_t st = (cudaStream_t)stream;
+  const std::unique_lock<std::mutex> lock = lock_calls(dv, st, workspace);
   Workspace ws;
   if ((v = run_grouped(kGroupedSwiGLU, c, plan_experts(T, k, E, true, dv.pairs), dv, workspace,
                        workspace_bytes, 0, &ws, st)) != SWIGLU_OK)
@@ -380,6 +390,7 @@ int swiglu_experts_down(const void* h, const void* w_down, const int32_t* offset
     return SWIGLU_OK;
   }
   const cudaStream_t st = (cudaStream_t)stream;
+  const std::unique_lock<std::mutex> lock = lock_calls(dv, st, workspace);
   Workspace ws;
   const float* z = nullptr;
   Work work{};

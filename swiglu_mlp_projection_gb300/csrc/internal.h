@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
 namespace swg {
 
 // Partial-sum layout shared by every split-K producer and the reduction:
@@ -130,6 +132,11 @@ struct Workspace {
   bool counters_clean = false;   // the counters are zero already
   void* pooled = nullptr;
 };
+// Held by a call from taking the library's workspace to its last launch, so
+// that calls of several host threads on one stream enqueue one after another:
+// the kernels of a call hand data over in the stream's buffer, and a call that
+// outgrows the buffer frees it in stream order.
+std::unique_lock<std::mutex> api_lock_enqueue(int dev, cudaStream_t st);
 int api_take_workspace(int dev, cudaStream_t st, void* caller, size_t caller_bytes,
                        size_t counter_bytes, size_t body_bytes, Workspace* ws);
 constexpr int64_t kSimtMaxGridYZ = 65535;

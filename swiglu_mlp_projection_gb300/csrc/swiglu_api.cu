@@ -199,10 +199,23 @@ void mark_workspaces_dirty(int dev) {
     if (e.dev == dev) e.dirty = true;
 }
 
+// The lock that orders the calls of one stream among host threads (see
+// api_lock_enqueue).  Streams share kEnqueueLocks of them; it is taken before
+// g_mu, never after.
+constexpr size_t kEnqueueLocks = 64;
+std::mutex g_enqueue_mu[kEnqueueLocks];
+
+std::unique_lock<std::mutex> lock_enqueue(int dev, cudaStream_t st) {
+  const cudaStream_t s = st == cudaStreamLegacy ? nullptr : st;   // two names of one stream
+  const uint64_t h = ((uint64_t)(uintptr_t)s + (uint64_t)dev) * 0x9E3779B97F4A7C15ull;
+  return std::unique_lock<std::mutex>(g_enqueue_mu[(h >> 32) % kEnqueueLocks]);
+}
+
 // Drops the cached buffer of stream `st` on `dev`: a stream-ordered free on
 // `st` itself, after the work already enqueued there.
 int release_stream_workspace(int dev, cudaStream_t st) {
   if (st == cudaStreamPerThread) return SWIGLU_OK;   // never cached
+  const std::unique_lock<std::mutex> lock = lock_enqueue(dev, st);
   unsigned long long id = 0;
   cudaError_t e = cudaStreamGetId(st, &id);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamGetId");
@@ -779,6 +792,7 @@ int run(const Call& c) {
                                : p.path == SWIGLU_PATH_TC   ? p.tile.counters_bytes
                                                             : p.simt.counters_bytes;
   cudaStream_t st = c.st;
+  std::unique_lock<std::mutex> lock;   // to the end of the call
   if (p.workspace > 0) {
     if (c.workspace) {
       if (c.ws_bytes < p.workspace || ((uintptr_t)c.workspace & 255u))
@@ -788,6 +802,7 @@ int run(const Call& c) {
       counters = (unsigned*)((char*)c.workspace + fp8_prefix);
       part = (float*)((char*)c.workspace + fp8_prefix + counter_bytes);
     } else {
+      lock = lock_enqueue(dev, st);
       Workspace ws;
       if ((v = take_workspace(dev, st, counter_bytes, p.workspace - counter_bytes, p.inject_oom,
                               &ws)) != SWIGLU_OK)
@@ -931,6 +946,10 @@ int api_max_pairs(int dev) {
   if (dev < 0 || dev >= kMaxDevices) return 0;
   std::lock_guard<std::mutex> lk(g_mu);
   return g_dev[dev].max_pairs;
+}
+
+std::unique_lock<std::mutex> api_lock_enqueue(int dev, cudaStream_t st) {
+  return lock_enqueue(dev, st);
 }
 
 int api_take_workspace(int dev, cudaStream_t st, void* caller, size_t caller_bytes,
