@@ -741,7 +741,11 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
     int kb0, kb1, e_at = 0;
     while (!skip && w.next(a, sch, pairs, u, kb0, kb1)) {
       const Unit un = find_unit<kCols>(a, s_row, s_chunk, u, e_at);
-      if (!mbar_wait(&tfull[acc], acc_phase, abort_flag, a.status, a.timeout_ns)) break;
+      // Both groups go on, or both end: what follows has barriers of one group
+      // and of both.
+      const bool ready = mbar_wait(&tfull[acc], acc_phase, abort_flag, a.status, a.timeout_ns);
+      __syncwarp();
+      if (!named_bar_all(kBothBar, 2 * kEpiThreads, ready)) break;
       tc_fence_after();
       const uint32_t t_acc = tmem + lane_off + (uint32_t)(acc * kAccCols);
       const bool whole = kb0 == 0 && kb1 == a.n_kb;

@@ -198,6 +198,23 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// Whether `ok` holds in each of the `nthreads` threads (whole warps) that meet
+// at the named barrier; the same answer for all of them.  A role of several
+// warps decides with it whether a wait has given up: a thread that went on
+// alone would meet a barrier that the others never reach.
+__device__ __forceinline__ bool named_bar_all(uint32_t id, uint32_t nthreads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(nthreads), "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
 // ---- thread-block clusters and distributed shared memory -------------------------
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
