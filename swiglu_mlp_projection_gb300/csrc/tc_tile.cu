@@ -446,7 +446,10 @@ tile_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
     while (!skip && w.next(a, n_units, t, kb0, kb1)) {
       int mb, nb;
       tile_coords(a, t, mb, nb);
-      if (!mbar_wait(&tfull[acc], acc_phase, abort_flag, a.status, a.timeout_ns)) break;
+      // every epilogue thread goes on, or none (named barriers follow)
+      const bool ready = mbar_wait(&tfull[acc], acc_phase, abort_flag, a.status, a.timeout_ns);
+      __syncwarp();
+      if (!named_bar_all(1, kEpiThreads, ready)) break;
       tc_fence_after();
       const int row_base = mb * C::kTileRows + (int)rank * kBM;
       const int64_t grow = (int64_t)row_base + row;       // output row of this thread

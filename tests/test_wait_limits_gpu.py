@@ -51,7 +51,7 @@ for _ in range(2):
 """
 
 
-@pytest.mark.parametrize("op", ["linear", "up", "down"])
+@pytest.mark.parametrize("op", ["linear", "up", "down", "tile", "tile_down"])
 def test_given_up_waits_end_the_call(cuda_lib, op):
     env = dict(os.environ, SWIGLU_WAIT_TIMEOUT_MS="1", SWIGLU_GR_CUT="0", SWIGLU_TILE_SK="0")
     r = subprocess.run([sys.executable, "-c", CHILD, op], cwd=ROOT, env=env, capture_output=True,
