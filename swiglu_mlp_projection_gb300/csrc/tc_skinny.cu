@@ -453,7 +453,9 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
     float* xb = reinterpret_cast<float*>(stages);
-    if (mbar_wait(&tfull[0], 0, abort_flag, a.status, a.timeout_ns)) {
+    // (tcgen05.ld takes whole warps: a warp waited to the end, or none of it did)
+    const bool ready = mbar_wait(&tfull[0], 0, abort_flag, a.status, a.timeout_ns);
+    if (__all_sync(0xffffffffu, ready)) {
       tc_fence_after();
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -484,7 +486,10 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
     while (t < u1) {
       const int64_t cg = t / a.n_kb;
       const int64_t seg_end = min(u1, (cg + 1) * (int64_t)a.n_kb);
-      if (!mbar_wait(&tfull[acc], acc_phase, abort_flag, a.status, a.timeout_ns)) break;
+      // every epilogue thread goes on, or none (named barriers follow)
+      const bool ready = mbar_wait(&tfull[acc], acc_phase, abort_flag, a.status, a.timeout_ns);
+      __syncwarp();
+      if (!named_bar_all(1, kEpiThreads, ready)) break;
       tc_fence_after();
       const int64_t c_lo = cta_of(cg * a.n_kb, U, G);
       const int64_t c_hi = cta_of((cg + 1) * a.n_kb - 1, U, G);

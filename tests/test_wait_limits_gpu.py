@@ -1,5 +1,5 @@
 """Waits that run out in the kernels themselves: with a limit of 1 ms, a call
-whose one unit of work sums over 2^21 products gives up waiting for it.  The
+whose units of work sum over a million products gives up waiting for them.  The
 call has to end, report a timeout, and leave the next calls right.  (The limit
 is read once per process, so the calls run in one of their own.)"""
 import os
@@ -27,6 +27,9 @@ def call(rows, K):
     if op == "tile":
         w = ones(K, 128)
         return swg.swiglu_up(ones(rows, K), w, w, path="tc")
+    if op in ("cluster", "stream"):      # 1 row; 6250 k blocks per CTA
+        n = 64 if op == "cluster" or K < 1024 else 1856
+        return swg.swiglu_up(ones(1, K), ones(K, n), ones(K, n), path="skinny")
     if op == "tile_down":
         return swg.swiglu_down(ones(rows, K), ones(K, 256), path="tc")
     rt = swg.dispatch(torch.zeros(rows, 1, device=dev, dtype=torch.int32), 1,
@@ -51,9 +54,11 @@ for _ in range(2):
 """
 
 
-@pytest.mark.parametrize("op", ["linear", "up", "down", "tile", "tile_down"])
+@pytest.mark.parametrize("op", ["linear", "up", "down", "tile", "tile_down", "cluster",
+                                "stream"])
 def test_given_up_waits_end_the_call(cuda_lib, op):
-    env = dict(os.environ, SWIGLU_WAIT_TIMEOUT_MS="1", SWIGLU_GR_CUT="0", SWIGLU_TILE_SK="0")
+    env = dict(os.environ, SWIGLU_WAIT_TIMEOUT_MS="1", SWIGLU_GR_CUT="0", SWIGLU_TILE_SK="0",
+               SWIGLU_SK_CLUSTER="2" if op == "cluster" else "0")
     r = subprocess.run([sys.executable, "-c", CHILD, op], cwd=ROOT, env=env, capture_output=True,
                        text=True, timeout=100)
     assert r.returncode == 0, r.stderr
