@@ -220,6 +220,13 @@ __device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity, unsig
   return mbar_wait(bar, parity, &never, status, timeout_ns);
 }
 
+// Lets a producer's loads land (those of the last round of the ring; earlier
+// ones have been waited for).
+__device__ __forceinline__ void drain_loads(uint64_t* full, int64_t issued, const Args& a) {
+  for (int64_t i = issued > a.stages ? issued - a.stages : 0; i < issued; ++i)
+    wait_drain(&full[i % a.stages], (uint32_t)((i / a.stages) & 1), a.status, a.timeout_ns);
+}
+
 // act(v).  f32 outputs use the accurate functions; bf16 outputs the fast
 // exponential and divide, whose error (about 2^-21 of the value) is far below
 // the half ulp (2^-9) of the rounding that follows.
@@ -467,12 +474,12 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
   if (MODE == kGroupedPlain && blockIdx.x == 0 && threadIdx.x == 32)
     *a.sched = make_uint4(sch.units, sch.whole, sch.cut_iters, sch.q);
 
+  int64_t issued = 0;   // a producer's stages
   if (warp == 0) {
     // ---------------- weights (TMA, one thread of each CTA) ----------------
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      int64_t issued = 0;
       bool ok = !skip;
       WorkIter w(sch, pair);
       uint32_t u;
@@ -510,12 +517,6 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
       // K = 14336, N = 4096: 26.6 us per call, 28.7 with its 32 joining blocks
       // placed at once, on the two SMs that have no work.)
       if (late) pdl_launch_dependents();
-      if (issued > 0 && !ok) {
-        // let the loads still in flight land before the CTA can exit
-        const int64_t first = issued > a.stages ? issued - a.stages : 0;
-        for (int64_t i = first; i < issued; ++i)
-          wait_drain(&full[i % a.stages], (uint32_t)((i / a.stages) & 1), a.status, a.timeout_ns);
-      }
     }
     __syncwarp();
   } else if (warp >= kRowWarp) {
@@ -588,7 +589,6 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
     } else if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      int64_t issued = 0;
       bool ok = !skip;
       WorkIter w(sch, pair);
       uint32_t u;
@@ -620,11 +620,6 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
             phase ^= 1u;
           }
         }
-      }
-      if (issued > 0 && !ok) {
-        const int64_t first = issued > a.stages ? issued - a.stages : 0;
-        for (int64_t i = first; i < issued; ++i)
-          wait_drain(&full[i % a.stages], (uint32_t)((i / a.stages) & 1), a.status, a.timeout_ns);
       }
     }
     __syncwarp();
@@ -924,6 +919,12 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
 
   tc_fence_before();
   __syncthreads();
+  // Where a wait has given up, loads may still be in flight, whichever role it
+  // was: they land before the CTA's shared memory goes away.
+  if (*abort_flag) {
+    drain_loads(full, issued, a);
+    __syncwarp();
+  }
   // Neither CTA of a pair leaves (or frees its TMEM) while the other may still
   // signal its barriers or read its shared memory.
   cluster_sync_all();

@@ -313,20 +313,16 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
   pdl_wait();
   pdl_launch_dependents();
 
+  int64_t issued = 0;   // the producer's stages
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (lane == 0) {
       const uint64_t evict_first = policy_evict_first();
       int stage = 0;
       uint32_t phase = 0;
-      int64_t issued = 0;
-      bool ok = true;
       for (int64_t t = u0; t < u1; ++t) {
         const int cg = (int)(t / a.n_kb), kbu = (int)(t - (int64_t)cg * a.n_kb);
-        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.status, a.timeout_ns)) {
-          ok = false;
-          break;
-        }
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.status, a.timeout_ns)) break;
         uint8_t* st = stages + (size_t)stage * C::kStageBytes;
         // k blocks of this unit inside K (a unit of KB > 1 blocks may end past it)
         const int nkb = KB > 1 ? min(KB, a.k64 - kbu * KB) : 1;
@@ -358,13 +354,6 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
           stage = 0;
           phase ^= 1u;
         }
-      }
-      if (!ok) {
-        // let the copies already issued land before the CTA's memory goes away
-        const int64_t first = issued > C::kStages ? issued - C::kStages : 0;
-        for (int64_t i = first; i < issued; ++i)
-          wait_drain(&full[i % C::kStages], (uint32_t)((i / C::kStages) & 1), a.status,
-                     a.timeout_ns);
       }
     }
     __syncwarp();
@@ -783,6 +772,13 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap tm_x,
 
   tc_fence_before();
   __syncthreads();
+  // Where a wait has given up, loads may still be in flight, whichever role it
+  // was: they land before the CTA's shared memory goes away.
+  if (*abort_flag) {
+    for (int64_t i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
+      wait_drain(&full[i % C::kStages], (uint32_t)((i / C::kStages) & 1), a.status, a.timeout_ns);
+    __syncwarp();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);

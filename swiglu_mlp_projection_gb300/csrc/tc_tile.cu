@@ -249,12 +249,12 @@ tile_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
   pdl_wait();
   pdl_launch_dependents();
 
+  int64_t issued = 0;   // the producer's stages
   if (warp == 0) {
     // ---------------- TMA producer (each CTA) ----------------
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      int64_t issued = 0;
       bool ok = !skip;
       WorkIter w(a, unit);
       int64_t t;
@@ -309,12 +309,6 @@ tile_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
             phase ^= 1u;
           }
         }
-      }
-      if (issued > 0 && !ok) {
-        // let the loads still in flight land before the CTA can exit
-        const int64_t first = issued > kStages ? issued - kStages : 0;
-        for (int64_t i = first; i < issued; ++i)
-          wait_drain(&full[i % kStages], (uint32_t)((i / kStages) & 1), a.status, a.timeout_ns);
       }
     }
     __syncwarp();
@@ -641,6 +635,13 @@ tile_tc_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__
 
   tc_fence_before();
   __syncthreads();
+  // Where a wait has given up, loads may still be in flight, whichever role it
+  // was: they land before the CTA's shared memory goes away.
+  if (*abort_flag) {
+    for (int64_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+      wait_drain(&full[i % kStages], (uint32_t)((i / kStages) & 1), a.status, a.timeout_ns);
+    __syncwarp();
+  }
   // Neither CTA of a pair leaves (or frees its TMEM) while the other may still
   // signal its barriers or read its shared memory.
   if constexpr (PAIR) cluster_sync_all();
