@@ -145,11 +145,12 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// (acquires at cluster scope: a stage's other half is the other CTA's)
 __device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
@@ -412,6 +413,7 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile unsigned* ticket_slot = reinterpret_cast<volatile unsigned*>(tmem_slot + 2);
+  uint32_t* half_slot = tmem_slot + 3;   // where rank 1's word about a stage is stored
   int* s_row = reinterpret_cast<int*>(tmem_slot + 4);
   int* s_chunk = s_row + a.E + 1;
 
@@ -423,8 +425,8 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
   if (threadIdx.x == 0) {
     // A stage is full once the weight box, this CTA's rows (one TMA arrival,
     // or one per gathering thread) and, on rank 0, rank 1's word that its
-    // half has landed have arrived.
-    const uint32_t arrivals = 1u + (GATHER ? (uint32_t)kGatherThreads : 1u) + (rank == 0 ? 1u : 0u);
+    // half has landed (4 bytes) have arrived.
+    const uint32_t arrivals = 1u + (GATHER ? (uint32_t)kGatherThreads : 1u);
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(&full[s], arrivals);
       mbar_init(&empty[s], 1);
@@ -495,7 +497,7 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
             break;
           }
           uint8_t* st = stages + (size_t)stage * a.stage_bytes;
-          mbar_arrive_expect_tx(&full[stage], kABytes);
+          mbar_arrive_expect_tx(&full[stage], kABytes + (rank == 0 ? 4u : 0u));
           if (a.kmajor) {
             tma_load_3d(st, &tm_wa, &full[stage], kb * kBK, ca, un.e);
             // (one 128-column box where the columns are neighbours)
@@ -693,8 +695,15 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- rank 1: tell rank 0 when this CTA's half has landed ----------------
+    // Gathered rows were written by this CTA's threads (cp.async, the generic
+    // proxy), and rank 0's MMAs read them, so the word has to release at
+    // cluster scope.  The completion of an asynchronous store does, and its
+    // issue does not wait for that (64 experts' up projection of 4096 tokens
+    // 193.1 us, 192.5 with an arrival that releases at CTA scope; an arrival
+    // that releases at cluster scope holds the thread: 632 us).
     if (lane == 0) {
       const uint32_t full0 = mapa_shared(smem_u32(full), 0u);
+      const uint32_t slot0 = mapa_shared(smem_u32(half_slot), 0u);
       int stage = 0;
       uint32_t phase = 0;
       bool ok = !skip;
@@ -708,7 +717,7 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
             break;
           }
           if constexpr (GATHER) fence_async_smem();
-          mbar_arrive_remote(full0 + (uint32_t)stage * 8u);
+          st_async_u32(slot0, 1u, full0 + (uint32_t)stage * 8u);
           if (++stage == a.stages) {
             stage = 0;
             phase ^= 1u;
@@ -920,9 +929,14 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   // Where a wait has given up, loads may still be in flight, whichever role it
-  // was: they land before the CTA's shared memory goes away.
+  // was: they land before the CTA's shared memory goes away.  So do rank 1's
+  // words that rank 0 no longer waits for: rank 1 lets 100 us pass after its
+  // last one, and rank 0 stays until then.  (Where rank 0 gives up before its
+  // last MMA, so does rank 1's epilogue.)
   if (*abort_flag) {
     drain_loads(full, issued, a);
+    const uint64_t t0 = globaltimer_ns();
+    while (rank == 1 && globaltimer_ns() - t0 < 100000u) __nanosleep(1000);
     __syncwarp();
   }
   // Neither CTA of a pair leaves (or frees its TMEM) while the other may still
