@@ -228,19 +228,27 @@ __device__ __forceinline__ void drain_loads(uint64_t* full, int64_t issued, cons
     wait_drain(&full[i % a.stages], (uint32_t)((i / a.stages) & 1), a.status, a.timeout_ns);
 }
 
-// act(v).  f32 outputs use the accurate functions; bf16 outputs the fast
-// exponential and divide, whose error (about 2^-21 of the value) is far below
-// the half ulp (2^-9) of the rounding that follows.
-// tanh form: 0.5 v (1 + tanh z) = v sigma(2 z), z = sqrt(2 / pi) (v + 0.044715 v^3).
+// v sigma(z).  For z < 0 it is v e^z / (1 + e^z): 1 + e^-z ends at z = -88.7,
+// where v e^z is still a normal number.  The accurate functions serve f32
+// outputs.  bf16 outputs take the fast exponential and divide: the error of
+// the exponential grows with |z|, to 2^-16 of the value where e^z ends, well
+// below the half ulp (2^-9) of the rounding that follows.
+template <bool ACCURATE>
+__device__ __forceinline__ float times_sigma(float v, float z) {
+  const float e = ACCURATE ? expf(-fabsf(z)) : __expf(-fabsf(z));
+  const float n = z >= 0.f ? v : v * e;
+  return ACCURATE ? n / (1.0f + e) : __fdividef(n, 1.0f + e);
+}
+
+// act(v).  tanh form: 0.5 v (1 + tanh z) = v sigma(2 z),
+// z = sqrt(2 / pi) (v + 0.044715 v^3).
 template <int ACT, bool ACCURATE>
 __device__ __forceinline__ float activate(float v) {
   if constexpr (ACT == kActRelu) return v > 0.f ? v : (v != v ? v : 0.f);
-  if constexpr (ACT == kActSilu) return ACCURATE ? silu_accurate(v) : silu_fast(v);
+  if constexpr (ACT == kActSilu) return times_sigma<ACCURATE>(v, v);
   if constexpr (ACT == kActGelu) return 0.5f * v * erfcf(-0.70710678118654752f * v);
-  if constexpr (ACT == kActGeluTanh) {
-    const float z2 = 1.5957691216057308f * (v + 0.044715f * v * v * v);
-    return ACCURATE ? v / (1.0f + expf(-z2)) : __fdividef(v, 1.0f + __expf(-z2));
-  }
+  if constexpr (ACT == kActGeluTanh)
+    return times_sigma<ACCURATE>(v, 1.5957691216057308f * (v + 0.044715f * v * v * v));
   return v;
 }
 
@@ -851,7 +859,7 @@ grouped_tc_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ 
             const float other = take[i * 64];
             const float g = is_up ? other : v[i];
             const float up = is_up ? v[16 + i] : other;
-            hrow[i * kHCols] = cvt_bf16(silu_fast(g) * up);
+            hrow[i * kHCols] = cvt_bf16(times_sigma<false>(g, g) * up);
           }
           named_bar_sync(gbar, kEpiThreads);
 #pragma unroll
