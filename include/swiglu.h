@@ -352,10 +352,11 @@ SWIGLU_API size_t swiglu_linear_workspace_bytes(int64_t M, int64_t K, int64_t N)
  *             index                                              [T, k]
  *     weights s of those, divided by their sum if `renormalize`, times `scale`
  *
- * Softmax runs over all of the token's experts, whatever the groups.  An
- * expert whose logit is -inf or NaN, or whose v is, is masked: it is never
- * chosen and has score 0 in the softmax.  Where fewer than k experts are
- * candidates, the rest of the row has id -1 and weight 0.
+ * Softmax runs over all of the token's experts, whatever the groups and the
+ * bias.  An expert whose logit is -inf or NaN is masked: it is never chosen and
+ * has score 0 in the softmax.  One whose bias makes v -inf or NaN is never
+ * chosen either, but keeps its share of the softmax.  Where fewer than k
+ * experts are candidates, the rest of the row has id -1 and weight 0.
  *
  * offsets, order, position (all three, or all NULL): the choices sorted by
  * expert, as swiglu_dispatch writes them.
@@ -410,7 +411,11 @@ SWIGLU_API size_t swiglu_experts_up_workspace_bytes(int64_t T, int64_t k, int64_
  *
  * The products of each row, and the sum over j (ascending, from the
  * residual), are f32; y is rounded once.  Two kernels; the rows' products
- * stay in the workspace in between.  workspace, errors as swiglu_experts_up.
+ * stay in the workspace in between, T k d f32 of it (537 MB for 4096 tokens,
+ * k = 8, d = 4096).  Above 256 MB a call without a workspace of its own
+ * allocates them from the library's pool, which keeps the memory until
+ * swiglu_release_workspaces; a captured call keeps its slice as long as the
+ * process (see swiglu_up).  workspace, errors as swiglu_experts_up.
  */
 SWIGLU_API int swiglu_experts_down(const void* h, const void* w_down, const int32_t* offsets,
                                    const int32_t* position, const float* weights,

@@ -36,7 +36,12 @@ struct Unit {
 };
 
 // A partial wave of at most three quarters of the pairs is cut: above that,
-// sharing the units out evenly saves less than adding the shares costs.
+// sharing the units out evenly saves less than adding the shares costs (64
+// units on 76 pairs, cut against whole: linear K = 4096, M = 8 26.6 / 24.9 us,
+// M = 256 45.7 / 32.5; one token's up projection 20.4 / 16.2).  Below it, short
+// chunks gain (40 units: M = 8 18.2 / 21.9, M = 64 22.4 / 25.0) and the longest
+// would do without from half the pairs up (50 units: M = 8 22.0 / 22.3, M = 64
+// 25.6 / 25.4, M = 256 39.0 / 29.6).
 __host__ __device__ inline Schedule make_schedule(const Work& w, uint32_t chunks, uint32_t pairs) {
   Schedule s;
   s.units = chunks * (uint32_t)w.ncg;

@@ -625,7 +625,8 @@ cudaError_t launch_scatter(const SortArgs& so, unsigned grid, cudaStream_t st) {
 }
 
 cudaError_t launch_scatter(const SortArgs& so, unsigned grid, cudaStream_t st) {
-  if (so.R <= 256) return launch_scatter<kFewThreads>(so, grid, st);   // (one block)
+  // (one block of given choices; 2 to 16 where 17 to 256 tokens were routed)
+  if (so.R <= 256) return launch_scatter<kFewThreads>(so, grid, st);
   return block_threads(so.E) == 1024 ? launch_scatter<1024>(so, grid, st)
                                      : launch_scatter<512>(so, grid, st);
 }
