@@ -184,24 +184,17 @@ def dispatch(ids, n_experts, weights=None, stream=None):
     return Routing(ids, weights, offsets, order, position)
 
 
-def _check_routing(torch, r):
-    """(device, T, k, E, addresses of offsets, order, position, weights), checked
-    in every call: a tensor's storage and sizes can change between two calls."""
-    i32, position = torch.int32, r.position
-    index = _first(position, "routing.position", i32)
-    if position.dim() != 2 or r.offsets.dim() != 1 or r.offsets.shape[0] < 2:
+def _routing_of(r, E, index):
+    """(T, k, address of offsets) of a routing over E experts on device `index`.
+    Every call reads the tensors anew (and checks those that it uses): their
+    storage and sizes can change between two calls."""
+    shape = r.position.shape
+    if len(shape) != 2 or r.offsets.dim() != 1:
         raise ValueError("expected position [T, k] and offsets [E + 1] in the routing")
-    T, k = position.shape
-    po = _check(r.offsets, "routing.offsets", index, i32)
-    pr = _check(r.order, "routing.order", index, i32)
-    if r.order.shape != (T * k,):
-        raise ValueError("expected order [T k] = [%d] in the routing" % (T * k))
-    pw = None
-    if r.weights is not None:
-        pw = _check(r.weights, "routing.weights", index, torch.float32)
-        if r.weights.shape != (T, k):
-            raise ValueError("expected weights [T, k] in the routing")
-    return index, T, k, r.offsets.shape[0] - 1, po, pr, position.data_ptr(), pw
+    po = _check(r.offsets, "routing.offsets", index, _torch().int32)
+    if r.offsets.numel() != E + 1:
+        raise ValueError("the routing is of %d experts, not %d" % (r.offsets.numel() - 1, E))
+    return shape[0], shape[1], po
 
 
 def experts_up(x, w_gate, w_up, routing, out=None, layout="kn", workspace=None, stream=None):
@@ -222,10 +215,13 @@ def experts_up(x, w_gate, w_up, routing, out=None, layout="kn", workspace=None, 
         raise ValueError("expected x [T, d] and w_gate, w_up [E, d, d_ff] or [E, d_ff, d]")
     T, d = x.shape
     E, d_ff = w_gate.shape[0], w_gate.shape[2 - lay]
-    rdev, rT, k, rE, po, pr, _, _ = _check_routing(torch, routing)
-    if rT != T or rE != E or rdev != index:
-        raise ValueError("the routing is of %d tokens and %d experts on device %d, not %d, %d, %d"
-                         % (rT, rE, rdev, T, E, index))
+    rT, k, po = _routing_of(routing, E, index)
+    if rT != T:
+        raise ValueError("the routing is of %d tokens, not %d" % (rT, T))
+    order = routing.order
+    pr = _check(order, "routing.order", index, torch.int32)
+    if order.dim() != 1 or order.numel() != T * k:
+        raise ValueError("expected order [T k] = [%d] in the routing" % (T * k))
     out = _out(torch, out, (T * k, d_ff), bf16, index, x.device, stream)
     ws, nws = _workspace(workspace, index)
     _call(index, _lib.load().swiglu_experts_up, x.data_ptr(), pg, pu, po, pr, out.data_ptr(), T, k,
@@ -251,11 +247,14 @@ def experts_down(h, w_down, routing, residual=None, out=None, layout="kn", works
         raise ValueError("expected h [T k, d_ff] and w_down [E, d_ff, d] or [E, d, d_ff]")
     d_ff = h.shape[1]
     E, d = w_down.shape[0], w_down.shape[2 - lay]
-    rdev, T, k, rE, po, _, pp, pt = _check_routing(torch, routing)
-    if rE != E or rdev != index:
-        raise ValueError("the routing is of %d experts on device %d, not %d, %d"
-                         % (rE, rdev, E, index))
-    if pt is None and T * k > 0:
+    T, k, po = _routing_of(routing, E, index)
+    pp = _check(routing.position, "routing.position", index, torch.int32)
+    weights, pt = routing.weights, None
+    if weights is not None:
+        pt = _check(weights, "routing.weights", index, torch.float32)
+        if weights.shape != routing.position.shape:
+            raise ValueError("expected weights [T, k] in the routing")
+    elif T * k > 0:
         raise ValueError("the routing needs weights")
     if h.shape[0] != T * k:
         raise ValueError("h has %d rows, the routing %d" % (h.shape[0], T * k))
