@@ -15,9 +15,9 @@
 //
 // Orientation: the weights are the MMA's A operand and the rows its B operand
 // (D^T = W^T x^T), because the count of rows varies from one to thousands and
-// N takes any multiple of 32, where M is 256.  64 experts of 512 +- 150 rows
-// would leave about a quarter of 256-row tiles empty; chunks of up to 256 rows,
-// rounded to 32, leave 6 %.
+// N takes any multiple of 32, where M is 256.  64 experts of 512 rows on
+// average, unevenly loaded, would leave 20 % of 256-row tiles empty; chunks of
+// up to 256 rows, rounded to 32, leave 7 %.
 //
 // A pair (cta_group::2) computes 256 rows of W^T times N <= 256 rows of x;
 // each CTA stages 128 weight columns and half of the x rows per 64-deep k
@@ -36,17 +36,21 @@
 // at M = 4096, K = 4096, N = 64; the join takes 4.)  The up projection's longer
 // chunks are not cut.  No output depends on an order of arrival.
 //
-// What bounds it, on a GB300 (6785 GB/s copy, 1878 TFLOP/s bf16):
-//   few rows: HBM.  8 experts of d = 4096, d_ff = 14336, 32 tokens: 264 us for
-//   1.88 GB (7.1 TB/s).  8 of 64 experts of d = 2048, d_ff = 1024 (67 MB, one
+// What bounds it, on a GB300 (6785 GB/s copy, 1878 TFLOP/s bf16 in a library
+// product), replayed from a graph in bursts of a few ms:
+//   few rows: HBM.  8 experts of d = 4096, d_ff = 14336, 32 tokens: 269 us for
+//   1.88 GB (7.0 TB/s).  8 of 64 experts of d = 2048, d_ff = 1024 (67 MB, one
 //   token): 16.3 us, 10 of them streaming, the rest the chain from the previous
 //   kernel's end through offsets, order, rows and the first stages;
 //   many rows: the MMAs, once operands arrive at 32 KB per CTA and k block:
-//   one group, 4096 rows, d = 4096, d_ff = 14336 476 us (2020 TFLOP/s); 64
-//   experts of 512 rows on average 190 us (1450 TFLOP/s: 11 % of the MMA
-//   columns are chunks short of 256 rows, the last wave is half empty); 8
-//   experts, K = 14336: 640 us (1500 TFLOP/s), bound by operand delivery (the
-//   loads alone take 0.36 us per k block there, 0.24 at K = 4096).
+//   one group, 4096 rows, d = 4096, d_ff = 14336 478-491 us (1960-2010 TFLOP/s);
+//   64 experts of 512 rows on average 189-195 us (1420 TFLOP/s: chunks have 220
+//   columns on average, 7 % of them padding, and the last wave is not full); 8
+//   experts, K = 14336: 700 us with the weighted sum (1370 TFLOP/s), 622 for the
+//   product alone under a profiler, the tensor pipe active 89 % of it at the
+//   power cap's clock (the loads alone take 0.36 us per k block there, 0.24 at
+//   K = 4096).  In loops of seconds the cap's clock (1540 MHz) bounds the others
+//   too: 224 us for the 64 experts.
 #include <atomic>
 
 #include "common.cuh"
