@@ -324,7 +324,8 @@ enum { SWIGLU_GROUP_MAX = 0,      /* a group's value is its best candidate's    
  * The bias is added to the f32 sum, the activation applied to that, the
  * residual added, and the result rounded once.  K is a multiple of 8, N any
  * number ([K, N] weights with N no multiple of 8 are copied to padded rows in
- * the workspace first, by a kernel of its own).  K == 0 gives
+ * the workspace first, in every call, by a kernel of its own that costs several
+ * times the product of a few rows; [N, K] weights are read as they are).  K == 0 gives
  * act(bias) + residual.  bf16 outputs use the fast exponential;
  * f32 outputs the accurate functions.
  * workspace: as swiglu_up_ex, swiglu_linear_workspace_bytes(M, K, N) bytes

@@ -1019,7 +1019,9 @@ empty_linear_kernel(const void* bias, int bias_f32, int act, const void* resid, 
 }
 
 // [K, N] weights whose rows are no multiple of 16 bytes, copied to rows of
-// round8(N) (zeros behind N), which TMA can read.
+// round8(N) (zeros behind N), which TMA can read.  Element by element, in every
+// call: K = 4096, N = 50257, M = 8 516 us, 74 with N = 50264, 67 with the same
+// weights as [N, K].
 __global__ void __launch_bounds__(256)
 pad_rows_kernel(const uint16_t* __restrict__ w, uint16_t* __restrict__ out, int64_t K, int64_t N,
                 int64_t Np) {

@@ -26,6 +26,7 @@
 // 67 % busy; the scatter's chain (counts, offsets, places) is L2 latency.  5001
 // tokens, E = 60: 8.6 us, latency of the two kernels.  One token: 3.6 us, launch.
 // Reading the next token's row ahead (prefetch) changed nothing: 26.0 us.
+// Dispatch alone: 4096 tokens, k = 8, E = 64 6.5 us, 40000 tokens, E = 256 10.7.
 #include "common.cuh"
 #include "grouped.h"
 #include "tc_common.cuh"
