@@ -55,7 +55,11 @@
 extern "C" {
 #endif
 
-typedef enum { SWIGLU_F32 = 0, SWIGLU_BF16 = 1 } swiglu_dtype;
+typedef enum {
+  SWIGLU_F32 = 0,
+  SWIGLU_BF16 = 1,
+  SWIGLU_E4M3 = 2   /* codes, with an f32 scale per row: swiglu_permute only */
+} swiglu_dtype;
 
 typedef enum {
   SWIGLU_OK = 0,
@@ -253,6 +257,19 @@ SWIGLU_API int swiglu_up_fp8(const void* x, const void* w8_gate, const void* w8_
 SWIGLU_API size_t swiglu_fp8_workspace_bytes(int64_t M, int64_t d, int64_t d_ff, int path);
 
 /*
+ * As swiglu_up_fp8, for rows that are quantized already (by
+ * swiglu_rms_norm_fp8, say): x8 e4m3 codes [M, d] and s_x their f32 row scales
+ * [M]; row i stands for x8[i] * s_x[i].  The same codes and scales give the
+ * bits that swiglu_up_fp8 gives.  A caller workspace of
+ * swiglu_fp8_workspace_bytes is enough (it holds no codes here).  No
+ * counterpart in the pages.
+ */
+SWIGLU_API int swiglu_up_fp8_rows(const void* x8, const float* s_x, const void* w8_gate,
+                                  const void* w8_up, const float* s_gate, const float* s_up,
+                                  void* h, int64_t M, int64_t d, int64_t d_ff, int path,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * The same FP8 contract for the down projection y = h . W_down (+ residual)
  * ("1 . Anatomie d'un transformeur sur GPU", section 1.6, kernels #10 and
  * #11): h [M, d_ff] bf16 is quantized per row inside the call, W_down once
@@ -425,6 +442,98 @@ SWIGLU_API int swiglu_experts_down(const void* h, const void* w_down, const int3
                                    size_t workspace_bytes, void* stream);
 SWIGLU_API size_t swiglu_experts_down_workspace_bytes(int64_t T, int64_t k, int64_t E,
                                                       int64_t d_ff, int64_t d);
+
+/*
+ * The norm that begins an MLP block ("1 . Anatomie d'un transformeur sur GPU",
+ * section 1.1, the RMSNorm before "Wgate, Wup"), with the residual's addition
+ * that precedes it:
+ *
+ *     s = x + residual                                     (s = x without one)
+ *     y = s / sqrt(mean(s^2) + eps) * weight               mean over the row
+ *
+ *     x, residual, s (`sum`), y [M, d] f32 or bf16 (dtype); weight [d] f32 or
+ *     bf16 (weight_dtype); eps > 0
+ *
+ * f32 throughout, from the operands on: y is computed from the sum before it is
+ * rounded, and s and y are each rounded once.  Squares are summed in f32, so
+ * values up to about 1e16 are served.  residual and sum are both given or both
+ * NULL.  y and sum may each be x or residual itself (not both the same one),
+ * and overlap nothing else.  Rows are dense; d is any number up to 32768 (up to
+ * 32752 if it is no multiple of 8, f32: 4).
+ * A row that holds an infinity or NaN gives NaN where it matters and no other
+ * row anything.  Errors: SWIGLU_ERR_INVALID_ARG, _UNSUPPORTED, _ALIGNMENT,
+ * _ARCH, _CUDA.
+ *
+ * swiglu_rms_norm_fp8: the same with y in e4m3, quantized per row as
+ *   swiglu_up_fp8 quantizes x, from the f32 values: codes [M, d], scales [M]
+ *   f32, y = codes * scales with scale = amax / 448, amax = max |y| of the row.
+ *   A row of zeros (and one whose values before the division by the root stay
+ *   below 2^-118) has scale 0; one with an infinity or NaN, scale NaN.  codes
+ *   and scales overlap nothing.
+ */
+SWIGLU_API int swiglu_rms_norm(const void* x, const void* residual, const void* weight, void* y,
+                               void* sum, int64_t M, int64_t d, float eps, int dtype,
+                               int weight_dtype, void* stream);
+SWIGLU_API int swiglu_rms_norm_fp8(const void* x, const void* residual, const void* weight,
+                                   void* codes, float* scales, void* sum, int64_t M, int64_t d,
+                                   float eps, int dtype, int weight_dtype, void* stream);
+
+/*
+ * The norm's gradient, at s (swiglu_rms_norm's sum, or x without a residual):
+ *
+ *     r = 1 / sqrt(mean(s^2) + eps),  g = dy * weight
+ *     dx = ds + r (g - s r^2 mean(g s))        the gradient of x and of residual
+ *     dweight = sum over the rows of dy s r
+ *
+ *     dy, s, ds, dx [M, d] (dtype); ds, the gradient that reaches s past the
+ *     norm, or NULL; dx may be dy, s or ds itself; dweight [d] (weight_dtype)
+ *
+ * f32 sums in a fixed order (dweight's by the CTAs' rows, then over the CTAs);
+ * each output is rounded once.  M == 0 gives dweight = 0.  Two kernels.  It
+ * serves swiglu_rms_norm_fp8 too, where the quantization counts as the
+ * identity.  workspace: as swiglu_up_ex, of
+ * swiglu_rms_norm_backward_workspace_bytes(M, d, dtype), or NULL for the
+ * library's own.  Errors as swiglu_rms_norm, _WORKSPACE, _OOM.
+ */
+SWIGLU_API int swiglu_rms_norm_backward(const void* dy, const void* s, const void* weight,
+                                        const void* ds, void* dx, void* dweight, int64_t M,
+                                        int64_t d, float eps, int dtype, int weight_dtype,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+SWIGLU_API size_t swiglu_rms_norm_backward_workspace_bytes(int64_t M, int64_t d, int dtype);
+
+/*
+ * Rows sorted by expert and back, for experts other than the SwiGLU ones above
+ * (which gather and sum rows themselves) and for training.  position and
+ * offsets are those of swiglu_route or swiglu_dispatch; T tokens, k <= 32
+ * choices each, E <= 1024 experts, d any number of elements to a row.  Positions
+ * outside 0 ... T k - 1 stand for no place; a routing that these did not write
+ * gives wrong rows, never an access outside the tensors.
+ *
+ * swiglu_permute:  out[position[t, j]] = x[t]; rows from offsets[E] on, which no
+ *   choice has, are zero.  x [T, d], out [T k, d] of f32, bf16 or e4m3 codes
+ *   (dtype; the bits are copied).  With e4m3 the rows' f32 scales [T] go along,
+ *   into out_scales [T k] (zero from offsets[E] on); otherwise both are NULL.
+ *   Its gradient is swiglu_unpermute without weights.
+ * swiglu_unpermute:  y[t] = residual[t] + sum_j weights[t, j] z[position[t, j]].
+ *   z [T k, d], residual (or NULL; may be y itself), y [T, d] f32 or bf16
+ *   (dtype); weights f32 [T, k], or NULL for ones.  Choices without a place add
+ *   nothing, whatever their weight.  f32, j ascending from the residual, rounded
+ *   once.
+ * swiglu_unpermute_backward:  dz[position[t, j]] = weights[t, j] dy[t], zero from
+ *   offsets[E] on; dweights[t, j] = dy[t] . z[position[t, j]] (f32 sums in a
+ *   fixed order), 0 where there is no place.  The residual's gradient is dy.
+ * Errors: SWIGLU_ERR_INVALID_ARG, _UNSUPPORTED, _ALIGNMENT, _ARCH, _CUDA.
+ */
+SWIGLU_API int swiglu_permute(const void* x, const float* scales, const int32_t* position,
+                              const int32_t* offsets, void* out, float* out_scales, int64_t T,
+                              int64_t k, int64_t E, int64_t d, int dtype, void* stream);
+SWIGLU_API int swiglu_unpermute(const void* z, const int32_t* position, const float* weights,
+                                const void* residual, void* y, int64_t T, int64_t k, int64_t d,
+                                int dtype, void* stream);
+SWIGLU_API int swiglu_unpermute_backward(const void* dy, const void* z, const int32_t* position,
+                                         const int32_t* offsets, const float* weights, void* dz,
+                                         float* dweights, int64_t T, int64_t k, int64_t E,
+                                         int64_t d, int dtype, void* stream);
 
 /*
  * As swiglu_up, for callers that cannot allocate device memory.  Some

@@ -5,6 +5,7 @@ The compute path is the CUDA library built from ``csrc/`` (a C ABI declared in
 and the current stream) into it.  The library is loaded on first use and its
 absence is an error: there is no CPU fallback.
 """
+import collections
 import ctypes
 
 from . import _lib
@@ -304,19 +305,36 @@ def fp8_workspace_bytes(M, d, d_ff, path="auto"):
     return n
 
 
+Fp8Rows = collections.namedtuple("Fp8Rows", "codes scales")
+Fp8Rows.__doc__ = """Rows quantized to e4m3: codes [M, d] (uint8) and float32 scales [M]; row i
+stands for codes[i] * scales[i] (``rms_norm_fp8`` and ``permute`` write them)."""
+
+
 def swiglu_up_fp8(x, w, out=None, path="auto", workspace=None, stream=None):
     """h = silu(x @ W_gate) * (x @ W_up) with e4m3 weights ``w`` (an
-    Fp8Weights) and x quantized per row to e4m3 inside the call; x [M, d] and
-    the result [M, d_ff] are bfloat16."""
+    Fp8Weights) and x [M, d]: a bfloat16 tensor, quantized per row to e4m3
+    inside the call, or an Fp8Rows, whose codes are used as they are.  The
+    result [M, d_ff] is bfloat16."""
     global _LIB
-    import torch
-    _check_cuda(x=x)
-    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != w.d:
-        raise ValueError("expected bfloat16 x [M, %d]" % w.d)
+    torch = _TORCH or _torch()
+    rows = isinstance(x, Fp8Rows)
+    if rows:
+        x, scales = x
+        _check_cuda(codes=x, scales=scales)
+        if x.dtype != torch.uint8 or x.dim() != 2 or x.shape[1] != w.d:
+            raise ValueError("expected uint8 codes [M, %d]" % w.d)
+        if scales.dtype != torch.float32 or scales.shape != x.shape[:1]:
+            raise ValueError("expected float32 scales [M] = [%d]" % x.shape[0])
+        if scales.device != x.device:
+            raise ValueError("codes and scales must be on one device")
+    else:
+        _check_cuda(x=x)
+        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != w.d:
+            raise ValueError("expected bfloat16 x [M, %d]" % w.d)
     M = x.shape[0]
     if out is None:
-        out = _empty(torch, (M, w.d_ff), x.dtype, x.device, stream)
-    elif out.shape != (M, w.d_ff) or out.dtype != x.dtype or not out.is_contiguous():
+        out = _empty(torch, (M, w.d_ff), torch.bfloat16, x.device, stream)
+    elif out.shape != (M, w.d_ff) or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out must be a contiguous bfloat16 [M, d_ff] tensor")
     index = x.device.index
     st = stream.cuda_stream if stream is not None else _raw_stream(index)
@@ -325,9 +343,12 @@ def swiglu_up_fp8(x, w, out=None, path="auto", workspace=None, stream=None):
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if _LIB is None:
         _LIB = _lib.load()
-    _call(index, _LIB.swiglu_up_fp8, x.data_ptr(), w.w8_gate.data_ptr(), w.w8_up.data_ptr(),
-          w.s_gate.data_ptr(), w.s_up.data_ptr(), out.data_ptr(), M, w.d, w.d_ff,
-          _path_code(path), ws_ptr, ws_bytes, st)
+    rest = (w.w8_gate.data_ptr(), w.w8_up.data_ptr(), w.s_gate.data_ptr(), w.s_up.data_ptr(),
+            out.data_ptr(), M, w.d, w.d_ff, _path_code(path), ws_ptr, ws_bytes, st)
+    if rows:
+        _call(index, _LIB.swiglu_up_fp8_rows, x.data_ptr(), scales.data_ptr(), *rest)
+    else:
+        _call(index, _LIB.swiglu_up_fp8, x.data_ptr(), *rest)
     return out
 
 
@@ -500,9 +521,13 @@ def version():
 
 from .moe import (Routing, dispatch, experts_down, experts_down_workspace_bytes,  # noqa: E402
                   experts_up, experts_up_workspace_bytes, linear, linear_workspace_bytes,
-                  route, swiglu_moe)
+                  permute, permute_backward, route, swiglu_moe, unpermute, unpermute_backward)
+from .block import (rms_norm, rms_norm_backward, rms_norm_backward_workspace_bytes,  # noqa: E402
+                    rms_norm_fp8, swiglu_block)
 
-__all__ = ["linear", "route", "dispatch", "experts_up", "experts_down", "swiglu_moe", "Routing",
+__all__ = ["rms_norm", "rms_norm_fp8", "rms_norm_backward", "rms_norm_backward_workspace_bytes",
+           "swiglu_block", "Fp8Rows", "permute", "permute_backward", "unpermute",
+           "unpermute_backward", "linear", "route", "dispatch", "experts_up", "experts_down", "swiglu_moe", "Routing",
            "linear_workspace_bytes", "experts_up_workspace_bytes",
            "experts_down_workspace_bytes", "swiglu_up", "swiglu_down", "swiglu_mlp", "workspace_bytes",
            "down_workspace_bytes", "plan", "down_plan", "split_k_slices",

@@ -12,7 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libswiglu_gb300.so")
 
 # swiglu_dtype / swiglu_path / swiglu_status values of include/swiglu.h
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 PATH_AUTO, PATH_SIMT, PATH_SKINNY, PATH_TC = 0, 1, 2, 3
 OK = 0
 STATUS_NAMES = {
@@ -64,6 +64,18 @@ SIGNATURES = {
     "swiglu_experts_down": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int,
                              _vp, _sz, _vp], _int),
     "swiglu_experts_down_workspace_bytes": ([_i64, _i64, _i64, _i64, _i64], _sz),
+    "swiglu_up_fp8_rows": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _sz,
+                            _vp], _int),
+    "swiglu_rms_norm": ([_vp, _vp, _vp, _vp, _vp, _i64, _i64, _flt, _int, _int, _vp], _int),
+    "swiglu_rms_norm_fp8": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _flt, _int, _int, _vp],
+                            _int),
+    "swiglu_rms_norm_backward": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _flt, _int, _int, _vp,
+                                  _sz, _vp], _int),
+    "swiglu_rms_norm_backward_workspace_bytes": ([_i64, _i64, _int], _sz),
+    "swiglu_permute": ([_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp], _int),
+    "swiglu_unpermute": ([_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp], _int),
+    "swiglu_unpermute_backward": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
+                                   _int, _vp], _int),
     "swiglu_down_plan": ([_i64, _i64, _i64, _int, _int, _int, ctypes.POINTER(PlanInfo)], _int),
     "swiglu_workspace_bytes": ([_i64, _i64, _i64, _int, _int], _sz),
     "swiglu_plan": ([_i64, _i64, _i64, _int, _int, _int, ctypes.POINTER(PlanInfo)], _int),

@@ -1,8 +1,7 @@
 // C ABI of the mixture-of-experts operators and the general linear product:
 // argument checks, workspace, launches.  See include/swiglu.h for the contract
 // of each entry point.
-#include <stdio.h>
-
+#include "api_checks.h"
 #include "grouped.h"
 #include "grouped_plan.cuh"
 #include "internal.h"
@@ -10,43 +9,6 @@
 
 namespace swg {
 namespace {
-
-struct Span {
-  const char* name;
-  const void* p;
-  size_t bytes;
-  unsigned align = 16;   // what the kernels' loads of it need
-};
-
-int failf(int status, const char* fmt, const char* a, const char* b = "") {
-  char text[256];
-  snprintf(text, sizeof text, fmt, a, b);
-  return api_fail(status, text);
-}
-
-// Every non-empty tensor has a pointer, aligned as its loads need.
-int check_spans(const Span* s, int n) {
-  for (int i = 0; i < n; ++i) {
-    if (s[i].bytes && !s[i].p)
-      return failf(SWIGLU_ERR_INVALID_ARG, "null pointer for a non-empty tensor (%s)", s[i].name);
-    if ((uintptr_t)s[i].p & (s[i].align - 1))
-      return failf(SWIGLU_ERR_ALIGNMENT, "%s must be %s-byte aligned", s[i].name,
-                   s[i].align == 16 ? "16" : s[i].align == 4 ? "4" : "2");
-  }
-  return SWIGLU_OK;
-}
-
-bool overlap(const Span& a, const Span& b) {
-  if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
-  const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-  return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-int check_apart(const Span& out, const Span* s, int n) {
-  for (int i = 0; i < n; ++i)
-    if (overlap(out, s[i])) return failf(SWIGLU_ERR_INVALID_ARG, "%s overlaps %s", out.name, s[i].name);
-  return SWIGLU_OK;
-}
 
 // Sizes of a product: within 31 bits, rows on 16-byte boundaries.
 // (any_n: N may be any number, see swiglu_linear)
@@ -81,8 +43,6 @@ int check_layout(int layout) {
 }
 
 int wlayout_of(int layout) { return layout == SWIGLU_WEIGHTS_NK ? kWeightsNK : kWeightsKN; }
-
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // The shares of cut units, and 256 bytes for the schedule.
 size_t part_region(const GroupedPlan& p) { return round256(p.part_bytes) + 256; }

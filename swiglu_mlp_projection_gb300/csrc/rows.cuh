@@ -1,0 +1,153 @@
+// Device helpers of the row operators: 16-byte pieces of bf16 or f32 rows.
+#pragma once
+
+#include <stdint.h>
+
+#include "common.cuh"
+#include "tc_common.cuh"
+
+namespace swg {
+
+template <bool F32> struct Row;
+template <> struct Row<true> {
+  using elem = float;
+  static constexpr int kVec = 4;   // elements of 16 bytes
+};
+template <> struct Row<false> {
+  using elem = uint16_t;
+  static constexpr int kVec = 8;
+};
+
+// (the instruction rounds to nearest even and keeps NaN)
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float elem_f32(float v) { return v; }
+__device__ __forceinline__ float elem_f32(uint16_t v) { return bf16_lo(v); }
+__device__ __forceinline__ void set_elem(float* p, float v) { *p = v; }
+__device__ __forceinline__ void set_elem(uint16_t* p, float v) { *p = (uint16_t)bf16x2(v, 0.f); }
+
+template <bool F32>
+__device__ __forceinline__ void unpack(const uint4& q, float (&v)[Row<F32>::kVec]) {
+  if constexpr (F32) {
+    v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
+    v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
+  } else {
+    v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+    v[4] = bf16_lo(q.z); v[5] = bf16_hi(q.z); v[6] = bf16_lo(q.w); v[7] = bf16_hi(q.w);
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ uint4 pack(const float (&v)[Row<F32>::kVec]) {
+  if constexpr (F32)
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+  else
+    return make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                      bf16x2(v[6], v[7]));
+}
+
+// 16 bytes that are read once.  (No .nc: the caller's output may be the input.)
+__device__ __forceinline__ uint4 load_once(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
+// A row of d elements in 16-byte pieces that start on 16-byte boundaries of
+// the tensor, whatever d is: piece i holds the row's elements i * kVec - shift
+// and on, of which those in 0 ... d - 1 are the row's own (the others are its
+// neighbours', and the first and last piece are then moved element by element).
+// Without RAGGED (d a multiple of kVec) shift is 0 and every piece is whole.
+template <bool F32, bool RAGGED>
+struct Pieces {
+  static constexpr int V = Row<F32>::kVec;
+  using E = typename Row<F32>::elem;
+  int64_t first;   // flat index of piece 0's first element
+  int shift, n, d;
+
+  __device__ __forceinline__ Pieces(int64_t row, int d_) : d(d_) {
+    const int64_t base = row * d_;
+    shift = RAGGED ? (int)(base & (V - 1)) : 0;
+    first = base - shift;
+    n = RAGGED ? (shift + d_ + V - 1) / V : d_ / V;
+  }
+  __device__ __forceinline__ int col(int i) const { return i * V - shift; }
+  __device__ __forceinline__ bool whole(int i) const {
+    return !RAGGED || (col(i) >= 0 && col(i) + V <= d);
+  }
+  __device__ __forceinline__ bool has(int i, int e) const {
+    return !RAGGED || (col(i) + e >= 0 && col(i) + e < d);
+  }
+
+  // Piece i of the tensor at `p`; elements that are not the row's are 0.
+  __device__ __forceinline__ uint4 load(const void* p, int i) const {
+    const E* q = (const E*)p + first + (int64_t)i * V;
+    if (whole(i)) return load_once(q);
+    float v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = has(i, e) ? elem_f32(q[e]) : 0.f;
+    return pack<F32>(v);   // (exact: the values are of the type)
+  }
+  __device__ __forceinline__ void store(void* p, int i, const float (&v)[V]) const {
+    E* q = (E*)p + first + (int64_t)i * V;
+    if (whole(i)) {
+      *reinterpret_cast<uint4*>(q) = pack<F32>(v);
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (has(i, e)) set_elem(q + e, v[e]);
+  }
+  // Piece i of a vector [d] of bf16 or f32 values (the norm's weight), 0 past its ends.
+  __device__ __forceinline__ void weight(const void* w, int w_f32, int i, float (&v)[V]) const {
+    if (!RAGGED) {
+      if (w_f32) {
+        const float4* q = reinterpret_cast<const float4*>((const float*)w + i * V);
+#pragma unroll
+        for (int h = 0; h < V / 4; ++h) {
+          const float4 f = q[h];
+          v[4 * h] = f.x; v[4 * h + 1] = f.y; v[4 * h + 2] = f.z; v[4 * h + 3] = f.w;
+        }
+      } else if constexpr (V == 8) {
+        unpack<false>(*reinterpret_cast<const uint4*>((const uint16_t*)w + i * V), v);
+      } else {
+        const uint2 q = *reinterpret_cast<const uint2*>((const uint16_t*)w + i * V);
+        v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+      }
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      v[e] = !has(i, e) ? 0.f
+             : w_f32    ? ((const float*)w)[col(i) + e]
+                        : bf16_lo(((const uint16_t*)w)[col(i) + e]);
+  }
+};
+
+// A launch that may begin while the previous kernel of the stream ends (the
+// kernel waits in pdl_wait before it touches memory).
+template <typename... Params, typename... Args>
+inline cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                                  cudaStream_t st, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
+}  // namespace swg

@@ -714,9 +714,11 @@ struct Call {
   size_t ws_bytes;
   cudaStream_t st;
   int wlayout;   // a WeightLayout: [K, n_out], [n_out, K] (torch.nn.Linear.weight) or packed
-  // FP8 up projection: x is bf16 and is quantized per row to e4m3 in the
-  // workspace; wa, wb are e4m3 codes [n_out, K] with column scales sw_a, sw_b.
+  // FP8: x is bf16 and is quantized per row to e4m3 in the workspace, or, with
+  // row scales sx, holds e4m3 codes already; wa, wb are e4m3 codes [n_out, K]
+  // with column scales sw_a, sw_b.
   bool fp8 = false;
+  const float* sx = nullptr;
   const float* sw_a = nullptr;
   const float* sw_b = nullptr;
 };
@@ -739,7 +741,8 @@ int run(const Call& c) {
     return v;
   if (c.fp8 && p.path == SWIGLU_PATH_SIMT && c.K > 0)
     return fail(SWIGLU_ERR_UNSUPPORTED, "FP8 weights are served by the tensor-core paths only");
-  const size_t fp8_prefix = c.fp8 && p.path != SWIGLU_PATH_SIMT ? fp8_prefix_bytes(c.M, c.K) : 0;
+  const bool codes = c.fp8 && p.path != SWIGLU_PATH_SIMT;   // the kernel reads e4m3 operands
+  const size_t fp8_prefix = codes && !c.sx ? fp8_prefix_bytes(c.M, c.K) : 0;
   p.workspace += fp8_prefix;
   if (c.wlayout == kWeightsNK && p.path == SWIGLU_PATH_SIMT && c.K > 0)
     return fail(SWIGLU_ERR_UNSUPPORTED,
@@ -817,7 +820,7 @@ int run(const Call& c) {
 
   cudaError_t e = cudaSuccess;
   const void* xg = c.x;   // what the GEMM kernels read as x
-  Fp8Scales fs{nullptr, c.sw_a, c.sw_b};
+  Fp8Scales fs{c.sx, c.sw_a, c.sw_b};
   if (fp8_prefix) {
     uint8_t* x8 = (uint8_t*)fp8_base;
     float* sx = (float*)(x8 + ((size_t)c.M * c.K + 255) / 256 * 256);
@@ -826,7 +829,7 @@ int run(const Call& c) {
     xg = x8;
     fs.sx = sx;
   }
-  const Fp8Scales* fsp = fp8_prefix ? &fs : nullptr;
+  const Fp8Scales* fsp = codes ? &fs : nullptr;
   if (p.path == SWIGLU_PATH_SIMT && p.simt.cluster) {
     e = launch_simt_cluster(c.x, c.wa, c.wb, c.out, c.M, c.K, c.n_out, c.dtype, p.simt.cluster,
                             c.wlayout == kWeightsPacked, st);
@@ -880,14 +883,16 @@ int validate_packed(const void* x, const void* wp, const void* h, int64_t M, int
   return SWIGLU_OK;
 }
 
-// x [M, d] bf16, w8 [d_ff, d] e4m3 codes (x2), scales [d_ff] f32 (x2), h [M, d_ff] bf16.
+// x [M, d] bf16 (or e4m3 codes: xbytes 1), w8 [d_ff, d] e4m3 codes (x2), scales [d_ff] f32
+// (x2), h [M, d_ff] bf16.
 int validate_fp8(const void* x, const void* w8g, const void* w8u, const float* sg,
-                 const float* su, const void* h, int64_t M, int64_t d, int64_t d_ff) {
+                 const float* su, const void* h, int64_t M, int64_t d, int64_t d_ff,
+                 int xbytes = 2) {
   int v = check_sizes(M, d, d_ff, SWIGLU_BF16);
   if (v != SWIGLU_OK) return v;
   if (d % 16 != 0)
     return fail(SWIGLU_ERR_ALIGNMENT, "d must be a multiple of 16 for e4m3 rows");
-  const size_t nx = (size_t)M * d * 2, nw = (size_t)d * d_ff, ns = (size_t)d_ff * 4;
+  const size_t nx = (size_t)M * d * xbytes, nw = (size_t)d * d_ff, ns = (size_t)d_ff * 4;
   const size_t nh = (size_t)M * d_ff * 2;
   if ((nx && !x) || (nw && (!w8g || !w8u || !sg || !su)) || (nh && !h))
     return fail(SWIGLU_ERR_INVALID_ARG, "null pointer for a non-empty tensor");
@@ -1165,6 +1170,26 @@ int swiglu_up_fp8(const void* x, const void* w8_gate, const void* w8_up, const f
   Call c{kOpUp, x, w8_gate, w8_up, nullptr, h, M, d, d_ff, SWIGLU_BF16, path, workspace,
          workspace_bytes, (cudaStream_t)stream, kWeightsNK};
   c.fp8 = true;
+  c.sw_a = s_gate;
+  c.sw_b = s_up;
+  return run(c);
+}
+
+int swiglu_up_fp8_rows(const void* x8, const float* s_x, const void* w8_gate, const void* w8_up,
+                       const float* s_gate, const float* s_up, void* h, int64_t M, int64_t d,
+                       int64_t d_ff, int path, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  int v = validate_fp8(x8, w8_gate, w8_up, s_gate, s_up, h, M, d, d_ff, 1);
+  if (v != SWIGLU_OK) return v;
+  if (M > 0 && d > 0 && !s_x)
+    return fail(SWIGLU_ERR_INVALID_ARG, "null pointer for a non-empty tensor");
+  if ((uintptr_t)s_x & 3u) return fail(SWIGLU_ERR_ALIGNMENT, "s_x must be 4-byte aligned");
+  if (overlaps(h, (size_t)M * d_ff * 2, s_x, (size_t)M * 4))
+    return fail(SWIGLU_ERR_INVALID_ARG, "h overlaps an input");
+  Call c{kOpUp, x8, w8_gate, w8_up, nullptr, h, M, d, d_ff, SWIGLU_BF16, path, workspace,
+         workspace_bytes, (cudaStream_t)stream, kWeightsNK};
+  c.fp8 = true;
+  c.sx = s_x;
   c.sw_a = s_gate;
   c.sw_b = s_up;
   return run(c);

@@ -1,7 +1,9 @@
 """The mixture-of-experts MLP and the general linear product (see
 ``include/swiglu.h`` for the exact definitions): ``linear``, ``route``,
 ``dispatch``, ``experts_up``, ``experts_down``, and ``swiglu_moe``, which runs
-them in turn.
+them in turn; and rows sorted by expert and back (``permute``, ``unpermute``,
+their gradients ``permute_backward``, ``unpermute_backward``) for experts of
+another kind.
 
 As the rest of the binding, these only marshal torch tensors into the C ABI;
 calls are asynchronous on torch's current stream (or ``stream``).  What a call
@@ -11,7 +13,7 @@ with a ``stream`` allocates belongs to that stream, as under
 import collections
 
 from . import _lib
-from . import _call, _empty, _raw_stream, _torch
+from . import Fp8Rows, _call, _empty, _raw_stream, _torch
 
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -286,6 +288,135 @@ def swiglu_moe(x, w_router, w_gate, w_up, w_down, k, router_bias=None, residual=
     r = route(logits, k, stream=stream, **routing)
     h = experts_up(x, w_gate, w_up, r, layout=layout, stream=stream)
     return experts_down(h, w_down, r, residual=residual, out=out, layout=layout, stream=stream), r
+
+
+def _sorted_of(r, index):
+    """(T, k, E, address of position, address of offsets) of a routing, read anew
+    as in _routing_of."""
+    i32 = _torch().int32
+    shape = r.position.shape
+    if len(shape) != 2 or r.offsets.dim() != 1 or r.offsets.numel() < 2:
+        raise ValueError("expected position [T, k] and offsets [E + 1] in the routing")
+    return (shape[0], shape[1], r.offsets.numel() - 1,
+            _check(r.position, "routing.position", index, i32),
+            _check(r.offsets, "routing.offsets", index, i32))
+
+
+def _weights_of(r, index):
+    """Address of a routing's weights [T, k] (0 where it has no pair)."""
+    w = r.weights
+    if w is None:
+        if r.position.numel():
+            raise ValueError("the routing needs weights")
+        return None
+    p = _check(w, "routing.weights", index, _torch().float32)
+    if w.shape != r.position.shape:
+        raise ValueError("expected weights [T, k] in the routing")
+    return p
+
+
+def _row_code(torch, t, name):
+    if t.dtype is torch.bfloat16:
+        return _lib.BF16
+    if t.dtype is torch.float32:
+        return _lib.F32
+    raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
+
+
+def permute(x, routing, out=None, stream=None):
+    """The rows of x at their sorted places: result[r] = x[t] for every (token t,
+    expert e) pair r of ``routing``, in its sorted order; rows of dropped
+    choices (at the end) are zero.
+
+    x [T, d] is a contiguous bfloat16 or float32 tensor, or an Fp8Rows (the
+    result is one too: the scales go along).  Returns [T k, d] of x's kind
+    (``out`` if given).
+    """
+    torch = _torch()
+    fp8 = isinstance(x, Fp8Rows)
+    x, scales = x if fp8 else (x, None)
+    index = _first(x, "codes" if fp8 else "x", torch.uint8 if fp8 else None)
+    dt = _lib.E4M3 if fp8 else _row_code(torch, x, "x")
+    if x.dim() != 2:
+        raise ValueError("expected x [T, d]")
+    T, d = x.shape
+    rT, k, E, pp, po = _sorted_of(routing, index)
+    if rT != T:
+        raise ValueError("the routing is of %d tokens, not %d" % (rT, T))
+    ps = pt = None
+    new, new_scales = out if fp8 and out is not None else (out, None)
+    new = _out(torch, new, (T * k, d), x.dtype, index, x.device, stream)
+    if fp8:
+        ps = _check(scales, "scales", index, torch.float32)
+        if scales.dim() != 1 or scales.shape[0] != T:
+            raise ValueError("expected scales [T] = [%d]" % T)
+        new_scales = _out(torch, new_scales, (T * k,), torch.float32, index, x.device, stream)
+        pt = new_scales.data_ptr()
+    _call(index, _lib.load().swiglu_permute, x.data_ptr(), ps, pp, po, new.data_ptr(), pt, T, k, E,
+          d, dt, stream.cuda_stream if stream is not None else _raw_stream(index))
+    return Fp8Rows(new, new_scales) if fp8 else new
+
+
+def _unpermute(z, routing, name, weighted, residual, out, stream):
+    torch = _torch()
+    index = _first(z, name)
+    dt = _row_code(torch, z, name)
+    T, k, _, pp, _ = _sorted_of(routing, index)
+    if z.dim() != 2 or z.shape[0] != T * k:
+        raise ValueError("expected %s [T k, d] with T k = %d" % (name, T * k))
+    d = z.shape[1]
+    pw = _weights_of(routing, index) if weighted else None
+    pr = None
+    if residual is not None:
+        pr = _check(residual, "residual", index, z.dtype)
+        if residual.shape != (T, d):
+            raise ValueError("residual must be [T, d] = [%d, %d]" % (T, d))
+    out = _out(torch, out, (T, d), z.dtype, index, z.device, stream)
+    _call(index, _lib.load().swiglu_unpermute, z.data_ptr(), pp, pw, pr, out.data_ptr(), T, k, d,
+          dt, stream.cuda_stream if stream is not None else _raw_stream(index))
+    return out
+
+
+def unpermute(z, routing, residual=None, out=None, stream=None):
+    """y[t] = residual[t] + sum_j weights[t, j] z[r(t, j)], summed in float32 in
+    the order of j and rounded once.
+
+    z [T k, d], in the routing's sorted order, is a contiguous bfloat16 or
+    float32 tensor; residual [T, d] of its dtype (may be ``out``) or None.
+    Returns y [T, d].
+    """
+    return _unpermute(z, routing, "z", True, residual, out, stream)
+
+
+def permute_backward(dout, routing, residual=None, out=None, stream=None):
+    """The gradient of ``permute``'s x: dx[t] = residual[t] + sum_j dout[r(t, j)],
+    residual being a gradient that reaches x another way, or None."""
+    return _unpermute(dout, routing, "dout", False, residual, out, stream)
+
+
+def unpermute_backward(dy, z, routing, out=None, stream=None):
+    """The gradients of ``unpermute``: (dz [T k, d], dweights [T, k]).
+
+    dy [T, d] and z [T k, d] are of one dtype, which dz has too (``out`` if
+    given); dweights is float32.  The residual's gradient is dy itself.  Rows of
+    dz that no choice has are zero, as are dweights of dropped choices.
+    """
+    torch = _torch()
+    index = _first(dy, "dy")
+    dt = _row_code(torch, dy, "dy")
+    pz = _check(z, "z", index, dy.dtype)
+    T, k, E, pp, po = _sorted_of(routing, index)
+    if dy.dim() != 2 or dy.shape[0] != T or z.dim() != 2 or z.shape != (T * k, dy.shape[1]):
+        raise ValueError("expected dy [T, d] and z [T k, d] of the routing's T = %d, k = %d"
+                         % (T, k))
+    d = dy.shape[1]
+    pw = _weights_of(routing, index)
+    dz = _out(torch, out, (T * k, d), dy.dtype, index, dy.device, stream)
+    dw = _empty(torch, (T, k), torch.float32, dy.device, stream)
+    _call(index, _lib.load().swiglu_unpermute_backward, dy.data_ptr(), pz, pp, po, pw, dz.data_ptr(),
+          dw.data_ptr(), T, k, E, d, dt,
+          stream.cuda_stream if stream is not None else _raw_stream(index))
+    return dz, dw
 
 
 def linear_workspace_bytes(M, K, N):
