@@ -505,7 +505,7 @@ SWIGLU_API size_t swiglu_rms_norm_backward_workspace_bytes(int64_t M, int64_t d,
  * Rows sorted by expert and back, for experts other than the SwiGLU ones above
  * (which gather and sum rows themselves) and for training.  position and
  * offsets are those of swiglu_route or swiglu_dispatch; T tokens, k <= 32
- * choices each, E <= 1024 experts, d any number of elements to a row.  Positions
+ * choices each, E <= 1024 experts, d any number of elements to a row (up to 2^28).  Positions
  * outside 0 ... T k - 1 stand for no place; a routing that these did not write
  * gives wrong rows, never an access outside the tensors.
  *

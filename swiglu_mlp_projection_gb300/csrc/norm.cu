@@ -66,8 +66,8 @@ norm_kernel(const __grid_constant__ NormArgs a) {
   for (int j = 0; j < VPT; ++j) {
     const int i = lane + j * lanes;
     if (i < pc.n) {
-      xr[j] = pc.load(a.x, i);
-      if (a.residual) rr[j] = pc.load(a.residual, i);
+      xr[j] = pc.load(a.x, a.M, i);
+      if (a.residual) rr[j] = pc.load(a.residual, a.M, i);
     }
   }
   float t[VPT][V];
@@ -77,9 +77,11 @@ norm_kernel(const __grid_constant__ NormArgs a) {
     const int i = lane + j * lanes;
     if (i >= pc.n) continue;
     unpack<F32>(xr[j], t[j]);
+    pc.mask(i, t[j]);
     if (a.residual) {
       float r[V];
       unpack<F32>(rr[j], r);
+      pc.mask(i, r);
 #pragma unroll
       for (int e = 0; e < V; ++e) t[j][e] += r[e];
       pc.store(a.sum, i, t[j]);
@@ -185,10 +187,11 @@ cudaError_t launch_type(const NormArgs& a, bool fp8, bool ragged, const Shape& s
 //   r = 1 / sqrt(mean(s^2) + eps), g = dy * weight
 //   dx = ds + r (g - s r^2 mean(g s)),  dweight = sum over rows of dy s r
 //
-// A CTA takes rows in a fixed order and keeps the columns' sums of dweight for
-// all of them (in registers, or in shared memory for the widest rows); each CTA
-// then writes one row of partial sums, and a second kernel adds those in a
-// fixed order.
+// A CTA takes rows in a fixed order, several at a time where they are short,
+// and keeps the columns' sums of dweight over all of them in registers; each
+// CTA then writes one row of partial sums, and a second kernel adds those in a
+// fixed order.  The next rows are on their way (cp.async, into slots that only
+// the copying thread reads) while one is reduced.
 
 struct BackArgs {
   const void* dy;
@@ -203,46 +206,183 @@ struct BackArgs {
   int weight_f32;
 };
 
-template <bool F32, int VPT, bool RAGGED, bool SMEM>
-__global__ void __launch_bounds__(SMEM ? 1024 : 512)
+// 16 bytes of which `bytes` are read and the rest zero.
+__device__ __forceinline__ void copy_piece(uint4* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// W warps to a row, two pieces to a thread.
+constexpr int kBackPieces = 2;
+constexpr int back_threads(int w) { return w <= 8 ? 256 : 32 * w; }
+constexpr int back_stages(int w) { return w <= 8 ? 3 : 2; }
+constexpr int back_ctas(int w) { return w <= 8 ? 3 : w == 16 ? 2 : 1; }   // per SM
+
+template <bool F32, int W, bool RAGGED>
+__global__ void __launch_bounds__(back_threads(W), back_ctas(W))
 norm_backward_kernel(const __grid_constant__ BackArgs a) {
+  constexpr int V = Row<F32>::kVec, P = kBackPieces, T = back_threads(W), S = back_stages(W);
+  constexpr int R = T / 32 / W;     // rows at a time
+  extern __shared__ uint4 ring[];   // [S][arrays][P][T]: a thread reads what it copied itself
+  __shared__ float2 red[2][T / 32];
+  tc::pdl_launch_dependents();
+  tc::pdl_wait();
+  const int warp = threadIdx.x >> 5, l = threadIdx.x & 31;
+  const int team = warp / W, lane = threadIdx.x - team * W * 32;
+  const int arrays = a.ds ? 3 : 2;
+  const int64_t unit = (int64_t)blockIdx.x * R + team, units = (int64_t)gridDim.x * R;
+  const int64_t total = a.M * a.d;
+  // (ragged: all rows of a team start at one place in their 16 bytes, since
+  // `units` is a multiple of 8 or every team has one row at most)
+  const Pieces<F32, RAGGED> pc(unit, a.d);
+  const auto slot = [&](int stage, int array, int j) {
+    return ring + ((stage * arrays + array) * P + j) * T + threadIdx.x;
+  };
+  const auto fetch = [&](int64_t row, int stage) {
+    if (row < a.M) {
+      const int64_t first = row * a.d - pc.shift;
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        const int i = lane + j * W * 32;
+        if (i >= pc.n) continue;
+        const int64_t at = first + (int64_t)i * V;
+        // (the last piece of the tensor may be cut short)
+        const int bytes = !RAGGED || total - at >= V ? 16 : (int)(total - at) * (16 / V);
+        copy_piece(slot(stage, 0, j), (const char*)a.s + at * (16 / V), bytes);
+        copy_piece(slot(stage, 1, j), (const char*)a.dy + at * (16 / V), bytes);
+        if (a.ds) copy_piece(slot(stage, 2, j), (const char*)a.ds + at * (16 / V), bytes);
+      }
+    }
+    copies_commit();
+  };
+
+  float w[P][V], acc[P][V];
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    const int i = lane + j * W * 32;
+    if (i < pc.n) pc.weight(a.weight, a.weight_f32, i, w[j]);
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[j][e] = 0.f;
+  }
+  const auto piece = [&](int stage, int array, int j, float (&v)[V]) {
+    unpack<F32>(*slot(stage, array, j), v);
+    pc.mask(lane + j * W * 32, v);
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) fetch(unit + i * units, i);
+  const float inv_d = 1.0f / (float)a.d;
+  int side = 0, stage = 0, next = S - 1;
+  for (int64_t row = unit; row < a.M; row += units) {
+    fetch(row + (S - 1) * units, next);
+    copies_wait<S - 1>();
+    float q = 0.f, p = 0.f;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      if (lane + j * W * 32 >= pc.n) continue;
+      float s[V], g[V];
+      piece(stage, 0, j, s);
+      piece(stage, 1, j, g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        q = fmaf(s[e], s[e], q);
+        p = fmaf(g[e] * w[j][e], s[e], p);
+      }
+    }
+    q = warp_sum(q);
+    p = warp_sum(p);
+    if (W > 1) {
+      if (l == 0) red[side][warp] = make_float2(q, p);
+      // (one barrier a row: the next row writes the other side)
+      if (R == 1) __syncthreads();
+      else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
+      const float2 v = l < W ? red[side][team * W + l] : make_float2(0.f, 0.f);
+      q = warp_sum(v.x);
+      p = warp_sum(v.y);
+    }
+    const float r = 1.0f / sqrtf(fmaf(q, inv_d, a.eps));
+    const float c = r * r * (p * inv_d);
+    const int64_t first = row * a.d - pc.shift;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const int i = lane + j * W * 32;
+      if (i >= pc.n) continue;
+      float s[V], g[V], o[V];
+      piece(stage, 0, j, s);
+      piece(stage, 1, j, g);
+      if (a.ds) {
+        piece(stage, 2, j, o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        acc[j][e] = fmaf(g[e], s[e] * r, acc[j][e]);
+        o[e] = fmaf(r, fmaf(g[e], w[j][e], -s[e] * c), o[e]);
+      }
+      pc.store_at(a.dx, first, i, o);
+    }
+    side ^= 1;
+    stage = stage + 1 == S ? 0 : stage + 1;
+    next = next + 1 == S ? 0 : next + 1;
+  }
+  // The CTA's sums, team after team.
+  copies_wait<0>();
+  __syncthreads();
+  float* part = a.part + (int64_t)blockIdx.x * a.d;
+  float* sums = R > 1 ? reinterpret_cast<float*>(ring) + team * a.d : part;
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    const int i = lane + j * W * 32;
+    if (i >= pc.n) continue;
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (pc.has(i, e)) sums[pc.col(i) + e] = acc[j][e];
+  }
+  if (R > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.d; c += T) {
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < R; ++i) v += reinterpret_cast<const float*>(ring)[i * a.d + c];
+      part[c] = v;
+    }
+  }
+}
+
+// Rows wider than 32 warps' two pieces: a CTA per row reads it twice (the
+// second time from L2) and keeps its sums of dweight in shared memory.
+template <bool F32, bool RAGGED>
+__global__ void __launch_bounds__(1024)
+norm_backward_wide_kernel(const __grid_constant__ BackArgs a) {
   constexpr int V = Row<F32>::kVec;
-  extern __shared__ float s_acc[];   // SMEM: [VPT][V][threads]
+  extern __shared__ float acc[];   // [V][pieces]
   __shared__ float2 red[2][32];
   tc::pdl_launch_dependents();
   tc::pdl_wait();
-  const int lanes = blockDim.x, warp = threadIdx.x >> 5, l = threadIdx.x & 31;
-  float acc[SMEM ? 1 : VPT][V];
+  const int warp = threadIdx.x >> 5, l = threadIdx.x & 31;
+  const Pieces<F32, RAGGED> p0(blockIdx.x, a.d);   // (the rows' shift: as above)
+  for (int i = threadIdx.x; i < p0.n; i += 1024)
 #pragma unroll
-  for (int j = 0; j < VPT; ++j)
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      if (SMEM) s_acc[(j * V + e) * lanes + threadIdx.x] = 0.f;
-      else acc[SMEM ? 0 : j][e] = 0.f;
-    }
+    for (int e = 0; e < V; ++e) acc[e * p0.n + i] = 0.f;
+  const float inv_d = 1.0f / (float)a.d;
   int side = 0;
-  // (ragged: all rows of a CTA start at one place in their 16 bytes, since
-  // gridDim.x is a multiple of 8 or every CTA has one row)
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, side ^= 1) {
     const Pieces<F32, RAGGED> pc(row, a.d);
-    uint4 sr[VPT], dr[VPT], er[VPT];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int i = threadIdx.x + j * lanes;
-      if (i < pc.n) {
-        sr[j] = pc.load(a.s, i);
-        dr[j] = pc.load(a.dy, i);
-        if (a.ds) er[j] = pc.load(a.ds, i);
-      }
-    }
     float q = 0.f, p = 0.f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int i = threadIdx.x + j * lanes;
-      if (i >= pc.n) continue;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < pc.n; i += 1024) {
       float s[V], g[V], w[V];
-      unpack<F32>(sr[j], s);
-      unpack<F32>(dr[j], g);
+      unpack<F32>(pc.load(a.s, a.M, i), s);
+      unpack<F32>(pc.load(a.dy, a.M, i), g);
+      pc.mask(i, s);
+      pc.mask(i, g);
       pc.weight(a.weight, a.weight_f32, i, w);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -253,47 +393,38 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
     q = warp_sum(q);
     p = warp_sum(p);
     if (l == 0) red[side][warp] = make_float2(q, p);
-    __syncthreads();   // (one is enough: the next row writes the other side)
-    const float2 v = l < (lanes >> 5) ? red[side][l] : make_float2(0.f, 0.f);
-    q = warp_sum(v.x);
-    p = warp_sum(v.y);
-    const float r = 1.0f / sqrtf(q / (float)a.d + a.eps);
-    const float c = r * r * (p / (float)a.d);
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int i = threadIdx.x + j * lanes;
-      if (i >= pc.n) continue;
+    __syncthreads();
+    q = warp_sum(red[side][l].x);
+    p = warp_sum(red[side][l].y);
+    const float r = 1.0f / sqrtf(fmaf(q, inv_d, a.eps));
+    const float c = r * r * (p * inv_d);
+#pragma unroll 2
+    for (int i = threadIdx.x; i < pc.n; i += 1024) {
       float s[V], g[V], w[V], o[V];
-      unpack<F32>(sr[j], s);
-      unpack<F32>(dr[j], g);
+      unpack<F32>(pc.load(a.s, a.M, i), s);
+      unpack<F32>(pc.load(a.dy, a.M, i), g);
+      pc.mask(i, s);
+      pc.mask(i, g);
       pc.weight(a.weight, a.weight_f32, i, w);
       if (a.ds) {
-        unpack<F32>(er[j], o);
+        unpack<F32>(pc.load(a.ds, a.M, i), o);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] = 0.f;
       }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float t = g[e] * (s[e] * r);
-        if (SMEM) s_acc[(j * V + e) * lanes + threadIdx.x] += t;
-        else acc[SMEM ? 0 : j][e] += t;
+        acc[e * pc.n + i] += g[e] * (s[e] * r);
         o[e] = fmaf(r, fmaf(g[e], w[e], -s[e] * c), o[e]);
       }
       pc.store(a.dx, i, o);
     }
   }
-  const Pieces<F32, RAGGED> pc(blockIdx.x, a.d);
   float* part = a.part + (int64_t)blockIdx.x * a.d;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int i = threadIdx.x + j * lanes;
-    if (i >= pc.n) continue;
+  for (int i = threadIdx.x; i < p0.n; i += 1024)
 #pragma unroll
     for (int e = 0; e < V; ++e)
-      if (pc.has(i, e))
-        part[pc.col(i) + e] = SMEM ? s_acc[(j * V + e) * lanes + threadIdx.x] : acc[SMEM ? 0 : j][e];
-  }
+      if (p0.has(i, e)) part[p0.col(i) + e] = acc[e * p0.n + i];
 }
 
 constexpr int kSumCols = 32, kSumRows = 32;
@@ -321,26 +452,48 @@ dweight_kernel(const float* __restrict__ part, int n, int d, void* __restrict__ 
   }
 }
 
-// CTAs of the gradient's kernel.
-int back_grid(int64_t M, int num_sms) {
-  const int64_t most = (int64_t)num_sms * 2 / 8 * 8;
-  return (int)(M < most ? M : most);
+// How the gradient's rows are dealt out: W warps to a row (0: the wide kernel),
+// `grid` CTAs.
+struct BackShape {
+  int warps, grid;
+};
+BackShape back_shape(int64_t M, int64_t d, bool f32, int num_sms) {
+  const int vec = f32 ? 4 : 8;
+  const int64_t pieces = d % vec ? d / vec + 2 : d / vec;
+  int w = 1;
+  while (w <= 32 && 32 * kBackPieces * w < pieces) w *= 2;
+  const int rows = w > 32 ? 1 : back_threads(w) / 32 / w;
+  int64_t grid = (M + rows - 1) / rows;
+  const int64_t most = (int64_t)num_sms * (w > 32 ? 1 : back_ctas(w)) / 8 * 8;
+  if (grid > most) grid = most;
+  return {w > 32 ? 0 : w, (int)grid};
+}
+
+template <bool F32, int W, bool RAGGED>
+cudaError_t launch_back_warps(const BackArgs& a, int grid, cudaStream_t st) {
+  const auto k = norm_backward_kernel<F32, W, RAGGED>;
+  size_t smem = (size_t)back_stages(W) * (a.ds ? 3 : 2) * kBackPieces * back_threads(W) * 16;
+  static_assert(back_stages(W) * 2 * kBackPieces * 16 * 32 * W >= 512 * W * 4, "no room for the sums");
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_chained(k, dim3(grid), dim3(back_threads(W)), smem, st, a);
 }
 
 template <bool F32, bool RAGGED>
-cudaError_t launch_back(const BackArgs& a, int64_t pieces, int grid, cudaStream_t st) {
-  constexpr int kTwo = 16 / Row<F32>::kVec;   // pieces of 16 elements
-  const auto threads = [&](int vpt) { return (int)((pieces + vpt * 32 - 1) / (vpt * 32) * 32); };
-  const int t = threads(kTwo);
-  if (t <= 512)
-    return launch_chained(norm_backward_kernel<F32, kTwo, RAGGED, false>, dim3(grid), dim3(t), 0,
-                          st, a);
-  const int w = threads(2 * kTwo);
-  const size_t smem = (size_t)w * 2 * 16 * sizeof(float);
-  const auto k = norm_backward_kernel<F32, 2 * kTwo, RAGGED, true>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+cudaError_t launch_back(const BackArgs& a, const BackShape& s, cudaStream_t st) {
+  switch (s.warps) {
+    case 1: return launch_back_warps<F32, 1, RAGGED>(a, s.grid, st);
+    case 2: return launch_back_warps<F32, 2, RAGGED>(a, s.grid, st);
+    case 4: return launch_back_warps<F32, 4, RAGGED>(a, s.grid, st);
+    case 8: return launch_back_warps<F32, 8, RAGGED>(a, s.grid, st);
+    case 16: return launch_back_warps<F32, 16, RAGGED>(a, s.grid, st);
+    case 32: return launch_back_warps<F32, 32, RAGGED>(a, s.grid, st);
+  }
+  const auto k = norm_backward_wide_kernel<F32, RAGGED>;
+  const size_t smem = (size_t)(a.d + 16) * sizeof(float);
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_chained(k, dim3(grid), dim3(w), smem, st, a);
+  return launch_chained(k, dim3(s.grid), dim3(1024), smem, st, a);
 }
 
 }  // namespace
@@ -358,27 +511,23 @@ cudaError_t launch_rms_norm(const NormCall& c, int num_sms, cudaStream_t st) {
 }
 
 size_t rms_norm_backward_bytes(int64_t M, int64_t d, int f32, int num_sms) {
-  return (size_t)back_grid(M, num_sms) * (size_t)d * sizeof(float);
+  return (size_t)back_shape(M, d, f32 != 0, num_sms).grid * (size_t)d * sizeof(float);
 }
 
 cudaError_t launch_rms_norm_backward(const NormBackwardCall& c, float* part, int num_sms,
                                      cudaStream_t st) {
   if (c.d == 0) return cudaSuccess;
-  const int grid = back_grid(c.M, num_sms);
+  const BackShape s = back_shape(c.M, c.d, c.f32 != 0, num_sms);
   if (c.M > 0) {
     const BackArgs a{c.dy, c.s, c.weight, c.ds, c.dx, part, c.M, (int)c.d, c.eps, c.weight_f32};
-    const int vec = c.f32 ? 4 : 8;
-    const bool ragged = c.d % vec != 0;
-    const int64_t pieces = ragged ? c.d / vec + 2 : c.d / vec;
+    const bool ragged = c.d % (c.f32 ? 4 : 8) != 0;
     const cudaError_t e =
-        c.f32 ? (ragged ? launch_back<true, true>(a, pieces, grid, st)
-                        : launch_back<true, false>(a, pieces, grid, st))
-              : (ragged ? launch_back<false, true>(a, pieces, grid, st)
-                        : launch_back<false, false>(a, pieces, grid, st));
+        c.f32 ? (ragged ? launch_back<true, true>(a, s, st) : launch_back<true, false>(a, s, st))
+              : (ragged ? launch_back<false, true>(a, s, st) : launch_back<false, false>(a, s, st));
     if (e != cudaSuccess) return e;
   }
   return launch_chained(dweight_kernel, dim3((unsigned)((c.d + kSumCols - 1) / kSumCols)),
-                        dim3(kSumCols * kSumRows), 0, st, (const float*)part, grid, (int)c.d,
+                        dim3(kSumCols * kSumRows), 0, st, (const float*)part, s.grid, (int)c.d,
                         c.dweight, c.weight_f32);
 }
 

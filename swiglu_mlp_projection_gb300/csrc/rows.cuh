@@ -61,11 +61,43 @@ __device__ __forceinline__ uint4 load_once(const void* p) {
   return r;
 }
 
+// The 16 bytes from byte `sh` (0 ... 15) of lo and hi, one after the other.
+__device__ __forceinline__ uint4 shift_bytes(const uint4& lo, const uint4& hi, int sh) {
+  uint32_t w[6] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y};
+  if (sh & 8) {
+    w[0] = w[2]; w[1] = w[3]; w[2] = w[4]; w[3] = w[5]; w[4] = hi.z; w[5] = hi.w;
+  }
+  if (sh & 4) {
+    w[0] = w[1]; w[1] = w[2]; w[2] = w[3]; w[3] = w[4]; w[4] = w[5];
+  }
+  const int b = 8 * (sh & 3);
+  return make_uint4(__funnelshift_r(w[0], w[1], b), __funnelshift_r(w[1], w[2], b),
+                    __funnelshift_r(w[2], w[3], b), __funnelshift_r(w[3], w[4], b));
+}
+
+// The 16 bytes at byte `at` (a multiple of 16) of a tensor of `total` bytes;
+// zero where that is outside it.  E: the tensor's elements.
+template <typename E>
+__device__ __forceinline__ uint4 load_inside(const void* p, int64_t at, int64_t total) {
+  if (at >= 0 && at + 16 <= total) return *reinterpret_cast<const uint4*>((const char*)p + at);
+  union {
+    uint4 q;
+    E e[16 / sizeof(E)];
+  } u;
+  u.q = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int i = 0; i < (int)(16 / sizeof(E)); ++i)
+    if (at >= 0 && at + (int64_t)(i * sizeof(E)) < total)
+      u.e[i] = *reinterpret_cast<const E*>((const char*)p + at + i * sizeof(E));
+  return u.q;
+}
+
 // A row of d elements in 16-byte pieces that start on 16-byte boundaries of
 // the tensor, whatever d is: piece i holds the row's elements i * kVec - shift
 // and on, of which those in 0 ... d - 1 are the row's own (the others are its
-// neighbours', and the first and last piece are then moved element by element).
-// Without RAGGED (d a multiple of kVec) shift is 0 and every piece is whole.
+// neighbours': not used when the first or last piece is read, not touched when
+// it is written).  Without RAGGED (d a multiple of kVec) shift is 0 and every
+// piece is whole.
 template <bool F32, bool RAGGED>
 struct Pieces {
   static constexpr int V = Row<F32>::kVec;
@@ -86,27 +118,37 @@ struct Pieces {
   __device__ __forceinline__ bool has(int i, int e) const {
     return !RAGGED || (col(i) + e >= 0 && col(i) + e < d);
   }
-
-  // Piece i of the tensor at `p`; elements that are not the row's are 0.
-  __device__ __forceinline__ uint4 load(const void* p, int i) const {
-    const E* q = (const E*)p + first + (int64_t)i * V;
-    if (whole(i)) return load_once(q);
-    float v[V];
+  // Elements that are not the row's become 0.
+  __device__ __forceinline__ void mask(int i, float (&v)[V]) const {
+    if (!whole(i)) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = has(i, e) ? elem_f32(q[e]) : 0.f;
-    return pack<F32>(v);   // (exact: the values are of the type)
+      for (int e = 0; e < V; ++e)
+        if (!has(i, e)) v[e] = 0.f;
+    }
+  }
+
+  // Piece i of the tensor of `rows` rows at `p`, with neighbours' elements (see mask).
+  __device__ __forceinline__ uint4 load(const void* p, int64_t rows, int i) const {
+    const int64_t at = first + (int64_t)i * V;
+    if (!RAGGED || at + V <= rows * d) return load_once((const E*)p + at);
+    return load_inside<E>(p, at * (16 / V), rows * d * (16 / V));
   }
   __device__ __forceinline__ void store(void* p, int i, const float (&v)[V]) const {
-    E* q = (E*)p + first + (int64_t)i * V;
+    store_at(p, first, i, v);
+  }
+  // Into another row that starts at the same place of its 16 bytes: its piece 0 at `at`.
+  __device__ __forceinline__ void store_at(void* p, int64_t at, int i, const float (&v)[V]) const {
+    E* q = (E*)p + at + (int64_t)i * V;
     if (whole(i)) {
       *reinterpret_cast<uint4*>(q) = pack<F32>(v);
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (has(i, e)) set_elem(q + e, v[e]);
+      for (int e = 0; e < V; ++e)
+        if (has(i, e)) set_elem(q + e, v[e]);
+    }
   }
-  // Piece i of a vector [d] of bf16 or f32 values (the norm's weight), 0 past its ends.
+  // What piece i of a vector [d] of bf16 or f32 values (the norm's weight) would
+  // be if it started where the row does; 0 past its ends.
   __device__ __forceinline__ void weight(const void* w, int w_f32, int i, float (&v)[V]) const {
     if (!RAGGED) {
       if (w_f32) {
@@ -122,13 +164,19 @@ struct Pieces {
         const uint2 q = *reinterpret_cast<const uint2*>((const uint16_t*)w + i * V);
         v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
       }
-      return;
-    }
+    } else if (w_f32 == (F32 ? 1 : 0)) {   // the row's own type: two pieces, shifted
+      constexpr int es = 16 / V;
+      const int64_t at = (int64_t)(shift ? i - 1 : i) * 16;
+      const uint4 lo = load_inside<E>(w, at, (int64_t)d * es);
+      const uint4 hi = load_inside<E>(w, at + 16, (int64_t)d * es);
+      unpack<F32>(shift_bytes(lo, hi, (16 - shift * es) & 15), v);
+    } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      v[e] = !has(i, e) ? 0.f
-             : w_f32    ? ((const float*)w)[col(i) + e]
-                        : bf16_lo(((const uint16_t*)w)[col(i) + e]);
+      for (int e = 0; e < V; ++e)
+        v[e] = !has(i, e) ? 0.f
+               : w_f32    ? ((const float*)w)[col(i) + e]
+                          : bf16_lo(((const uint16_t*)w)[col(i) + e]);
+    }
   }
 };
 

@@ -37,8 +37,10 @@ int check_norm(int64_t M, int64_t d, float eps, int dtype, int weight_dtype) {
 int check_pairs(int64_t T, int64_t k, int64_t d) {
   if (T < 0 || k < 0 || d < 0) return api_fail(SWIGLU_ERR_INVALID_ARG, "negative size");
   if (k > kMaxTopK) return api_fail(SWIGLU_ERR_UNSUPPORTED, "more than 32 choices per token");
-  if (T > (int64_t)1 << 30 || T * k > (int64_t)1 << 30 || d > (int64_t)1 << 30)
+  if (T > (int64_t)1 << 30 || T * k > (int64_t)1 << 30)
     return api_fail(SWIGLU_ERR_UNSUPPORTED, "a size exceeds 2^30");
+  if (d > (int64_t)1 << 28)   // (a row's bytes are counted in 32 bits)
+    return api_fail(SWIGLU_ERR_UNSUPPORTED, "a row of more than 2^28 elements");
   return SWIGLU_OK;
 }
 

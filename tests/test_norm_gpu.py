@@ -213,10 +213,11 @@ def test_refusals(cuda_lib):
         with pytest.raises(TypeError):
             call()
     odd = torch.empty(4 * 64 + 1, device=DEV, dtype=BF)[1:].view(4, 64)
+    short = torch.empty(swg.rms_norm_backward_workspace_bytes(4, 64) - 1, device=DEV, dtype=torch.uint8)
     for call in (lambda: swg.rms_norm(x, w, eps=0.0), lambda: swg.rms_norm(odd, w),
                  lambda: swg.rms_norm(x, w, out=w.expand(4, 64).contiguous()[:4], residual=r,
                                       sum_out=r[:4], eps=-1.0),
-                 lambda: swg.rms_norm_backward(x, x, w, workspace=torch.empty(64, device=DEV))):
+                 lambda: swg.rms_norm_backward(x, x, w, workspace=short)):
         with pytest.raises(swg.SwiGLUError):
             call()
 

@@ -72,7 +72,7 @@ INVALID, UNSUPPORTED, ALIGN = 1, 2, 3
     (permute, dict(osc=5 * A), INVALID), (permute, dict(dt=2), INVALID),
     (permute, dict(dt=2, sc=5 * A), INVALID), (permute, dict(dt=2, sc=5 * A, osc=4 * A), INVALID),
     (permute, dict(dt=2, sc=5 * A, osc=5 * A), INVALID), (permute, dict(x=A + 2), ALIGN),
-    (permute, dict(pos=2 * A + 2), ALIGN),
+    (permute, dict(pos=2 * A + 2), ALIGN), (permute, dict(d=(1 << 28) + 1), UNSUPPORTED),
     (unpermute, dict(z=None), INVALID), (unpermute, dict(pos=None), INVALID),
     (unpermute, dict(y=None), INVALID), (unpermute, dict(y=A), INVALID),
     (unpermute, dict(r=4 * A + 16), INVALID), (unpermute, dict(dt=2), INVALID),
