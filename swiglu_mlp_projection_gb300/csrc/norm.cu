@@ -30,9 +30,9 @@ struct NormArgs {
 // Below this max |t| a row is 0 in 8 bits (448 / max |t| would leave binary32).
 constexpr float kLeastAmax = 0x1p-118f;
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+__device__ __forceinline__ uint32_t e4m3x2(float2 v) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(v.y), "f"(v.x));
   return r;
 }
 
@@ -41,16 +41,70 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// Largest of values that are not negative (their bits order like the values; NaN is largest).
+// Largest of values that are not negative (their bits order like the values).
 __device__ __forceinline__ float warp_max(float v) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+}
+
+// A piece of the row on its way: s (stored where there is a residual), t = s * w,
+// the sums so far.
+template <bool F32, bool FP8, bool RAGGED>
+__device__ __forceinline__ void add_piece(const Pieces<F32, RAGGED>& pc, const NormArgs& a,
+                                          int64_t first, int i, const uint4& xq, const uint4& rq,
+                                          const float2 (&w)[Row<F32>::kVec / 2],
+                                          float2 (&t)[Row<F32>::kVec / 2], float2& q, float& m) {
+  constexpr int H = Row<F32>::kVec / 2;
+  unpack<F32>(xq, t);
+  if (a.residual) {
+    float2 r[H];
+    unpack<F32>(rq, r);
+#pragma unroll
+    for (int h = 0; h < H; ++h) t[h] = add2(t[h], r[h]);
+  }
+  pc.mask(i, t);
+  if (a.residual) pc.store_at(a.sum, first, i, t);
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    q = fma2(t[h], t[h], q);
+    t[h] = mul2(t[h], w[h]);
+    if (FP8) m = fmaxf(m, fmaxf(fabsf(t[h].x), fabsf(t[h].y)));
+  }
+}
+
+// ... and on its way out, as t * f.
+template <bool F32, bool FP8, bool RAGGED>
+__device__ __forceinline__ void put_piece(const Pieces<F32, RAGGED>& pc, void* out, int64_t first,
+                                          int i, float2 (&t)[Row<F32>::kVec / 2], float f) {
+  constexpr int V = Row<F32>::kVec;
+#pragma unroll
+  for (int h = 0; h < V / 2; ++h) t[h] = mul2(t[h], make_float2(f, f));
+  if constexpr (FP8) {
+    uint32_t c[V / 4];
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) c[h] = e4m3x2(t[2 * h]) | (e4m3x2(t[2 * h + 1]) << 16);
+    pc.store_codes(out, first, i, c);
+  } else {
+    pc.store_at(out, first, i, t);
+  }
+}
+
+struct RowFactors {
+  float f;       // of t
+  float scale;   // FP8: the row's
+};
+template <bool FP8>
+__device__ __forceinline__ RowFactors row_factors(float q, float m, const NormArgs& a) {
+  const float r = 1.0f / sqrtf(q / (float)a.d + a.eps);
+  if (!FP8) return {r, 0.f};
+  const bool some = m >= kLeastAmax;
+  return {some ? 448.0f / m : 0.f, (some ? m : 0.f) * r / 448.0f};
 }
 
 // One row per warp (WARP) or per CTA; VPT 16-byte pieces per thread.
 template <bool F32, int VPT, bool FP8, bool RAGGED, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 1024)
 norm_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int V = Row<F32>::kVec;
+  constexpr int H = Row<F32>::kVec / 2;
   __shared__ float red_sum[32], red_max[32];
   tc::pdl_launch_dependents();
   tc::pdl_wait();
@@ -70,32 +124,18 @@ norm_kernel(const __grid_constant__ NormArgs a) {
       if (a.residual) rr[j] = pc.load(a.residual, a.M, i);
     }
   }
-  float t[VPT][V];
-  float q = 0.f, m = 0.f;
+  float2 t[VPT][H];
+  float2 q2 = make_float2(0.f, 0.f);
+  float m = 0.f;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int i = lane + j * lanes;
     if (i >= pc.n) continue;
-    unpack<F32>(xr[j], t[j]);
-    pc.mask(i, t[j]);
-    if (a.residual) {
-      float r[V];
-      unpack<F32>(rr[j], r);
-      pc.mask(i, r);
-#pragma unroll
-      for (int e = 0; e < V; ++e) t[j][e] += r[e];
-      pc.store(a.sum, i, t[j]);
-    }
-    float w[V];
+    float2 w[H];
     pc.weight(a.weight, a.weight_f32, i, w);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      q = fmaf(t[j][e], t[j][e], q);
-      t[j][e] *= w[e];
-      if (FP8) m = fmaxf(m, fabsf(t[j][e]));
-    }
+    add_piece<F32, FP8, RAGGED>(pc, a, pc.first, i, xr[j], rr[j], w, t[j], q2, m);
   }
-  q = warp_sum(q);
+  float q = warp_sum(q2.x + q2.y);
   if (FP8) m = warp_max(m);
   if (!WARP) {
     const int warp = threadIdx.x >> 5, l = threadIdx.x & 31;
@@ -108,33 +148,128 @@ norm_kernel(const __grid_constant__ NormArgs a) {
     q = warp_sum(in ? red_sum[l] : 0.f);
     if (FP8) m = warp_max(in ? red_max[l] : 0.f);
   }
-  const float r = 1.0f / sqrtf(q / (float)a.d + a.eps);
-  const float f = FP8 ? (m >= kLeastAmax ? 448.0f / m : 0.f) : r;
+  const RowFactors rf = row_factors<FP8>(q, m, a);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int i = lane + j * lanes;
-    if (i >= pc.n) continue;
-#pragma unroll
-    for (int e = 0; e < V; ++e) t[j][e] *= f;
-    if constexpr (FP8) {
-      uint8_t* o = (uint8_t*)a.out + pc.first + (int64_t)i * V;
-      uint32_t c[V / 4];
-#pragma unroll
-      for (int h = 0; h < V / 4; ++h)
-        c[h] = e4m3x2(t[j][4 * h], t[j][4 * h + 1]) | (e4m3x2(t[j][4 * h + 2], t[j][4 * h + 3]) << 16);
-      if (pc.whole(i)) {
-        if constexpr (V == 8) *reinterpret_cast<uint2*>(o) = make_uint2(c[0], c[1]);
-        else *reinterpret_cast<uint32_t*>(o) = c[0];
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          if (pc.has(i, e)) o[e] = (uint8_t)(c[e / 4] >> (8 * (e & 3)));
-      }
-    } else {
-      pc.store(a.out, i, t[j]);
-    }
+    if (i < pc.n) put_piece<F32, FP8, RAGGED>(pc, a.out, pc.first, i, t[j], rf.f);
   }
-  if (FP8 && lane == 0) a.scales[row] = (m >= kLeastAmax ? m : 0.f) * r / 448.0f;
+  if (FP8 && lane == 0) a.scales[row] = rf.scale;
+}
+
+// ---- rows that stream through a CTA ---------------------------------------------
+//
+// The gradient, and the norm of rows that are no multiple of 16 bytes, keep
+// something per column across rows (sums of dweight; the weight, moved to where
+// such rows start).  One CTA per SM holds R teams of W warps; a team takes row
+// after row, two pieces to a thread, and copies the next rows (cp.async) into
+// slots that only the copying thread reads, while one is reduced.  Rows go to
+// the CTAs first, then to their teams.
+
+constexpr int kPieces = 2;
+constexpr int team_threads(int w) { return w <= 8 ? 768 : 32 * w; }
+constexpr int team_rows(int w) { return team_threads(w) / 32 / w; }   // R
+constexpr int team_stages(int w) { return w <= 8 ? 3 : w == 16 ? 4 : 2; }
+
+template <bool F32, int W, bool RAGGED>
+struct Team {
+  static constexpr int V = Row<F32>::kVec, P = kPieces, T = team_threads(W), S = team_stages(W),
+                       R = team_rows(W);
+  int warp, l, team, lane;
+  int64_t unit, units;   // rows unit, unit + units, ...
+  int64_t M;
+  int arrays;
+  uint4* slots;
+  // (ragged: all rows of a team start at one place of their 16 bytes, since
+  // `units` is a multiple of 8 or every team has one row at most)
+  Pieces<F32, RAGGED> pc;
+
+  __device__ __forceinline__ Team(uint4* ring, int arrays_, int64_t M_, int d)
+      : warp(threadIdx.x >> 5), l(threadIdx.x & 31), team(warp / W),
+        lane(threadIdx.x - team * W * 32), unit(blockIdx.x + (int64_t)team * gridDim.x),
+        units((int64_t)gridDim.x * R), M(M_), arrays(arrays_), slots(ring + threadIdx.x),
+        pc(unit, d) {}
+  __device__ __forceinline__ int piece(int j) const { return lane + j * W * 32; }
+  __device__ __forceinline__ uint4* slot(int stage, int array, int j) const {
+    return slots + ((stage * arrays + array) * P + j) * T;
+  }
+  __device__ __forceinline__ int64_t first(int64_t row) const { return row * pc.d - pc.shift; }
+  // This thread's pieces of `row`, a group of copies (an empty one past the last row).
+  __device__ __forceinline__ void fetch(int64_t row, int stage, const void* p0, const void* p1,
+                                        const void* p2) const {
+    if (row < M) {
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        const int i = piece(j);
+        if (i >= pc.n) continue;
+        const int64_t at = first(row) + (int64_t)i * V, left = M * pc.d - at;
+        // (the last piece of the tensor may be cut short)
+        const int bytes = !RAGGED || left >= V ? 16 : (int)left * (16 / V);
+        copy_piece(slot(stage, 0, j), (const char*)p0 + at * (16 / V), bytes);
+        if (p1) copy_piece(slot(stage, 1, j), (const char*)p1 + at * (16 / V), bytes);
+        if (p2) copy_piece(slot(stage, 2, j), (const char*)p2 + at * (16 / V), bytes);
+      }
+    }
+    copies_commit();
+  }
+  // All warps of the team.
+  __device__ __forceinline__ void sync() const {
+    if (W == 1) __syncwarp();
+    else if (R == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
+  }
+  __device__ __forceinline__ static int after(int stage) { return stage + 1 == S ? 0 : stage + 1; }
+};
+
+template <bool F32, int W, bool FP8>
+__global__ void __launch_bounds__(team_threads(W), 1)
+norm_stream_kernel(const __grid_constant__ NormArgs a) {
+  using Tm = Team<F32, W, true>;
+  constexpr int P = Tm::P, H = Tm::V / 2, S = Tm::S;
+  extern __shared__ uint4 ring[];
+  __shared__ float2 red[2][32];
+  tc::pdl_launch_dependents();
+  tc::pdl_wait();
+  const Tm tm(ring, a.residual ? 2 : 1, a.M, a.d);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) tm.fetch(tm.unit + i * tm.units, i, a.x, a.residual, nullptr);
+  float2 w[P][H];
+#pragma unroll
+  for (int j = 0; j < P; ++j)
+    if (tm.piece(j) < tm.pc.n) tm.pc.weight(a.weight, a.weight_f32, tm.piece(j), w[j]);
+  int side = 0, stage = 0, next = S - 1;
+  for (int64_t row = tm.unit; row < a.M; row += tm.units) {
+    tm.fetch(row + (S - 1) * tm.units, next, a.x, a.residual, nullptr);
+    copies_wait<S - 1>();
+    float2 t[P][H], q2 = make_float2(0.f, 0.f);
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const int i = tm.piece(j);
+      if (i >= tm.pc.n) continue;
+      add_piece<F32, FP8, true>(tm.pc, a, tm.first(row), i, *tm.slot(stage, 0, j),
+                                a.residual ? *tm.slot(stage, 1, j) : uint4{}, w[j], t[j], q2, m);
+    }
+    float q = warp_sum(q2.x + q2.y);
+    if (FP8) m = warp_max(m);
+    if (W > 1) {   // (one barrier a row: the next row writes the other side)
+      if (tm.l == 0) red[side][tm.warp] = make_float2(q, m);
+      tm.sync();
+      const float2 v = tm.l < W ? red[side][tm.team * W + tm.l] : make_float2(0.f, 0.f);
+      q = warp_sum(v.x);
+      if (FP8) m = warp_max(v.y);
+    }
+    const RowFactors rf = row_factors<FP8>(q, m, a);
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const int i = tm.piece(j);
+      if (i < tm.pc.n) put_piece<F32, FP8, true>(tm.pc, a.out, tm.first(row), i, t[j], rf.f);
+    }
+    if (FP8 && tm.lane == 0) a.scales[row] = rf.scale;
+    side ^= 1;
+    stage = tm.after(stage);
+    next = tm.after(next);
+  }
 }
 
 // How a row's pieces are dealt out.
@@ -158,28 +293,61 @@ Shape shape_of(int64_t pieces, int vec, int64_t M, int num_sms) {
   return {vpt, (int)((pieces + vpt * 32 - 1) / (vpt * 32) * 32), false};
 }
 
+int64_t pieces_of(int64_t d, int vec) { return d % vec ? d / vec + 2 : d / vec; }
+
+// Warps per row of the streaming kernels, or 0 for rows too wide for them.
+int team_warps(int64_t d, int vec) {
+  int w = 1;
+  while (w <= 32 && 32 * kPieces * w < pieces_of(d, vec)) w *= 2;
+  return w > 32 ? 0 : w;
+}
+
+// A streaming kernel's launch: M rows (at least 1) over at most one CTA per SM
+// (152 or another multiple of 8, see Team::pc).
+int team_grid(int64_t M, int num_sms) {
+  const int64_t most = num_sms / 8 * 8;
+  return (int)(M < most ? M : most);
+}
+template <typename A>
+cudaError_t launch_team(void (*kernel)(A), const A& a, int w, int arrays, int grid,
+                        cudaStream_t st) {
+  const int smem = team_stages(w) * arrays * kPieces * team_threads(w) * 16;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_chained(kernel, dim3(grid), dim3(team_threads(w)), smem, st, a);
+}
+
 template <bool F32, int VPT, bool FP8, bool RAGGED>
 cudaError_t launch_norm(const NormArgs& a, const Shape& s, cudaStream_t st) {
-  if (s.warp)
-    return launch_chained(norm_kernel<F32, VPT, FP8, RAGGED, true>, dim3((unsigned)((a.M + 7) / 8)),
-                          dim3(256), 0, st, a);
+  if constexpr (!RAGGED)
+    if (s.warp)
+      return launch_chained(norm_kernel<F32, VPT, FP8, RAGGED, true>,
+                            dim3((unsigned)((a.M + 7) / 8)), dim3(256), 0, st, a);
   return launch_chained(norm_kernel<F32, VPT, FP8, RAGGED, false>, dim3((unsigned)a.M),
                         dim3(s.threads), 0, st, a);
 }
 
-template <bool F32, bool FP8, bool RAGGED>
-cudaError_t launch_vpt(const NormArgs& a, const Shape& s, cudaStream_t st) {
-  constexpr int base = 8 / Row<F32>::kVec;   // pieces of 8 elements
-  if (s.vpt == base) return launch_norm<F32, base, FP8, RAGGED>(a, s, st);
-  if (s.vpt == 2 * base) return launch_norm<F32, 2 * base, FP8, RAGGED>(a, s, st);
-  return launch_norm<F32, 4 * base, FP8, RAGGED>(a, s, st);
-}
-
-template <bool F32>
-cudaError_t launch_type(const NormArgs& a, bool fp8, bool ragged, const Shape& s, cudaStream_t st) {
-  if (fp8)
-    return ragged ? launch_vpt<F32, true, true>(a, s, st) : launch_vpt<F32, true, false>(a, s, st);
-  return ragged ? launch_vpt<F32, false, true>(a, s, st) : launch_vpt<F32, false, false>(a, s, st);
+template <bool F32, bool FP8>
+cudaError_t launch_rows(const NormArgs& a, int num_sms, cudaStream_t st) {
+  constexpr int V = Row<F32>::kVec, base = 8 / V;   // pieces of 8 elements
+  if (a.d % V == 0) {
+    const Shape s = shape_of(a.d / V, V, a.M, num_sms);
+    if (s.vpt == base) return launch_norm<F32, base, FP8, false>(a, s, st);
+    if (s.vpt == 2 * base) return launch_norm<F32, 2 * base, FP8, false>(a, s, st);
+    return launch_norm<F32, 4 * base, FP8, false>(a, s, st);
+  }
+  const int w = team_warps(a.d, V), arrays = a.residual ? 2 : 1, grid = team_grid(a.M, num_sms);
+  switch (w) {
+    case 1: return launch_team(norm_stream_kernel<F32, 1, FP8>, a, w, arrays, grid, st);
+    case 2: return launch_team(norm_stream_kernel<F32, 2, FP8>, a, w, arrays, grid, st);
+    case 4: return launch_team(norm_stream_kernel<F32, 4, FP8>, a, w, arrays, grid, st);
+    case 8: return launch_team(norm_stream_kernel<F32, 8, FP8>, a, w, arrays, grid, st);
+    case 16: return launch_team(norm_stream_kernel<F32, 16, FP8>, a, w, arrays, grid, st);
+    case 32: return launch_team(norm_stream_kernel<F32, 32, FP8>, a, w, arrays, grid, st);
+  }
+  const int vpt = 4 * base;
+  const Shape wide{vpt, (int)((pieces_of(a.d, V) + vpt * 32 - 1) / (vpt * 32) * 32), false};
+  return launch_norm<F32, 4 * base, FP8, true>(a, wide, st);
 }
 
 // ---- gradient -------------------------------------------------------------------
@@ -187,11 +355,9 @@ cudaError_t launch_type(const NormArgs& a, bool fp8, bool ragged, const Shape& s
 //   r = 1 / sqrt(mean(s^2) + eps), g = dy * weight
 //   dx = ds + r (g - s r^2 mean(g s)),  dweight = sum over rows of dy s r
 //
-// A CTA takes rows in a fixed order, several at a time where they are short,
-// and keeps the columns' sums of dweight over all of them in registers; each
+// A team's columns' sums of dweight stay in registers over all of its rows; each
 // CTA then writes one row of partial sums, and a second kernel adds those in a
-// fixed order.  The next rows are on their way (cp.async, into slots that only
-// the copying thread reads) while one is reduced.
+// fixed order.
 
 struct BackArgs {
   const void* dy;
@@ -206,151 +372,107 @@ struct BackArgs {
   int weight_f32;
 };
 
-// 16 bytes of which `bytes` are read and the rest zero.
-__device__ __forceinline__ void copy_piece(uint4* dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src),
-               "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// W warps to a row, two pieces to a thread.
-constexpr int kBackPieces = 2;
-constexpr int back_threads(int w) { return w <= 8 ? 256 : 32 * w; }
-constexpr int back_stages(int w) { return w <= 8 ? 3 : 2; }
-constexpr int back_ctas(int w) { return w <= 8 ? 3 : w == 16 ? 2 : 1; }   // per SM
-
 template <bool F32, int W, bool RAGGED>
-__global__ void __launch_bounds__(back_threads(W), back_ctas(W))
+__global__ void __launch_bounds__(team_threads(W), 1)
 norm_backward_kernel(const __grid_constant__ BackArgs a) {
-  constexpr int V = Row<F32>::kVec, P = kBackPieces, T = back_threads(W), S = back_stages(W);
-  constexpr int R = T / 32 / W;     // rows at a time
-  extern __shared__ uint4 ring[];   // [S][arrays][P][T]: a thread reads what it copied itself
-  __shared__ float2 red[2][T / 32];
+  using Tm = Team<F32, W, RAGGED>;
+  constexpr int P = Tm::P, H = Tm::V / 2, S = Tm::S, R = Tm::R;
+  extern __shared__ uint4 ring[];
+  __shared__ float2 red[2][32];
   tc::pdl_launch_dependents();
   tc::pdl_wait();
-  const int warp = threadIdx.x >> 5, l = threadIdx.x & 31;
-  const int team = warp / W, lane = threadIdx.x - team * W * 32;
-  const int arrays = a.ds ? 3 : 2;
-  const int64_t unit = (int64_t)blockIdx.x * R + team, units = (int64_t)gridDim.x * R;
-  const int64_t total = a.M * a.d;
-  // (ragged: all rows of a team start at one place in their 16 bytes, since
-  // `units` is a multiple of 8 or every team has one row at most)
-  const Pieces<F32, RAGGED> pc(unit, a.d);
-  const auto slot = [&](int stage, int array, int j) {
-    return ring + ((stage * arrays + array) * P + j) * T + threadIdx.x;
-  };
-  const auto fetch = [&](int64_t row, int stage) {
-    if (row < a.M) {
-      const int64_t first = row * a.d - pc.shift;
+  const Tm tm(ring, a.ds ? 3 : 2, a.M, a.d);
 #pragma unroll
-      for (int j = 0; j < P; ++j) {
-        const int i = lane + j * W * 32;
-        if (i >= pc.n) continue;
-        const int64_t at = first + (int64_t)i * V;
-        // (the last piece of the tensor may be cut short)
-        const int bytes = !RAGGED || total - at >= V ? 16 : (int)(total - at) * (16 / V);
-        copy_piece(slot(stage, 0, j), (const char*)a.s + at * (16 / V), bytes);
-        copy_piece(slot(stage, 1, j), (const char*)a.dy + at * (16 / V), bytes);
-        if (a.ds) copy_piece(slot(stage, 2, j), (const char*)a.ds + at * (16 / V), bytes);
-      }
-    }
-    copies_commit();
-  };
-
-  float w[P][V], acc[P][V];
+  for (int i = 0; i < S - 1; ++i) tm.fetch(tm.unit + i * tm.units, i, a.s, a.dy, a.ds);
+  float2 w[P][H], acc[P][H];
 #pragma unroll
   for (int j = 0; j < P; ++j) {
-    const int i = lane + j * W * 32;
-    if (i < pc.n) pc.weight(a.weight, a.weight_f32, i, w[j]);
+    if (tm.piece(j) < tm.pc.n) tm.pc.weight(a.weight, a.weight_f32, tm.piece(j), w[j]);
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[j][e] = 0.f;
+    for (int h = 0; h < H; ++h) acc[j][h] = make_float2(0.f, 0.f);
   }
-  const auto piece = [&](int stage, int array, int j, float (&v)[V]) {
-    unpack<F32>(*slot(stage, array, j), v);
-    pc.mask(lane + j * W * 32, v);
-  };
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) fetch(unit + i * units, i);
   const float inv_d = 1.0f / (float)a.d;
   int side = 0, stage = 0, next = S - 1;
-  for (int64_t row = unit; row < a.M; row += units) {
-    fetch(row + (S - 1) * units, next);
+  for (int64_t row = tm.unit; row < a.M; row += tm.units) {
+    tm.fetch(row + (S - 1) * tm.units, next, a.s, a.dy, a.ds);
     copies_wait<S - 1>();
-    float q = 0.f, p = 0.f;
+    float2 q2 = make_float2(0.f, 0.f), p2 = q2;
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-      if (lane + j * W * 32 >= pc.n) continue;
-      float s[V], g[V];
-      piece(stage, 0, j, s);
-      piece(stage, 1, j, g);
+      const int i = tm.piece(j);
+      if (i >= tm.pc.n) continue;
+      float2 s[H], g[H];
+      unpack<F32>(*tm.slot(stage, 0, j), s);
+      unpack<F32>(*tm.slot(stage, 1, j), g);
+      tm.pc.mask(i, s);
+      tm.pc.mask(i, g);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        q = fmaf(s[e], s[e], q);
-        p = fmaf(g[e] * w[j][e], s[e], p);
+      for (int h = 0; h < H; ++h) {
+        q2 = fma2(s[h], s[h], q2);
+        p2 = fma2(mul2(g[h], w[j][h]), s[h], p2);
       }
     }
-    q = warp_sum(q);
-    p = warp_sum(p);
-    if (W > 1) {
-      if (l == 0) red[side][warp] = make_float2(q, p);
-      // (one barrier a row: the next row writes the other side)
-      if (R == 1) __syncthreads();
-      else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
-      const float2 v = l < W ? red[side][team * W + l] : make_float2(0.f, 0.f);
+    float q = warp_sum(q2.x + q2.y), p = warp_sum(p2.x + p2.y);
+    if (W > 1) {   // (one barrier a row: the next row writes the other side)
+      if (tm.l == 0) red[side][tm.warp] = make_float2(q, p);
+      tm.sync();
+      const float2 v = tm.l < W ? red[side][tm.team * W + tm.l] : make_float2(0.f, 0.f);
       q = warp_sum(v.x);
       p = warp_sum(v.y);
     }
-    const float r = 1.0f / sqrtf(fmaf(q, inv_d, a.eps));
-    const float c = r * r * (p * inv_d);
-    const int64_t first = row * a.d - pc.shift;
+    // t = s r:  dx = ds + r g - t r^2 mean(g s),  dweight += dy t
+    const float r = rsqrtf(fmaf(q, inv_d, a.eps));
+    const float c = -r * r * (p * inv_d);
+    const float2 r2 = make_float2(r, r), c2 = make_float2(c, c);
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-      const int i = lane + j * W * 32;
-      if (i >= pc.n) continue;
-      float s[V], g[V], o[V];
-      piece(stage, 0, j, s);
-      piece(stage, 1, j, g);
+      const int i = tm.piece(j);
+      if (i >= tm.pc.n) continue;
+      float2 t[H], g[H], o[H];
+      unpack<F32>(*tm.slot(stage, 0, j), t);
+      unpack<F32>(*tm.slot(stage, 1, j), g);
+      tm.pc.mask(i, t);
+      tm.pc.mask(i, g);
       if (a.ds) {
-        piece(stage, 2, j, o);
+        unpack<F32>(*tm.slot(stage, 2, j), o);
       } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = 0.f;
+        for (int h = 0; h < H; ++h) o[h] = make_float2(0.f, 0.f);
       }
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        acc[j][e] = fmaf(g[e], s[e] * r, acc[j][e]);
-        o[e] = fmaf(r, fmaf(g[e], w[j][e], -s[e] * c), o[e]);
+      for (int h = 0; h < H; ++h) {
+        t[h] = mul2(t[h], r2);
+        acc[j][h] = fma2(g[h], t[h], acc[j][h]);
+        o[h] = fma2(c2, t[h], fma2(r2, mul2(g[h], w[j][h]), o[h]));
       }
-      pc.store_at(a.dx, first, i, o);
+      tm.pc.store_at(a.dx, tm.first(row), i, o);
     }
     side ^= 1;
-    stage = stage + 1 == S ? 0 : stage + 1;
-    next = next + 1 == S ? 0 : next + 1;
+    stage = tm.after(stage);
+    next = tm.after(next);
   }
   // The CTA's sums, team after team.
   copies_wait<0>();
   __syncthreads();
   float* part = a.part + (int64_t)blockIdx.x * a.d;
-  float* sums = R > 1 ? reinterpret_cast<float*>(ring) + team * a.d : part;
+  float* all = reinterpret_cast<float*>(ring);
+  float* sums = R > 1 ? all + tm.team * a.d : part;
 #pragma unroll
   for (int j = 0; j < P; ++j) {
-    const int i = lane + j * W * 32;
-    if (i >= pc.n) continue;
+    const int i = tm.piece(j);
+    if (i >= tm.pc.n) continue;
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (pc.has(i, e)) sums[pc.col(i) + e] = acc[j][e];
+    for (int h = 0; h < H; ++h) {
+      if (tm.pc.has(i, 2 * h)) sums[tm.pc.col(i) + 2 * h] = acc[j][h].x;
+      if (tm.pc.has(i, 2 * h + 1)) sums[tm.pc.col(i) + 2 * h + 1] = acc[j][h].y;
+    }
   }
   if (R > 1) {
     __syncthreads();
-    for (int c = threadIdx.x; c < a.d; c += T) {
+    for (int c = threadIdx.x; c < a.d; c += Tm::T) {
       float v = 0.f;
 #pragma unroll
-      for (int i = 0; i < R; ++i) v += reinterpret_cast<const float*>(ring)[i * a.d + c];
+      for (int i = 0; i < R; ++i) v += all[i * a.d + c];
       part[c] = v;
     }
   }
@@ -361,61 +483,62 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
 template <bool F32, bool RAGGED>
 __global__ void __launch_bounds__(1024)
 norm_backward_wide_kernel(const __grid_constant__ BackArgs a) {
-  constexpr int V = Row<F32>::kVec;
-  extern __shared__ float acc[];   // [V][pieces]
+  constexpr int H = Row<F32>::kVec / 2;
+  extern __shared__ float2 sums[];   // [H][pieces]
   __shared__ float2 red[2][32];
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   const int warp = threadIdx.x >> 5, l = threadIdx.x & 31;
-  const Pieces<F32, RAGGED> p0(blockIdx.x, a.d);   // (the rows' shift: as above)
+  const Pieces<F32, RAGGED> p0(blockIdx.x, a.d);   // (the rows' shift: see Team::pc)
   for (int i = threadIdx.x; i < p0.n; i += 1024)
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e * p0.n + i] = 0.f;
+    for (int h = 0; h < H; ++h) sums[h * p0.n + i] = make_float2(0.f, 0.f);
   const float inv_d = 1.0f / (float)a.d;
   int side = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, side ^= 1) {
     const Pieces<F32, RAGGED> pc(row, a.d);
-    float q = 0.f, p = 0.f;
+    float2 q2 = make_float2(0.f, 0.f), p2 = q2;
 #pragma unroll 2
     for (int i = threadIdx.x; i < pc.n; i += 1024) {
-      float s[V], g[V], w[V];
+      float2 s[H], g[H], w[H];
       unpack<F32>(pc.load(a.s, a.M, i), s);
       unpack<F32>(pc.load(a.dy, a.M, i), g);
       pc.mask(i, s);
       pc.mask(i, g);
       pc.weight(a.weight, a.weight_f32, i, w);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        q = fmaf(s[e], s[e], q);
-        p = fmaf(g[e] * w[e], s[e], p);
+      for (int h = 0; h < H; ++h) {
+        q2 = fma2(s[h], s[h], q2);
+        p2 = fma2(mul2(g[h], w[h]), s[h], p2);
       }
     }
-    q = warp_sum(q);
-    p = warp_sum(p);
+    float q = warp_sum(q2.x + q2.y), p = warp_sum(p2.x + p2.y);
     if (l == 0) red[side][warp] = make_float2(q, p);
     __syncthreads();
     q = warp_sum(red[side][l].x);
     p = warp_sum(red[side][l].y);
-    const float r = 1.0f / sqrtf(fmaf(q, inv_d, a.eps));
-    const float c = r * r * (p * inv_d);
+    const float r = rsqrtf(fmaf(q, inv_d, a.eps));
+    const float c = -r * r * (p * inv_d);
+    const float2 r2 = make_float2(r, r), c2 = make_float2(c, c);
 #pragma unroll 2
     for (int i = threadIdx.x; i < pc.n; i += 1024) {
-      float s[V], g[V], w[V], o[V];
-      unpack<F32>(pc.load(a.s, a.M, i), s);
+      float2 t[H], g[H], w[H], o[H];
+      unpack<F32>(pc.load(a.s, a.M, i), t);
       unpack<F32>(pc.load(a.dy, a.M, i), g);
-      pc.mask(i, s);
+      pc.mask(i, t);
       pc.mask(i, g);
       pc.weight(a.weight, a.weight_f32, i, w);
       if (a.ds) {
         unpack<F32>(pc.load(a.ds, a.M, i), o);
       } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = 0.f;
+        for (int h = 0; h < H; ++h) o[h] = make_float2(0.f, 0.f);
       }
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        acc[e * pc.n + i] += g[e] * (s[e] * r);
-        o[e] = fmaf(r, fmaf(g[e], w[e], -s[e] * c), o[e]);
+      for (int h = 0; h < H; ++h) {
+        t[h] = mul2(t[h], r2);
+        sums[h * pc.n + i] = fma2(g[h], t[h], sums[h * pc.n + i]);
+        o[h] = fma2(c2, t[h], fma2(r2, mul2(g[h], w[h]), o[h]));
       }
       pc.store(a.dx, i, o);
     }
@@ -423,8 +546,11 @@ norm_backward_wide_kernel(const __grid_constant__ BackArgs a) {
   float* part = a.part + (int64_t)blockIdx.x * a.d;
   for (int i = threadIdx.x; i < p0.n; i += 1024)
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (p0.has(i, e)) part[p0.col(i) + e] = acc[e * p0.n + i];
+    for (int h = 0; h < H; ++h) {
+      const float2 v = sums[h * p0.n + i];
+      if (p0.has(i, 2 * h)) part[p0.col(i) + 2 * h] = v.x;
+      if (p0.has(i, 2 * h + 1)) part[p0.col(i) + 2 * h + 1] = v.y;
+    }
 }
 
 constexpr int kSumCols = 32, kSumRows = 32;
@@ -439,7 +565,7 @@ dweight_kernel(const float* __restrict__ part, int n, int d, void* __restrict__ 
   const int c = blockIdx.x * kSumCols + x;
   float v = 0.f;
   if (c < d) {
-#pragma unroll 4
+#pragma unroll 5
     for (int i = y; i < n; i += kSumRows) v += part[(int64_t)i * d + c];
   }
   red[y][x] = v;
@@ -452,48 +578,24 @@ dweight_kernel(const float* __restrict__ part, int n, int d, void* __restrict__ 
   }
 }
 
-// How the gradient's rows are dealt out: W warps to a row (0: the wide kernel),
-// `grid` CTAs.
-struct BackShape {
-  int warps, grid;
-};
-BackShape back_shape(int64_t M, int64_t d, bool f32, int num_sms) {
-  const int vec = f32 ? 4 : 8;
-  const int64_t pieces = d % vec ? d / vec + 2 : d / vec;
-  int w = 1;
-  while (w <= 32 && 32 * kBackPieces * w < pieces) w *= 2;
-  const int rows = w > 32 ? 1 : back_threads(w) / 32 / w;
-  int64_t grid = (M + rows - 1) / rows;
-  const int64_t most = (int64_t)num_sms * (w > 32 ? 1 : back_ctas(w)) / 8 * 8;
-  if (grid > most) grid = most;
-  return {w > 32 ? 0 : w, (int)grid};
-}
-
-template <bool F32, int W, bool RAGGED>
-cudaError_t launch_back_warps(const BackArgs& a, int grid, cudaStream_t st) {
-  const auto k = norm_backward_kernel<F32, W, RAGGED>;
-  size_t smem = (size_t)back_stages(W) * (a.ds ? 3 : 2) * kBackPieces * back_threads(W) * 16;
-  static_assert(back_stages(W) * 2 * kBackPieces * 16 * 32 * W >= 512 * W * 4, "no room for the sums");
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  return launch_chained(k, dim3(grid), dim3(back_threads(W)), smem, st, a);
-}
-
 template <bool F32, bool RAGGED>
-cudaError_t launch_back(const BackArgs& a, const BackShape& s, cudaStream_t st) {
-  switch (s.warps) {
-    case 1: return launch_back_warps<F32, 1, RAGGED>(a, s.grid, st);
-    case 2: return launch_back_warps<F32, 2, RAGGED>(a, s.grid, st);
-    case 4: return launch_back_warps<F32, 4, RAGGED>(a, s.grid, st);
-    case 8: return launch_back_warps<F32, 8, RAGGED>(a, s.grid, st);
-    case 16: return launch_back_warps<F32, 16, RAGGED>(a, s.grid, st);
-    case 32: return launch_back_warps<F32, 32, RAGGED>(a, s.grid, st);
+cudaError_t launch_back(const BackArgs& a, int grid, cudaStream_t st) {
+  const int w = team_warps(a.d, Row<F32>::kVec), arrays = a.ds ? 3 : 2;
+  // (the teams' sums take the place of their stages: R rows of at most 512 W
+  // elements, 2 KB, and each stage has as much)
+  switch (w) {
+    case 1: return launch_team(norm_backward_kernel<F32, 1, RAGGED>, a, w, arrays, grid, st);
+    case 2: return launch_team(norm_backward_kernel<F32, 2, RAGGED>, a, w, arrays, grid, st);
+    case 4: return launch_team(norm_backward_kernel<F32, 4, RAGGED>, a, w, arrays, grid, st);
+    case 8: return launch_team(norm_backward_kernel<F32, 8, RAGGED>, a, w, arrays, grid, st);
+    case 16: return launch_team(norm_backward_kernel<F32, 16, RAGGED>, a, w, arrays, grid, st);
+    case 32: return launch_team(norm_backward_kernel<F32, 32, RAGGED>, a, w, arrays, grid, st);
   }
   const auto k = norm_backward_wide_kernel<F32, RAGGED>;
-  const size_t smem = (size_t)(a.d + 16) * sizeof(float);
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const int smem = (a.d + 16) * (int)sizeof(float);
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_chained(k, dim3(s.grid), dim3(1024), smem, st, a);
+  return launch_chained(k, dim3(grid), dim3(1024), smem, st, a);
 }
 
 }  // namespace
@@ -502,32 +604,32 @@ cudaError_t launch_rms_norm(const NormCall& c, int num_sms, cudaStream_t st) {
   if (c.M == 0 || c.d == 0) return cudaSuccess;
   const NormArgs a{c.x, c.residual, c.weight, c.out, c.scales, c.sum, c.M, (int)c.d, c.eps,
                    c.weight_f32};
-  const int vec = c.f32 ? 4 : 8;
-  const bool ragged = c.d % vec != 0;
-  const int64_t pieces = ragged ? c.d / vec + 2 : c.d / vec;
-  const Shape s = shape_of(pieces, vec, c.M, num_sms);
-  return c.f32 ? launch_type<true>(a, c.scales != nullptr, ragged, s, st)
-               : launch_type<false>(a, c.scales != nullptr, ragged, s, st);
+  if (c.f32)
+    return c.scales ? launch_rows<true, true>(a, num_sms, st)
+                    : launch_rows<true, false>(a, num_sms, st);
+  return c.scales ? launch_rows<false, true>(a, num_sms, st)
+                  : launch_rows<false, false>(a, num_sms, st);
 }
 
-size_t rms_norm_backward_bytes(int64_t M, int64_t d, int f32, int num_sms) {
-  return (size_t)back_shape(M, d, f32 != 0, num_sms).grid * (size_t)d * sizeof(float);
+size_t rms_norm_backward_bytes(int64_t M, int64_t d, int num_sms) {
+  return (size_t)team_grid(M, num_sms) * (size_t)d * sizeof(float);
 }
 
 cudaError_t launch_rms_norm_backward(const NormBackwardCall& c, float* part, int num_sms,
                                      cudaStream_t st) {
   if (c.d == 0) return cudaSuccess;
-  const BackShape s = back_shape(c.M, c.d, c.f32 != 0, num_sms);
+  const int grid = team_grid(c.M, num_sms);
   if (c.M > 0) {
     const BackArgs a{c.dy, c.s, c.weight, c.ds, c.dx, part, c.M, (int)c.d, c.eps, c.weight_f32};
     const bool ragged = c.d % (c.f32 ? 4 : 8) != 0;
     const cudaError_t e =
-        c.f32 ? (ragged ? launch_back<true, true>(a, s, st) : launch_back<true, false>(a, s, st))
-              : (ragged ? launch_back<false, true>(a, s, st) : launch_back<false, false>(a, s, st));
+        c.f32 ? (ragged ? launch_back<true, true>(a, grid, st) : launch_back<true, false>(a, grid, st))
+              : (ragged ? launch_back<false, true>(a, grid, st)
+                        : launch_back<false, false>(a, grid, st));
     if (e != cudaSuccess) return e;
   }
   return launch_chained(dweight_kernel, dim3((unsigned)((c.d + kSumCols - 1) / kSumCols)),
-                        dim3(kSumCols * kSumRows), 0, st, (const float*)part, s.grid, (int)c.d,
+                        dim3(kSumCols * kSumRows), 0, st, (const float*)part, grid, (int)c.d,
                         c.dweight, c.weight_f32);
 }
 

@@ -15,16 +15,14 @@
 // Rows are moved in 16-byte pieces that start on 16-byte boundaries of the
 // tensor that is written.  Where a row's bytes are no multiple of 16 (RAGGED),
 // the source starts elsewhere in its 16 bytes: two of its pieces are read (the
-// second is a neighbour's first, from L1) and shifted together.
+// second is the next thread's first, from L1) and shifted together.
 #include "rows.cuh"
 #include "rows.h"
 
 namespace swg {
 namespace {
 
-constexpr int kBatch = 8;   // choices whose loads are in flight together
-
-// A CTA has blockDim.y tokens, blockDim.x threads for a piece of each row.
+// A CTA has blockDim.y tokens, blockDim.x threads (whole warps) for a piece of each row.
 __device__ __forceinline__ int64_t token() {
   return (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
 }
@@ -34,7 +32,32 @@ __device__ __forceinline__ int64_t sorted_end(const int* offsets, int E, int64_t
   return n < 0 ? 0 : n < rows ? n : rows;
 }
 
-// Rows of `bytes` bytes (a multiple of sizeof(E)), row r's at byte r * bytes.
+// A token's choices (k <= 32), one per lane: place (-1: none) and weight, which
+// a warp reads once and hands around.
+struct Choices {
+  int p;
+  float w;
+  __device__ __forceinline__ Choices(const int* position, const float* weights, int64_t t, int k,
+                                     int64_t rows)
+      : p(-1), w(0.f) {
+    const int l = threadIdx.x & 31;
+    if (l < k) {
+      p = position[t * k + l];
+      if (p >= rows) p = -1;
+      if (p >= 0) w = weights ? weights[t * k + l] : 1.f;
+    }
+  }
+  __device__ __forceinline__ int place(int j) const { return __shfl_sync(0xffffffffu, p, j); }
+  __device__ __forceinline__ float weight(int j) const { return __shfl_sync(0xffffffffu, w, j); }
+};
+
+// 16 bytes that may be in two pieces of their tensor.
+struct Two {
+  uint4 lo, hi;
+};
+
+// Rows of `bytes` bytes (a multiple of sizeof(E)); this one in 16-byte pieces
+// that start on 16-byte boundaries of its tensor.
 template <typename E, bool RAGGED>
 struct Span16 {
   int64_t base;     // the row's first byte
@@ -45,15 +68,33 @@ struct Span16 {
     shift = RAGGED ? (int)(base & 15) : 0;
     n = RAGGED ? (shift + bytes_ + 15) / 16 : bytes_ / 16;
   }
-  // Bytes 16 i - shift ... of row `src`, that is, what piece i of this row would
-  // be if it held that row; neighbours' bytes where they are not the row's.
-  __device__ __forceinline__ uint4 of(const void* p, int64_t src, int64_t total, int i) const {
+  // What piece i of this row would be if it held row `src` of the tensor of
+  // `total` bytes at `p`: the loads, and afterwards the value, with neighbours'
+  // bytes where they are not the row's.  (In two steps, and without a branch
+  // around the loads, so that the loads of several rows are under way together.
+  // The tensor's last bytes, where they fill no 16, are read one by one.)
+  __device__ __forceinline__ Two begin(const void* p, int64_t src, int64_t total, int i) const {
     const int64_t at = src * bytes + (int64_t)i * 16 - shift;
-    if (!RAGGED) return __ldg(reinterpret_cast<const uint4*>((const char*)p + at));
+    Two q;
+    if (!RAGGED) {
+      q.lo = load_once((const char*)p + at);
+    } else {
+      const int64_t last = (total & ~(int64_t)15) - 16, a0 = at & ~(int64_t)15;
+      const int64_t l = a0 < 0 ? 0 : a0 < last ? a0 : last, h = a0 + 16 < last ? a0 + 16 : last;
+      if (last >= 0) {
+        q.lo = *reinterpret_cast<const uint4*>((const char*)p + l);
+        q.hi = *reinterpret_cast<const uint4*>((const char*)p + h);
+      }
+    }
+    return q;
+  }
+  __device__ __forceinline__ uint4 end(const Two& q, const void* p, int64_t src, int64_t total,
+                                       int i) const {
+    if (!RAGGED) return q.lo;
+    const int64_t at = src * bytes + (int64_t)i * 16 - shift, a0 = at & ~(int64_t)15;
     const int sh = (int)(at & 15);
-    const uint4 lo = load_inside<E>(p, at - sh, total);
-    if (sh == 0) return lo;
-    return shift_bytes(lo, load_inside<E>(p, at - sh + 16, total), sh);
+    if (a0 + 32 <= total) return shift_bytes(q.lo, q.hi, sh);
+    return shift_bytes(load_inside<E>(p, a0, total), load_inside<E>(p, a0 + 16, total), sh);
   }
   __device__ __forceinline__ void put(void* p, int i, const uint4& q) const {
     char* o = (char*)p + base + (int64_t)i * 16 - shift;
@@ -74,12 +115,12 @@ struct Span16 {
   }
 };
 
-template <typename E, bool RAGGED>
+// Rows of whole 16-byte pieces, `per` of them.
 __global__ void __launch_bounds__(256)
-permute_kernel(const void* __restrict__ x, const float* __restrict__ scales,
+permute_kernel(const uint4* __restrict__ x, const float* __restrict__ scales,
                const int* __restrict__ position, const int* __restrict__ offsets,
-               void* __restrict__ out, float* __restrict__ out_scales, int64_t T, int k, int n_exp,
-               int bytes) {
+               uint4* __restrict__ out, float* __restrict__ out_scales, int64_t T, int k, int n_exp,
+               int per) {
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   const int64_t t = token();
@@ -87,28 +128,12 @@ permute_kernel(const void* __restrict__ x, const float* __restrict__ scales,
   const int64_t rows = T * k, end = sorted_end(offsets, n_exp, rows), f0 = t * k;
   const int* pos = position + f0;
   const int w0 = blockIdx.y * blockDim.x + threadIdx.x, step = gridDim.y * blockDim.x;
-  if constexpr (RAGGED) {
+  for (int w = w0; w < per; w += step) {
+    const uint4 v = __ldg(x + t * per + w);
     for (int j = 0; j < k; ++j) {
       const int p = pos[j];
-      if (p >= 0 && p < rows) {
-        const Span16<E, true> o(p, bytes);
-        for (int i = w0; i < o.n; i += step) o.put(out, i, o.of(x, t, T * bytes, i));
-      }
-      if (f0 + j >= end) {
-        const Span16<E, true> o(f0 + j, bytes);
-        for (int i = w0; i < o.n; i += step) o.put(out, i, make_uint4(0u, 0u, 0u, 0u));
-      }
-    }
-  } else {
-    const int per = bytes / 16;
-    uint4* o = (uint4*)out;
-    for (int w = w0; w < per; w += step) {
-      const uint4 v = __ldg((const uint4*)x + t * per + w);
-      for (int j = 0; j < k; ++j) {
-        const int p = pos[j];
-        if (p >= 0 && p < rows) o[(int64_t)p * per + w] = v;
-        if (f0 + j >= end) o[(f0 + j) * per + w] = make_uint4(0u, 0u, 0u, 0u);
-      }
+      if (p >= 0 && p < rows) out[(int64_t)p * per + w] = v;
+      if (f0 + j >= end) out[(f0 + j) * per + w] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
   if (scales && w0 == 0) {
@@ -121,51 +146,317 @@ permute_kernel(const void* __restrict__ x, const float* __restrict__ scales,
   }
 }
 
+// ---- rows that stream through a warp ---------------------------------------------
+//
+// A warp takes items (a token and 32 U pieces of its row) one after the other,
+// B choices at a time, and copies what the next steps need (cp.async) into its
+// own slots in shared memory while it works on one: no barrier but the warp's,
+// no registers for what is under way, and a row that starts elsewhere in its 16
+// bytes is read once, each thread taking its second half from its neighbour's
+// slot.
+
+constexpr int kWarps = 12;          // of unpermute's CTA, one CTA per SM
+constexpr int kPermuteWarps = 16;   // of permute's for ragged rows, two per SM
+
+// Pieces m of 16 bytes from byte `at` of a tensor of `total` bytes into
+// slots[m], m < count <= N; zero where they are outside it.
+template <bool RAGGED, int N>
+__device__ __forceinline__ void copy_row(uint4* slots, const void* p, int64_t at, int64_t total,
+                                         int count, int l) {
+  const char* src = (const char*)p + at;
+  const bool inside = !RAGGED || (at >= 0 && at + (int64_t)count * 16 <= total);
+#pragma unroll
+  for (int i = 0; i < (N + 31) / 32; ++i) {
+    const int m = l + 32 * i;
+    if (m >= count || m >= N) continue;
+    if (inside) {
+      copy_piece(slots + m, src + m * 16, 16);
+    } else {
+      const int64_t a = at + m * 16;
+      const int bytes = a < 0 || a >= total ? 0 : total - a < 16 ? (int)(total - a) : 16;
+      copy_piece(slots + m, bytes ? src + m * 16 : (const char*)p, bytes);
+    }
+  }
+}
+
+// The steps of a warp: tokens t, `segs` segments of their rows, and choices j,
+// j + 1, ... j + B - 1 of k (at least one step to a segment).
+template <int B>
+struct Steps {
+  int64_t t, dt;
+  int seg, segs, dseg, j, k;
+  __device__ __forceinline__ Steps(int segs_, int k_) : segs(segs_), j(0), k(k_) {
+    const int64_t g = (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+    const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
+    t = g / segs;
+    seg = (int)(g - t * segs);
+    dt = step / segs;
+    dseg = (int)(step - dt * segs);
+  }
+  __device__ __forceinline__ bool last() const { return j + B >= k; }
+  __device__ __forceinline__ void next() {
+    j += B;
+    if (j < k) return;
+    j = 0;
+    t += dt;
+    seg += dseg;
+    if (seg >= segs) {
+      seg -= segs;
+      ++t;
+    }
+  }
+};
+
+// Ragged permute: a warp's stages hold 64 pieces of a token's row, with one more
+// on either side; the token's choices are copied S - 1 steps earlier.
+struct PermuteSlots {
+  static constexpr int S = 4, C = 2 * S - 1, U = 2;
+  uint4 x[S][32 * U + 2];
+  float scale[S][4];
+  int place[C][32];
+};
+
+template <typename E>
+__global__ void __launch_bounds__(32 * kPermuteWarps, 2)
+permute_ragged_kernel(const void* __restrict__ x, const float* __restrict__ scales,
+                      const int* __restrict__ position, const int* __restrict__ offsets,
+                      void* __restrict__ out, float* __restrict__ out_scales, int64_t T, int k,
+                      int n_exp, int bytes, int segs) {
+  constexpr int S = PermuteSlots::S, C = PermuteSlots::C, U = PermuteSlots::U;
+  extern __shared__ uint4 smem[];
+  tc::pdl_launch_dependents();
+  tc::pdl_wait();
+  const int l = threadIdx.x & 31;
+  PermuteSlots& slots = reinterpret_cast<PermuteSlots*>(smem)[threadIdx.x >> 5];
+  const int64_t rows = T * k, end = sorted_end(offsets, n_exp, rows);
+  Steps<32> ask(segs, 1), in(segs, 1), out_s(segs, 1);   // (all choices in one step)
+  int ask_c = 0, out_c = 0;
+  const auto choices = [&]() {
+    if (l < k) copy_word(&slots.place[ask_c][l], position + (ask.t < T ? ask.t * k + l : 0), ask.t < T);
+    ask.next();
+    ask_c = ask_c + 1 == C ? 0 : ask_c + 1;
+  };
+  const auto fetch = [&](int stage) {
+    if (in.t < T) {
+      const int64_t base = in.t * bytes;
+      copy_row<true, 32 * U + 2>(slots.x[stage], x, (base & ~(int64_t)15) + ((int64_t)in.seg * 32 * U - 1) * 16,
+                                 T * bytes, 32 * U + 2, l);
+      if (scales && l == 0) copy_word(&slots.scale[stage][0], scales + in.t, true);
+    }
+    in.next();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) choices();
+  copies_commit();
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) {
+    fetch(i);
+    choices();
+    copies_commit();
+  }
+  int stage = 0, free_stage = S - 1;
+  while (out_s.t < T) {
+    copies_wait<S - 2>();
+    __syncwarp();
+    fetch(free_stage);
+    choices();
+    copies_commit();
+    const int64_t t = out_s.t, f0 = t * k, src = t * bytes;
+    const int i0 = out_s.seg * 32 * U;
+    for (int j = 0; j < k; ++j) {
+      const int p = slots.place[out_c][j];
+      if (p >= 0 && p < rows) {
+        const Span16<E, true> o(p, bytes);
+        // piece i of the output is in the source's pieces i + off and i + off + 1
+        const int off = (int)(((src - o.shift) >> 4) - (src >> 4));
+        const int sh = (int)((src - o.shift) & 15);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int m = l + 32 * u;
+          if (i0 + m < o.n)
+            o.put(out, i0 + m, shift_bytes(slots.x[stage][m + 1 + off], slots.x[stage][m + 2 + off], sh));
+        }
+        if (scales && out_s.seg == 0 && l == 0) out_scales[p] = slots.scale[stage][0];
+      }
+      if (f0 + j >= end) {
+        const Span16<E, true> o(f0 + j, bytes);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i0 + l + 32 * u < o.n) o.put(out, i0 + l + 32 * u, make_uint4(0u, 0u, 0u, 0u));
+        if (scales && out_s.seg == 0 && l == 0) out_scales[f0 + j] = 0.f;
+      }
+    }
+    out_s.next();
+    out_c = out_c + 1 == C ? 0 : out_c + 1;
+    stage = stage + 1 == S ? 0 : stage + 1;
+    free_stage = free_stage + 1 == S ? 0 : free_stage + 1;
+  }
+}
+
+// Few pieces: each has a thread of its own, and nothing is copied ahead.
 template <bool F32, bool RAGGED>
-__global__ void __launch_bounds__(256, RAGGED ? 2 : 4)
-unpermute_kernel(const void* __restrict__ z, const int* __restrict__ position,
-                 const float* __restrict__ weights, const void* residual, void* y, int64_t T, int k,
-                 int bytes) {
+__global__ void __launch_bounds__(256)
+unpermute_few_kernel(const void* __restrict__ z, const int* __restrict__ position,
+                     const float* __restrict__ weights, const void* residual, void* y, int64_t T,
+                     int k, int bytes) {
   using E = typename Row<F32>::elem;
-  constexpr int V = Row<F32>::kVec;
+  constexpr int H = Row<F32>::kVec / 2, B = 8;
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   const int64_t t = token();
   if (t >= T) return;
   const int64_t rows = T * k;
-  const int* pos = position + t * k;
-  const float* wt = weights ? weights + t * k : nullptr;
+  const Choices ch(position, weights, t, k, rows);
   const Span16<E, RAGGED> o(t, bytes);
-  for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < o.n; i += gridDim.y * blockDim.x) {
-    // (the residual is used only after the first rows' loads are under way)
-    uint4 rq = make_uint4(0u, 0u, 0u, 0u);
-    if (residual) {
-      const int64_t at = o.base - o.shift + (int64_t)i * 16;
-      rq = RAGGED ? load_inside<E>(residual, at, T * bytes) : load_once((const char*)residual + at);
+  const int i = blockIdx.y * blockDim.x + threadIdx.x;
+  uint4 rq = make_uint4(0u, 0u, 0u, 0u);
+  if (residual && i < o.n) rq = load_inside<E>(residual, o.base - o.shift + (int64_t)i * 16, T * bytes);
+  float2 acc[H];
+  unpack<F32>(rq, acc);
+  for (int j0 = 0; j0 < k; j0 += B) {
+    Two q[B];
+    int p[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      p[b] = ch.place(j0 + b);
+      if (p[b] >= 0 && i < o.n) q[b] = o.begin(z, p[b], rows * bytes, i);
     }
-    float acc[V];
-    for (int j0 = 0; j0 == 0 || j0 < k; j0 += kBatch) {
-      uint4 q[kBatch];
-      float c[kBatch];
-      bool live[kBatch];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int p = j0 + b < k ? pos[j0 + b] : -1;
-        live[b] = p >= 0 && p < rows;
-        c[b] = !live[b] ? 0.f : wt ? wt[j0 + b] : 1.f;
-        if (live[b]) q[b] = o.of(z, p, rows * bytes, i);
+    for (int b = 0; b < B; ++b) {
+      const float c = ch.weight(j0 + b);
+      if (p[b] < 0 || i >= o.n) continue;
+      float2 v[H];
+      unpack<F32>(o.end(q[b], z, p[b], rows * bytes, i), v);
+#pragma unroll
+      for (int h = 0; h < H; ++h) acc[h] = fma2(make_float2(c, c), v[h], acc[h]);
+    }
+  }
+  if (i < o.n) o.put(y, i, pack<F32>(acc));
+}
+
+// What a warp of unpermute keeps: S stages of pieces, and the steps' choices,
+// which are copied S - 1 steps before the rows that they name.
+template <bool F32, bool RAGGED, int B, int U>
+struct UnpermuteSlots {
+  static constexpr int S = U == 1 && !RAGGED ? 4 : 3, C = 2 * S - 1;
+  uint4 z[S][B][32 * U + (RAGGED ? 1 : 0)];
+  uint4 residual[S][32 * U];
+  int place[C][8];
+  float weight[C][8];
+};
+
+// B choices of U pieces each to a step.
+template <bool F32, bool RAGGED, int B, int U>
+__global__ void __launch_bounds__(32 * kWarps, 1)
+unpermute_kernel(const void* __restrict__ z, const int* __restrict__ position,
+                 const float* __restrict__ weights, const void* residual, void* y, int64_t T, int k,
+                 int bytes, int segs) {
+  using E = typename Row<F32>::elem;
+  using Slots = UnpermuteSlots<F32, RAGGED, B, U>;
+  constexpr int H = Row<F32>::kVec / 2, S = Slots::S, C = Slots::C;
+  extern __shared__ uint4 smem[];
+  tc::pdl_launch_dependents();
+  tc::pdl_wait();
+  const int l = threadIdx.x & 31;
+  Slots& slots = reinterpret_cast<Slots*>(smem)[threadIdx.x >> 5];
+  const int64_t rows = T * k;
+
+  Steps<B> ask(segs, k), in(segs, k), out(segs, k);   // choices copied, rows copied, at work
+  int ask_c = 0, in_c = 0, out_c = 0;                 // ... and their places among the C
+  const auto choices = [&]() {   // lanes 0 ... B - 1: places, 8 ... 8 + B - 1: weights
+    const int b = l & 7;
+    if (l < 16 && b < B) {
+      const bool some = ask.t < T && ask.j + b < k;
+      const int64_t f = some ? ask.t * k + ask.j + b : 0;
+      if (l < 8) copy_word(&slots.place[ask_c][b], position + f, some);
+      else if (weights) copy_word(&slots.weight[ask_c][b], weights + f, some);
+    }
+    ask.next();
+    ask_c = ask_c + 1 == C ? 0 : ask_c + 1;
+  };
+  // Choice b of a step as copied: its place, or -1.
+  const auto place = [&](const Steps<B>& s, int c, int b) {
+    const int p = slots.place[c][b];
+    return s.j + b < k && p >= 0 && p < rows ? p : -1;
+  };
+  const auto fetch = [&](int stage) {
+    if (in.t < T) {
+      const Span16<E, RAGGED> o(in.t, bytes);
+      const int i0 = in.seg * 32 * U;
+      const int count = o.n - i0 < 32 * U ? o.n - i0 : 32 * U;
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int p = place(in, in_c, b);
+        if (p < 0) continue;
+        const int64_t at = (int64_t)p * bytes + (int64_t)i0 * 16 - o.shift;
+        copy_row<RAGGED, 32 * U + (RAGGED ? 1 : 0)>(slots.z[stage][b], z, at & ~(int64_t)15,
+                                                    rows * bytes, RAGGED ? count + 1 : count, l);
       }
-      if (j0 == 0) unpack<F32>(rq, acc);
+      if (residual && in.j == 0)
+        copy_row<RAGGED, 32 * U>(slots.residual[stage], residual,
+                                 o.base - o.shift + (int64_t)i0 * 16, T * bytes, count, l);
+    }
+    in.next();
+    in_c = in_c + 1 == C ? 0 : in_c + 1;
+  };
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        if (!live[b]) continue;
-        float v[V];
-        unpack<F32>(q[b], v);
+  for (int i = 0; i < S - 1; ++i) choices();
+  copies_commit();
+  copies_wait<0>();
+  __syncwarp();
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(c[b], v[e], acc[e]);
+  for (int i = 0; i < S - 1; ++i) {
+    fetch(i);
+    choices();
+    copies_commit();
+  }
+  int stage = 0, free_stage = S - 1;
+  float2 acc[U][H];
+  while (out.t < T) {
+    // this step's rows are here, and the choices of the step S - 1 ahead
+    copies_wait<S - 2>();
+    __syncwarp();
+    fetch(free_stage);
+    choices();
+    copies_commit();
+    const Span16<E, RAGGED> o(out.t, bytes);
+    const int i0 = out.seg * 32 * U;
+    if (out.j == 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (residual) {
+          unpack<F32>(slots.residual[stage][l + 32 * u], acc[u]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < H; ++h) acc[u][h] = make_float2(0.f, 0.f);
+        }
       }
     }
-    o.put(y, i, pack<F32>(acc));
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int p = place(out, out_c, b);
+      if (p < 0) continue;
+      const float w = weights ? slots.weight[out_c][b] : 1.f;
+      const int sh = RAGGED ? (int)(((int64_t)p * bytes - o.shift) & 15) : 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        uint4 q = slots.z[stage][b][l + 32 * u];
+        if (RAGGED) q = shift_bytes(q, slots.z[stage][b][l + 32 * u + 1], sh);
+        float2 v[H];
+        unpack<F32>(q, v);
+#pragma unroll
+        for (int h = 0; h < H; ++h) acc[u][h] = fma2(make_float2(w, w), v[h], acc[u][h]);
+      }
+    }
+    if (out.last()) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + l + 32 * u < o.n) o.put(y, i0 + l + 32 * u, pack<F32>(acc[u]));
+    }
+    out.next();
+    out_c = out_c + 1 == C ? 0 : out_c + 1;
+    stage = stage + 1 == S ? 0 : stage + 1;
+    free_stage = free_stage + 1 == S ? 0 : free_stage + 1;
   }
 }
 
@@ -189,16 +480,18 @@ __device__ __forceinline__ float warp_sums8(float (&v)[8], int lane) {
 }
 
 // blockDim.x threads to a token; the warps' sums of the dot products meet in
-// shared memory.
-template <bool F32, bool RAGGED>
-__global__ void __launch_bounds__(256, RAGGED ? 2 : 3)
+// shared memory.  B, U: as above.  Ragged rows are taken in the pieces of z's
+// and dz's row, so that these move as they are and dy is shifted.
+template <bool F32, bool RAGGED, int B, int U>
+__global__ void __launch_bounds__(256, 3)
 unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ z,
                           const int* __restrict__ position, const int* __restrict__ offsets,
                           const float* __restrict__ weights, void* __restrict__ dz,
                           float* __restrict__ dweights, int64_t T, int k, int n_exp, int bytes) {
   using E = typename Row<F32>::elem;
-  constexpr int V = Row<F32>::kVec;
-  __shared__ float red[8][kBatch];   // by warp of the CTA
+  constexpr int V = Row<F32>::kVec, H = V / 2;
+  __shared__ float red[8][8];   // by warp of the CTA
+  __shared__ uint4 dys[RAGGED ? 8 : 1][RAGGED ? 32 * U + 2 : 1];   // ragged: a warp's pieces of dy
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   const int64_t t = token();
@@ -206,64 +499,88 @@ unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ 
   const int64_t rows = T * k, end = sorted_end(offsets, n_exp, rows), f0 = t * k;
   const int warps = blockDim.x >> 5;   // of a token
   const int warp = (threadIdx.y * blockDim.x + threadIdx.x) >> 5, l = threadIdx.x & 31;
-  for (int j0 = 0; j0 < k; j0 += kBatch) {
-    int p[kBatch];
-    float c[kBatch], dot[kBatch];
+  const Choices ch(position, weights, t, here ? k : 0, rows);
+  const int most = RAGGED ? bytes / 16 + 2 : bytes / 16;   // pieces of a row
+  for (int j0 = 0; j0 < k; j0 += B) {
+    int p[B];
+    float c[B], dot[8];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const bool in = here && j0 + b < k;
-      p[b] = in ? position[f0 + j0 + b] : -1;
-      if (p[b] >= rows) p[b] = -1;
-      c[b] = in && p[b] >= 0 ? weights[f0 + j0 + b] : 0.f;
-      dot[b] = 0.f;
+    for (int b = 0; b < 8; ++b) dot[b] = 0.f;
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      p[b] = ch.place(j0 + b);
+      c[b] = ch.weight(j0 + b);
     }
-    if constexpr (RAGGED) {
-      // in the pieces of z's and dz's row, so that these move as they are
+    // (pieces i0, i0 + 32, ... of this lane; ragged: the warp's neighbours are its own)
+    for (int w0 = (warp - threadIdx.y * warps) * 32 * U; here && w0 < most; w0 += U * blockDim.x) {
+      uint4 q[B][U];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        if (p[b] >= 0) {
-          const Span16<E, true> o(p[b], bytes);
-          for (int i = threadIdx.x; i < o.n; i += blockDim.x) {
-            const uint4 zq = load_inside<E>(z, o.base - o.shift + (int64_t)i * 16, rows * bytes);
-            float g[V], v[V];
-            unpack<F32>(o.of(dy, t, T * bytes, i), g);
-            unpack<F32>(zq, v);
-            const int c0 = i * V - o.shift / (16 / V), d = bytes / (16 / V);
+      for (int b = 0; b < B; ++b) {
+        const Span16<E, RAGGED> o(p[b], bytes);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-              const bool own = c0 + e >= 0 && c0 + e < d;
-              dot[b] = own ? fmaf(g[e], v[e], dot[b]) : dot[b];
-              g[e] *= c[b];
-            }
-            o.put(dz, i, pack<F32>(g));
-          }
+        for (int u = 0; u < U; ++u) {
+          const int i = w0 + l + 32 * u;
+          if (p[b] < 0 || i >= o.n) continue;
+          const int64_t at = o.base - o.shift + (int64_t)i * 16;
+          // (the tensor's last row may end inside 16 bytes)
+          if (!RAGGED || p[b] + 1 < rows) q[b][u] = load_once((const char*)z + at);
+          else q[b][u] = load_inside<E>(z, at, rows * bytes);
         }
       }
-    } else {
-      for (int i = threadIdx.x; here && i < bytes / 16; i += blockDim.x) {
-        uint4 q[kBatch];
-        const uint4 gq = __ldg(reinterpret_cast<const uint4*>((const char*)dy + t * bytes) + i);
+      float2 g[RAGGED ? 1 : U][H];
+      const int64_t src = t * bytes;
+      if constexpr (RAGGED) {
+        __syncwarp();
+        for (int m = l; m < 32 * U + 2; m += 32)
+          dys[warp][m] = load_inside<E>(dy, (src & ~(int64_t)15) + (int64_t)(w0 + m - 1) * 16, T * bytes);
+        __syncwarp();
+      } else {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-          if (p[b] >= 0) q[b] = load_once((const char*)z + (int64_t)p[b] * bytes + (int64_t)i * 16);
-        float g[V];
-        unpack<F32>(gq, g);
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          if (p[b] < 0) continue;
-          float v[V];
-          unpack<F32>(q[b], v);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            dot[b] = fmaf(g[e], v[e], dot[b]);
-            v[e] = c[b] * g[e];
-          }
-          *reinterpret_cast<uint4*>((char*)dz + (int64_t)p[b] * bytes + (int64_t)i * 16) = pack<F32>(v);
+        for (int u = 0; u < U; ++u) {
+          const int i = w0 + l + 32 * u;
+          if (i < most) unpack<F32>(__ldg(reinterpret_cast<const uint4*>((const char*)dy + src) + i), g[u]);
         }
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        if (p[b] < 0) continue;
+        const Span16<E, RAGGED> o(p[b], bytes);
+        const int off = RAGGED ? (int)(((src - o.shift) >> 4) - (src >> 4)) : 0;
+        const int sh = RAGGED ? (int)((src - o.shift) & 15) : 0;
+        float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = w0 + l + 32 * u;
+          if (i >= o.n) continue;
+          float2 v[H], m[H];
+          unpack<F32>(q[b][u], v);
+          if constexpr (RAGGED) {
+            const uint4* d4 = &dys[warp][l + 32 * u + 1 + off];
+            unpack<F32>(shift_bytes(d4[0], d4[1], sh), m);
+            const int c0 = i * V - o.shift / (16 / V), d = bytes / (16 / V);
+            if (c0 < 0 || c0 + V > d) {   // (v, m: not neighbours' values, which may be NaN)
+#pragma unroll
+              for (int h = 0; h < H; ++h) {
+                if (c0 + 2 * h < 0 || c0 + 2 * h >= d) v[h].x = m[h].x = 0.f;
+                if (c0 + 2 * h + 1 < 0 || c0 + 2 * h + 1 >= d) v[h].y = m[h].y = 0.f;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < H; ++h) m[h] = g[u][h];
+          }
+#pragma unroll
+          for (int h = 0; h < H; ++h) {
+            s = fma2(m[h], v[h], s);
+            v[h] = mul2(make_float2(c[b], c[b]), m[h]);
+          }
+          o.put(dz, i, pack<F32>(v));
+        }
+        dot[b] += s.x + s.y;
       }
     }
     // rows of no pair
-    for (int j = j0; here && j < k && j < j0 + kBatch; ++j) {
+    for (int j = j0; here && j < k && j < j0 + B; ++j) {
       if (f0 + j < end) continue;
       const Span16<E, RAGGED> o(f0 + j, bytes);
       for (int i = threadIdx.x; i < o.n; i += blockDim.x) o.put(dz, i, make_uint4(0u, 0u, 0u, 0u));
@@ -271,12 +588,12 @@ unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ 
     const float s = warp_sums8(dot, l);
     if ((l & 3) == 0) red[warp][l >> 2] = s;
     __syncthreads();
-    if (here && threadIdx.x < kBatch && j0 + (int)threadIdx.x < k) {
+    if (here && threadIdx.x < B && j0 + (int)threadIdx.x < k) {
       float v = 0.f;
       for (int i = 0; i < warps; ++i) v += red[threadIdx.y * warps + i][threadIdx.x];
       dweights[f0 + j0 + threadIdx.x] = v;
     }
-    if (j0 + kBatch < k) __syncthreads();
+    if (j0 + B < k) __syncthreads();
   }
 }
 
@@ -297,64 +614,109 @@ dim3 grid_of(int64_t T, int64_t per, dim3 block) {
 
 int64_t pieces_of(int64_t bytes) { return bytes % 16 ? bytes / 16 + 2 : bytes / 16; }
 
-template <typename E, bool RAGGED>
-cudaError_t permute_rows(const PermuteCall& c, cudaStream_t st) {
-  const int64_t bytes = c.d * c.elem, per = pieces_of(bytes);
-  const int tx = row_threads(per);
-  const dim3 block(tx, 256 / tx);
-  return launch_chained(permute_kernel<E, RAGGED>, grid_of(c.T, per, block), block, 0, st, c.x,
-                        c.scales, c.position, c.offsets, c.out, c.out_scales, c.T, (int)c.k,
-                        (int)c.E, (int)bytes);
+// CTAs of a streaming kernel: no more than there are items.
+int stream_grid(int64_t items, int most) { return (int)(items < most ? items : most); }
+
+template <typename E>
+cudaError_t permute_ragged(const PermuteCall& c, int num_sms, cudaStream_t st) {
+  const auto kernel = permute_ragged_kernel<E>;
+  const int smem = kPermuteWarps * (int)sizeof(PermuteSlots);
+  static_assert(2 * kPermuteWarps * sizeof(PermuteSlots) <= 225 * 1024, "shared memory");
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t bytes = c.d * c.elem, piece = 32 * PermuteSlots::U;
+  const int64_t segs = (pieces_of(bytes) + piece - 1) / piece;
+  return launch_chained(kernel, dim3(stream_grid(c.T * segs, 2 * num_sms)), dim3(32 * kPermuteWarps),
+                        smem, st, c.x, c.scales, c.position, c.offsets, c.out, c.out_scales, c.T,
+                        (int)c.k, (int)c.E, (int)bytes, (int)segs);
 }
 
+// Up to this many 16-byte pieces of y a thread each, one wave of them.
+constexpr int64_t kFewPieces = 152 * 512;
+
 template <bool F32, bool RAGGED>
-cudaError_t unpermute_rows(const UnpermuteCall& c, int64_t bytes, cudaStream_t st) {
+cudaError_t unpermute_few(const UnpermuteCall& c, int64_t bytes, cudaStream_t st) {
   const int64_t per = pieces_of(bytes);
   const int tx = row_threads(per);
   const dim3 block(tx, 256 / tx);
-  return launch_chained(unpermute_kernel<F32, RAGGED>, grid_of(c.T, per, block), block, 0, st, c.z,
-                        c.position, c.weights, c.residual, c.y, c.T, (int)c.k, (int)bytes);
+  return launch_chained(unpermute_few_kernel<F32, RAGGED>,
+                        dim3((unsigned)((c.T + block.y - 1) / block.y), (unsigned)((per + tx - 1) / tx)),
+                        block, 0, st, c.z, c.position, c.weights, c.residual, c.y, c.T, (int)c.k,
+                        (int)bytes);
+}
+
+template <bool F32, bool RAGGED, int B, int U>
+cudaError_t unpermute_batch(const UnpermuteCall& c, int64_t bytes, int num_sms, cudaStream_t st) {
+  const auto kernel = unpermute_kernel<F32, RAGGED, B, U>;
+  const int smem = kWarps * (int)sizeof(UnpermuteSlots<F32, RAGGED, B, U>);
+  static_assert(kWarps * sizeof(UnpermuteSlots<F32, RAGGED, B, U>) <= 232448, "shared memory");
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t segs = (pieces_of(bytes) + 32 * U - 1) / (32 * U);
+  return launch_chained(kernel, dim3(stream_grid(c.T * segs, num_sms)), dim3(32 * kWarps), smem, st,
+                        c.z, c.position, c.weights, c.residual, c.y, c.T, (int)c.k, (int)bytes,
+                        (int)segs);
 }
 
 template <bool F32, bool RAGGED>
-cudaError_t backward_rows(const UnpermuteBackwardCall& c, int64_t bytes, cudaStream_t st) {
-  const int tx = row_threads(pieces_of(bytes));
+cudaError_t unpermute_rows(const UnpermuteCall& c, int64_t bytes, int num_sms, cudaStream_t st) {
+  if (c.T * pieces_of(bytes) <= kFewPieces) return unpermute_few<F32, RAGGED>(c, bytes, st);
+  if (c.k > 4) return unpermute_batch<F32, RAGGED, 8, 1>(c, bytes, num_sms, st);
+  if (c.k > 2) return unpermute_batch<F32, RAGGED, 4, 2>(c, bytes, num_sms, st);
+  return unpermute_batch<F32, RAGGED, 2, 4>(c, bytes, num_sms, st);
+}
+
+template <bool F32, bool RAGGED, int B, int U>
+cudaError_t backward_batch(const UnpermuteBackwardCall& c, int64_t bytes, cudaStream_t st) {
+  const int tx = row_threads((pieces_of(bytes) + U - 1) / U);
   const dim3 block(tx, 256 / tx);
-  return launch_chained(unpermute_backward_kernel<F32, RAGGED>,
+  return launch_chained(unpermute_backward_kernel<F32, RAGGED, B, U>,
                         dim3((unsigned)((c.T + block.y - 1) / block.y)), block, 0, st, c.dy, c.z,
                         c.position, c.offsets, c.weights, c.dz, c.dweights, c.T, (int)c.k,
                         (int)c.E, (int)bytes);
+}
+
+template <bool F32>
+cudaError_t backward_rows(const UnpermuteBackwardCall& c, int64_t bytes, cudaStream_t st) {
+  if (bytes % 16)
+    return c.k > 2 ? backward_batch<F32, true, 4, 1>(c, bytes, st)
+                   : backward_batch<F32, true, 2, 2>(c, bytes, st);
+  if (c.k > 4) return backward_batch<F32, false, 8, 1>(c, bytes, st);
+  if (c.k > 2) return backward_batch<F32, false, 4, 2>(c, bytes, st);
+  return backward_batch<F32, false, 2, 2>(c, bytes, st);
 }
 
 }  // namespace
 
 cudaError_t launch_permute(const PermuteCall& c, int num_sms, cudaStream_t st) {
   if (c.T == 0 || c.k == 0 || (c.d == 0 && !c.scales)) return cudaSuccess;
-  if (c.d * c.elem % 16 == 0) return permute_rows<uint8_t, false>(c, st);
-  if (c.elem == 4) return permute_rows<uint32_t, true>(c, st);
-  if (c.elem == 2) return permute_rows<uint16_t, true>(c, st);
-  return permute_rows<uint8_t, true>(c, st);
+  if (c.d * c.elem % 16) {
+    if (c.elem == 4) return permute_ragged<uint32_t>(c, num_sms, st);
+    if (c.elem == 2) return permute_ragged<uint16_t>(c, num_sms, st);
+    return permute_ragged<uint8_t>(c, num_sms, st);
+  }
+  const int64_t per = c.d * c.elem / 16;
+  const int tx = row_threads(per);
+  const dim3 block(tx, 256 / tx);
+  return launch_chained(permute_kernel, grid_of(c.T, per, block), block, 0, st, (const uint4*)c.x,
+                        c.scales, c.position, c.offsets, (uint4*)c.out, c.out_scales, c.T, (int)c.k,
+                        (int)c.E, (int)per);
 }
 
 cudaError_t launch_unpermute(const UnpermuteCall& c, int num_sms, cudaStream_t st) {
   if (c.T == 0 || c.d == 0) return cudaSuccess;
   const int64_t bytes = c.d * (c.f32 ? 4 : 2);
   if (c.f32)
-    return bytes % 16 ? unpermute_rows<true, true>(c, bytes, st)
-                      : unpermute_rows<true, false>(c, bytes, st);
-  return bytes % 16 ? unpermute_rows<false, true>(c, bytes, st)
-                    : unpermute_rows<false, false>(c, bytes, st);
+    return bytes % 16 ? unpermute_rows<true, true>(c, bytes, num_sms, st)
+                      : unpermute_rows<true, false>(c, bytes, num_sms, st);
+  return bytes % 16 ? unpermute_rows<false, true>(c, bytes, num_sms, st)
+                    : unpermute_rows<false, false>(c, bytes, num_sms, st);
 }
 
 cudaError_t launch_unpermute_backward(const UnpermuteBackwardCall& c, int num_sms,
                                       cudaStream_t st) {
   if (c.T == 0 || c.k == 0) return cudaSuccess;
-  const int64_t bytes = c.d * (c.f32 ? 4 : 2);
-  if (c.f32)
-    return bytes % 16 ? backward_rows<true, true>(c, bytes, st)
-                      : backward_rows<true, false>(c, bytes, st);
-  return bytes % 16 ? backward_rows<false, true>(c, bytes, st)
-                    : backward_rows<false, false>(c, bytes, st);
+  return c.f32 ? backward_rows<true>(c, c.d * 4, st) : backward_rows<false>(c, c.d * 2, st);
 }
 
 }  // namespace swg

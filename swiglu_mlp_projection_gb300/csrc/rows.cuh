@@ -30,25 +30,52 @@ __device__ __forceinline__ float elem_f32(uint16_t v) { return bf16_lo(v); }
 __device__ __forceinline__ void set_elem(float* p, float v) { *p = v; }
 __device__ __forceinline__ void set_elem(uint16_t* p, float v) { *p = (uint16_t)bf16x2(v, 0.f); }
 
+// 16 bytes as pairs of f32 values, and back.
 template <bool F32>
-__device__ __forceinline__ void unpack(const uint4& q, float (&v)[Row<F32>::kVec]) {
+__device__ __forceinline__ void unpack(const uint4& q, float2 (&v)[Row<F32>::kVec / 2]) {
   if constexpr (F32) {
-    v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
-    v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
+    v[0] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+    v[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
   } else {
-    v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
-    v[4] = bf16_lo(q.z); v[5] = bf16_hi(q.z); v[6] = bf16_lo(q.w); v[7] = bf16_hi(q.w);
+    v[0] = make_float2(bf16_lo(q.x), bf16_hi(q.x));
+    v[1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
+    v[2] = make_float2(bf16_lo(q.z), bf16_hi(q.z));
+    v[3] = make_float2(bf16_lo(q.w), bf16_hi(q.w));
   }
 }
 
 template <bool F32>
-__device__ __forceinline__ uint4 pack(const float (&v)[Row<F32>::kVec]) {
+__device__ __forceinline__ uint4 pack(const float2 (&v)[Row<F32>::kVec / 2]) {
   if constexpr (F32)
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                      __float_as_uint(v[3]));
+    return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                      __float_as_uint(v[1].y));
   else
-    return make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
-                      bf16x2(v[6], v[7]));
+    return make_uint4(bf16x2(v[0].x, v[0].y), bf16x2(v[1].x, v[1].y), bf16x2(v[2].x, v[2].y),
+                      bf16x2(v[3].x, v[3].y));
+}
+
+// Two f32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
 }
 
 // 16 bytes that are read once.  (No .nc: the caller's output may be the input.)
@@ -119,11 +146,13 @@ struct Pieces {
     return !RAGGED || (col(i) + e >= 0 && col(i) + e < d);
   }
   // Elements that are not the row's become 0.
-  __device__ __forceinline__ void mask(int i, float (&v)[V]) const {
+  __device__ __forceinline__ void mask(int i, float2 (&v)[V / 2]) const {
     if (!whole(i)) {
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (!has(i, e)) v[e] = 0.f;
+      for (int h = 0; h < V / 2; ++h) {
+        if (!has(i, 2 * h)) v[h].x = 0.f;
+        if (!has(i, 2 * h + 1)) v[h].y = 0.f;
+      }
     }
   }
 
@@ -133,52 +162,91 @@ struct Pieces {
     if (!RAGGED || at + V <= rows * d) return load_once((const E*)p + at);
     return load_inside<E>(p, at * (16 / V), rows * d * (16 / V));
   }
-  __device__ __forceinline__ void store(void* p, int i, const float (&v)[V]) const {
+  __device__ __forceinline__ void store(void* p, int i, const float2 (&v)[V / 2]) const {
     store_at(p, first, i, v);
   }
   // Into another row that starts at the same place of its 16 bytes: its piece 0 at `at`.
-  __device__ __forceinline__ void store_at(void* p, int64_t at, int i, const float (&v)[V]) const {
+  __device__ __forceinline__ void store_at(void* p, int64_t at, int i,
+                                           const float2 (&v)[V / 2]) const {
     E* q = (E*)p + at + (int64_t)i * V;
     if (whole(i)) {
       *reinterpret_cast<uint4*>(q) = pack<F32>(v);
     } else {
 #pragma unroll
+      for (int h = 0; h < V / 2; ++h) {
+        if (has(i, 2 * h)) set_elem(q + 2 * h, v[h].x);
+        if (has(i, 2 * h + 1)) set_elem(q + 2 * h + 1, v[h].y);
+      }
+    }
+  }
+  // The piece's e4m3 codes into a tensor of codes, which has V bytes where this one has 16.
+  __device__ __forceinline__ void store_codes(void* p, int64_t at, int i,
+                                              const uint32_t (&c)[V / 4]) const {
+    uint8_t* o = (uint8_t*)p + at + (int64_t)i * V;
+    if (whole(i)) {
+      if constexpr (V == 8) *reinterpret_cast<uint2*>(o) = make_uint2(c[0], c[1]);
+      else *reinterpret_cast<uint32_t*>(o) = c[0];
+    } else {
+#pragma unroll
       for (int e = 0; e < V; ++e)
-        if (has(i, e)) set_elem(q + e, v[e]);
+        if (has(i, e)) o[e] = (uint8_t)(c[e / 4] >> (8 * (e & 3)));
     }
   }
   // What piece i of a vector [d] of bf16 or f32 values (the norm's weight) would
   // be if it started where the row does; 0 past its ends.
-  __device__ __forceinline__ void weight(const void* w, int w_f32, int i, float (&v)[V]) const {
+  __device__ __forceinline__ void weight(const void* w, int w_f32, int i,
+                                         float2 (&v)[V / 2]) const {
     if (!RAGGED) {
       if (w_f32) {
         const float4* q = reinterpret_cast<const float4*>((const float*)w + i * V);
 #pragma unroll
         for (int h = 0; h < V / 4; ++h) {
           const float4 f = q[h];
-          v[4 * h] = f.x; v[4 * h + 1] = f.y; v[4 * h + 2] = f.z; v[4 * h + 3] = f.w;
+          v[2 * h] = make_float2(f.x, f.y);
+          v[2 * h + 1] = make_float2(f.z, f.w);
         }
       } else if constexpr (V == 8) {
         unpack<false>(*reinterpret_cast<const uint4*>((const uint16_t*)w + i * V), v);
       } else {
         const uint2 q = *reinterpret_cast<const uint2*>((const uint16_t*)w + i * V);
-        v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+        v[0] = make_float2(bf16_lo(q.x), bf16_hi(q.x));
+        v[1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
       }
     } else if (w_f32 == (F32 ? 1 : 0)) {   // the row's own type: two pieces, shifted
       constexpr int es = 16 / V;
       const int64_t at = (int64_t)(shift ? i - 1 : i) * 16;
       const uint4 lo = load_inside<E>(w, at, (int64_t)d * es);
       const uint4 hi = load_inside<E>(w, at + 16, (int64_t)d * es);
-      unpack<F32>(shift_bytes(lo, hi, (16 - shift * es) & 15), v);
+      unpack<F32>(shift ? shift_bytes(lo, hi, 16 - shift * es) : lo, v);
     } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        v[e] = !has(i, e) ? 0.f
+      const auto one = [&](int e) {
+        return !has(i, e) ? 0.f
                : w_f32    ? ((const float*)w)[col(i) + e]
                           : bf16_lo(((const uint16_t*)w)[col(i) + e]);
+      };
+#pragma unroll
+      for (int h = 0; h < V / 2; ++h) v[h] = make_float2(one(2 * h), one(2 * h + 1));
     }
   }
 };
+
+// 16 bytes of which `bytes` are read and the rest zero.
+__device__ __forceinline__ void copy_piece(uint4* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+// 4 bytes, or (if not `some`) zero.
+__device__ __forceinline__ void copy_word(void* dst, const void* src, bool some) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)), "l"(src),
+               "r"(some ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // A launch that may begin while the previous kernel of the stream ends (the
 // kernel waits in pdl_wait before it touches memory).
