@@ -167,47 +167,55 @@ norm_kernel(const __grid_constant__ NormArgs a) {
 // the CTAs first, then to their teams.
 
 constexpr int kPieces = 2;
-constexpr int team_threads(int w) { return w <= 8 ? 768 : 32 * w; }
+constexpr int team_threads(int w) { return 24 % w ? 32 * w : 768; }
 constexpr int team_rows(int w) { return team_threads(w) / 32 / w; }   // R
-constexpr int team_stages(int w) { return w <= 8 ? 3 : w == 16 ? 4 : 2; }
+constexpr int team_stages(int w) { return w == 32 ? 2 : w == 16 ? 4 : 3; }
 
-template <bool F32, int W, bool RAGGED>
+// The sum over lanes 0 ... W - 1 of values that are 0 in the others, in every lane.
+template <int W>
+__device__ __forceinline__ float team_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < W) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return W > 16 ? v : __shfl_sync(0xffffffffu, v, 0);
+}
+
+template <bool F32, int W, bool RAGGED, int ARRAYS>
 struct Team {
   static constexpr int V = Row<F32>::kVec, P = kPieces, T = team_threads(W), S = team_stages(W),
                        R = team_rows(W);
   int warp, l, team, lane;
   int64_t unit, units;   // rows unit, unit + units, ...
   int64_t M;
-  int arrays;
   uint4* slots;
   // (ragged: all rows of a team start at one place of their 16 bytes, since
   // `units` is a multiple of 8 or every team has one row at most)
   Pieces<F32, RAGGED> pc;
 
-  __device__ __forceinline__ Team(uint4* ring, int arrays_, int64_t M_, int d)
+  __device__ __forceinline__ Team(uint4* ring, int64_t M_, int d)
       : warp(threadIdx.x >> 5), l(threadIdx.x & 31), team(warp / W),
         lane(threadIdx.x - team * W * 32), unit(blockIdx.x + (int64_t)team * gridDim.x),
-        units((int64_t)gridDim.x * R), M(M_), arrays(arrays_), slots(ring + threadIdx.x),
+        units((int64_t)gridDim.x * R), M(M_), slots(ring + threadIdx.x),
         pc(unit, d) {}
   __device__ __forceinline__ int piece(int j) const { return lane + j * W * 32; }
   __device__ __forceinline__ uint4* slot(int stage, int array, int j) const {
-    return slots + ((stage * arrays + array) * P + j) * T;
+    return slots + stage * (ARRAYS * P * T) + (array * P + j) * T;
   }
   __device__ __forceinline__ int64_t first(int64_t row) const { return row * pc.d - pc.shift; }
   // This thread's pieces of `row`, a group of copies (an empty one past the last row).
   __device__ __forceinline__ void fetch(int64_t row, int stage, const void* p0, const void* p1,
                                         const void* p2) const {
     if (row < M) {
+      const int64_t at = (first(row) + (int64_t)lane * V) * (16 / V);   // in bytes
+      const int64_t left = M * pc.d * (16 / V) - at;
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        const int i = piece(j);
-        if (i >= pc.n) continue;
-        const int64_t at = first(row) + (int64_t)i * V, left = M * pc.d - at;
+        if (piece(j) >= pc.n) continue;
         // (the last piece of the tensor may be cut short)
-        const int bytes = !RAGGED || left >= V ? 16 : (int)left * (16 / V);
-        copy_piece(slot(stage, 0, j), (const char*)p0 + at * (16 / V), bytes);
-        if (p1) copy_piece(slot(stage, 1, j), (const char*)p1 + at * (16 / V), bytes);
-        if (p2) copy_piece(slot(stage, 2, j), (const char*)p2 + at * (16 / V), bytes);
+        const int to = j * W * 32 * 16, bytes = !RAGGED || left >= to + 16 ? 16 : (int)left - to;
+        copy_piece(slot(stage, 0, j), (const char*)p0 + at + to, bytes);
+        if (p1) copy_piece(slot(stage, 1, j), (const char*)p1 + at + to, bytes);
+        if (p2) copy_piece(slot(stage, 2, j), (const char*)p2 + at + to, bytes);
       }
     }
     copies_commit();
@@ -224,13 +232,13 @@ struct Team {
 template <bool F32, int W, bool FP8>
 __global__ void __launch_bounds__(team_threads(W), 1)
 norm_stream_kernel(const __grid_constant__ NormArgs a) {
-  using Tm = Team<F32, W, true>;
+  using Tm = Team<F32, W, true, 2>;
   constexpr int P = Tm::P, H = Tm::V / 2, S = Tm::S;
   extern __shared__ uint4 ring[];
   __shared__ float2 red[2][32];
   tc::pdl_launch_dependents();
   tc::pdl_wait();
-  const Tm tm(ring, a.residual ? 2 : 1, a.M, a.d);
+  const Tm tm(ring, a.M, a.d);
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) tm.fetch(tm.unit + i * tm.units, i, a.x, a.residual, nullptr);
   float2 w[P][H];
@@ -256,7 +264,7 @@ norm_stream_kernel(const __grid_constant__ NormArgs a) {
       if (tm.l == 0) red[side][tm.warp] = make_float2(q, m);
       tm.sync();
       const float2 v = tm.l < W ? red[side][tm.team * W + tm.l] : make_float2(0.f, 0.f);
-      q = warp_sum(v.x);
+      q = team_sum<W>(v.x);
       if (FP8) m = warp_max(v.y);
     }
     const RowFactors rf = row_factors<FP8>(q, m, a);
@@ -297,9 +305,9 @@ int64_t pieces_of(int64_t d, int vec) { return d % vec ? d / vec + 2 : d / vec; 
 
 // Warps per row of the streaming kernels, or 0 for rows too wide for them.
 int team_warps(int64_t d, int vec) {
-  int w = 1;
-  while (w <= 32 && 32 * kPieces * w < pieces_of(d, vec)) w *= 2;
-  return w > 32 ? 0 : w;
+  for (int w : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32})
+    if (32 * kPieces * w >= pieces_of(d, vec)) return w;
+  return 0;
 }
 
 // A streaming kernel's launch: M rows (at least 1) over at most one CTA per SM
@@ -336,13 +344,17 @@ cudaError_t launch_rows(const NormArgs& a, int num_sms, cudaStream_t st) {
     if (s.vpt == 2 * base) return launch_norm<F32, 2 * base, FP8, false>(a, s, st);
     return launch_norm<F32, 4 * base, FP8, false>(a, s, st);
   }
-  const int w = team_warps(a.d, V), arrays = a.residual ? 2 : 1, grid = team_grid(a.M, num_sms);
+  const int w = team_warps(a.d, V), arrays = 2, grid = team_grid(a.M, num_sms);
   switch (w) {
     case 1: return launch_team(norm_stream_kernel<F32, 1, FP8>, a, w, arrays, grid, st);
     case 2: return launch_team(norm_stream_kernel<F32, 2, FP8>, a, w, arrays, grid, st);
+    case 3: return launch_team(norm_stream_kernel<F32, 3, FP8>, a, w, arrays, grid, st);
     case 4: return launch_team(norm_stream_kernel<F32, 4, FP8>, a, w, arrays, grid, st);
+    case 6: return launch_team(norm_stream_kernel<F32, 6, FP8>, a, w, arrays, grid, st);
     case 8: return launch_team(norm_stream_kernel<F32, 8, FP8>, a, w, arrays, grid, st);
+    case 12: return launch_team(norm_stream_kernel<F32, 12, FP8>, a, w, arrays, grid, st);
     case 16: return launch_team(norm_stream_kernel<F32, 16, FP8>, a, w, arrays, grid, st);
+    case 24: return launch_team(norm_stream_kernel<F32, 24, FP8>, a, w, arrays, grid, st);
     case 32: return launch_team(norm_stream_kernel<F32, 32, FP8>, a, w, arrays, grid, st);
   }
   const int vpt = 4 * base;
@@ -375,13 +387,13 @@ struct BackArgs {
 template <bool F32, int W, bool RAGGED>
 __global__ void __launch_bounds__(team_threads(W), 1)
 norm_backward_kernel(const __grid_constant__ BackArgs a) {
-  using Tm = Team<F32, W, RAGGED>;
+  using Tm = Team<F32, W, RAGGED, 3>;
   constexpr int P = Tm::P, H = Tm::V / 2, S = Tm::S, R = Tm::R;
   extern __shared__ uint4 ring[];
   __shared__ float2 red[2][32];
   tc::pdl_launch_dependents();
   tc::pdl_wait();
-  const Tm tm(ring, a.ds ? 3 : 2, a.M, a.d);
+  const Tm tm(ring, a.M, a.d);
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) tm.fetch(tm.unit + i * tm.units, i, a.s, a.dy, a.ds);
   float2 w[P][H], acc[P][H];
@@ -417,8 +429,8 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
       if (tm.l == 0) red[side][tm.warp] = make_float2(q, p);
       tm.sync();
       const float2 v = tm.l < W ? red[side][tm.team * W + tm.l] : make_float2(0.f, 0.f);
-      q = warp_sum(v.x);
-      p = warp_sum(v.y);
+      q = team_sum<W>(v.x);
+      p = team_sum<W>(v.y);
     }
     // t = s r:  dx = ds + r g - t r^2 mean(g s),  dweight += dy t
     const float r = rsqrtf(fmaf(q, inv_d, a.eps));
@@ -580,15 +592,19 @@ dweight_kernel(const float* __restrict__ part, int n, int d, void* __restrict__ 
 
 template <bool F32, bool RAGGED>
 cudaError_t launch_back(const BackArgs& a, int grid, cudaStream_t st) {
-  const int w = team_warps(a.d, Row<F32>::kVec), arrays = a.ds ? 3 : 2;
+  const int w = team_warps(a.d, Row<F32>::kVec), arrays = 3;
   // (the teams' sums take the place of their stages: R rows of at most 512 W
   // elements, 2 KB, and each stage has as much)
   switch (w) {
     case 1: return launch_team(norm_backward_kernel<F32, 1, RAGGED>, a, w, arrays, grid, st);
     case 2: return launch_team(norm_backward_kernel<F32, 2, RAGGED>, a, w, arrays, grid, st);
+    case 3: return launch_team(norm_backward_kernel<F32, 3, RAGGED>, a, w, arrays, grid, st);
     case 4: return launch_team(norm_backward_kernel<F32, 4, RAGGED>, a, w, arrays, grid, st);
+    case 6: return launch_team(norm_backward_kernel<F32, 6, RAGGED>, a, w, arrays, grid, st);
     case 8: return launch_team(norm_backward_kernel<F32, 8, RAGGED>, a, w, arrays, grid, st);
+    case 12: return launch_team(norm_backward_kernel<F32, 12, RAGGED>, a, w, arrays, grid, st);
     case 16: return launch_team(norm_backward_kernel<F32, 16, RAGGED>, a, w, arrays, grid, st);
+    case 24: return launch_team(norm_backward_kernel<F32, 24, RAGGED>, a, w, arrays, grid, st);
     case 32: return launch_team(norm_backward_kernel<F32, 32, RAGGED>, a, w, arrays, grid, st);
   }
   const auto k = norm_backward_wide_kernel<F32, RAGGED>;

@@ -437,9 +437,10 @@ unpermute_kernel(const void* __restrict__ z, const int* __restrict__ position,
       const int p = place(out, out_c, b);
       if (p < 0) continue;
       const float w = weights ? slots.weight[out_c][b] : 1.f;
-      const int sh = RAGGED ? (int)(((int64_t)p * bytes - o.shift) & 15) : 0;
+      const int sh = RAGGED ? (int)((unsigned)p * (unsigned)bytes - o.shift) & 15 : 0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        if (i0 + 32 * u >= o.n) break;
         uint4 q = slots.z[stage][b][l + 32 * u];
         if (RAGGED) q = shift_bytes(q, slots.z[stage][b][l + 32 * u + 1], sh);
         float2 v[H];
@@ -479,19 +480,215 @@ __device__ __forceinline__ float warp_sums8(float (&v)[8], int lane) {
   return s;
 }
 
-// blockDim.x threads to a token; the warps' sums of the dot products meet in
-// shared memory.  B, U: as above.  Ragged rows are taken in the pieces of z's
-// and dz's row, so that these move as they are and dy is shifted.
-template <bool F32, bool RAGGED, int B, int U>
-__global__ void __launch_bounds__(256, 3)
+// dz and the sums of the dot product, of one piece: dz's row o has it at piece i,
+// m is dy there and zq z.
+template <bool F32, bool RAGGED, typename S>
+__device__ __forceinline__ void backward_piece(const S& o, void* dz, int i, const uint4& dyq,
+                                               const uint4& zq, float w, float2& dot) {
+  constexpr int V = Row<F32>::kVec, H = V / 2;
+  float2 v[H], m[H];
+  unpack<F32>(zq, v);
+  unpack<F32>(dyq, m);
+  if (RAGGED) {
+    const int c0 = i * V - o.shift / (16 / V), d = o.bytes / (16 / V);
+    if (c0 < 0 || c0 + V > d) {   // (not the neighbours' values, which may be NaN)
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        if (c0 + 2 * h < 0 || c0 + 2 * h >= d) v[h].x = m[h].x = 0.f;
+        if (c0 + 2 * h + 1 < 0 || c0 + 2 * h + 1 >= d) v[h].y = m[h].y = 0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    dot = fma2(m[h], v[h], dot);
+    v[h] = mul2(make_float2(w, w), m[h]);
+  }
+  o.put(dz, i, pack<F32>(v));
+}
+
+// Gradient of unpermute.  A team of W warps has a token at a time: its warps
+// take segments of the row in turn, all choices B at a time, and their sums of
+// the dot products meet in shared memory.  The pieces are those of z's and dz's
+// row, so that these move as they are; dy, where it starts elsewhere in its 16
+// bytes, is shifted.
+template <bool RAGGED, int B, int U>
+struct BackwardSlots {
+  static constexpr int S = U == 1 ? 4 : 3, C = 2 * S - 1;
+  uint4 z[S][B][32 * U];
+  uint4 dy[S][32 * U + (RAGGED ? 2 : 0)];   // ragged: one more on either side
+  int place[C][8];
+  float weight[C][8];
+};
+
+// Steps of a warp: tokens t, batches of choices j, segments seg.
+template <int B, int W>
+struct TeamSteps {
+  int64_t t, dt;
+  int j, seg, segs, k, first;
+  __device__ __forceinline__ TeamSteps(int segs_, int k_) : j(0), segs(segs_), k(k_) {
+    const int warp = threadIdx.x >> 5, teams = (blockDim.x >> 5) / W;
+    t = (int64_t)(warp / W) * gridDim.x + blockIdx.x;
+    dt = (int64_t)gridDim.x * teams;
+    first = seg = warp % W;
+  }
+  __device__ __forceinline__ bool last_segment() const { return seg + W >= segs; }
+  __device__ __forceinline__ void next() {
+    seg += W;
+    if (seg < segs) return;
+    seg = first;
+    j += B;
+    if (j < k) return;
+    j = 0;
+    t += dt;
+  }
+};
+
+template <bool F32, bool RAGGED, int B, int U, int W>
+__global__ void __launch_bounds__(32 * kWarps, 1)
 unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ z,
                           const int* __restrict__ position, const int* __restrict__ offsets,
                           const float* __restrict__ weights, void* __restrict__ dz,
-                          float* __restrict__ dweights, int64_t T, int k, int n_exp, int bytes) {
+                          float* __restrict__ dweights, int64_t T, int k, int n_exp, int bytes,
+                          int segs) {
   using E = typename Row<F32>::elem;
-  constexpr int V = Row<F32>::kVec, H = V / 2;
+  using Slots = BackwardSlots<RAGGED, B, U>;
+  constexpr int S = Slots::S, C = Slots::C;
+  extern __shared__ uint4 smem[];
+  __shared__ float red[2][kWarps][8];
+  tc::pdl_launch_dependents();
+  tc::pdl_wait();
+  const int l = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Slots& slots = reinterpret_cast<Slots*>(smem)[warp];
+  const int64_t rows = T * k, end = sorted_end(offsets, n_exp, rows);
+
+  TeamSteps<B, W> ask(segs, k), in(segs, k), out(segs, k);
+  int ask_c = 0, in_c = 0, out_c = 0;
+  const auto choices = [&]() {   // lanes 0 ... B - 1: places, 8 ... 8 + B - 1: weights
+    const int b = l & 7;
+    if (l < 16 && b < B) {
+      const bool some = ask.t < T && ask.j + b < k;
+      const int64_t f = some ? ask.t * k + ask.j + b : 0;
+      if (l < 8) copy_word(&slots.place[ask_c][b], position + f, some);
+      else copy_word(&slots.weight[ask_c][b], weights + f, some);
+    }
+    ask.next();
+    ask_c = ask_c + 1 == C ? 0 : ask_c + 1;
+  };
+  const auto place = [&](const TeamSteps<B, W>& s, int c, int b) {
+    const int p = slots.place[c][b];
+    return s.j + b < k && p >= 0 && p < rows ? p : -1;
+  };
+  const auto fetch = [&](int stage) {
+    if (in.t < T) {
+      const int i0 = in.seg * 32 * U;
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int p = place(in, in_c, b);
+        if (p < 0) continue;
+        const Span16<E, RAGGED> o(p, bytes);
+        copy_row<RAGGED, 32 * U>(slots.z[stage][b], z, o.base - o.shift + (int64_t)i0 * 16,
+                                 rows * bytes, o.n - i0, l);
+      }
+      const int64_t src = in.t * bytes;
+      if (RAGGED)
+        copy_row<true, 32 * U + 2>(slots.dy[stage], dy, (src & ~(int64_t)15) + (int64_t)(i0 - 1) * 16,
+                                   T * bytes, 32 * U + 2, l);
+      else
+        copy_row<false, 32 * U>(slots.dy[stage], dy, src + (int64_t)i0 * 16, T * bytes,
+                                bytes / 16 - i0, l);
+    }
+    in.next();
+    in_c = in_c + 1 == C ? 0 : in_c + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) choices();
+  copies_commit();
+  copies_wait<0>();
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) {
+    fetch(i);
+    choices();
+    copies_commit();
+  }
+  int stage = 0, free_stage = S - 1, side = 0;
+  float2 dot[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b) dot[b] = make_float2(0.f, 0.f);
+  while (out.t < T) {
+    copies_wait<S - 2>();
+    __syncwarp();
+    fetch(free_stage);
+    choices();
+    copies_commit();
+    const int i0 = out.seg * 32 * U;
+    const int64_t f0 = out.t * k + out.j;
+    const unsigned src = (unsigned)out.t * (unsigned)bytes;   // (its low bits count)
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int p = place(out, out_c, b);
+      if (p >= 0) {
+        const Span16<E, RAGGED> o(p, bytes);
+        const float w = slots.weight[out_c][b];
+        // dy's bytes for piece i are in its pieces i + off and i + off + 1
+        const int off = RAGGED ? ((int)(src & 15) < o.shift ? -1 : 0) : 0;
+        const int sh = RAGGED ? (int)(src - o.shift) & 15 : 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int m = l + 32 * u, i = i0 + m;
+          if (i >= o.n) continue;
+          const uint4* d4 = &slots.dy[stage][RAGGED ? m + 1 + off : m];
+          backward_piece<F32, RAGGED>(o, dz, i, RAGGED ? shift_bytes(d4[0], d4[1], sh) : d4[0],
+                                      slots.z[stage][b][m], w, dot[b]);
+        }
+      }
+      if (out.j + b < k && f0 + b >= end) {   // a row of no pair
+        const Span16<E, RAGGED> o(f0 + b, bytes);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i0 + l + 32 * u < o.n) o.put(dz, i0 + l + 32 * u, make_uint4(0u, 0u, 0u, 0u));
+      }
+    }
+    if (out.last_segment()) {
+      float sums[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) sums[b] = b < B ? dot[b].x + dot[b].y : 0.f;
+#pragma unroll
+      for (int b = 0; b < B; ++b) dot[b] = make_float2(0.f, 0.f);
+      float v = warp_sums8(sums, l);
+      if (W > 1) {   // (one barrier: the next batch writes the other side)
+        if ((l & 3) == 0) red[side][warp][l >> 2] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(warp / W + 1), "n"(W * 32) : "memory");
+        if (warp % W == 0 && l < B) {
+          v = 0.f;
+#pragma unroll
+          for (int i = 0; i < W; ++i) v += red[side][warp + i][l];
+        }
+        side ^= 1;
+      } else {
+        v = __shfl_sync(0xffffffffu, v, (4 * l) & 31);
+      }
+      if (warp % W == 0 && l < B && out.j + l < k) dweights[f0 + l] = v;
+    }
+    out.next();
+    out_c = out_c + 1 == C ? 0 : out_c + 1;
+    stage = stage + 1 == S ? 0 : stage + 1;
+    free_stage = free_stage + 1 == S ? 0 : free_stage + 1;
+  }
+}
+
+// Few pieces: blockDim.x threads to a token, and nothing is copied ahead.
+template <bool F32, bool RAGGED>
+__global__ void __launch_bounds__(256)
+unpermute_backward_few_kernel(const void* __restrict__ dy, const void* __restrict__ z,
+                              const int* __restrict__ position, const int* __restrict__ offsets,
+                              const float* __restrict__ weights, void* __restrict__ dz,
+                              float* __restrict__ dweights, int64_t T, int k, int n_exp,
+                              int bytes) {
+  using E = typename Row<F32>::elem;
+  constexpr int B = 8;
   __shared__ float red[8][8];   // by warp of the CTA
-  __shared__ uint4 dys[RAGGED ? 8 : 1][RAGGED ? 32 * U + 2 : 1];   // ragged: a warp's pieces of dy
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   const int64_t t = token();
@@ -503,80 +700,34 @@ unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ 
   const int most = RAGGED ? bytes / 16 + 2 : bytes / 16;   // pieces of a row
   for (int j0 = 0; j0 < k; j0 += B) {
     int p[B];
-    float c[B], dot[8];
-#pragma unroll
-    for (int b = 0; b < 8; ++b) dot[b] = 0.f;
+    float c[B];
+    float2 dot[B];
 #pragma unroll
     for (int b = 0; b < B; ++b) {
       p[b] = ch.place(j0 + b);
       c[b] = ch.weight(j0 + b);
+      dot[b] = make_float2(0.f, 0.f);
     }
-    // (pieces i0, i0 + 32, ... of this lane; ragged: the warp's neighbours are its own)
-    for (int w0 = (warp - threadIdx.y * warps) * 32 * U; here && w0 < most; w0 += U * blockDim.x) {
-      uint4 q[B][U];
+    for (int i = threadIdx.x; here && i < most; i += blockDim.x) {
+      uint4 q[B];
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         const Span16<E, RAGGED> o(p[b], bytes);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = w0 + l + 32 * u;
-          if (p[b] < 0 || i >= o.n) continue;
-          const int64_t at = o.base - o.shift + (int64_t)i * 16;
-          // (the tensor's last row may end inside 16 bytes)
-          if (!RAGGED || p[b] + 1 < rows) q[b][u] = load_once((const char*)z + at);
-          else q[b][u] = load_inside<E>(z, at, rows * bytes);
-        }
+        if (p[b] < 0 || i >= o.n) continue;
+        const int64_t at = o.base - o.shift + (int64_t)i * 16;
+        // (the tensor's last row may end inside 16 bytes)
+        if (!RAGGED || p[b] + 1 < rows) q[b] = load_once((const char*)z + at);
+        else q[b] = load_inside<E>(z, at, rows * bytes);
       }
-      float2 g[RAGGED ? 1 : U][H];
-      const int64_t src = t * bytes;
-      if constexpr (RAGGED) {
-        __syncwarp();
-        for (int m = l; m < 32 * U + 2; m += 32)
-          dys[warp][m] = load_inside<E>(dy, (src & ~(int64_t)15) + (int64_t)(w0 + m - 1) * 16, T * bytes);
-        __syncwarp();
-      } else {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = w0 + l + 32 * u;
-          if (i < most) unpack<F32>(__ldg(reinterpret_cast<const uint4*>((const char*)dy + src) + i), g[u]);
-        }
-      }
+      Two g;
+      if (!RAGGED) g.lo = load_once((const char*)dy + t * bytes + (int64_t)i * 16);
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         if (p[b] < 0) continue;
         const Span16<E, RAGGED> o(p[b], bytes);
-        const int off = RAGGED ? (int)(((src - o.shift) >> 4) - (src >> 4)) : 0;
-        const int sh = RAGGED ? (int)((src - o.shift) & 15) : 0;
-        float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = w0 + l + 32 * u;
-          if (i >= o.n) continue;
-          float2 v[H], m[H];
-          unpack<F32>(q[b][u], v);
-          if constexpr (RAGGED) {
-            const uint4* d4 = &dys[warp][l + 32 * u + 1 + off];
-            unpack<F32>(shift_bytes(d4[0], d4[1], sh), m);
-            const int c0 = i * V - o.shift / (16 / V), d = bytes / (16 / V);
-            if (c0 < 0 || c0 + V > d) {   // (v, m: not neighbours' values, which may be NaN)
-#pragma unroll
-              for (int h = 0; h < H; ++h) {
-                if (c0 + 2 * h < 0 || c0 + 2 * h >= d) v[h].x = m[h].x = 0.f;
-                if (c0 + 2 * h + 1 < 0 || c0 + 2 * h + 1 >= d) v[h].y = m[h].y = 0.f;
-              }
-            }
-          } else {
-#pragma unroll
-            for (int h = 0; h < H; ++h) m[h] = g[u][h];
-          }
-#pragma unroll
-          for (int h = 0; h < H; ++h) {
-            s = fma2(m[h], v[h], s);
-            v[h] = mul2(make_float2(c[b], c[b]), m[h]);
-          }
-          o.put(dz, i, pack<F32>(v));
-        }
-        dot[b] += s.x + s.y;
+        if (i >= o.n) continue;
+        if (RAGGED) g = o.begin(dy, t, T * bytes, i);
+        backward_piece<F32, RAGGED>(o, dz, i, o.end(g, dy, t, T * bytes, i), q[b], c[b], dot[b]);
       }
     }
     // rows of no pair
@@ -585,7 +736,10 @@ unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ 
       const Span16<E, RAGGED> o(f0 + j, bytes);
       for (int i = threadIdx.x; i < o.n; i += blockDim.x) o.put(dz, i, make_uint4(0u, 0u, 0u, 0u));
     }
-    const float s = warp_sums8(dot, l);
+    float sums[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) sums[b] = dot[b].x + dot[b].y;
+    const float s = warp_sums8(sums, l);
     if ((l & 3) == 0) red[warp][l >> 2] = s;
     __syncthreads();
     if (here && threadIdx.x < B && j0 + (int)threadIdx.x < k) {
@@ -660,30 +814,50 @@ cudaError_t unpermute_batch(const UnpermuteCall& c, int64_t bytes, int num_sms, 
 
 template <bool F32, bool RAGGED>
 cudaError_t unpermute_rows(const UnpermuteCall& c, int64_t bytes, int num_sms, cudaStream_t st) {
-  if (c.T * pieces_of(bytes) <= kFewPieces) return unpermute_few<F32, RAGGED>(c, bytes, st);
-  if (c.k > 4) return unpermute_batch<F32, RAGGED, 8, 1>(c, bytes, num_sms, st);
-  if (c.k > 2) return unpermute_batch<F32, RAGGED, 4, 2>(c, bytes, num_sms, st);
-  return unpermute_batch<F32, RAGGED, 2, 4>(c, bytes, num_sms, st);
+  const int64_t per = pieces_of(bytes);
+  if (c.T * per <= kFewPieces) return unpermute_few<F32, RAGGED>(c, bytes, st);
+  if (per >= 128 || c.k <= 2) return unpermute_batch<F32, RAGGED, 2, 4>(c, bytes, num_sms, st);
+  if (per >= 64 || c.k <= 4) return unpermute_batch<F32, RAGGED, 4, 2>(c, bytes, num_sms, st);
+  return unpermute_batch<F32, RAGGED, 8, 1>(c, bytes, num_sms, st);
+}
+
+template <bool F32, bool RAGGED, int B, int U, int W>
+cudaError_t backward_team(const UnpermuteBackwardCall& c, int64_t bytes, int64_t segs, int num_sms,
+                          cudaStream_t st) {
+  const auto kernel = unpermute_backward_kernel<F32, RAGGED, B, U, W>;
+  const int smem = kWarps * (int)sizeof(BackwardSlots<RAGGED, B, U>);
+  static_assert(kWarps * sizeof(BackwardSlots<RAGGED, B, U>) + 1024 <= 232448, "shared memory");
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_chained(kernel, dim3(stream_grid(c.T, num_sms)), dim3(32 * kWarps), smem, st, c.dy,
+                        c.z, c.position, c.offsets, c.weights, c.dz, c.dweights, c.T, (int)c.k,
+                        (int)c.E, (int)bytes, (int)segs);
 }
 
 template <bool F32, bool RAGGED, int B, int U>
-cudaError_t backward_batch(const UnpermuteBackwardCall& c, int64_t bytes, cudaStream_t st) {
-  const int tx = row_threads((pieces_of(bytes) + U - 1) / U);
-  const dim3 block(tx, 256 / tx);
-  return launch_chained(unpermute_backward_kernel<F32, RAGGED, B, U>,
-                        dim3((unsigned)((c.T + block.y - 1) / block.y)), block, 0, st, c.dy, c.z,
-                        c.position, c.offsets, c.weights, c.dz, c.dweights, c.T, (int)c.k,
-                        (int)c.E, (int)bytes);
+cudaError_t backward_batch(const UnpermuteBackwardCall& c, int64_t bytes, int num_sms,
+                           cudaStream_t st) {
+  const int64_t segs = (pieces_of(bytes) + 32 * U - 1) / (32 * U);
+  if (segs >= 4) return backward_team<F32, RAGGED, B, U, 4>(c, bytes, segs, num_sms, st);
+  if (segs >= 2) return backward_team<F32, RAGGED, B, U, 2>(c, bytes, segs, num_sms, st);
+  return backward_team<F32, RAGGED, B, U, 1>(c, bytes, segs, num_sms, st);
 }
 
-template <bool F32>
-cudaError_t backward_rows(const UnpermuteBackwardCall& c, int64_t bytes, cudaStream_t st) {
-  if (bytes % 16)
-    return c.k > 2 ? backward_batch<F32, true, 4, 1>(c, bytes, st)
-                   : backward_batch<F32, true, 2, 2>(c, bytes, st);
-  if (c.k > 4) return backward_batch<F32, false, 8, 1>(c, bytes, st);
-  if (c.k > 2) return backward_batch<F32, false, 4, 2>(c, bytes, st);
-  return backward_batch<F32, false, 2, 2>(c, bytes, st);
+template <bool F32, bool RAGGED>
+cudaError_t backward_rows(const UnpermuteBackwardCall& c, int64_t bytes, int num_sms,
+                          cudaStream_t st) {
+  const int64_t per = pieces_of(bytes);
+  if (c.T * per <= kFewPieces || c.d == 0) {
+    const int tx = row_threads(per);
+    const dim3 block(tx, 256 / tx);
+    return launch_chained(unpermute_backward_few_kernel<F32, RAGGED>,
+                          dim3((unsigned)((c.T + block.y - 1) / block.y)), block, 0, st, c.dy, c.z,
+                          c.position, c.offsets, c.weights, c.dz, c.dweights, c.T, (int)c.k,
+                          (int)c.E, (int)bytes);
+  }
+  if (per < 512 && c.k > 4) return backward_batch<F32, RAGGED, 8, 1>(c, bytes, num_sms, st);
+  if (per < 512 && c.k > 2) return backward_batch<F32, RAGGED, 4, 2>(c, bytes, num_sms, st);
+  return backward_batch<F32, RAGGED, 2, 4>(c, bytes, num_sms, st);
 }
 
 }  // namespace
@@ -716,7 +890,12 @@ cudaError_t launch_unpermute(const UnpermuteCall& c, int num_sms, cudaStream_t s
 cudaError_t launch_unpermute_backward(const UnpermuteBackwardCall& c, int num_sms,
                                       cudaStream_t st) {
   if (c.T == 0 || c.k == 0) return cudaSuccess;
-  return c.f32 ? backward_rows<true>(c, c.d * 4, st) : backward_rows<false>(c, c.d * 2, st);
+  const int64_t bytes = c.d * (c.f32 ? 4 : 2);
+  if (c.f32)
+    return bytes % 16 ? backward_rows<true, true>(c, bytes, num_sms, st)
+                      : backward_rows<true, false>(c, bytes, num_sms, st);
+  return bytes % 16 ? backward_rows<false, true>(c, bytes, num_sms, st)
+                    : backward_rows<false, false>(c, bytes, num_sms, st);
 }
 
 }  // namespace swg
