@@ -179,33 +179,59 @@ __device__ __forceinline__ void copy_row(uint4* slots, const void* p, int64_t at
   }
 }
 
-// The steps of a warp: tokens t, `segs` segments of their rows, and choices j,
-// j + 1, ... j + B - 1 of k (at least one step to a segment).
-template <int B>
+// The steps of a warp: its items (token t, part a of na) are spread over the
+// warps of the grid, and each takes nb steps b.
 struct Steps {
   int64_t t, dt;
-  int seg, segs, dseg, j, k;
-  __device__ __forceinline__ Steps(int segs_, int k_) : segs(segs_), j(0), k(k_) {
+  int a, na, da, b, nb;
+  __device__ __forceinline__ Steps(int na_, int nb_) : na(na_), b(0), nb(nb_) {
     const int64_t g = (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x;
     const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 5);
-    t = g / segs;
-    seg = (int)(g - t * segs);
-    dt = step / segs;
-    dseg = (int)(step - dt * segs);
+    t = g / na;
+    a = (int)(g - t * na);
+    dt = step / na;
+    da = (int)(step - dt * na);
   }
-  __device__ __forceinline__ bool last() const { return j + B >= k; }
+  __device__ __forceinline__ bool last() const { return b + 1 == nb; }
   __device__ __forceinline__ void next() {
-    j += B;
-    if (j < k) return;
-    j = 0;
+    if (++b < nb) return;
+    b = 0;
     t += dt;
-    seg += dseg;
-    if (seg >= segs) {
-      seg -= segs;
+    a += da;
+    if (a >= na) {
+      a -= na;
       ++t;
     }
   }
 };
+// k choices B at a time (one step where there are none).
+template <int B>
+__device__ __forceinline__ int batches(int k) {
+  return k > B ? (k + B - 1) / B : 1;
+}
+
+// Choices as they are copied (into slots c of place and weight): choice b of the
+// B from j on of token t.  Lanes 0 ... B - 1 take the places, 8 ... 8 + B - 1
+// the weights.
+template <int B, typename Slots>
+__device__ __forceinline__ void copy_choices(Slots& slots, int c, const int* position,
+                                             const float* weights, int64_t t, int64_t T, int j,
+                                             int k) {
+  const int l = threadIdx.x & 31, b = l & 7;
+  if (l >= 16 || b >= B) return;
+  const bool some = t < T && j + b < k;
+  const int64_t f = some ? t * k + j + b : 0;
+  if (l < 8) copy_word(&slots.place[c][b], position + f, some);
+  else if (weights) copy_word(&slots.weight[c][b], weights + f, some);
+}
+// ... and its place, or -1.
+template <typename Slots>
+__device__ __forceinline__ int choice_place(const Slots& slots, int c, int j, int b, int k,
+                                            int64_t rows) {
+  const int p = slots.place[c][b];
+  return j + b < k && p >= 0 && p < rows ? p : -1;
+}
+__device__ __forceinline__ int wrap(int i, int n) { return i + 1 == n ? 0 : i + 1; }
 
 // Ragged permute: a warp's stages hold 64 pieces of a token's row, with one more
 // on either side; the token's choices are copied S - 1 steps earlier.
@@ -229,17 +255,17 @@ permute_ragged_kernel(const void* __restrict__ x, const float* __restrict__ scal
   const int l = threadIdx.x & 31;
   PermuteSlots& slots = reinterpret_cast<PermuteSlots*>(smem)[threadIdx.x >> 5];
   const int64_t rows = T * k, end = sorted_end(offsets, n_exp, rows);
-  Steps<32> ask(segs, 1), in(segs, 1), out_s(segs, 1);   // (all choices in one step)
+  Steps ask(segs, 1), in(segs, 1), out_s(segs, 1);   // a: segments, all choices in one step
   int ask_c = 0, out_c = 0;
   const auto choices = [&]() {
     if (l < k) copy_word(&slots.place[ask_c][l], position + (ask.t < T ? ask.t * k + l : 0), ask.t < T);
     ask.next();
-    ask_c = ask_c + 1 == C ? 0 : ask_c + 1;
+    ask_c = wrap(ask_c, C);
   };
   const auto fetch = [&](int stage) {
     if (in.t < T) {
       const int64_t base = in.t * bytes;
-      copy_row<true, 32 * U + 2>(slots.x[stage], x, (base & ~(int64_t)15) + ((int64_t)in.seg * 32 * U - 1) * 16,
+      copy_row<true, 32 * U + 2>(slots.x[stage], x, (base & ~(int64_t)15) + ((int64_t)in.a * 32 * U - 1) * 16,
                                  T * bytes, 32 * U + 2, l);
       if (scales && l == 0) copy_word(&slots.scale[stage][0], scales + in.t, true);
     }
@@ -262,7 +288,7 @@ permute_ragged_kernel(const void* __restrict__ x, const float* __restrict__ scal
     choices();
     copies_commit();
     const int64_t t = out_s.t, f0 = t * k, src = t * bytes;
-    const int i0 = out_s.seg * 32 * U;
+    const int i0 = out_s.a * 32 * U;
     for (int j = 0; j < k; ++j) {
       const int p = slots.place[out_c][j];
       if (p >= 0 && p < rows) {
@@ -276,20 +302,20 @@ permute_ragged_kernel(const void* __restrict__ x, const float* __restrict__ scal
           if (i0 + m < o.n)
             o.put(out, i0 + m, shift_bytes(slots.x[stage][m + 1 + off], slots.x[stage][m + 2 + off], sh));
         }
-        if (scales && out_s.seg == 0 && l == 0) out_scales[p] = slots.scale[stage][0];
+        if (scales && out_s.a == 0 && l == 0) out_scales[p] = slots.scale[stage][0];
       }
       if (f0 + j >= end) {
         const Span16<E, true> o(f0 + j, bytes);
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (i0 + l + 32 * u < o.n) o.put(out, i0 + l + 32 * u, make_uint4(0u, 0u, 0u, 0u));
-        if (scales && out_s.seg == 0 && l == 0) out_scales[f0 + j] = 0.f;
+        if (scales && out_s.a == 0 && l == 0) out_scales[f0 + j] = 0.f;
       }
     }
     out_s.next();
-    out_c = out_c + 1 == C ? 0 : out_c + 1;
-    stage = stage + 1 == S ? 0 : stage + 1;
-    free_stage = free_stage + 1 == S ? 0 : free_stage + 1;
+    out_c = wrap(out_c, C);
+    stage = wrap(stage, S);
+    free_stage = wrap(free_stage, S);
   }
 }
 
@@ -361,43 +387,33 @@ unpermute_kernel(const void* __restrict__ z, const int* __restrict__ position,
   Slots& slots = reinterpret_cast<Slots*>(smem)[threadIdx.x >> 5];
   const int64_t rows = T * k;
 
-  Steps<B> ask(segs, k), in(segs, k), out(segs, k);   // choices copied, rows copied, at work
-  int ask_c = 0, in_c = 0, out_c = 0;                 // ... and their places among the C
-  const auto choices = [&]() {   // lanes 0 ... B - 1: places, 8 ... 8 + B - 1: weights
-    const int b = l & 7;
-    if (l < 16 && b < B) {
-      const bool some = ask.t < T && ask.j + b < k;
-      const int64_t f = some ? ask.t * k + ask.j + b : 0;
-      if (l < 8) copy_word(&slots.place[ask_c][b], position + f, some);
-      else if (weights) copy_word(&slots.weight[ask_c][b], weights + f, some);
-    }
+  // choices copied, rows copied, at work (a: segments, b: batches of choices)
+  Steps ask(segs, batches<B>(k)), in = ask, out = ask;
+  int ask_c = 0, in_c = 0, out_c = 0;   // their places among the C
+  const auto choices = [&]() {
+    copy_choices<B>(slots, ask_c, position, weights, ask.t, T, ask.b * B, k);
     ask.next();
-    ask_c = ask_c + 1 == C ? 0 : ask_c + 1;
-  };
-  // Choice b of a step as copied: its place, or -1.
-  const auto place = [&](const Steps<B>& s, int c, int b) {
-    const int p = slots.place[c][b];
-    return s.j + b < k && p >= 0 && p < rows ? p : -1;
+    ask_c = wrap(ask_c, C);
   };
   const auto fetch = [&](int stage) {
     if (in.t < T) {
       const Span16<E, RAGGED> o(in.t, bytes);
-      const int i0 = in.seg * 32 * U;
+      const int i0 = in.a * 32 * U;
       const int count = o.n - i0 < 32 * U ? o.n - i0 : 32 * U;
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        const int p = place(in, in_c, b);
+        const int p = choice_place(slots, in_c, in.b * B, b, k, rows);
         if (p < 0) continue;
         const int64_t at = (int64_t)p * bytes + (int64_t)i0 * 16 - o.shift;
         copy_row<RAGGED, 32 * U + (RAGGED ? 1 : 0)>(slots.z[stage][b], z, at & ~(int64_t)15,
                                                     rows * bytes, RAGGED ? count + 1 : count, l);
       }
-      if (residual && in.j == 0)
+      if (residual && in.b == 0)
         copy_row<RAGGED, 32 * U>(slots.residual[stage], residual,
                                  o.base - o.shift + (int64_t)i0 * 16, T * bytes, count, l);
     }
     in.next();
-    in_c = in_c + 1 == C ? 0 : in_c + 1;
+    in_c = wrap(in_c, C);
   };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) choices();
@@ -420,8 +436,8 @@ unpermute_kernel(const void* __restrict__ z, const int* __restrict__ position,
     choices();
     copies_commit();
     const Span16<E, RAGGED> o(out.t, bytes);
-    const int i0 = out.seg * 32 * U;
-    if (out.j == 0) {
+    const int i0 = out.a * 32 * U;
+    if (out.b == 0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (residual) {
@@ -434,7 +450,7 @@ unpermute_kernel(const void* __restrict__ z, const int* __restrict__ position,
     }
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      const int p = place(out, out_c, b);
+      const int p = choice_place(slots, out_c, out.b * B, b, k, rows);
       if (p < 0) continue;
       const float w = weights ? slots.weight[out_c][b] : 1.f;
       const int sh = RAGGED ? (int)((unsigned)p * (unsigned)bytes - o.shift) & 15 : 0;
@@ -455,9 +471,9 @@ unpermute_kernel(const void* __restrict__ z, const int* __restrict__ position,
         if (i0 + l + 32 * u < o.n) o.put(y, i0 + l + 32 * u, pack<F32>(acc[u]));
     }
     out.next();
-    out_c = out_c + 1 == C ? 0 : out_c + 1;
-    stage = stage + 1 == S ? 0 : stage + 1;
-    free_stage = free_stage + 1 == S ? 0 : free_stage + 1;
+    out_c = wrap(out_c, C);
+    stage = wrap(stage, S);
+    free_stage = wrap(free_stage, S);
   }
 }
 
@@ -507,11 +523,11 @@ __device__ __forceinline__ void backward_piece(const S& o, void* dz, int i, cons
   o.put(dz, i, pack<F32>(v));
 }
 
-// Gradient of unpermute.  A team of W warps has a token at a time: its warps
-// take segments of the row in turn, all choices B at a time, and their sums of
-// the dot products meet in shared memory.  The pieces are those of z's and dz's
-// row, so that these move as they are; dy, where it starts elsewhere in its 16
-// bytes, is shifted.
+// Gradient of unpermute.  A warp has B choices of a token for the whole row, so
+// that it ends with their dot products: nothing is shared between warps, and
+// there are enough items for an even spread (dy is read again for the next B,
+// from L2).  The pieces are those of z's and dz's row, so that these move as they
+// are; dy, where it starts elsewhere in its 16 bytes, is shifted.
 template <bool RAGGED, int B, int U>
 struct BackwardSlots {
   static constexpr int S = U == 1 ? 4 : 3, C = 2 * S - 1;
@@ -521,30 +537,7 @@ struct BackwardSlots {
   float weight[C][8];
 };
 
-// Steps of a warp: tokens t, batches of choices j, segments seg.
-template <int B, int W>
-struct TeamSteps {
-  int64_t t, dt;
-  int j, seg, segs, k, first;
-  __device__ __forceinline__ TeamSteps(int segs_, int k_) : j(0), segs(segs_), k(k_) {
-    const int warp = threadIdx.x >> 5, teams = (blockDim.x >> 5) / W;
-    t = (int64_t)(warp / W) * gridDim.x + blockIdx.x;
-    dt = (int64_t)gridDim.x * teams;
-    first = seg = warp % W;
-  }
-  __device__ __forceinline__ bool last_segment() const { return seg + W >= segs; }
-  __device__ __forceinline__ void next() {
-    seg += W;
-    if (seg < segs) return;
-    seg = first;
-    j += B;
-    if (j < k) return;
-    j = 0;
-    t += dt;
-  }
-};
-
-template <bool F32, bool RAGGED, int B, int U, int W>
+template <bool F32, bool RAGGED, int B, int U>
 __global__ void __launch_bounds__(32 * kWarps, 1)
 unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ z,
                           const int* __restrict__ position, const int* __restrict__ offsets,
@@ -555,36 +548,26 @@ unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ 
   using Slots = BackwardSlots<RAGGED, B, U>;
   constexpr int S = Slots::S, C = Slots::C;
   extern __shared__ uint4 smem[];
-  __shared__ float red[2][kWarps][8];
   tc::pdl_launch_dependents();
   tc::pdl_wait();
-  const int l = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Slots& slots = reinterpret_cast<Slots*>(smem)[warp];
+  const int l = threadIdx.x & 31;
+  Slots& slots = reinterpret_cast<Slots*>(smem)[threadIdx.x >> 5];
   const int64_t rows = T * k, end = sorted_end(offsets, n_exp, rows);
 
-  TeamSteps<B, W> ask(segs, k), in(segs, k), out(segs, k);
+  // choices copied, rows copied, at work (a: batches of choices, b: segments)
+  Steps ask(batches<B>(k), segs), in = ask, out = ask;
   int ask_c = 0, in_c = 0, out_c = 0;
-  const auto choices = [&]() {   // lanes 0 ... B - 1: places, 8 ... 8 + B - 1: weights
-    const int b = l & 7;
-    if (l < 16 && b < B) {
-      const bool some = ask.t < T && ask.j + b < k;
-      const int64_t f = some ? ask.t * k + ask.j + b : 0;
-      if (l < 8) copy_word(&slots.place[ask_c][b], position + f, some);
-      else copy_word(&slots.weight[ask_c][b], weights + f, some);
-    }
+  const auto choices = [&]() {
+    copy_choices<B>(slots, ask_c, position, weights, ask.t, T, ask.a * B, k);
     ask.next();
-    ask_c = ask_c + 1 == C ? 0 : ask_c + 1;
-  };
-  const auto place = [&](const TeamSteps<B, W>& s, int c, int b) {
-    const int p = slots.place[c][b];
-    return s.j + b < k && p >= 0 && p < rows ? p : -1;
+    ask_c = wrap(ask_c, C);
   };
   const auto fetch = [&](int stage) {
     if (in.t < T) {
-      const int i0 = in.seg * 32 * U;
+      const int i0 = in.b * 32 * U;
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        const int p = place(in, in_c, b);
+        const int p = choice_place(slots, in_c, in.a * B, b, k, rows);
         if (p < 0) continue;
         const Span16<E, RAGGED> o(p, bytes);
         copy_row<RAGGED, 32 * U>(slots.z[stage][b], z, o.base - o.shift + (int64_t)i0 * 16,
@@ -599,7 +582,7 @@ unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ 
                                 bytes / 16 - i0, l);
     }
     in.next();
-    in_c = in_c + 1 == C ? 0 : in_c + 1;
+    in_c = wrap(in_c, C);
   };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) choices();
@@ -612,7 +595,7 @@ unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ 
     choices();
     copies_commit();
   }
-  int stage = 0, free_stage = S - 1, side = 0;
+  int stage = 0, free_stage = S - 1;
   float2 dot[B];
 #pragma unroll
   for (int b = 0; b < B; ++b) dot[b] = make_float2(0.f, 0.f);
@@ -622,12 +605,12 @@ unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ 
     fetch(free_stage);
     choices();
     copies_commit();
-    const int i0 = out.seg * 32 * U;
-    const int64_t f0 = out.t * k + out.j;
+    const int i0 = out.b * 32 * U, j0 = out.a * B;
+    const int64_t f0 = out.t * k + j0;
     const unsigned src = (unsigned)out.t * (unsigned)bytes;   // (its low bits count)
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      const int p = place(out, out_c, b);
+      const int p = choice_place(slots, out_c, j0, b, k, rows);
       if (p >= 0) {
         const Span16<E, RAGGED> o(p, bytes);
         const float w = slots.weight[out_c][b];
@@ -643,38 +626,26 @@ unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ 
                                       slots.z[stage][b][m], w, dot[b]);
         }
       }
-      if (out.j + b < k && f0 + b >= end) {   // a row of no pair
+      if (j0 + b < k && f0 + b >= end) {   // a row of no pair
         const Span16<E, RAGGED> o(f0 + b, bytes);
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (i0 + l + 32 * u < o.n) o.put(dz, i0 + l + 32 * u, make_uint4(0u, 0u, 0u, 0u));
       }
     }
-    if (out.last_segment()) {
+    if (out.last()) {
       float sums[8];
 #pragma unroll
       for (int b = 0; b < 8; ++b) sums[b] = b < B ? dot[b].x + dot[b].y : 0.f;
 #pragma unroll
       for (int b = 0; b < B; ++b) dot[b] = make_float2(0.f, 0.f);
-      float v = warp_sums8(sums, l);
-      if (W > 1) {   // (one barrier: the next batch writes the other side)
-        if ((l & 3) == 0) red[side][warp][l >> 2] = v;
-        asm volatile("bar.sync %0, %1;" ::"r"(warp / W + 1), "n"(W * 32) : "memory");
-        if (warp % W == 0 && l < B) {
-          v = 0.f;
-#pragma unroll
-          for (int i = 0; i < W; ++i) v += red[side][warp + i][l];
-        }
-        side ^= 1;
-      } else {
-        v = __shfl_sync(0xffffffffu, v, (4 * l) & 31);
-      }
-      if (warp % W == 0 && l < B && out.j + l < k) dweights[f0 + l] = v;
+      const float v = warp_sums8(sums, l);
+      if ((l & 3) == 0 && (l >> 2) < B && j0 + (l >> 2) < k) dweights[f0 + (l >> 2)] = v;
     }
     out.next();
-    out_c = out_c + 1 == C ? 0 : out_c + 1;
-    stage = stage + 1 == S ? 0 : stage + 1;
-    free_stage = free_stage + 1 == S ? 0 : free_stage + 1;
+    out_c = wrap(out_c, C);
+    stage = wrap(stage, S);
+    free_stage = wrap(free_stage, S);
   }
 }
 
@@ -821,26 +792,18 @@ cudaError_t unpermute_rows(const UnpermuteCall& c, int64_t bytes, int num_sms, c
   return unpermute_batch<F32, RAGGED, 8, 1>(c, bytes, num_sms, st);
 }
 
-template <bool F32, bool RAGGED, int B, int U, int W>
-cudaError_t backward_team(const UnpermuteBackwardCall& c, int64_t bytes, int64_t segs, int num_sms,
-                          cudaStream_t st) {
-  const auto kernel = unpermute_backward_kernel<F32, RAGGED, B, U, W>;
-  const int smem = kWarps * (int)sizeof(BackwardSlots<RAGGED, B, U>);
-  static_assert(kWarps * sizeof(BackwardSlots<RAGGED, B, U>) + 1024 <= 232448, "shared memory");
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  return launch_chained(kernel, dim3(stream_grid(c.T, num_sms)), dim3(32 * kWarps), smem, st, c.dy,
-                        c.z, c.position, c.offsets, c.weights, c.dz, c.dweights, c.T, (int)c.k,
-                        (int)c.E, (int)bytes, (int)segs);
-}
-
 template <bool F32, bool RAGGED, int B, int U>
 cudaError_t backward_batch(const UnpermuteBackwardCall& c, int64_t bytes, int num_sms,
                            cudaStream_t st) {
+  const auto kernel = unpermute_backward_kernel<F32, RAGGED, B, U>;
+  const int smem = kWarps * (int)sizeof(BackwardSlots<RAGGED, B, U>);
+  static_assert(kWarps * sizeof(BackwardSlots<RAGGED, B, U>) <= 232448, "shared memory");
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   const int64_t segs = (pieces_of(bytes) + 32 * U - 1) / (32 * U);
-  if (segs >= 4) return backward_team<F32, RAGGED, B, U, 4>(c, bytes, segs, num_sms, st);
-  if (segs >= 2) return backward_team<F32, RAGGED, B, U, 2>(c, bytes, segs, num_sms, st);
-  return backward_team<F32, RAGGED, B, U, 1>(c, bytes, segs, num_sms, st);
+  return launch_chained(kernel, dim3(stream_grid(c.T * ((c.k + B - 1) / B), num_sms)),
+                        dim3(32 * kWarps), smem, st, c.dy, c.z, c.position, c.offsets, c.weights,
+                        c.dz, c.dweights, c.T, (int)c.k, (int)c.E, (int)bytes, (int)segs);
 }
 
 template <bool F32, bool RAGGED>
@@ -855,9 +818,9 @@ cudaError_t backward_rows(const UnpermuteBackwardCall& c, int64_t bytes, int num
                           c.position, c.offsets, c.weights, c.dz, c.dweights, c.T, (int)c.k,
                           (int)c.E, (int)bytes);
   }
-  if (per < 512 && c.k > 4) return backward_batch<F32, RAGGED, 8, 1>(c, bytes, num_sms, st);
-  if (per < 512 && c.k > 2) return backward_batch<F32, RAGGED, 4, 2>(c, bytes, num_sms, st);
-  return backward_batch<F32, RAGGED, 2, 4>(c, bytes, num_sms, st);
+  if (per >= 128 || c.k <= 2) return backward_batch<F32, RAGGED, 2, 4>(c, bytes, num_sms, st);
+  if (per >= 64 || c.k <= 4) return backward_batch<F32, RAGGED, 4, 2>(c, bytes, num_sms, st);
+  return backward_batch<F32, RAGGED, 8, 1>(c, bytes, num_sms, st);
 }
 
 }  // namespace
