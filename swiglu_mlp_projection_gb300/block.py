@@ -14,20 +14,17 @@ from . import swiglu_down, swiglu_down_fp8, swiglu_up, swiglu_up_fp8
 from .moe import _bytes, _check, _first, _out, _row_code, _workspace
 
 
-def _rows(x, weight, x_name):
-    """Checks of the rows and the weight; (torch, device, dtype code, weight's
-    address and dtype code, M, d)."""
-    torch = _torch()
+def _rows(torch, x, weight, x_name):
+    """Checks of rows x [M, d] and weight [d]: (device, codes of their dtypes)."""
     index = _first(x, x_name)
     dt = _row_code(torch, x, x_name)
     if x.dim() != 2:
         raise ValueError("expected %s [M, d]" % x_name)
-    pw = _check(weight, "weight", index)
+    _check(weight, "weight", index)
     wt = _row_code(torch, weight, "weight")
-    M, d = x.shape
-    if weight.dim() != 1 or weight.shape[0] != d:
-        raise ValueError("weight must be [d] = [%d]" % d)
-    return torch, index, dt, pw, wt, M, d
+    if weight.dim() != 1 or weight.shape[0] != x.shape[1]:
+        raise ValueError("weight must be [d] = [%d]" % x.shape[1])
+    return index, dt, wt
 
 
 def _like(t, name, x, index):
@@ -46,17 +43,20 @@ def rms_norm(x, weight, residual=None, eps=1e-6, out=None, sum_out=None, stream=
     a residual (y, s).  ``out`` takes y and ``sum_out`` s; each may be x or
     residual itself.
     """
-    torch, index, dt, pw, wt, M, d = _rows(x, weight, "x")
+    torch = _torch()
+    index, dt, wt = _rows(torch, x, weight, "x")
+    shape, dtype, dev = x.shape, x.dtype, x.device
     pr = ps = s = None
     if residual is not None:
         pr = _like(residual, "residual", x, index)
-        s = _out(torch, sum_out, x.shape, x.dtype, index, x.device, stream)
+        s = _out(torch, sum_out, shape, dtype, index, dev, stream)
         ps = s.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
-    y = _out(torch, out, x.shape, x.dtype, index, x.device, stream)
-    _call(index, _lib.load().swiglu_rms_norm, x.data_ptr(), pr, pw, y.data_ptr(), ps, M, d, eps, dt,
-          wt, stream.cuda_stream if stream is not None else _raw_stream(index))
+    y = _out(torch, out, shape, dtype, index, dev, stream)
+    M, d = shape
+    _call(index, _lib.load().swiglu_rms_norm, x.data_ptr(), pr, weight.data_ptr(), y.data_ptr(), ps,
+          M, d, eps, dt, wt, stream.cuda_stream if stream is not None else _raw_stream(index))
     return y if residual is None else (y, s)
 
 
@@ -64,19 +64,22 @@ def rms_norm_fp8(x, weight, residual=None, eps=1e-6, out=None, sum_out=None, str
     """As ``rms_norm``, with y as an Fp8Rows: e4m3 codes [M, d] (uint8) and
     float32 scales [M], quantized per row from the float32 values, which
     ``swiglu_up_fp8`` and ``permute`` take as they are.  ``out``: an Fp8Rows."""
-    torch, index, dt, pw, wt, M, d = _rows(x, weight, "x")
+    torch = _torch()
+    index, dt, wt = _rows(torch, x, weight, "x")
+    shape, dev = x.shape, x.device
+    M, d = shape
     pr = ps = s = None
     if residual is not None:
         pr = _like(residual, "residual", x, index)
-        s = _out(torch, sum_out, x.shape, x.dtype, index, x.device, stream)
+        s = _out(torch, sum_out, shape, x.dtype, index, dev, stream)
         ps = s.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual")
     codes, scales = (None, None) if out is None else out
-    codes = _out(torch, codes, x.shape, torch.uint8, index, x.device, stream)
-    scales = _out(torch, scales, (M,), torch.float32, index, x.device, stream)
-    _call(index, _lib.load().swiglu_rms_norm_fp8, x.data_ptr(), pr, pw, codes.data_ptr(),
-          scales.data_ptr(), ps, M, d, eps, dt, wt,
+    codes = _out(torch, codes, shape, torch.uint8, index, dev, stream)
+    scales = _out(torch, scales, (M,), torch.float32, index, dev, stream)
+    _call(index, _lib.load().swiglu_rms_norm_fp8, x.data_ptr(), pr, weight.data_ptr(),
+          codes.data_ptr(), scales.data_ptr(), ps, M, d, eps, dt, wt,
           stream.cuda_stream if stream is not None else _raw_stream(index))
     y = Fp8Rows(codes, scales)
     return y if residual is None else (y, s)
@@ -91,13 +94,16 @@ def rms_norm_backward(dy, s, weight, ds=None, eps=1e-6, out=None, workspace=None
     of the residual (``out`` if given; it may be dy, s or ds), and dweight [d] of
     weight's dtype.
     """
-    torch, index, dt, pw, wt, M, d = _rows(s, weight, "s")
+    torch = _torch()
+    index, dt, wt = _rows(torch, s, weight, "s")
+    M, d = s.shape
     py = _like(dy, "dy", s, index)
     pd = None if ds is None else _like(ds, "ds", s, index)
     dx = _out(torch, out, s.shape, s.dtype, index, s.device, stream)
     dw = _empty(torch, (d,), weight.dtype, s.device, stream)
     ws, nws = _workspace(workspace, index)
-    _call(index, _lib.load().swiglu_rms_norm_backward, py, s.data_ptr(), pw, pd, dx.data_ptr(),
+    _call(index, _lib.load().swiglu_rms_norm_backward, py, s.data_ptr(), weight.data_ptr(),
+          pd, dx.data_ptr(),
           dw.data_ptr(), M, d, eps, dt, wt, ws, nws,
           stream.cuda_stream if stream is not None else _raw_stream(index))
     return dx, dw

@@ -171,13 +171,20 @@ constexpr int team_threads(int w) { return 24 % w ? 32 * w : 768; }
 constexpr int team_rows(int w) { return team_threads(w) / 32 / w; }   // R
 constexpr int team_stages(int w) { return w == 32 ? 2 : w == 16 ? 4 : 3; }
 
-// The sum over lanes 0 ... W - 1 of values that are 0 in the others, in every lane.
+// The sum of v[0 ... W - 1], one of which each lane holds (lane l that of l % W
+// where W is a power of two; otherwise l's, and 0 from W on), in every lane.
 template <int W>
 __device__ __forceinline__ float team_sum(float v) {
+  if constexpr ((W & (W - 1)) != 0) return warp_sum(v);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     if (o < W) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return W > 16 ? v : __shfl_sync(0xffffffffu, v, 0);
+  return v;
+}
+template <int W>
+__device__ __forceinline__ float2 team_value(const float2* v, int l) {
+  if (W & (W - 1)) return l < W ? v[l] : make_float2(0.f, 0.f);
+  return v[l & (W - 1)];
 }
 
 template <bool F32, int W, bool RAGGED, int ARRAYS>
@@ -263,7 +270,7 @@ norm_stream_kernel(const __grid_constant__ NormArgs a) {
     if (W > 1) {   // (one barrier a row: the next row writes the other side)
       if (tm.l == 0) red[side][tm.warp] = make_float2(q, m);
       tm.sync();
-      const float2 v = tm.l < W ? red[side][tm.team * W + tm.l] : make_float2(0.f, 0.f);
+      const float2 v = team_value<W>(red[side] + tm.team * W, tm.l);
       q = team_sum<W>(v.x);
       if (FP8) m = warp_max(v.y);
     }
@@ -316,13 +323,10 @@ int team_grid(int64_t M, int num_sms) {
   const int64_t most = num_sms / 8 * 8;
   return (int)(M < most ? M : most);
 }
-template <typename A>
-cudaError_t launch_team(void (*kernel)(A), const A& a, int w, int arrays, int grid,
-                        cudaStream_t st) {
-  const int smem = team_stages(w) * arrays * kPieces * team_threads(w) * 16;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  return launch_chained(kernel, dim3(grid), dim3(team_threads(w)), smem, st, a);
+template <auto kernel, int W, int ARRAYS, typename A>
+cudaError_t launch_team(const A& a, int grid, cudaStream_t st) {
+  constexpr int smem = team_stages(W) * ARRAYS * kPieces * team_threads(W) * 16;
+  return launch_chained_smem<kernel>(smem, dim3(grid), dim3(team_threads(W)), smem, st, a);
 }
 
 template <bool F32, int VPT, bool FP8, bool RAGGED>
@@ -344,18 +348,18 @@ cudaError_t launch_rows(const NormArgs& a, int num_sms, cudaStream_t st) {
     if (s.vpt == 2 * base) return launch_norm<F32, 2 * base, FP8, false>(a, s, st);
     return launch_norm<F32, 4 * base, FP8, false>(a, s, st);
   }
-  const int w = team_warps(a.d, V), arrays = 2, grid = team_grid(a.M, num_sms);
-  switch (w) {
-    case 1: return launch_team(norm_stream_kernel<F32, 1, FP8>, a, w, arrays, grid, st);
-    case 2: return launch_team(norm_stream_kernel<F32, 2, FP8>, a, w, arrays, grid, st);
-    case 3: return launch_team(norm_stream_kernel<F32, 3, FP8>, a, w, arrays, grid, st);
-    case 4: return launch_team(norm_stream_kernel<F32, 4, FP8>, a, w, arrays, grid, st);
-    case 6: return launch_team(norm_stream_kernel<F32, 6, FP8>, a, w, arrays, grid, st);
-    case 8: return launch_team(norm_stream_kernel<F32, 8, FP8>, a, w, arrays, grid, st);
-    case 12: return launch_team(norm_stream_kernel<F32, 12, FP8>, a, w, arrays, grid, st);
-    case 16: return launch_team(norm_stream_kernel<F32, 16, FP8>, a, w, arrays, grid, st);
-    case 24: return launch_team(norm_stream_kernel<F32, 24, FP8>, a, w, arrays, grid, st);
-    case 32: return launch_team(norm_stream_kernel<F32, 32, FP8>, a, w, arrays, grid, st);
+  const int grid = team_grid(a.M, num_sms);
+  switch (team_warps(a.d, V)) {
+    case 1: return launch_team<norm_stream_kernel<F32, 1, FP8>, 1, 2>(a, grid, st);
+    case 2: return launch_team<norm_stream_kernel<F32, 2, FP8>, 2, 2>(a, grid, st);
+    case 3: return launch_team<norm_stream_kernel<F32, 3, FP8>, 3, 2>(a, grid, st);
+    case 4: return launch_team<norm_stream_kernel<F32, 4, FP8>, 4, 2>(a, grid, st);
+    case 6: return launch_team<norm_stream_kernel<F32, 6, FP8>, 6, 2>(a, grid, st);
+    case 8: return launch_team<norm_stream_kernel<F32, 8, FP8>, 8, 2>(a, grid, st);
+    case 12: return launch_team<norm_stream_kernel<F32, 12, FP8>, 12, 2>(a, grid, st);
+    case 16: return launch_team<norm_stream_kernel<F32, 16, FP8>, 16, 2>(a, grid, st);
+    case 24: return launch_team<norm_stream_kernel<F32, 24, FP8>, 24, 2>(a, grid, st);
+    case 32: return launch_team<norm_stream_kernel<F32, 32, FP8>, 32, 2>(a, grid, st);
   }
   const int vpt = 4 * base;
   const Shape wide{vpt, (int)((pieces_of(a.d, V) + vpt * 32 - 1) / (vpt * 32) * 32), false};
@@ -428,7 +432,7 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
     if (W > 1) {   // (one barrier a row: the next row writes the other side)
       if (tm.l == 0) red[side][tm.warp] = make_float2(q, p);
       tm.sync();
-      const float2 v = tm.l < W ? red[side][tm.team * W + tm.l] : make_float2(0.f, 0.f);
+      const float2 v = team_value<W>(red[side] + tm.team * W, tm.l);
       q = team_sum<W>(v.x);
       p = team_sum<W>(v.y);
     }
@@ -592,26 +596,23 @@ dweight_kernel(const float* __restrict__ part, int n, int d, void* __restrict__ 
 
 template <bool F32, bool RAGGED>
 cudaError_t launch_back(const BackArgs& a, int grid, cudaStream_t st) {
-  const int w = team_warps(a.d, Row<F32>::kVec), arrays = 3;
   // (the teams' sums take the place of their stages: R rows of at most 512 W
   // elements, 2 KB, and each stage has as much)
-  switch (w) {
-    case 1: return launch_team(norm_backward_kernel<F32, 1, RAGGED>, a, w, arrays, grid, st);
-    case 2: return launch_team(norm_backward_kernel<F32, 2, RAGGED>, a, w, arrays, grid, st);
-    case 3: return launch_team(norm_backward_kernel<F32, 3, RAGGED>, a, w, arrays, grid, st);
-    case 4: return launch_team(norm_backward_kernel<F32, 4, RAGGED>, a, w, arrays, grid, st);
-    case 6: return launch_team(norm_backward_kernel<F32, 6, RAGGED>, a, w, arrays, grid, st);
-    case 8: return launch_team(norm_backward_kernel<F32, 8, RAGGED>, a, w, arrays, grid, st);
-    case 12: return launch_team(norm_backward_kernel<F32, 12, RAGGED>, a, w, arrays, grid, st);
-    case 16: return launch_team(norm_backward_kernel<F32, 16, RAGGED>, a, w, arrays, grid, st);
-    case 24: return launch_team(norm_backward_kernel<F32, 24, RAGGED>, a, w, arrays, grid, st);
-    case 32: return launch_team(norm_backward_kernel<F32, 32, RAGGED>, a, w, arrays, grid, st);
+  switch (team_warps(a.d, Row<F32>::kVec)) {
+    case 1: return launch_team<norm_backward_kernel<F32, 1, RAGGED>, 1, 3>(a, grid, st);
+    case 2: return launch_team<norm_backward_kernel<F32, 2, RAGGED>, 2, 3>(a, grid, st);
+    case 3: return launch_team<norm_backward_kernel<F32, 3, RAGGED>, 3, 3>(a, grid, st);
+    case 4: return launch_team<norm_backward_kernel<F32, 4, RAGGED>, 4, 3>(a, grid, st);
+    case 6: return launch_team<norm_backward_kernel<F32, 6, RAGGED>, 6, 3>(a, grid, st);
+    case 8: return launch_team<norm_backward_kernel<F32, 8, RAGGED>, 8, 3>(a, grid, st);
+    case 12: return launch_team<norm_backward_kernel<F32, 12, RAGGED>, 12, 3>(a, grid, st);
+    case 16: return launch_team<norm_backward_kernel<F32, 16, RAGGED>, 16, 3>(a, grid, st);
+    case 24: return launch_team<norm_backward_kernel<F32, 24, RAGGED>, 24, 3>(a, grid, st);
+    case 32: return launch_team<norm_backward_kernel<F32, 32, RAGGED>, 32, 3>(a, grid, st);
   }
-  const auto k = norm_backward_wide_kernel<F32, RAGGED>;
-  const int smem = (a.d + 16) * (int)sizeof(float);
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  return launch_chained(k, dim3(grid), dim3(1024), smem, st, a);
+  return launch_chained_smem<norm_backward_wide_kernel<F32, RAGGED>>(
+      (kMaxNormWidth + 16) * (int)sizeof(float), dim3(grid), dim3(1024),
+      (a.d + 16) * sizeof(float), st, a);
 }
 
 }  // namespace

@@ -744,16 +744,14 @@ int stream_grid(int64_t items, int most) { return (int)(items < most ? items : m
 
 template <typename E>
 cudaError_t permute_ragged(const PermuteCall& c, int num_sms, cudaStream_t st) {
-  const auto kernel = permute_ragged_kernel<E>;
-  const int smem = kPermuteWarps * (int)sizeof(PermuteSlots);
-  static_assert(2 * kPermuteWarps * sizeof(PermuteSlots) <= 225 * 1024, "shared memory");
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  constexpr int smem = kPermuteWarps * (int)sizeof(PermuteSlots);
+  static_assert(2 * smem <= 225 * 1024, "shared memory");
   const int64_t bytes = c.d * c.elem, piece = 32 * PermuteSlots::U;
   const int64_t segs = (pieces_of(bytes) + piece - 1) / piece;
-  return launch_chained(kernel, dim3(stream_grid(c.T * segs, 2 * num_sms)), dim3(32 * kPermuteWarps),
-                        smem, st, c.x, c.scales, c.position, c.offsets, c.out, c.out_scales, c.T,
-                        (int)c.k, (int)c.E, (int)bytes, (int)segs);
+  return launch_chained_smem<permute_ragged_kernel<E>>(
+      smem, dim3(stream_grid(c.T * segs, 2 * num_sms)), dim3(32 * kPermuteWarps), smem, st, c.x,
+      c.scales, c.position, c.offsets, c.out, c.out_scales, c.T, (int)c.k, (int)c.E, (int)bytes,
+      (int)segs);
 }
 
 // Up to this many 16-byte pieces of y a thread each, one wave of them.
@@ -772,15 +770,12 @@ cudaError_t unpermute_few(const UnpermuteCall& c, int64_t bytes, cudaStream_t st
 
 template <bool F32, bool RAGGED, int B, int U>
 cudaError_t unpermute_batch(const UnpermuteCall& c, int64_t bytes, int num_sms, cudaStream_t st) {
-  const auto kernel = unpermute_kernel<F32, RAGGED, B, U>;
-  const int smem = kWarps * (int)sizeof(UnpermuteSlots<F32, RAGGED, B, U>);
-  static_assert(kWarps * sizeof(UnpermuteSlots<F32, RAGGED, B, U>) <= 232448, "shared memory");
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  constexpr int smem = kWarps * (int)sizeof(UnpermuteSlots<F32, RAGGED, B, U>);
+  static_assert(smem <= 232448, "shared memory");
   const int64_t segs = (pieces_of(bytes) + 32 * U - 1) / (32 * U);
-  return launch_chained(kernel, dim3(stream_grid(c.T * segs, num_sms)), dim3(32 * kWarps), smem, st,
-                        c.z, c.position, c.weights, c.residual, c.y, c.T, (int)c.k, (int)bytes,
-                        (int)segs);
+  return launch_chained_smem<unpermute_kernel<F32, RAGGED, B, U>>(
+      smem, dim3(stream_grid(c.T * segs, num_sms)), dim3(32 * kWarps), smem, st, c.z, c.position,
+      c.weights, c.residual, c.y, c.T, (int)c.k, (int)bytes, (int)segs);
 }
 
 template <bool F32, bool RAGGED>
@@ -795,15 +790,13 @@ cudaError_t unpermute_rows(const UnpermuteCall& c, int64_t bytes, int num_sms, c
 template <bool F32, bool RAGGED, int B, int U>
 cudaError_t backward_batch(const UnpermuteBackwardCall& c, int64_t bytes, int num_sms,
                            cudaStream_t st) {
-  const auto kernel = unpermute_backward_kernel<F32, RAGGED, B, U>;
-  const int smem = kWarps * (int)sizeof(BackwardSlots<RAGGED, B, U>);
-  static_assert(kWarps * sizeof(BackwardSlots<RAGGED, B, U>) <= 232448, "shared memory");
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  constexpr int smem = kWarps * (int)sizeof(BackwardSlots<RAGGED, B, U>);
+  static_assert(smem <= 232448, "shared memory");
   const int64_t segs = (pieces_of(bytes) + 32 * U - 1) / (32 * U);
-  return launch_chained(kernel, dim3(stream_grid(c.T * ((c.k + B - 1) / B), num_sms)),
-                        dim3(32 * kWarps), smem, st, c.dy, c.z, c.position, c.offsets, c.weights,
-                        c.dz, c.dweights, c.T, (int)c.k, (int)c.E, (int)bytes, (int)segs);
+  return launch_chained_smem<unpermute_backward_kernel<F32, RAGGED, B, U>>(
+      smem, dim3(stream_grid(c.T * ((c.k + B - 1) / B), num_sms)), dim3(32 * kWarps), smem, st, c.dy,
+      c.z, c.position, c.offsets, c.weights, c.dz, c.dweights, c.T, (int)c.k, (int)c.E, (int)bytes,
+      (int)segs);
 }
 
 template <bool F32, bool RAGGED>

@@ -3,6 +3,8 @@
 
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "tc_common.cuh"
 
@@ -264,6 +266,23 @@ inline cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, dim3 blo
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
+// The same for a kernel that needs up to `most` bytes of shared memory, which is
+// asked for once on each device.
+template <auto kernel, typename... Args>
+inline cudaError_t launch_chained_smem(int most, dim3 grid, dim3 block, size_t smem,
+                                       cudaStream_t st, Args... args) {
+  static std::atomic<int> configured[64];   // zero: not yet set on that device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) configured[dev].store(1, std::memory_order_release);
+  }
+  return launch_chained(kernel, grid, block, smem, st, args...);
 }
 
 }  // namespace swg

@@ -641,9 +641,10 @@ struct Plan {
 // max_pairs: 2-CTA clusters that fit on the device at once (num_sms / 2 when
 // planning without a device).
 // nk: the weights are [n_out, K] (served by the tensor-core paths only).
+// fp8_rows: an FP8 call whose rows come quantized.
 int make_plan(int op, int64_t M, int64_t K, int64_t n_out, int dtype, int path, int num_sms,
               int max_pairs, Plan* p, bool fp8 = false, const int* sk_caps = nullptr,
-              bool nk = false, const int* simt_caps = nullptr) {
+              bool nk = false, const int* simt_caps = nullptr, bool fp8_rows = false) {
   int rp = 0;
   int st = resolve_path(op, M, K, n_out, dtype, path, &rp, num_sms, sk_caps);
   if (st != SWIGLU_OK) return st;
@@ -683,6 +684,13 @@ int make_plan(int op, int64_t M, int64_t K, int64_t n_out, int dtype, int path, 
     }
   } else if (rp == SWIGLU_PATH_SKINNY) {
     p->skinny = plan_skinny(M, K, n_out, num_sms, plain, fp8, sk_caps, tn);
+    // Rows that come quantized: no kernel of the call's own runs before the
+    // product, and a second one that adds its sums (the same bits) lets the next
+    // call's product start earlier.  Calls back to back, one kernel / two: d =
+    // 4096, d_ff = 14336, M = 1 / 16 / 32 23.3 / 24.0 / 26.2 against 21.6 / 23.4
+    // / 23.7 us, behind their norm 23.9 / 25.1 / 27.5 against 23.5 / 23.9 / 24.7;
+    // d = 8192, d_ff = 29568, M = 16 79.3 against 78.4.
+    if (fp8_rows && !plain && !p->skinny.cluster && tn.sk_split < 0) p->skinny.split = 1;
     // K slices per column group: the cluster size, or (stream-K) at most maxq
     p->slices = p->skinny.cluster ? p->skinny.cluster : p->skinny.maxq;
     p->grid = p->skinny.grid;
@@ -737,7 +745,8 @@ int run(const Call& c) {
   // FP8: the GEMM kernels see each row of e4m3 codes as K / 2 byte pairs
   const int64_t Kg = c.fp8 ? c.K / 2 : c.K;
   if ((v = make_plan(c.op, c.M, Kg, c.n_out, c.dtype, c.path, di.num_sms, di.max_pairs, &p,
-                     c.fp8, di.sk_caps, c.wlayout == kWeightsNK, di.simt_caps)) != SWIGLU_OK)
+                     c.fp8, di.sk_caps, c.wlayout == kWeightsNK, di.simt_caps,
+                     c.sx != nullptr)) != SWIGLU_OK)
     return v;
   if (c.fp8 && p.path == SWIGLU_PATH_SIMT && c.K > 0)
     return fail(SWIGLU_ERR_UNSUPPORTED, "FP8 weights are served by the tensor-core paths only");
