@@ -46,13 +46,11 @@ __device__ __forceinline__ float warp_max(float v) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
-// A piece of the row on its way: s (stored where there is a residual), t = s * w,
-// the sums so far.
-template <bool F32, bool FP8, bool RAGGED>
+// A piece of the row on its way: s (stored where there is a residual) and its squares ...
+template <bool F32, bool RAGGED>
 __device__ __forceinline__ void add_piece(const Pieces<F32, RAGGED>& pc, const NormArgs& a,
                                           int64_t first, int i, const uint4& xq, const uint4& rq,
-                                          const float2 (&w)[Row<F32>::kVec / 2],
-                                          float2 (&t)[Row<F32>::kVec / 2], float2& q, float& m) {
+                                          float2 (&t)[Row<F32>::kVec / 2], float2& q) {
   constexpr int H = Row<F32>::kVec / 2;
   unpack<F32>(xq, t);
   if (a.residual) {
@@ -64,8 +62,13 @@ __device__ __forceinline__ void add_piece(const Pieces<F32, RAGGED>& pc, const N
   pc.mask(i, t);
   if (a.residual) pc.store_at(a.sum, first, i, t);
 #pragma unroll
+  for (int h = 0; h < H; ++h) q = fma2(t[h], t[h], q);
+}
+// ... then t = s * w, and the largest so far.
+template <bool FP8, int H>
+__device__ __forceinline__ void weigh(float2 (&t)[H], const float2 (&w)[H], float& m) {
+#pragma unroll
   for (int h = 0; h < H; ++h) {
-    q = fma2(t[h], t[h], q);
     t[h] = mul2(t[h], w[h]);
     if (FP8) m = fmaxf(m, fmaxf(fabsf(t[h].x), fabsf(t[h].y)));
   }
@@ -131,9 +134,10 @@ norm_kernel(const __grid_constant__ NormArgs a) {
   for (int j = 0; j < VPT; ++j) {
     const int i = lane + j * lanes;
     if (i >= pc.n) continue;
+    add_piece<F32, RAGGED>(pc, a, pc.first, i, xr[j], rr[j], t[j], q2);
     float2 w[H];
     pc.weight(a.weight, a.weight_f32, i, w);
-    add_piece<F32, FP8, RAGGED>(pc, a, pc.first, i, xr[j], rr[j], w, t[j], q2, m);
+    weigh<FP8>(t[j], w, m);
   }
   float q = warp_sum(q2.x + q2.y);
   if (FP8) m = warp_max(m);
@@ -262,8 +266,9 @@ norm_stream_kernel(const __grid_constant__ NormArgs a) {
     for (int j = 0; j < P; ++j) {
       const int i = tm.piece(j);
       if (i >= tm.pc.n) continue;
-      add_piece<F32, FP8, true>(tm.pc, a, tm.first(row), i, *tm.slot(stage, 0, j),
-                                a.residual ? *tm.slot(stage, 1, j) : uint4{}, w[j], t[j], q2, m);
+      add_piece<F32, true>(tm.pc, a, tm.first(row), i, *tm.slot(stage, 0, j),
+                           a.residual ? *tm.slot(stage, 1, j) : uint4{}, t[j], q2);
+      weigh<FP8>(t[j], w[j], m);
     }
     float q = warp_sum(q2.x + q2.y);
     if (FP8) m = warp_max(m);
@@ -296,12 +301,13 @@ struct Shape {
 Shape shape_of(int64_t pieces, int vec, int64_t M, int num_sms) {
   // Many rows of up to 1024 elements: a warp each.  Otherwise a CTA with 16
   // elements per thread: 8 where the rows are few and only latency counts, 32
-  // where 1024 threads would not do.
+  // where 512 threads would not do (4096 rows of 16384, bf16: 81 us, against 88
+  // with 16 elements and 1024 threads, of which one CTA fits on an SM).
   int e = 8;
   if (M > num_sms) {
     while (e < 32 && 32 * (e / vec) < pieces) e *= 2;
     if (32 * (e / vec) >= pieces) return {e / vec, 32, true};
-    e = 16;
+    e = 512 * (16 / vec) < pieces ? 32 : 16;
   }
   while (e < 32 && 1024 * (e / vec) < pieces) e *= 2;
   const int vpt = e / vec;

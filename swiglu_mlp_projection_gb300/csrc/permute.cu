@@ -319,7 +319,7 @@ permute_ragged_kernel(const void* __restrict__ x, const float* __restrict__ scal
   }
 }
 
-// Few pieces: each has a thread of its own, and nothing is copied ahead.
+// Few pieces (see kFewPieces): each has a thread of its own.
 template <bool F32, bool RAGGED>
 __global__ void __launch_bounds__(256)
 unpermute_few_kernel(const void* __restrict__ z, const int* __restrict__ position,
@@ -649,7 +649,7 @@ unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ 
   }
 }
 
-// Few pieces: blockDim.x threads to a token, and nothing is copied ahead.
+// Few pieces (see kFewPieces): blockDim.x threads to a token.
 template <bool F32, bool RAGGED>
 __global__ void __launch_bounds__(256)
 unpermute_backward_few_kernel(const void* __restrict__ dy, const void* __restrict__ z,
@@ -754,8 +754,15 @@ cudaError_t permute_ragged(const PermuteCall& c, int num_sms, cudaStream_t st) {
       (int)segs);
 }
 
-// Up to this many 16-byte pieces of y a thread each, one wave of them.
-constexpr int64_t kFewPieces = 152 * 512;
+// Up to this many 16-byte pieces of y (or dy) each has a thread, and nothing is
+// copied ahead: one wave of threads, or little more.  In a graph, few / streamed:
+// unpermute d = 4096, k = 2, 64 tokens (32768 pieces) 2.3 / 2.5 us, 256 tokens
+// 2.5 / 2.8, 512 tokens 4.6 / 3.9; its gradient 2.7 / 5.1, 3.0 / 5.1, 6.1 / 5.2,
+// and d = 1024, k = 8, 512 tokens (65536 pieces) 3.5 / 4.3, 1024 tokens 7.7 / 5.9.
+// With more than four choices, unpermute's threads have as much under way
+// themselves: d = 4096, k = 8, 256 tokens 4.2 / 4.8, 1024 tokens 13.7 / 15.8, 2048
+// tokens 25.0 / 28.4, 4096 tokens 53.8 / 53.3.
+constexpr int64_t kFewPieces = 152 * 640, kFewPiecesManyChoices = (int64_t)1 << 20;
 
 template <bool F32, bool RAGGED>
 cudaError_t unpermute_few(const UnpermuteCall& c, int64_t bytes, cudaStream_t st) {
@@ -781,7 +788,8 @@ cudaError_t unpermute_batch(const UnpermuteCall& c, int64_t bytes, int num_sms, 
 template <bool F32, bool RAGGED>
 cudaError_t unpermute_rows(const UnpermuteCall& c, int64_t bytes, int num_sms, cudaStream_t st) {
   const int64_t per = pieces_of(bytes);
-  if (c.T * per <= kFewPieces) return unpermute_few<F32, RAGGED>(c, bytes, st);
+  if (c.T * per <= (c.k > 4 ? kFewPiecesManyChoices : kFewPieces))
+    return unpermute_few<F32, RAGGED>(c, bytes, st);
   if (per >= 128 || c.k <= 2) return unpermute_batch<F32, RAGGED, 2, 4>(c, bytes, num_sms, st);
   if (per >= 64 || c.k <= 4) return unpermute_batch<F32, RAGGED, 4, 2>(c, bytes, num_sms, st);
   return unpermute_batch<F32, RAGGED, 8, 1>(c, bytes, num_sms, st);

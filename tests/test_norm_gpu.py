@@ -64,7 +64,10 @@ def check_fp8(rows, x, residual, w, eps):
 SIZES = [(1, 1), (1, 8), (1, 4096), (1, 4099), (1, 32768), (1, 32752), (1, 32751), (2, 7), (3, 64), (5, 896),
          (7, 897), (16, 4096), (33, 2047), (150, 8192), (151, 129), (153, 1), (200, 8), (200, 13),
          (300, 130), (333, 896), (400, 1000), (400, 1024), (300, 1031), (260, 2056), (257, 4100), (160, 16384),
-         (154, 16391), (155, 32768), (156, 32737), (1000, 509)]
+         (154, 16391), (155, 32768), (156, 32737), (1000, 509),
+         # each number of warps that may share a row, and several rows for each of them
+         (170, 1400), (333, 1801), (160, 2048), (157, 3301), (155, 5000), (159, 7001), (154, 9001), (153, 10000),
+         (170, 13001), (15001, 40), (15001, 43), (8000, 601), (2100, 4099), (2100, 4096)]
 
 
 @pytest.mark.parametrize("dtype,wdtype", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])

@@ -45,9 +45,15 @@ CASES = [  # T, E, k, d, dropped
     (300, 7, 2, 136, 0.2), (1000, 128, 8, 768, 0.05), (2500, 4, 2, 20, 0), (40, 1024, 17, 65, 0.1),
     (333, 8, 2, 896, 1.0), (9, 8, 8, 16384, 0.1)]
 
+# enough tokens for the kernels that copy rows ahead: long, middle and short rows, with few
+# choices and many, in whole 16-byte pieces and not
+LARGE = [(9000, 64, 8, 1024, 0.05), (8500, 64, 6, 1027, 0.05), (7000, 8, 2, 128, 0.1), (7000, 8, 1, 130, 0),
+         (17000, 16, 6, 520, 0.02), (17000, 16, 5, 519, 0.02), (7000, 8, 3, 128, 0), (7000, 60, 4, 133, 0.3),
+         (40000, 32, 9, 256, 0.02), (36000, 32, 7, 251, 0), (30000, 40, 17, 300, 0.1), (3000, 8, 2, 4096, 0.01)]
+
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("T,E,k,d,dropped", CASES)
+@pytest.mark.parametrize("T,E,k,d,dropped", CASES + LARGE[:4])
 def test_permute(cuda_lib, T, E, k, d, dropped, dtype):
     rt = routing(T, E, k, T + d, dropped)
     x = randn(1, T, d, dtype=dtype)
@@ -67,7 +73,7 @@ def test_permute(cuda_lib, T, E, k, d, dropped, dtype):
         assert bool((err <= ref.abs() * HALF[dtype] + (k + 1) * U * size).all())
 
 
-@pytest.mark.parametrize("T,E,k,d,dropped", CASES)
+@pytest.mark.parametrize("T,E,k,d,dropped", CASES + LARGE[:4])
 def test_permute_fp8(cuda_lib, T, E, k, d, dropped):
     rt = routing(T, E, k, T + d, dropped)
     g = gen(4)
@@ -85,7 +91,7 @@ def test_permute_fp8(cuda_lib, T, E, k, d, dropped):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("T,E,k,d,dropped", CASES)
+@pytest.mark.parametrize("T,E,k,d,dropped", CASES + LARGE)
 def test_unpermute(cuda_lib, T, E, k, d, dropped, dtype):
     rt = routing(T, E, k, T + d, dropped)
     z, r = randn(1, T * k, d, dtype=dtype), randn(3, T, d, dtype=dtype)
@@ -106,7 +112,7 @@ def test_unpermute(cuda_lib, T, E, k, d, dropped, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("T,E,k,d,dropped", CASES)
+@pytest.mark.parametrize("T,E,k,d,dropped", CASES + LARGE)
 def test_unpermute_backward(cuda_lib, T, E, k, d, dropped, dtype):
     rt = routing(T, E, k, T + d, dropped)
     z, dy = randn(1, T * k, d, dtype=dtype), randn(3, T, d, dtype=dtype)
@@ -158,10 +164,11 @@ def test_gradients_against_differences(cuda_lib):
             assert abs(got - diff) <= 2.0 ** -19 * size
 
 
-@pytest.mark.parametrize("d", [64, 65])
-def test_a_routing_of_another_making_stays_inside(cuda_lib, d):
+@pytest.mark.parametrize("T,k,d", [(40, 3, 64), (40, 3, 65), (7000, 3, 128), (7000, 2, 130), (40000, 9, 256),
+                                   (36000, 7, 251)])
+def test_a_routing_of_another_making_stays_inside(cuda_lib, T, k, d):
     """Positions and offsets out of range move nothing outside the tensors."""
-    T, E, k = 40, 6, 3
+    E = 6
     g = gen(5)
     pos = torch.randint(-(1 << 30), 1 << 30, (T, k), generator=g, device=DEV).int()
     pos[::3] = torch.randint(0, T * k, pos[::3].shape, generator=g, device=DEV).int()
