@@ -2,7 +2,7 @@
 timing and profiling.
 
     python -m swiglu_mlp_projection_gb300 --M 16 --d 4096 --d_ff 14336 [--dtype bf16]
-        [--op up|down|moe] [--path auto|simt|skinny|tc] [--iters 20] [--warmup 3]
+        [--op up|down|moe|block|rows] [--path auto|simt|skinny|tc] [--iters 20] [--warmup 3]
         [--copies 1] [--fp8] [--experts 8] [--top_k 2]
 
 --op down times y = h . W_down + residual (bf16; h [M, d_ff], W_down
@@ -13,6 +13,12 @@ timing and profiling.
 --op moe times the mixture-of-experts MLP (bf16; M tokens through top_k of the
 experts, each of d, d_ff): router logits, routing, the experts' up and down
 projections and the residual, with the time of each step.
+
+--op block times the pre-norm MLP block (bf16, or --fp8) and each of its steps:
+the norm with the residual's addition, the up and the down projection.  --op
+rows times a training step's row operators on M tokens through top_k of the
+experts (bf16): the norm and its gradient, rows sorted by expert and back, and
+their gradients.
 
 Inputs are the seeded synthetic operands of swiglu_mlp_projection_gb300.inputs.
 Prints the median time per call and the achieved GB/s and TFLOP/s.
@@ -37,7 +43,7 @@ def main():
     ap.add_argument("--warmup", type=int, default=3)
     ap.add_argument("--copies", type=int, default=1, help="weight copies rotated per call")
     ap.add_argument("--fp8", action="store_true", help="e4m3 weights (swiglu_up_fp8)")
-    ap.add_argument("--op", default="up", choices=["up", "down", "moe"])
+    ap.add_argument("--op", default="up", choices=["up", "down", "moe", "block", "rows"])
     ap.add_argument("--experts", type=int, default=8)
     ap.add_argument("--top_k", type=int, default=2)
     a = ap.parse_args()
@@ -46,6 +52,10 @@ def main():
         return run_down(a, dev)
     if a.op == "moe":
         return run_moe(a, dev)
+    if a.op == "block":
+        return run_block(a, dev)
+    if a.op == "rows":
+        return run_rows(a, dev)
     x, wg, wu = inputs.make_inputs(a.M, a.d, a.d_ff, a.dtype, seed=0)
     x = x.to(dev)
     ws = [(wg.to(dev), wu.to(dev)) for _ in range(a.copies)]
@@ -102,14 +112,12 @@ def run_moe(a, dev):
     if a.dtype != "bf16" or a.fp8:
         raise SystemExit("the mixture of experts takes bf16")
     gen = torch.Generator(device=dev).manual_seed(0)
-
-    def normal(*shape, scale=1.0):
-        return (torch.randn(*shape, generator=gen, device=dev) * scale).to(torch.bfloat16)
     E, k = a.experts, a.top_k
-    x = normal(a.M, a.d)
-    wr = normal(a.d, E, scale=a.d ** -0.5)
-    ws = [(normal(E, a.d, a.d_ff, scale=a.d ** -0.5), normal(E, a.d, a.d_ff, scale=a.d ** -0.5),
-           normal(E, a.d_ff, a.d, scale=a.d_ff ** -0.5)) for _ in range(a.copies)]
+    x = normal(gen, a.M, a.d)
+    wr = normal(gen, a.d, E, scale=a.d ** -0.5)
+    ws = [(normal(gen, E, a.d, a.d_ff, scale=a.d ** -0.5),
+           normal(gen, E, a.d, a.d_ff, scale=a.d ** -0.5),
+           normal(gen, E, a.d_ff, a.d, scale=a.d_ff ** -0.5)) for _ in range(a.copies)]
     wg, wu, wd = ws[0]
     logits = swg.linear(x, wr, out_dtype=torch.float32)
     r = swg.route(logits, k)
@@ -130,6 +138,76 @@ def run_moe(a, dev):
                       "experts_reached": reached, "us": us,
                       "GB/s": round(by / us["all"] / 1e3, 1),
                       "TFLOP/s": round(fl / us["all"] / 1e6, 2)}))
+
+
+def normal(gen, *shape, scale=1.0):
+    import torch
+    return (torch.randn(*shape, generator=gen, device=gen.device) * scale).to(torch.bfloat16)
+
+
+def run_block(a, dev):
+    import torch
+    import swiglu_mlp_projection_gb300 as swg
+    if a.dtype != "bf16":
+        raise SystemExit("the MLP block takes bf16")
+    gen = torch.Generator(device=dev).manual_seed(0)
+    x, r = normal(gen, a.M, a.d), normal(gen, a.M, a.d)
+    nw = normal(gen, a.d, scale=0.1) + 1
+    sets = []
+    for _ in range(a.copies):
+        wg, wu = (normal(gen, a.d, a.d_ff, scale=a.d ** -0.5) for _ in range(2))
+        wd = normal(gen, a.d_ff, a.d, scale=a.d_ff ** -0.5)
+        sets.append((swg.quantize_weights_fp8(wg, wu), swg.quantize_weight_fp8(wd)) if a.fp8
+                    else ((wg, wu), wd))
+    if a.fp8:
+        norm, up = swg.rms_norm_fp8, swg.swiglu_up_fp8
+        down = swg.swiglu_down_fp8
+    else:
+        norm, down = swg.rms_norm, swg.swiglu_down
+        up = lambda n, w: swg.swiglu_up(n, *w)
+    n, s = norm(x, nw, residual=r)
+    h = up(n, sets[0][0])
+    steps = {
+        "norm": lambda i: norm(x, nw, residual=r),
+        "up": lambda i: up(n, sets[i % a.copies][0]),
+        "down": lambda i: down(h, sets[i % a.copies][1], residual=s),
+        "all": lambda i: swg.swiglu_block(x, nw, *sets[i % a.copies], residual=r),
+    }
+    us = {k: round(time_calls(f, a.warmup, a.iters) * 1e3, 2) for k, f in steps.items()}
+    swg.check_device_status()
+    by = 3 * a.d * a.d_ff * (1 if a.fp8 else 2) + 3 * 2 * a.M * a.d
+    fl = 6 * a.M * a.d * a.d_ff
+    print(json.dumps({"op": "block", "M": a.M, "d": a.d, "d_ff": a.d_ff,
+                      "dtype": "e4m3" if a.fp8 else "bf16", "us": us,
+                      "GB/s": round(by / us["all"] / 1e3, 1),
+                      "TFLOP/s": round(fl / us["all"] / 1e6, 2)}))
+
+
+def run_rows(a, dev):
+    import torch
+    import swiglu_mlp_projection_gb300 as swg
+    if a.dtype != "bf16" or a.fp8:
+        raise SystemExit("the row operators are timed in bf16")
+    gen = torch.Generator(device=dev).manual_seed(0)
+    x, r, dy = (normal(gen, a.M, a.d) for _ in range(3))
+    nw = normal(gen, a.d, scale=0.1) + 1
+    rt = swg.route(torch.randn(a.M, a.experts, generator=gen, device=dev), a.top_k)
+    z = normal(gen, a.M * a.top_k, a.d)
+    row = 2 * a.M * a.d            # bytes of the tokens' rows, and of the sorted ones
+    rows = row * a.top_k
+    steps = {
+        "norm": (lambda i: swg.rms_norm(x, nw, residual=r), 4 * row),
+        "norm_fp8": (lambda i: swg.rms_norm_fp8(x, nw, residual=r), 3 * row + row // 2),
+        "norm_backward": (lambda i: swg.rms_norm_backward(dy, x, nw, ds=r), 4 * row),
+        "permute": (lambda i: swg.permute(x, rt), row + rows),
+        "permute_backward": (lambda i: swg.permute_backward(z, rt), row + rows),
+        "unpermute": (lambda i: swg.unpermute(z, rt, residual=x), 2 * row + rows),
+        "unpermute_backward": (lambda i: swg.unpermute_backward(dy, z, rt), row + 2 * rows),
+    }
+    us = {k: round(time_calls(f, a.warmup, a.iters) * 1e3, 2) for k, (f, _) in steps.items()}
+    print(json.dumps({"op": "rows", "M": a.M, "d": a.d, "experts": a.experts, "top_k": a.top_k,
+                      "us": us, "GB/s": {k: round(b / us[k] / 1e3, 1)
+                                         for k, (_, b) in steps.items()}}))
 
 
 def time_calls(call, warmup, iters):
