@@ -173,16 +173,20 @@ norm_kernel(const __grid_constant__ NormArgs a) {
 constexpr int kPieces = 2;
 constexpr int team_threads(int w) { return 24 % w ? 32 * w : 768; }
 constexpr int team_rows(int w) { return team_threads(w) / 32 / w; }   // R
-constexpr int team_stages(int w) { return w == 32 ? 2 : w == 16 ? 4 : 3; }
+// Stages of the copies, of `arrays` tensors each.  More is not better: the
+// gradient of 8192 x 4096 takes 44.3 us with two and 47.0 with three, 8192 x 4096
+// f32 80.8 and 84.7; only the lightest stages gain from a third (16384 x 256 9.2
+// and 8.8; the norm of 5001 x 897 f32 7.8 and 7.5).
+constexpr int team_stages(int w, int arrays) { return w == 16 || w <= (arrays == 3 ? 1 : 4) ? 3 : 2; }
 
 // The sum of v[0 ... W - 1], one of which each lane holds (lane l that of l % W
 // where W is a power of two; otherwise l's, and 0 from W on), in every lane.
 template <int W>
 __device__ __forceinline__ float team_sum(float v) {
-  if constexpr ((W & (W - 1)) != 0) return warp_sum(v);
+  constexpr int top = (W & (W - 1)) != 0 ? 32 : W;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    if (o < W) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (o < top) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 template <int W>
@@ -193,8 +197,8 @@ __device__ __forceinline__ float2 team_value(const float2* v, int l) {
 
 template <bool F32, int W, bool RAGGED, int ARRAYS>
 struct Team {
-  static constexpr int V = Row<F32>::kVec, P = kPieces, T = team_threads(W), S = team_stages(W),
-                       R = team_rows(W);
+  static constexpr int V = Row<F32>::kVec, P = kPieces, T = team_threads(W),
+                       S = team_stages(W, ARRAYS), R = team_rows(W);
   int warp, l, team, lane;
   int64_t unit, units;   // rows unit, unit + units, ...
   int64_t M;
@@ -331,7 +335,7 @@ int team_grid(int64_t M, int num_sms) {
 }
 template <auto kernel, int W, int ARRAYS, typename A>
 cudaError_t launch_team(const A& a, int grid, cudaStream_t st) {
-  constexpr int smem = team_stages(W) * ARRAYS * kPieces * team_threads(W) * 16;
+  constexpr int smem = team_stages(W, ARRAYS) * ARRAYS * kPieces * team_threads(W) * 16;
   return launch_chained_smem<kernel>(smem, dim3(grid), dim3(team_threads(W)), smem, st, a);
 }
 
@@ -451,10 +455,9 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
       const int i = tm.piece(j);
       if (i >= tm.pc.n) continue;
       float2 t[H], g[H], o[H];
+      // (ragged: what is a neighbour's is not stored)
       unpack<F32>(*tm.slot(stage, 0, j), t);
       unpack<F32>(*tm.slot(stage, 1, j), g);
-      tm.pc.mask(i, t);
-      tm.pc.mask(i, g);
       if (a.ds) {
         unpack<F32>(*tm.slot(stage, 2, j), o);
       } else {
@@ -547,8 +550,6 @@ norm_backward_wide_kernel(const __grid_constant__ BackArgs a) {
       float2 t[H], g[H], w[H], o[H];
       unpack<F32>(pc.load(a.s, a.M, i), t);
       unpack<F32>(pc.load(a.dy, a.M, i), g);
-      pc.mask(i, t);
-      pc.mask(i, g);
       pc.weight(a.weight, a.weight_f32, i, w);
       if (a.ds) {
         unpack<F32>(pc.load(a.ds, a.M, i), o);

@@ -155,8 +155,7 @@ permute_kernel(const uint4* __restrict__ x, const float* __restrict__ scales,
 // bytes is read once, each thread taking its second half from its neighbour's
 // slot.
 
-constexpr int kWarps = 12;          // of unpermute's CTA, one CTA per SM
-constexpr int kPermuteWarps = 16;   // of permute's for ragged rows, two per SM
+constexpr int kPermuteWarps = 16;   // of permute's CTA for ragged rows, two per SM
 
 // Pieces m of 16 bytes from byte `at` of a tensor of `total` bytes into
 // slots[m], m < count <= N; zero where they are outside it.
@@ -364,7 +363,9 @@ unpermute_few_kernel(const void* __restrict__ z, const int* __restrict__ positio
 // which are copied S - 1 steps before the rows that they name.
 template <bool F32, bool RAGGED, int B, int U>
 struct UnpermuteSlots {
-  static constexpr int S = U == 1 && !RAGGED ? 4 : 3, C = 2 * S - 1;
+  static constexpr int kWarps = 16;   // of a CTA, one CTA per SM (12 with a stage more: 51.2 us
+                                      // for 4096 tokens, k = 8, d = 4096, where 16 take 49.6)
+  static constexpr int S = U == 1 && !RAGGED ? 3 : 2, C = 2 * S - 1;
   uint4 z[S][B][32 * U + (RAGGED ? 1 : 0)];
   uint4 residual[S][32 * U];
   int place[C][8];
@@ -373,7 +374,7 @@ struct UnpermuteSlots {
 
 // B choices of U pieces each to a step.
 template <bool F32, bool RAGGED, int B, int U>
-__global__ void __launch_bounds__(32 * kWarps, 1)
+__global__ void __launch_bounds__(32 * UnpermuteSlots<F32, RAGGED, B, U>::kWarps, 1)
 unpermute_kernel(const void* __restrict__ z, const int* __restrict__ position,
                  const float* __restrict__ weights, const void* residual, void* y, int64_t T, int k,
                  int bytes, int segs) {
@@ -530,7 +531,11 @@ __device__ __forceinline__ void backward_piece(const S& o, void* dz, int i, cons
 // are; dy, where it starts elsewhere in its 16 bytes, is shifted.
 template <bool RAGGED, int B, int U>
 struct BackwardSlots {
-  static constexpr int S = U == 1 ? 4 : 3, C = 2 * S - 1;
+  // Of a CTA, one CTA per SM.  With runs of 256 pieces there may also be too much
+  // under way: 8 / 10 / 12 / 14 warps take 88.5 / 86.5 / 95.8 / 98.6 us for 4096
+  // tokens, k = 8, d = 4096, and 44.6 / 42.6 / 43.0 / 44.6 for d = 2048.
+  static constexpr int kWarps = U == 8 ? 10 : 16;
+  static constexpr int S = U == 1 ? 3 : 2, C = 2 * S - 1;
   uint4 z[S][B][32 * U];
   uint4 dy[S][32 * U + (RAGGED ? 2 : 0)];   // ragged: one more on either side
   int place[C][8];
@@ -538,7 +543,7 @@ struct BackwardSlots {
 };
 
 template <bool F32, bool RAGGED, int B, int U>
-__global__ void __launch_bounds__(32 * kWarps, 1)
+__global__ void __launch_bounds__(32 * BackwardSlots<RAGGED, B, U>::kWarps, 1)
 unpermute_backward_kernel(const void* __restrict__ dy, const void* __restrict__ z,
                           const int* __restrict__ position, const int* __restrict__ offsets,
                           const float* __restrict__ weights, void* __restrict__ dz,
@@ -777,12 +782,13 @@ cudaError_t unpermute_few(const UnpermuteCall& c, int64_t bytes, cudaStream_t st
 
 template <bool F32, bool RAGGED, int B, int U>
 cudaError_t unpermute_batch(const UnpermuteCall& c, int64_t bytes, int num_sms, cudaStream_t st) {
-  constexpr int smem = kWarps * (int)sizeof(UnpermuteSlots<F32, RAGGED, B, U>);
+  using Slots = UnpermuteSlots<F32, RAGGED, B, U>;
+  constexpr int smem = Slots::kWarps * (int)sizeof(Slots);
   static_assert(smem <= 232448, "shared memory");
   const int64_t segs = (pieces_of(bytes) + 32 * U - 1) / (32 * U);
   return launch_chained_smem<unpermute_kernel<F32, RAGGED, B, U>>(
-      smem, dim3(stream_grid(c.T * segs, num_sms)), dim3(32 * kWarps), smem, st, c.z, c.position,
-      c.weights, c.residual, c.y, c.T, (int)c.k, (int)bytes, (int)segs);
+      smem, dim3(stream_grid(c.T * segs, num_sms)), dim3(32 * Slots::kWarps), smem, st, c.z,
+      c.position, c.weights, c.residual, c.y, c.T, (int)c.k, (int)bytes, (int)segs);
 }
 
 template <bool F32, bool RAGGED>
@@ -798,12 +804,13 @@ cudaError_t unpermute_rows(const UnpermuteCall& c, int64_t bytes, int num_sms, c
 template <bool F32, bool RAGGED, int B, int U>
 cudaError_t backward_batch(const UnpermuteBackwardCall& c, int64_t bytes, int num_sms,
                            cudaStream_t st) {
-  constexpr int smem = kWarps * (int)sizeof(BackwardSlots<RAGGED, B, U>);
+  using Slots = BackwardSlots<RAGGED, B, U>;
+  constexpr int smem = Slots::kWarps * (int)sizeof(Slots);
   static_assert(smem <= 232448, "shared memory");
   const int64_t segs = (pieces_of(bytes) + 32 * U - 1) / (32 * U);
   return launch_chained_smem<unpermute_backward_kernel<F32, RAGGED, B, U>>(
-      smem, dim3(stream_grid(c.T * ((c.k + B - 1) / B), num_sms)), dim3(32 * kWarps), smem, st, c.dy,
-      c.z, c.position, c.offsets, c.weights, c.dz, c.dweights, c.T, (int)c.k, (int)c.E, (int)bytes,
+      smem, dim3(stream_grid(c.T * ((c.k + B - 1) / B), num_sms)), dim3(32 * Slots::kWarps), smem, st,
+      c.dy, c.z, c.position, c.offsets, c.weights, c.dz, c.dweights, c.T, (int)c.k, (int)c.E, (int)bytes,
       (int)segs);
 }
 
@@ -819,6 +826,13 @@ cudaError_t backward_rows(const UnpermuteBackwardCall& c, int64_t bytes, int num
                           c.position, c.offsets, c.weights, c.dz, c.dweights, c.T, (int)c.k,
                           (int)c.E, (int)bytes);
   }
+  // Long rows: the longer a run of a row that a step moves, the better, also at
+  // the price of reading dy once for each choice (from L2; 4096 tokens, k = 8, d =
+  // 2048: 51.9 us in runs of 32 pieces, 46.7 of 64, 44.6 of 128, 42.7 of 256).
+  // Ragged ones, which are bound by instructions, are better off with two choices
+  // (d = 2047: 80 us with one, 60 with two).
+  if constexpr (!RAGGED)
+    if (per >= 256) return backward_batch<F32, RAGGED, 1, 8>(c, bytes, num_sms, st);
   if (per >= 128 || c.k <= 2) return backward_batch<F32, RAGGED, 2, 4>(c, bytes, num_sms, st);
   if (per >= 64 || c.k <= 4) return backward_batch<F32, RAGGED, 4, 2>(c, bytes, num_sms, st);
   return backward_batch<F32, RAGGED, 8, 1>(c, bytes, num_sms, st);
