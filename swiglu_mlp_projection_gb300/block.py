@@ -124,6 +124,8 @@ def swiglu_block(x, norm_weight, up, down, residual=None, eps=1e-6, layout="kn",
     Fp8Weights and down an Fp8Matrix: the norm then writes the e4m3 rows that
     the up projection reads.  Returns y [M, d].
     """
+    if x.dtype is not _torch().bfloat16:
+        raise TypeError("x must be bfloat16, got %s" % x.dtype)
     fp8 = isinstance(up, Fp8Weights)
     n = (rms_norm_fp8 if fp8 else rms_norm)(x, norm_weight, residual=residual, eps=eps,
                                             stream=stream)

@@ -238,10 +238,8 @@ __device__ __forceinline__ void copy_piece(uint4* dst, const void* src, int byte
                "r"(bytes)
                : "memory");
 }
-// 4 bytes, or (if not `some`) zero.
-__device__ __forceinline__ void copy_word(void* dst, const void* src, bool some) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(dst)), "l"(src),
-               "r"(some ? 4 : 0)
+__device__ __forceinline__ void copy_word(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src)
                : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -251,7 +249,9 @@ __device__ __forceinline__ void copies_wait() {
 }
 
 // A launch that may begin while the previous kernel of the stream ends (the
-// kernel waits in pdl_wait before it touches memory).
+// kernel waits in pdl_wait before it touches memory; it is running while that one
+// still writes, so it reads nothing through the non-coherent path: no __ldg, no
+// const __restrict__).
 template <typename... Params, typename... Args>
 inline cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
                                   cudaStream_t st, Args... args) {
