@@ -11,7 +11,7 @@ autograd does not see them: a gradient is a call of its own.
 from . import _lib
 from . import Fp8Rows, Fp8Weights, _call, _empty, _raw_stream, _torch
 from . import swiglu_down, swiglu_down_fp8, swiglu_up, swiglu_up_fp8
-from .moe import _bytes, _check, _first, _out, _row_code, _workspace
+from .moe import _check, _first, _out, _row_code, _workspace
 
 
 def _rows(torch, x, weight, x_name):
@@ -111,8 +111,11 @@ def rms_norm_backward(dy, s, weight, ds=None, eps=1e-6, out=None, workspace=None
 
 def rms_norm_backward_workspace_bytes(M, d, dtype="bf16"):
     """Workspace bytes ``rms_norm_backward`` needs on the current device."""
-    return _bytes(_lib.load().swiglu_rms_norm_backward_workspace_bytes(
+    n = int(_lib.load().swiglu_rms_norm_backward_workspace_bytes(
         M, d, _lib.BF16 if dtype in ("bf16", _lib.BF16) else _lib.F32))
+    if n == 0 and M != 0 and d != 0:   # a call with rows needs some
+        _lib.check(1)
+    return n
 
 
 def swiglu_block(x, norm_weight, up, down, residual=None, eps=1e-6, layout="kn", stream=None):

@@ -7,8 +7,9 @@ the rounding of s, so mean(s^2) + eps is off by at most 46 u, the root of it by
 the root and s itself add 3 u more: y is off by less than 32 u = 2^-19 of
 itself, and by half a step of its type (2^-8 in bf16).  e4m3 codes: half a step,
 2^-4 of the value or 2^-10 below the normal range, and 2^-18 for the two f32
-values whose quotient it rounds.  Gradient: r^3 is off by 78 u, mean(g s) by
-46 u of mean |g s|, products by 8 u: less than 2^-16 of the terms' sizes.
+values whose quotient it rounds.  Gradient: r is off by 28 u (4 of them
+its approximation), r^3 by 84 u, mean(g s) by
+48 u of mean |g s|, products by 8 u: less than 2^-16 of the terms' sizes.
 dweight adds each row's term (32 u) over the rows of a CTA (at most M / 64, or
 64), 32 groups and 32 lanes.
 """
@@ -198,6 +199,9 @@ def test_nothing_to_do(cuda_lib):
         assert rows.codes.shape == (M, d) and not bool(rows.scales.any())
         dx, dw = swg.rms_norm_backward(x, x, w)
         assert dx.shape == (M, d) and dw.shape == (d,) and not bool(dw.any())
+        assert swg.rms_norm_backward_workspace_bytes(M, d) == 0
+    with pytest.raises(swg.SwiGLUError):
+        swg.rms_norm_backward_workspace_bytes(4, -1)
 
 
 def test_refusals(cuda_lib):
