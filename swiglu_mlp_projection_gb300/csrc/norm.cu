@@ -249,7 +249,23 @@ struct Team {
     else if (R == 1) __syncthreads();
     else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
   }
-  __device__ __forceinline__ static int after(int stage) { return stage + 1 == S ? 0 : stage + 1; }
+  // step(row, stage) for each row of the team, its pieces at hand and the next rows
+  // on their way.  (unrolled, so that the slots' addresses are constants)
+  template <typename Step>
+  __device__ __forceinline__ void rows(const void* p0, const void* p1, const void* p2,
+                                       Step step) const {
+    int64_t row = unit;
+    while (true) {
+#pragma unroll
+      for (int stage = 0; stage < S; ++stage) {
+        if (row >= M) return;
+        fetch(row + (S - 1) * units, (stage + S - 1) % S, p0, p1, p2);
+        copies_wait<S - 1>();
+        step(row, stage);
+        row += units;
+      }
+    }
+  }
 };
 
 template <bool F32, int W, bool FP8>
@@ -258,7 +274,7 @@ norm_stream_kernel(const __grid_constant__ NormArgs a) {
   using Tm = Team<F32, W, true, 2>;
   constexpr int P = Tm::P, H = Tm::V / 2, S = Tm::S;
   extern __shared__ uint4 ring[];
-  __shared__ float2 red[2][32];
+  __shared__ float2 red[S][32];
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   const Tm tm(ring, a.M, a.d);
@@ -268,10 +284,7 @@ norm_stream_kernel(const __grid_constant__ NormArgs a) {
 #pragma unroll
   for (int j = 0; j < P; ++j)
     if (tm.piece(j) < tm.pc.n) tm.pc.weight(a.weight, a.weight_f32, tm.piece(j), w[j]);
-  int side = 0, stage = 0, next = S - 1;
-  for (int64_t row = tm.unit; row < a.M; row += tm.units) {
-    tm.fetch(row + (S - 1) * tm.units, next, a.x, a.residual, nullptr);
-    copies_wait<S - 1>();
+  tm.rows(a.x, a.residual, nullptr, [&](int64_t row, int stage) {
     float2 t[P][H], q2 = make_float2(0.f, 0.f);
     float m = 0.f;
 #pragma unroll
@@ -284,10 +297,10 @@ norm_stream_kernel(const __grid_constant__ NormArgs a) {
     }
     float q = warp_sum(q2.x + q2.y);
     if (FP8) m = warp_max(m);
-    if (W > 1) {   // (one barrier a row: the next row writes the other side)
-      if (tm.l == 0) red[side][tm.warp] = make_float2(q, m);
+    if (W > 1) {   // (one barrier a row: the next row writes another place)
+      if (tm.l == 0) red[stage][tm.warp] = make_float2(q, m);
       tm.sync();
-      const float2 v = team_value<W>(red[side] + tm.team * W, tm.l);
+      const float2 v = team_value<W>(red[stage] + tm.team * W, tm.l);
       q = team_sum<W>(v.x);
       if (FP8) m = warp_max(v.y);
     }
@@ -298,10 +311,7 @@ norm_stream_kernel(const __grid_constant__ NormArgs a) {
       if (i < tm.pc.n) put_piece<F32, FP8, true>(tm.pc, a.out, tm.first(row), i, t[j], rf.f);
     }
     if (FP8 && tm.lane == 0) a.scales[row] = rf.scale;
-    side ^= 1;
-    stage = tm.after(stage);
-    next = tm.after(next);
-  }
+  });
 }
 
 // How a row's pieces are dealt out.
@@ -414,8 +424,9 @@ __global__ void __launch_bounds__(team_threads(W), 1)
 norm_backward_kernel(const __grid_constant__ BackArgs a) {
   using Tm = Team<F32, W, RAGGED, 3>;
   constexpr int P = Tm::P, H = Tm::V / 2, S = Tm::S, R = Tm::R;
+  constexpr bool kHold = F32 || Tm::T <= 512;   // a row's values stay unpacked for both uses
   extern __shared__ uint4 ring[];
-  __shared__ float2 red[2][32];
+  __shared__ float2 red[S][32];
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   const Tm tm(ring, a.M, a.d);
@@ -429,31 +440,28 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
     for (int h = 0; h < H; ++h) acc[j][h] = make_float2(0.f, 0.f);
   }
   const float inv_d = 1.0f / (float)a.d;
-  int side = 0, stage = 0, next = S - 1;
-  for (int64_t row = tm.unit; row < a.M; row += tm.units) {
-    tm.fetch(row + (S - 1) * tm.units, next, a.s, a.dy, a.ds);
-    copies_wait<S - 1>();
+  tm.rows(a.s, a.dy, a.ds, [&](int64_t row, int stage) {
     float2 q2 = make_float2(0.f, 0.f), p2 = q2;
+    float2 s[P][H], g[P][H];   // (unpacked twice where registers are short)
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       const int i = tm.piece(j);
       if (i >= tm.pc.n) continue;
-      float2 s[H], g[H];
-      unpack<F32>(*tm.slot(stage, 0, j), s);
-      unpack<F32>(*tm.slot(stage, 1, j), g);
-      tm.pc.mask(i, s);
-      tm.pc.mask(i, g);
+      unpack<F32>(*tm.slot(stage, 0, j), s[j]);
+      unpack<F32>(*tm.slot(stage, 1, j), g[j]);
+      tm.pc.mask(i, s[j]);
+      tm.pc.mask(i, g[j]);
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        q2 = fma2(s[h], s[h], q2);
-        p2 = fma2(mul2(g[h], w[j][h]), s[h], p2);
+        q2 = fma2(s[j][h], s[j][h], q2);
+        p2 = fma2(mul2(g[j][h], w[j][h]), s[j][h], p2);
       }
     }
     float q = warp_sum(q2.x + q2.y), p = warp_sum(p2.x + p2.y);
-    if (W > 1) {   // (one barrier a row: the next row writes the other side)
-      if (tm.l == 0) red[side][tm.warp] = make_float2(q, p);
+    if (W > 1) {   // (one barrier a row: the next row writes another place)
+      if (tm.l == 0) red[stage][tm.warp] = make_float2(q, p);
       tm.sync();
-      const float2 v = team_value<W>(red[side] + tm.team * W, tm.l);
+      const float2 v = team_value<W>(red[stage] + tm.team * W, tm.l);
       q = team_sum<W>(v.x);
       p = team_sum<W>(v.y);
     }
@@ -465,10 +473,11 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
     for (int j = 0; j < P; ++j) {
       const int i = tm.piece(j);
       if (i >= tm.pc.n) continue;
-      float2 t[H], g[H], o[H];
-      // (ragged: what is a neighbour's is not stored)
-      unpack<F32>(*tm.slot(stage, 0, j), t);
-      unpack<F32>(*tm.slot(stage, 1, j), g);
+      float2 o[H];
+      if (!kHold) {   // (ragged: what is a neighbour's is not stored)
+        unpack<F32>(*tm.slot(stage, 0, j), s[j]);
+        unpack<F32>(*tm.slot(stage, 1, j), g[j]);
+      }
       if (a.ds) {
         unpack<F32>(*tm.slot(stage, 2, j), o);
       } else {
@@ -477,16 +486,13 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
       }
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        t[h] = mul2(t[h], r2);
-        acc[j][h] = fma2(g[h], t[h], acc[j][h]);
-        o[h] = fma2(c2, t[h], fma2(r2, mul2(g[h], w[j][h]), o[h]));
+        const float2 t = mul2(s[j][h], r2);
+        acc[j][h] = fma2(g[j][h], t, acc[j][h]);
+        o[h] = fma2(c2, t, fma2(r2, mul2(g[j][h], w[j][h]), o[h]));
       }
       tm.pc.store_at(a.dx, tm.first(row), i, o);
     }
-    side ^= 1;
-    stage = tm.after(stage);
-    next = tm.after(next);
-  }
+  });
   // The CTA's sums, team after team.
   copies_wait<0>();
   __syncthreads();
