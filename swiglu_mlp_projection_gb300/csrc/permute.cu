@@ -254,10 +254,9 @@ struct PermuteSlots {
 
 template <typename E>
 __global__ void __launch_bounds__(32 * kPermuteWarps, 2)
-permute_ragged_kernel(const void* x, const float* scales,
-                      const int* position, const int* offsets,
-                      void* out, float* out_scales, int64_t T, int k,
-                      int n_exp, int bytes, int segs) {
+permute_ragged_kernel(const void* x, const float* scales, const int* position,
+                      const int* offsets, void* out, float* out_scales, int64_t T, int k, int n_exp,
+                      int bytes, int segs) {
   constexpr int S = PermuteSlots::S, C = PermuteSlots::C, U = PermuteSlots::U;
   extern __shared__ uint4 smem[];
   tc::pdl_launch_dependents();
@@ -265,7 +264,7 @@ permute_ragged_kernel(const void* x, const float* scales,
   const int l = threadIdx.x & 31;
   PermuteSlots& slots = reinterpret_cast<PermuteSlots*>(smem)[threadIdx.x >> 5];
   const int64_t rows = T * k, end = sorted_end(offsets, n_exp, rows);
-  Steps ask(segs, 1), in(segs, 1), out_s(segs, 1);   // a: segments, all choices in one step
+  Steps ask(segs, 1), in = ask, out_s = ask;   // a: segments, all choices in one step
   int ask_c = 0, out_c = 0;
   const auto choices = [&]() {
     if (l < k && ask.t < T) copy_word(&slots.place[ask_c][l], position + ask.t * k + l);
@@ -332,9 +331,8 @@ permute_ragged_kernel(const void* x, const float* scales,
 // Few pieces (see kFewPieces): each has a thread of its own.
 template <bool F32, bool RAGGED>
 __global__ void __launch_bounds__(256)
-unpermute_few_kernel(const void* z, const int* position,
-                     const float* weights, const void* residual, void* y, int64_t T,
-                     int k, int bytes) {
+unpermute_few_kernel(const void* z, const int* position, const float* weights,
+                     const void* residual, void* y, int64_t T, int k, int bytes) {
   using E = typename Row<F32>::elem;
   constexpr int H = Row<F32>::kVec / 2, B = 8;
   tc::pdl_launch_dependents();
@@ -386,9 +384,8 @@ struct UnpermuteSlots {
 // B choices of U pieces each to a step.
 template <bool F32, bool RAGGED, int B, int U>
 __global__ void __launch_bounds__(32 * UnpermuteSlots<F32, RAGGED, B, U>::kWarps, 1)
-unpermute_kernel(const void* z, const int* position,
-                 const float* weights, const void* residual, void* y, int64_t T, int k,
-                 int bytes, int segs) {
+unpermute_kernel(const void* z, const int* position, const float* weights, const void* residual,
+                 void* y, int64_t T, int k, int bytes, int segs) {
   using E = typename Row<F32>::elem;
   using Slots = UnpermuteSlots<F32, RAGGED, B, U>;
   constexpr int H = Row<F32>::kVec / 2, S = Slots::S, C = Slots::C;
@@ -508,8 +505,8 @@ __device__ __forceinline__ float warp_sums8(float (&v)[8], int lane) {
   return s;
 }
 
-// dz and the sums of the dot product, of one piece: dz's row o has it at piece i,
-// m is dy there and zq z.
+// One piece of dz and of the dot product: piece i of row o of dz and z, where dyq
+// and zq are dy's and z's values.
 template <bool F32, bool RAGGED, typename S>
 __device__ __forceinline__ void backward_piece(const S& o, void* dz, int i, const uint4& dyq,
                                                const uint4& zq, float w, float2& dot) {
@@ -555,11 +552,9 @@ struct BackwardSlots {
 
 template <bool F32, bool RAGGED, int B, int U>
 __global__ void __launch_bounds__(32 * BackwardSlots<RAGGED, B, U>::kWarps, 1)
-unpermute_backward_kernel(const void* dy, const void* z,
-                          const int* position, const int* offsets,
-                          const float* weights, void* dz,
-                          float* dweights, int64_t T, int k, int n_exp, int bytes,
-                          int segs) {
+unpermute_backward_kernel(const void* dy, const void* z, const int* position, const int* offsets,
+                          const float* weights, void* dz, float* dweights, int64_t T, int k,
+                          int n_exp, int bytes, int segs) {
   using E = typename Row<F32>::elem;
   using Slots = BackwardSlots<RAGGED, B, U>;
   constexpr int S = Slots::S, C = Slots::C;
@@ -668,11 +663,9 @@ unpermute_backward_kernel(const void* dy, const void* z,
 // Few pieces (see kFewPieces): blockDim.x threads to a token.
 template <bool F32, bool RAGGED>
 __global__ void __launch_bounds__(256)
-unpermute_backward_few_kernel(const void* dy, const void* z,
-                              const int* position, const int* offsets,
-                              const float* weights, void* dz,
-                              float* dweights, int64_t T, int k, int n_exp,
-                              int bytes) {
+unpermute_backward_few_kernel(const void* dy, const void* z, const int* position,
+                              const int* offsets, const float* weights, void* dz, float* dweights,
+                              int64_t T, int k, int n_exp, int bytes) {
   using E = typename Row<F32>::elem;
   constexpr int B = 8;
   __shared__ float red[8][8];   // by warp of the CTA

@@ -191,6 +191,21 @@ def test_backward_against_differences(cuda_lib, M, d):
             + 2.0 ** -16 * dy.to(D).abs().sum()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,d", [(3, 4096), (200, 896), (200, 1001), (5, 20000)])
+@pytest.mark.parametrize("scale,eps", [(2.0 ** 45, 1e-6), (2.0 ** -50, 1e-30), (2.0 ** -20, 1.0), (1.0, 1e30)])
+def test_sizes_of_values(cuda_lib, M, d, dtype, scale, eps):
+    x, dy, w = inputs(M, d, dtype, F32, 90)
+    x, r = x * scale, randn(93, M, d, dtype=dtype) * scale
+    y, s = swg.rms_norm(x, w, residual=r, eps=eps)
+    check_norm(y, s, x, r, w, eps)
+    if scale > 2.0 ** -40 and eps < 1e10:   # (elsewhere t, or the scale, leaves the normal range)
+        rows, s2 = swg.rms_norm_fp8(x, w, residual=r, eps=eps)
+        check_fp8(rows, x, r, w, eps)
+        assert torch.equal(s, s2)
+    check_backward(*swg.rms_norm_backward(dy, s, w, eps=eps), dy, s, w, None, eps)
+
+
 def test_nothing_to_do(cuda_lib):
     for M, d in ((0, 64), (4, 0), (0, 0)):
         x, w = torch.empty(M, d, device=DEV, dtype=BF), torch.ones(d, device=DEV, dtype=BF)
