@@ -111,7 +111,7 @@ __device__ __forceinline__ RowFactors row_factors(float q, float m, const NormAr
   return {some ? 448.0f / m : 0.f, (some ? m : 0.f) * r / 448.0f};
 }
 
-// One row per warp (WARP) or per CTA; VPT 16-byte pieces per thread.
+// One row per warp (WARP) or per CTA; VPT pieces per thread.
 template <bool F32, int VPT, bool FP8, bool RAGGED, bool WARP>
 __global__ void __launch_bounds__(WARP ? 256 : 1024)
 norm_kernel(const __grid_constant__ NormArgs a) {
@@ -176,7 +176,8 @@ norm_kernel(const __grid_constant__ NormArgs a) {
 // such rows start).  One CTA per SM holds R teams of W warps; a team takes row
 // after row, two pieces to a thread, and copies the next rows (cp.async) into
 // slots that only the copying thread reads, while one is reduced.  Rows go to
-// the CTAs first, then to their teams.
+// the CTAs first, then to their teams.  The gradient's widest rows are shared by
+// the CTAs of a cluster, whose warps hand their sums to all of them.
 
 constexpr int kPieces = 2;
 constexpr int team_threads(int w) { return 24 % w ? 32 * w : 768; }
@@ -185,42 +186,36 @@ constexpr int team_rows(int w) { return team_threads(w) / 32 / w; }   // R
 // gradient of 8192 x 4096 takes 44.3 us with two and 47.0 with three, 8192 x 4096
 // f32 80.8 and 84.7; only the lightest stages gain from a third (16384 x 256 9.2
 // and 8.8; the norm of 5001 x 897 f32 7.8 and 7.5).
-constexpr int team_stages(int w, int arrays) { return w == 16 || w <= (arrays == 3 ? 1 : 4) ? 3 : 2; }
-
-// The sum of v[0 ... W - 1], one of which each lane holds (lane l that of l % W
-// where W is a power of two; otherwise l's, and 0 from W on), in every lane.
-template <int W>
-__device__ __forceinline__ float team_sum(float v) {
-  constexpr int top = (W & (W - 1)) != 0 ? 32 : W;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    if (o < top) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-template <int W>
-__device__ __forceinline__ float2 team_value(const float2* v, int l) {
-  if (W & (W - 1)) return l < W ? v[l] : make_float2(0.f, 0.f);
-  return v[l & (W - 1)];
+constexpr int team_stages(int w, int arrays, int cluster) {
+  if (cluster > 1) return w == 16 ? 4 : 3;
+  return w == 16 || w <= (arrays == 3 ? 1 : 4) ? 3 : 2;
 }
 
-template <bool F32, int W, bool RAGGED, int ARRAYS>
+enum Second { kNone, kSum, kMax };   // what becomes of the second value of join
+
+// ARRAYS tensors are copied; C CTAs share a row (C > 1: one team to a CTA).
+template <bool F32, int W, bool RAGGED, int ARRAYS, int C>
 struct Team {
   static constexpr int V = Row<F32>::kVec, P = kPieces, T = team_threads(W),
-                       S = team_stages(W, ARRAYS), R = team_rows(W);
-  int warp, l, team, lane;
+                       S = team_stages(W, ARRAYS, C), R = team_rows(W);
+  static_assert(C == 1 || R == 1, "a cluster's CTAs meet once a row");
+  using Shared = float2[S][C > 1 ? C * W : 32];   // the warps' values
+  int warp, l, team, rank, lane;
   int64_t unit, units;   // rows unit, unit + units, ...
   int64_t M;
   uint4* slots;
   // (ragged: all rows of a team start at one place of their 16 bytes, since
-  // `units` is a multiple of 8 or every team has one row at most)
+  // `units` is a multiple of row_period or every team has one row at most)
   Pieces<F32, RAGGED> pc;
 
   __device__ __forceinline__ Team(uint4* ring, int64_t M_, int d)
       : warp(threadIdx.x >> 5), l(threadIdx.x & 31), team(warp / W),
-        lane(threadIdx.x - team * W * 32), unit(blockIdx.x + (int64_t)team * gridDim.x),
-        units((int64_t)gridDim.x * R), M(M_), slots(ring + threadIdx.x),
-        pc(unit, d) {}
-  __device__ __forceinline__ int piece(int j) const { return lane + j * W * 32; }
+        rank(C > 1 ? blockIdx.x % C : 0), lane(threadIdx.x - team * W * 32),
+        unit(blockIdx.x / C + (int64_t)team * (gridDim.x / C)),
+        units((int64_t)(gridDim.x / C) * R), M(M_), slots(ring + threadIdx.x), pc(unit, d) {
+    if (C > 1) tc::cluster_sync_all();   // the others run: their shared memory is there
+  }
+  __device__ __forceinline__ int piece(int j) const { return rank * (P * W * 32) + lane + j * W * 32; }
   __device__ __forceinline__ uint4* slot(int stage, int array, int j) const {
     return slots + stage * (ARRAYS * P * T) + (array * P + j) * T;
   }
@@ -229,7 +224,7 @@ struct Team {
   __device__ __forceinline__ void fetch(int64_t row, int stage, const void* p0, const void* p1,
                                         const void* p2) const {
     if (row < M) {
-      const int64_t at = (first(row) + (int64_t)lane * V) * (16 / V);   // in bytes
+      const int64_t at = (first(row) + (int64_t)piece(0) * V) * (16 / V);   // in bytes
       const int64_t left = M * pc.d * (16 / V) - at;
 #pragma unroll
       for (int j = 0; j < P; ++j) {
@@ -243,25 +238,94 @@ struct Team {
     }
     copies_commit();
   }
-  // All warps of the team.
-  __device__ __forceinline__ void sync() const {
-    if (W == 1) __syncwarp();
-    else if (R == 1) __syncthreads();
-    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
+  // The first rows' copies.
+  __device__ __forceinline__ void begin(const void* p0, const void* p1, const void* p2) const {
+#pragma unroll
+    for (int i = 0; i < (C > 1 ? S : S - 1); ++i) fetch(unit + i * units, i, p0, p1, p2);
   }
-  // step(row, stage) for each row of the team, its pieces at hand and the next rows
-  // on their way.  (unrolled, so that the slots' addresses are constants)
-  template <typename Step>
-  __device__ __forceinline__ void rows(const void* p0, const void* p1, const void* p2,
-                                       Step step) const {
+  // Values of the threads added up (the second: see Second) over the row's threads,
+  // in a fixed order: a warp's ...
+  template <Second SECOND>
+  __device__ __forceinline__ static float2 of_warp(float2 v) {
+    v.x = warp_sum(v.x);
+    if (SECOND != kNone) v.y = SECOND == kMax ? warp_max(v.y) : warp_sum(v.y);
+    return v;
+  }
+  // ... and the row's (one barrier a row: the next row writes another stage's place).
+  template <Second SECOND>
+  __device__ __forceinline__ float2 join(Shared& red, int stage, float2 v) const {
+    if (W == 1) return v;
+    if (l == 0) red[stage][warp] = v;
+    if (R == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
+    if (W & (W - 1)) return of_warp<SECOND>(l < W ? red[stage][team * W + l] : make_float2(0.f, 0.f));
+    // (a power of two takes log2 W steps: 5001 x 897 f32 7.5 us, with five 7.7)
+    v = red[stage][team * W + l % W];
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) {
+      v.x += __shfl_xor_sync(~0u, v.x, o);
+      if (SECOND == kNone) continue;
+      const float u = __shfl_xor_sync(~0u, v.y, o);
+      v.y = SECOND == kMax ? fmaxf(v.y, u) : v.y + u;
+    }
+    return v;
+  }
+  // The same among a cluster's CTAs, in two halves.
+  __device__ __forceinline__ void send(Shared& red, int stage, float2 v) const {
+    if (l < C) {
+      const uint32_t to = tc::mapa_shared(tc::smem_u32(&red[stage][rank * W + warp]), l);
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(v.x), "f"(v.y)
+                   : "memory");
+    }
+    __syncwarp();   // (the barrier wants the warp together)
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
+  template <Second SECOND>
+  __device__ __forceinline__ float2 receive(const Shared& red, int stage) const {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < C * W; i += 32) {
+      const float2 u = i + l < C * W ? red[stage][i + l] : make_float2(0.f, 0.f);
+      v.x += u.x;
+      v.y = SECOND == kMax ? fmaxf(v.y, u.y) : v.y + u.y;
+    }
+    return of_warp<SECOND>(v);
+  }
+  // For each row of the team: first(row, stage) gives a thread's values, and
+  // second(row, stage, v) gets the row's.  The next rows are on their way.  A
+  // cluster's barrier takes longer than a CTA's, so there the first half of the
+  // next row stands between its two ends, and the second half of the row before.
+  // (unrolled, so that the slots' addresses are constants)
+  template <Second SECOND, typename First, typename Last>
+  __device__ __forceinline__ void rows(const void* p0, const void* p1, const void* p2, Shared& red,
+                                       First first_half, Last second_half) const {
     int64_t row = unit;
+    if constexpr (C > 1) {
+      copies_wait<S - 1>();
+      send(red, 0, of_warp<SECOND>(first_half(row, 0)));
+    }
     while (true) {
 #pragma unroll
       for (int stage = 0; stage < S; ++stage) {
         if (row >= M) return;
-        fetch(row + (S - 1) * units, (stage + S - 1) % S, p0, p1, p2);
-        copies_wait<S - 1>();
-        step(row, stage);
+        if constexpr (C > 1) {
+          const bool more = row + units < M;
+          float2 mine = make_float2(0.f, 0.f);
+          if (more) {
+            copies_wait<S - 2>();
+            mine = of_warp<SECOND>(first_half(row + units, (stage + 1) % S));
+          }
+          const float2 v = receive<SECOND>(red, stage);
+          if (more) send(red, (stage + 1) % S, mine);
+          second_half(row, stage, v);
+          fetch(row + S * units, stage, p0, p1, p2);
+        } else {
+          fetch(row + (S - 1) * units, (stage + S - 1) % S, p0, p1, p2);
+          copies_wait<S - 1>();
+          second_half(row, stage,
+                      join<SECOND>(red, stage, of_warp<SECOND>(first_half(row, stage))));
+        }
         row += units;
       }
     }
@@ -271,47 +335,42 @@ struct Team {
 template <bool F32, int W, bool FP8>
 __global__ void __launch_bounds__(team_threads(W), 1)
 norm_stream_kernel(const __grid_constant__ NormArgs a) {
-  using Tm = Team<F32, W, true, 2>;
-  constexpr int P = Tm::P, H = Tm::V / 2, S = Tm::S;
+  using Tm = Team<F32, W, true, 2, 1>;
+  constexpr int P = Tm::P, H = Tm::V / 2;
   extern __shared__ uint4 ring[];
-  __shared__ float2 red[S][32];
+  __shared__ typename Tm::Shared red;
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   const Tm tm(ring, a.M, a.d);
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) tm.fetch(tm.unit + i * tm.units, i, a.x, a.residual, nullptr);
-  float2 w[P][H];
+  tm.begin(a.x, a.residual, nullptr);
+  float2 w[P][H], t[P][H];
 #pragma unroll
   for (int j = 0; j < P; ++j)
     if (tm.piece(j) < tm.pc.n) tm.pc.weight(a.weight, a.weight_f32, tm.piece(j), w[j]);
-  tm.rows(a.x, a.residual, nullptr, [&](int64_t row, int stage) {
-    float2 t[P][H], q2 = make_float2(0.f, 0.f);
+  const auto add = [&](int64_t row, int stage) {
+    float2 q = make_float2(0.f, 0.f);
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       const int i = tm.piece(j);
       if (i >= tm.pc.n) continue;
       add_piece<F32, true>(tm.pc, a, tm.first(row), i, *tm.slot(stage, 0, j),
-                           a.residual ? *tm.slot(stage, 1, j) : uint4{}, t[j], q2);
+                           a.residual ? *tm.slot(stage, 1, j) : uint4{}, t[j], q);
       weigh<FP8>(t[j], w[j], m);
     }
-    float q = warp_sum(q2.x + q2.y);
-    if (FP8) m = warp_max(m);
-    if (W > 1) {   // (one barrier a row: the next row writes another place)
-      if (tm.l == 0) red[stage][tm.warp] = make_float2(q, m);
-      tm.sync();
-      const float2 v = team_value<W>(red[stage] + tm.team * W, tm.l);
-      q = team_sum<W>(v.x);
-      if (FP8) m = warp_max(v.y);
-    }
-    const RowFactors rf = row_factors<FP8>(q, m, a);
+    return make_float2(q.x + q.y, m);
+  };
+  const auto put = [&](int64_t row, int stage, float2 v) {
+    const RowFactors rf = row_factors<FP8>(v.x, v.y, a);
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       const int i = tm.piece(j);
-      if (i < tm.pc.n) put_piece<F32, FP8, true>(tm.pc, a.out, tm.first(row), i, t[j], rf.f);
+      if (i >= tm.pc.n) continue;
+      put_piece<F32, FP8, true>(tm.pc, a.out, tm.first(row), i, t[j], rf.f);
     }
     if (FP8 && tm.lane == 0) a.scales[row] = rf.scale;
-  });
+  };
+  tm.template rows<FP8 ? kMax : kNone>(a.x, a.residual, nullptr, red, add, put);
 }
 
 // How a row's pieces are dealt out.
@@ -338,32 +397,50 @@ Shape shape_of(int64_t pieces, int vec, int64_t M, int num_sms) {
 
 int64_t pieces_of(int64_t d, int vec) { return d % vec ? d / vec + 2 : d / vec; }
 
-// Warps per row of the streaming kernels, or 0 for rows too wide for them.
-int team_warps(int64_t d, int vec) {
-  for (int w : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32})
-    if (32 * kPieces * w >= pieces_of(d, vec)) return w;
-  return 0;
+// How a streaming kernel is launched: `warps` of each CTA to a row, the CTAs of a
+// cluster to the widest rows (of more than 2048 pieces), `units` CTAs or clusters.
+struct TeamShape {
+  int warps, cluster, units;
+};
+constexpr int64_t kOneCtaPieces = 32 * kPieces * 32;
+TeamShape team_shape(int64_t M, int64_t d, int vec, int num_sms) {
+  const int64_t pieces = pieces_of(d, vec);
+  TeamShape s{0, 1, 0};
+  for (int w : {32, 24, 16, 12, 8, 6, 4, 3, 2, 1})
+    if (32 * kPieces * w >= pieces) s.warps = w;
+  // (Two CTAs of 16 warps for 2048 pieces lose to one of 32: 2048 x 16384 58.8 us
+  // against 56.1.  Above, one CTA that reads rows twice and keeps dweight's sums in
+  // shared memory took 109 us for 2048 x 12288 f32, 146 for 2048 x 16384 f32 and 99
+  // for 1024 x 32768 bf16, where the clusters take 68, 97 and 63.)
+  if (!s.warps) {
+    constexpr int kOf24 = 24 * 32 * kPieces;   // what a CTA of 24 warps holds
+    s.cluster = pieces <= 2 * kOf24 ? 2 : pieces <= 4 * kOf24 ? 4 : 8;
+    s.warps = pieces <= 1024 * s.cluster ? 16 : 24;
+  }
+  // (clusters of 4 and 8 must fit whole parts of the GPU: 36 and 15 do)
+  int64_t most = num_sms / s.cluster;
+  if (s.cluster == 4) most = most * 95 / 100;
+  if (s.cluster == 8) most = most * 80 / 100;
+  // Rows so many apart start at one place of their 16 bytes: see Team::pc.
+  int period = vec;
+  for (int64_t low = d; period > 1 && low % 2 == 0; low /= 2) period /= 2;
+  most = most < period ? period : most / period * period;
+  s.units = (int)(M < most ? M : most);
+  return s;
 }
 
-// A streaming kernel's launch: M rows (at least 1) over at most one CTA per SM
-// (152 or another multiple of 8, see Team::pc).
-int team_grid(int64_t M, int num_sms) {
-  const int64_t most = num_sms / 8 * 8;
-  return (int)(M < most ? M : most);
-}
-template <auto kernel, int W, int ARRAYS, typename A>
-cudaError_t launch_team(const A& a, int grid, cudaStream_t st) {
-  constexpr int smem = team_stages(W, ARRAYS) * ARRAYS * kPieces * team_threads(W) * 16;
-  return launch_chained_smem<kernel>(smem, dim3(grid), dim3(team_threads(W)), smem, st, a);
+template <auto kernel, int W, int ARRAYS, int C, typename A>
+cudaError_t launch_team(const A& a, int units, cudaStream_t st) {
+  constexpr int smem = team_stages(W, ARRAYS, C) * ARRAYS * kPieces * team_threads(W) * 16;
+  return launch_chained_smem<kernel, C>(smem, dim3(units * C), dim3(team_threads(W)), smem, st, a);
 }
 
-template <bool F32, int VPT, bool FP8, bool RAGGED>
+template <bool F32, int VPT, bool FP8>
 cudaError_t launch_norm(const NormArgs& a, const Shape& s, cudaStream_t st) {
-  if constexpr (!RAGGED)
-    if (s.warp)
-      return launch_chained(norm_kernel<F32, VPT, FP8, RAGGED, true>,
-                            dim3((unsigned)((a.M + 7) / 8)), dim3(256), 0, st, a);
-  return launch_chained(norm_kernel<F32, VPT, FP8, RAGGED, false>, dim3((unsigned)a.M),
+  if (s.warp)
+    return launch_chained(norm_kernel<F32, VPT, FP8, false, true>, dim3((unsigned)((a.M + 7) / 8)),
+                          dim3(256), 0, st, a);
+  return launch_chained(norm_kernel<F32, VPT, FP8, false, false>, dim3((unsigned)a.M),
                         dim3(s.threads), 0, st, a);
 }
 
@@ -372,26 +449,28 @@ cudaError_t launch_rows(const NormArgs& a, int num_sms, cudaStream_t st) {
   constexpr int V = Row<F32>::kVec, base = 8 / V;   // pieces of 8 elements
   if (a.d % V == 0) {
     const Shape s = shape_of(a.d / V, V, a.M, num_sms);
-    if (s.vpt == base) return launch_norm<F32, base, FP8, false>(a, s, st);
-    if (s.vpt == 2 * base) return launch_norm<F32, 2 * base, FP8, false>(a, s, st);
-    return launch_norm<F32, 4 * base, FP8, false>(a, s, st);
+    if (s.vpt == base) return launch_norm<F32, base, FP8>(a, s, st);
+    if (s.vpt == 2 * base) return launch_norm<F32, 2 * base, FP8>(a, s, st);
+    return launch_norm<F32, 4 * base, FP8>(a, s, st);
   }
-  const int grid = team_grid(a.M, num_sms);
-  switch (team_warps(a.d, V)) {
-    case 1: return launch_team<norm_stream_kernel<F32, 1, FP8>, 1, 2>(a, grid, st);
-    case 2: return launch_team<norm_stream_kernel<F32, 2, FP8>, 2, 2>(a, grid, st);
-    case 3: return launch_team<norm_stream_kernel<F32, 3, FP8>, 3, 2>(a, grid, st);
-    case 4: return launch_team<norm_stream_kernel<F32, 4, FP8>, 4, 2>(a, grid, st);
-    case 6: return launch_team<norm_stream_kernel<F32, 6, FP8>, 6, 2>(a, grid, st);
-    case 8: return launch_team<norm_stream_kernel<F32, 8, FP8>, 8, 2>(a, grid, st);
-    case 12: return launch_team<norm_stream_kernel<F32, 12, FP8>, 12, 2>(a, grid, st);
-    case 16: return launch_team<norm_stream_kernel<F32, 16, FP8>, 16, 2>(a, grid, st);
-    case 24: return launch_team<norm_stream_kernel<F32, 24, FP8>, 24, 2>(a, grid, st);
-    case 32: return launch_team<norm_stream_kernel<F32, 32, FP8>, 32, 2>(a, grid, st);
+  const int64_t pieces = pieces_of(a.d, V);
+  if (pieces > kOneCtaPieces)   // too wide for a team: as the others, with partial pieces
+    return launch_chained(norm_kernel<F32, 4 * base, FP8, true, false>, dim3((unsigned)a.M),
+                          dim3((unsigned)((pieces + 128 * base - 1) / (128 * base) * 32)), 0, st, a);
+  const TeamShape s = team_shape(a.M, a.d, V, num_sms);
+  switch (s.warps) {
+    case 1: return launch_team<norm_stream_kernel<F32, 1, FP8>, 1, 2, 1>(a, s.units, st);
+    case 2: return launch_team<norm_stream_kernel<F32, 2, FP8>, 2, 2, 1>(a, s.units, st);
+    case 3: return launch_team<norm_stream_kernel<F32, 3, FP8>, 3, 2, 1>(a, s.units, st);
+    case 4: return launch_team<norm_stream_kernel<F32, 4, FP8>, 4, 2, 1>(a, s.units, st);
+    case 6: return launch_team<norm_stream_kernel<F32, 6, FP8>, 6, 2, 1>(a, s.units, st);
+    case 8: return launch_team<norm_stream_kernel<F32, 8, FP8>, 8, 2, 1>(a, s.units, st);
+    case 12: return launch_team<norm_stream_kernel<F32, 12, FP8>, 12, 2, 1>(a, s.units, st);
+    case 16: return launch_team<norm_stream_kernel<F32, 16, FP8>, 16, 2, 1>(a, s.units, st);
+    case 24: return launch_team<norm_stream_kernel<F32, 24, FP8>, 24, 2, 1>(a, s.units, st);
+    case 32: return launch_team<norm_stream_kernel<F32, 32, FP8>, 32, 2, 1>(a, s.units, st);
   }
-  const int vpt = 4 * base;
-  const Shape wide{vpt, (int)((pieces_of(a.d, V) + vpt * 32 - 1) / (vpt * 32) * 32), false};
-  return launch_norm<F32, 4 * base, FP8, true>(a, wide, st);
+  return cudaErrorInvalidValue;   // (team_shape gives none other)
 }
 
 // ---- gradient -------------------------------------------------------------------
@@ -412,27 +491,27 @@ struct BackArgs {
   const void* weight;
   const void* ds;
   void* dx;
-  float* part;   // [gridDim.x, d]
+  float* part;   // [teams' CTAs or clusters, d]
   int64_t M;
   int d;
   float eps;
   int weight_f32;
 };
 
-template <bool F32, int W, bool RAGGED>
+template <bool F32, int W, bool RAGGED, int C>
 __global__ void __launch_bounds__(team_threads(W), 1)
 norm_backward_kernel(const __grid_constant__ BackArgs a) {
-  using Tm = Team<F32, W, RAGGED, 3>;
-  constexpr int P = Tm::P, H = Tm::V / 2, S = Tm::S, R = Tm::R;
-  constexpr bool kHold = F32 || Tm::T <= 512;   // a row's values stay unpacked for both uses
+  using Tm = Team<F32, W, RAGGED, 3, C>;
+  constexpr int P = Tm::P, H = Tm::V / 2, R = Tm::R;
+  // whether a row's values stay unpacked for both halves
+  constexpr bool kHold = C == 1 && (F32 || Tm::T <= 512);
   extern __shared__ uint4 ring[];
-  __shared__ float2 red[S][32];
+  __shared__ typename Tm::Shared red;
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   const Tm tm(ring, a.M, a.d);
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) tm.fetch(tm.unit + i * tm.units, i, a.s, a.dy, a.ds);
-  float2 w[P][H], acc[P][H];
+  tm.begin(a.s, a.dy, a.ds);
+  float2 w[P][H], acc[P][H], s[P][H], g[P][H];
 #pragma unroll
   for (int j = 0; j < P; ++j) {
     if (tm.piece(j) < tm.pc.n) tm.pc.weight(a.weight, a.weight_f32, tm.piece(j), w[j]);
@@ -440,9 +519,8 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
     for (int h = 0; h < H; ++h) acc[j][h] = make_float2(0.f, 0.f);
   }
   const float inv_d = 1.0f / (float)a.d;
-  tm.rows(a.s, a.dy, a.ds, [&](int64_t row, int stage) {
-    float2 q2 = make_float2(0.f, 0.f), p2 = q2;
-    float2 s[P][H], g[P][H];   // (unpacked twice where registers are short)
+  const auto sums_of = [&](int64_t, int stage) {   // s^2, g s
+    float2 q = make_float2(0.f, 0.f), p = q;
 #pragma unroll
     for (int j = 0; j < P; ++j) {
       const int i = tm.piece(j);
@@ -453,21 +531,16 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
       tm.pc.mask(i, g[j]);
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        q2 = fma2(s[j][h], s[j][h], q2);
-        p2 = fma2(mul2(g[j][h], w[j][h]), s[j][h], p2);
+        q = fma2(s[j][h], s[j][h], q);
+        p = fma2(mul2(g[j][h], w[j][h]), s[j][h], p);
       }
     }
-    float q = warp_sum(q2.x + q2.y), p = warp_sum(p2.x + p2.y);
-    if (W > 1) {   // (one barrier a row: the next row writes another place)
-      if (tm.l == 0) red[stage][tm.warp] = make_float2(q, p);
-      tm.sync();
-      const float2 v = team_value<W>(red[stage] + tm.team * W, tm.l);
-      q = team_sum<W>(v.x);
-      p = team_sum<W>(v.y);
-    }
-    // t = s r:  dx = ds + r g - t r^2 mean(g s),  dweight += dy t
-    const float r = rsqrtf(fmaf(q, inv_d, a.eps));
-    const float c = -r * r * (p * inv_d);
+    return make_float2(q.x + q.y, p.x + p.y);
+  };
+  // t = s r:  dx = ds + r g - t r^2 mean(g s),  dweight += dy t
+  const auto put = [&](int64_t row, int stage, float2 v) {
+    const float r = rsqrtf(fmaf(v.x, inv_d, a.eps));
+    const float c = -r * r * (v.y * inv_d);
     const float2 r2 = make_float2(r, r), c2 = make_float2(c, c);
 #pragma unroll
     for (int j = 0; j < P; ++j) {
@@ -492,11 +565,12 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
       }
       tm.pc.store_at(a.dx, tm.first(row), i, o);
     }
-  });
+  };
+  tm.template rows<kSum>(a.s, a.dy, a.ds, red, sums_of, put);
   // The CTA's sums, team after team.
   copies_wait<0>();
   __syncthreads();
-  float* part = a.part + (int64_t)blockIdx.x * a.d;
+  float* part = a.part + (int64_t)(blockIdx.x / C) * a.d;
   float* all = reinterpret_cast<float*>(ring);
   float* sums = R > 1 ? all + tm.team * a.d : part;
 #pragma unroll
@@ -518,79 +592,6 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
       part[c] = v;
     }
   }
-}
-
-// Rows wider than 32 warps' two pieces: a CTA per row reads it twice (the
-// second time from L2) and keeps its sums of dweight in shared memory.
-template <bool F32, bool RAGGED>
-__global__ void __launch_bounds__(1024)
-norm_backward_wide_kernel(const __grid_constant__ BackArgs a) {
-  constexpr int H = Row<F32>::kVec / 2;
-  extern __shared__ float2 sums[];   // [H][pieces]
-  __shared__ float2 red[2][32];
-  tc::pdl_launch_dependents();
-  tc::pdl_wait();
-  const int warp = threadIdx.x >> 5, l = threadIdx.x & 31;
-  const Pieces<F32, RAGGED> p0(blockIdx.x, a.d);   // (the rows' shift: see Team::pc)
-  for (int i = threadIdx.x; i < p0.n; i += 1024)
-#pragma unroll
-    for (int h = 0; h < H; ++h) sums[h * p0.n + i] = make_float2(0.f, 0.f);
-  const float inv_d = 1.0f / (float)a.d;
-  int side = 0;
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, side ^= 1) {
-    const Pieces<F32, RAGGED> pc(row, a.d);
-    float2 q2 = make_float2(0.f, 0.f), p2 = q2;
-#pragma unroll 2
-    for (int i = threadIdx.x; i < pc.n; i += 1024) {
-      float2 s[H], g[H], w[H];
-      unpack<F32>(pc.load(a.s, a.M, i), s);
-      unpack<F32>(pc.load(a.dy, a.M, i), g);
-      pc.mask(i, s);
-      pc.mask(i, g);
-      pc.weight(a.weight, a.weight_f32, i, w);
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        q2 = fma2(s[h], s[h], q2);
-        p2 = fma2(mul2(g[h], w[h]), s[h], p2);
-      }
-    }
-    float q = warp_sum(q2.x + q2.y), p = warp_sum(p2.x + p2.y);
-    if (l == 0) red[side][warp] = make_float2(q, p);
-    __syncthreads();
-    q = warp_sum(red[side][l].x);
-    p = warp_sum(red[side][l].y);
-    const float r = rsqrtf(fmaf(q, inv_d, a.eps));
-    const float c = -r * r * (p * inv_d);
-    const float2 r2 = make_float2(r, r), c2 = make_float2(c, c);
-#pragma unroll 2
-    for (int i = threadIdx.x; i < pc.n; i += 1024) {
-      float2 t[H], g[H], w[H], o[H];
-      unpack<F32>(pc.load(a.s, a.M, i), t);
-      unpack<F32>(pc.load(a.dy, a.M, i), g);
-      pc.weight(a.weight, a.weight_f32, i, w);
-      if (a.ds) {
-        unpack<F32>(pc.load(a.ds, a.M, i), o);
-      } else {
-#pragma unroll
-        for (int h = 0; h < H; ++h) o[h] = make_float2(0.f, 0.f);
-      }
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        t[h] = mul2(t[h], r2);
-        sums[h * pc.n + i] = fma2(g[h], t[h], sums[h * pc.n + i]);
-        o[h] = fma2(c2, t[h], fma2(r2, mul2(g[h], w[h]), o[h]));
-      }
-      pc.store(a.dx, i, o);
-    }
-  }
-  float* part = a.part + (int64_t)blockIdx.x * a.d;
-  for (int i = threadIdx.x; i < p0.n; i += 1024)
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const float2 v = sums[h * p0.n + i];
-      if (p0.has(i, 2 * h)) part[p0.col(i) + 2 * h] = v.x;
-      if (p0.has(i, 2 * h + 1)) part[p0.col(i) + 2 * h + 1] = v.y;
-    }
 }
 
 constexpr int kSumCols = 32, kSumRows = 32;
@@ -619,24 +620,26 @@ dweight_kernel(const float* part, int n, int d, void* out, int f32) {
 }
 
 template <bool F32, bool RAGGED>
-cudaError_t launch_back(const BackArgs& a, int grid, cudaStream_t st) {
+cudaError_t launch_back(const BackArgs& a, const TeamShape& s, cudaStream_t st) {
   // (the teams' sums take the place of their stages: R rows of at most 512 W
   // elements, 2 KB, and each stage has as much)
-  switch (team_warps(a.d, Row<F32>::kVec)) {
-    case 1: return launch_team<norm_backward_kernel<F32, 1, RAGGED>, 1, 3>(a, grid, st);
-    case 2: return launch_team<norm_backward_kernel<F32, 2, RAGGED>, 2, 3>(a, grid, st);
-    case 3: return launch_team<norm_backward_kernel<F32, 3, RAGGED>, 3, 3>(a, grid, st);
-    case 4: return launch_team<norm_backward_kernel<F32, 4, RAGGED>, 4, 3>(a, grid, st);
-    case 6: return launch_team<norm_backward_kernel<F32, 6, RAGGED>, 6, 3>(a, grid, st);
-    case 8: return launch_team<norm_backward_kernel<F32, 8, RAGGED>, 8, 3>(a, grid, st);
-    case 12: return launch_team<norm_backward_kernel<F32, 12, RAGGED>, 12, 3>(a, grid, st);
-    case 16: return launch_team<norm_backward_kernel<F32, 16, RAGGED>, 16, 3>(a, grid, st);
-    case 24: return launch_team<norm_backward_kernel<F32, 24, RAGGED>, 24, 3>(a, grid, st);
-    case 32: return launch_team<norm_backward_kernel<F32, 32, RAGGED>, 32, 3>(a, grid, st);
+  switch (s.cluster > 1 ? 100 * s.cluster + s.warps : s.warps) {
+    case 1: return launch_team<norm_backward_kernel<F32, 1, RAGGED, 1>, 1, 3, 1>(a, s.units, st);
+    case 2: return launch_team<norm_backward_kernel<F32, 2, RAGGED, 1>, 2, 3, 1>(a, s.units, st);
+    case 3: return launch_team<norm_backward_kernel<F32, 3, RAGGED, 1>, 3, 3, 1>(a, s.units, st);
+    case 4: return launch_team<norm_backward_kernel<F32, 4, RAGGED, 1>, 4, 3, 1>(a, s.units, st);
+    case 6: return launch_team<norm_backward_kernel<F32, 6, RAGGED, 1>, 6, 3, 1>(a, s.units, st);
+    case 8: return launch_team<norm_backward_kernel<F32, 8, RAGGED, 1>, 8, 3, 1>(a, s.units, st);
+    case 12: return launch_team<norm_backward_kernel<F32, 12, RAGGED, 1>, 12, 3, 1>(a, s.units, st);
+    case 16: return launch_team<norm_backward_kernel<F32, 16, RAGGED, 1>, 16, 3, 1>(a, s.units, st);
+    case 24: return launch_team<norm_backward_kernel<F32, 24, RAGGED, 1>, 24, 3, 1>(a, s.units, st);
+    case 32: return launch_team<norm_backward_kernel<F32, 32, RAGGED, 1>, 32, 3, 1>(a, s.units, st);
+    case 224: return launch_team<norm_backward_kernel<F32, 24, RAGGED, 2>, 24, 3, 2>(a, s.units, st);
+    case 416: return launch_team<norm_backward_kernel<F32, 16, RAGGED, 4>, 16, 3, 4>(a, s.units, st);
+    case 424: return launch_team<norm_backward_kernel<F32, 24, RAGGED, 4>, 24, 3, 4>(a, s.units, st);
+    case 816: return launch_team<norm_backward_kernel<F32, 16, RAGGED, 8>, 16, 3, 8>(a, s.units, st);
   }
-  return launch_chained_smem<norm_backward_wide_kernel<F32, RAGGED>>(
-      (kMaxNormWidth + 16) * (int)sizeof(float), dim3(grid), dim3(1024),
-      (a.d + 16) * sizeof(float), st, a);
+  return cudaErrorInvalidValue;   // (team_shape gives none other)
 }
 
 }  // namespace
@@ -652,25 +655,24 @@ cudaError_t launch_rms_norm(const NormCall& c, int num_sms, cudaStream_t st) {
                   : launch_rows<false, false>(a, num_sms, st);
 }
 
-size_t rms_norm_backward_bytes(int64_t M, int64_t d, int num_sms) {
-  return (size_t)team_grid(M, num_sms) * (size_t)d * sizeof(float);
+size_t rms_norm_backward_bytes(int64_t M, int64_t d, int f32, int num_sms) {
+  return (size_t)team_shape(M, d, f32 ? 4 : 8, num_sms).units * (size_t)d * sizeof(float);
 }
 
 cudaError_t launch_rms_norm_backward(const NormBackwardCall& c, float* part, int num_sms,
                                      cudaStream_t st) {
   if (c.d == 0) return cudaSuccess;
-  const int grid = team_grid(c.M, num_sms);
+  const TeamShape s = team_shape(c.M, c.d, c.f32 ? 4 : 8, num_sms);
   if (c.M > 0) {
     const BackArgs a{c.dy, c.s, c.weight, c.ds, c.dx, part, c.M, (int)c.d, c.eps, c.weight_f32};
     const bool ragged = c.d % (c.f32 ? 4 : 8) != 0;
     const cudaError_t e =
-        c.f32 ? (ragged ? launch_back<true, true>(a, grid, st) : launch_back<true, false>(a, grid, st))
-              : (ragged ? launch_back<false, true>(a, grid, st)
-                        : launch_back<false, false>(a, grid, st));
+        c.f32 ? (ragged ? launch_back<true, true>(a, s, st) : launch_back<true, false>(a, s, st))
+              : (ragged ? launch_back<false, true>(a, s, st) : launch_back<false, false>(a, s, st));
     if (e != cudaSuccess) return e;
   }
   return launch_chained(dweight_kernel, dim3((unsigned)((c.d + kSumCols - 1) / kSumCols)),
-                        dim3(kSumCols * kSumRows), 0, st, (const float*)part, grid, (int)c.d,
+                        dim3(kSumCols * kSumRows), 0, st, (const float*)part, s.units, (int)c.d,
                         c.dweight, c.weight_f32);
 }
 

@@ -252,25 +252,35 @@ __device__ __forceinline__ void copies_wait() {
 // kernel waits in pdl_wait before it touches memory; it is running while that one
 // still writes, so it reads nothing through the non-coherent path: no __ldg, no
 // const __restrict__).
+// `cluster` CTAs in a row are a cluster.
 template <typename... Params, typename... Args>
-inline cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
-                                  cudaStream_t st, Args... args) {
-  cudaLaunchAttribute attr[1];
+inline cudaError_t launch_clustered(int cluster, void (*kernel)(Params...), dim3 grid, dim3 block,
+                                    size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+template <typename... Params, typename... Args>
+inline cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                                  cudaStream_t st, Args... args) {
+  return launch_clustered(1, kernel, grid, block, smem, st, args...);
 }
 
 // The same for a kernel that needs up to `most` bytes of shared memory, which is
 // asked for once on each device.
-template <auto kernel, typename... Args>
+template <auto kernel, int CLUSTER = 1, typename... Args>
 inline cudaError_t launch_chained_smem(int most, dim3 grid, dim3 block, size_t smem,
                                        cudaStream_t st, Args... args) {
   static std::atomic<int> configured[64];   // zero: not yet set on that device
@@ -282,7 +292,7 @@ inline cudaError_t launch_chained_smem(int most, dim3 grid, dim3 block, size_t s
     if (e != cudaSuccess) return e;
     if (dev < 64) configured[dev].store(1, std::memory_order_release);
   }
-  return launch_chained(kernel, grid, block, smem, st, args...);
+  return launch_clustered(CLUSTER, kernel, grid, block, smem, st, args...);
 }
 
 }  // namespace swg

@@ -36,8 +36,8 @@ struct NormBackwardCall {
   float eps;
   int f32, weight_f32;
 };
-// The partial sums of dweight: one row of d f32 values per CTA.
-size_t rms_norm_backward_bytes(int64_t M, int64_t d, int num_sms);
+// The partial sums of dweight: one row of d f32 values per CTA or cluster.
+size_t rms_norm_backward_bytes(int64_t M, int64_t d, int f32, int num_sms);
 cudaError_t launch_rms_norm_backward(const NormBackwardCall& c, float* part, int num_sms,
                                      cudaStream_t st);
 

@@ -119,7 +119,7 @@ size_t swiglu_rms_norm_backward_workspace_bytes(int64_t M, int64_t d, int dtype)
   int dev, num_sms;
   if (api_current_device(&dev, &num_sms) != SWIGLU_OK) return 0;
   api_clear_error();
-  return round256(rms_norm_backward_bytes(M, d, num_sms));
+  return round256(rms_norm_backward_bytes(M, d, dtype == SWIGLU_F32, num_sms));
 }
 
 int swiglu_rms_norm_backward(const void* dy, const void* s, const void* weight, const void* ds,
@@ -149,7 +149,7 @@ int swiglu_rms_norm_backward(const void* dy, const void* s, const void* weight, 
   const std::unique_lock<std::mutex> lock =
       workspace ? std::unique_lock<std::mutex>() : api_lock_enqueue(dev, st);
   Workspace ws;
-  const size_t body = round256(rms_norm_backward_bytes(M, d, num_sms));
+  const size_t body = round256(rms_norm_backward_bytes(M, d, dtype == SWIGLU_F32, num_sms));
   if (body && (v = api_take_workspace(dev, st, workspace, workspace_bytes, 0, body, &ws)) != SWIGLU_OK)
     return v;
   cudaError_t e = launch_rms_norm_backward(

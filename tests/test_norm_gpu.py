@@ -68,7 +68,9 @@ SIZES = [(1, 1), (1, 8), (1, 4096), (1, 4099), (1, 32768), (1, 32752), (1, 32751
          (154, 16391), (155, 32768), (156, 32737), (1000, 509),
          # each number of warps that may share a row, and several rows for each of them
          (170, 1400), (333, 1801), (160, 2048), (157, 3301), (155, 5000), (159, 7001), (154, 9001), (153, 10000),
-         (170, 13001), (15001, 40), (15001, 43), (8000, 601), (2100, 4099), (2100, 4096)]
+         (170, 13001), (15001, 40), (15001, 43), (8000, 601), (2100, 4099), (2100, 4096),
+         # rows that several CTAs share
+         (200, 20000), (160, 20003), (240, 12000), (230, 9003), (90, 24571)]
 
 
 @pytest.mark.parametrize("dtype,wdtype", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
