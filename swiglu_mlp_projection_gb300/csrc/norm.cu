@@ -14,7 +14,7 @@
 // which fit on an SM to keep its loads under way: 8192 x 8192 bf16 with a residual
 // to e4m3 70.5 us in a graph (6670 GB/s, where a copy reaches 6780), 16384 x 2048
 // 41.3 us, 8192 x 8192 f32 158 us; one row of 4096 takes 1.7 us, the launch.  Other
-// widths stream through teams of warps (below): 8192 x 4099 45.5 us, 5001 x 897 f32
+// widths stream through teams of warps (below): 8192 x 4099 44.9 us, 5001 x 897 f32
 // 7.5 us (as the first kind, with partial pieces moved one by one, 58 and 9.3 us).
 #include "rows.cuh"
 #include "rows.h"
@@ -55,7 +55,7 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // A piece of the row on its way: s (stored where there is a residual) and its squares ...
-template <bool F32, bool RAGGED>
+template <bool F32, bool RAGGED, bool MASK>
 __device__ __forceinline__ void add_piece(const Pieces<F32, RAGGED>& pc, const NormArgs& a,
                                           int64_t first, int i, const uint4& xq, const uint4& rq,
                                           float2 (&t)[Row<F32>::kVec / 2], float2& q) {
@@ -67,7 +67,7 @@ __device__ __forceinline__ void add_piece(const Pieces<F32, RAGGED>& pc, const N
 #pragma unroll
     for (int h = 0; h < H; ++h) t[h] = add2(t[h], r[h]);
   }
-  pc.mask(i, t);
+  if (MASK) pc.mask(i, t);
   if (a.residual) pc.store_at(a.sum, first, i, t);
 #pragma unroll
   for (int h = 0; h < H; ++h) q = fma2(t[h], t[h], q);
@@ -142,7 +142,7 @@ norm_kernel(const __grid_constant__ NormArgs a) {
   for (int j = 0; j < VPT; ++j) {
     const int i = lane + j * lanes;
     if (i >= pc.n) continue;
-    add_piece<F32, RAGGED>(pc, a, pc.first, i, xr[j], rr[j], t[j], q2);
+    add_piece<F32, RAGGED, true>(pc, a, pc.first, i, xr[j], rr[j], t[j], q2);
     float2 w[H];
     pc.weight(a.weight, a.weight_f32, i, w);
     weigh<FP8>(t[j], w, m);
@@ -218,6 +218,29 @@ struct Team {
   __device__ __forceinline__ int piece(int j) const { return rank * (P * W * 32) + lane + j * W * 32; }
   __device__ __forceinline__ uint4* slot(int stage, int array, int j) const {
     return slots + stage * (ARRAYS * P * T) + (array * P + j) * T;
+  }
+  // The row's first and last piece: ones where it has elements.  The threads that
+  // have them keep them, because the others wait for those every row.  (Not for
+  // f32, whose four elements are masked as fast: 8192 x 4095 90 us, so 92; nor with
+  // 32 warps, whose 64 registers it overruns: 2048 x 16001 58.5 us, so 65.6.)
+  static constexpr bool kEdges = RAGGED && !F32 && W < 32;
+  using Edges = uint4[kEdges ? R : 1][2];
+  __device__ __forceinline__ void find_edges(Edges& edges) const {
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const int i = piece(j);
+      if (kEdges && (i == 0 || i == pc.n - 1)) edges[team][i != 0] = pc.ones(i);
+    }
+  }
+  // A piece of a row, with kEdges 0 where it is a neighbour's.
+  __device__ __forceinline__ uint4 read(int stage, int array, int j, const Edges& edges) const {
+    uint4 q = *slot(stage, array, j);
+    const int i = piece(j);
+    if (kEdges && !pc.whole(i)) {
+      const uint4 m = edges[team][i != 0];
+      q = make_uint4(q.x & m.x, q.y & m.y, q.z & m.z, q.w & m.w);
+    }
+    return q;
   }
   __device__ __forceinline__ int64_t first(int64_t row) const { return row * pc.d - pc.shift; }
   // This thread's pieces of `row`, a group of copies (an empty one past the last row).
@@ -339,10 +362,12 @@ norm_stream_kernel(const __grid_constant__ NormArgs a) {
   constexpr int P = Tm::P, H = Tm::V / 2;
   extern __shared__ uint4 ring[];
   __shared__ typename Tm::Shared red;
+  __shared__ typename Tm::Edges edges;
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   const Tm tm(ring, a.M, a.d);
   tm.begin(a.x, a.residual, nullptr);
+  tm.find_edges(edges);
   float2 w[P][H], t[P][H];
 #pragma unroll
   for (int j = 0; j < P; ++j)
@@ -354,8 +379,8 @@ norm_stream_kernel(const __grid_constant__ NormArgs a) {
     for (int j = 0; j < P; ++j) {
       const int i = tm.piece(j);
       if (i >= tm.pc.n) continue;
-      add_piece<F32, true>(tm.pc, a, tm.first(row), i, *tm.slot(stage, 0, j),
-                           a.residual ? *tm.slot(stage, 1, j) : uint4{}, t[j], q);
+      add_piece<F32, true, !Tm::kEdges>(tm.pc, a, tm.first(row), i, tm.read(stage, 0, j, edges),
+                                  a.residual ? tm.read(stage, 1, j, edges) : uint4{}, t[j], q);
       weigh<FP8>(t[j], w[j], m);
     }
     return make_float2(q.x + q.y, m);
@@ -507,10 +532,12 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
   constexpr bool kHold = C == 1 && (F32 || Tm::T <= 512);
   extern __shared__ uint4 ring[];
   __shared__ typename Tm::Shared red;
+  __shared__ typename Tm::Edges edges;
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   const Tm tm(ring, a.M, a.d);
   tm.begin(a.s, a.dy, a.ds);
+  tm.find_edges(edges);
   float2 w[P][H], acc[P][H], s[P][H], g[P][H];
 #pragma unroll
   for (int j = 0; j < P; ++j) {
@@ -525,10 +552,12 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
     for (int j = 0; j < P; ++j) {
       const int i = tm.piece(j);
       if (i >= tm.pc.n) continue;
-      unpack<F32>(*tm.slot(stage, 0, j), s[j]);
-      unpack<F32>(*tm.slot(stage, 1, j), g[j]);
-      tm.pc.mask(i, s[j]);
-      tm.pc.mask(i, g[j]);
+      unpack<F32>(tm.read(stage, 0, j, edges), s[j]);
+      unpack<F32>(tm.read(stage, 1, j, edges), g[j]);
+      if (!Tm::kEdges) {
+        tm.pc.mask(i, s[j]);
+        tm.pc.mask(i, g[j]);
+      }
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         q = fma2(s[j][h], s[j][h], q);

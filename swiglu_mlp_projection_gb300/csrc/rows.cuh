@@ -147,6 +147,14 @@ struct Pieces {
   __device__ __forceinline__ bool has(int i, int e) const {
     return !RAGGED || (col(i) + e >= 0 && col(i) + e < d);
   }
+  // Piece i of bf16 with all bits set where it has the row's elements.
+  __device__ __forceinline__ uint4 ones(int i) const {
+    uint32_t m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      m[k] = (has(i, 2 * k) ? 0xffffu : 0u) | (has(i, 2 * k + 1) ? 0xffff0000u : 0u);
+    return make_uint4(m[0], m[1], m[2], m[3]);
+  }
   // Elements that are not the row's become 0.
   __device__ __forceinline__ void mask(int i, float2 (&v)[V / 2]) const {
     if (!whole(i)) {
@@ -174,11 +182,38 @@ struct Pieces {
     if (whole(i)) {
       *reinterpret_cast<uint4*>(q) = pack<F32>(v);
     } else {
+      if constexpr (F32) {
 #pragma unroll
-      for (int h = 0; h < V / 2; ++h) {
-        if (has(i, 2 * h)) set_elem(q + 2 * h, v[h].x);
-        if (has(i, 2 * h + 1)) set_elem(q + 2 * h + 1, v[h].y);
+        for (int h = 0; h < V / 2; ++h) {
+          if (has(i, 2 * h)) q[2 * h] = v[h].x;
+          if (has(i, 2 * h + 1)) q[2 * h + 1] = v[h].y;
+        }
+      } else {
+        store_part(q, pack<F32>(v), col(i) < 0 ? -col(i) : 0, col(i) + V <= d ? V : d - col(i));
       }
+    }
+  }
+  // Elements [lo, hi) of eight, and not all: the warps that have a row's ends keep
+  // the others waiting, so three stores at most in place of one for each element
+  // (with the norm's masks of such pieces, the gradient of 4096 x 8191 72 -> 57 us,
+  // of 2048 x 12001 54 -> 46; of f32's four elements the plain form is the faster).
+  __device__ __forceinline__ static void store_part(uint16_t* q, const uint4& u, int lo, int hi) {
+    if (lo == 0) {   // 4, 2 and 1 of them, as hi has them
+      const bool four = hi & 4, two = hi & 2;
+      if (four) *reinterpret_cast<uint2*>(q) = make_uint2(u.x, u.y);
+      if (two) *reinterpret_cast<uint32_t*>(q + (hi & 4)) = four ? u.z : u.x;
+      if (hi & 1) q[hi - 1] = (uint16_t)(four ? (two ? u.w : u.z) : two ? u.y : u.x);
+    } else if (hi == 8) {   // the same from the end
+      const int n = 8 - lo;
+      const bool four = n & 4, two = n & 2;
+      if (four) *reinterpret_cast<uint2*>(q + 4) = make_uint2(u.z, u.w);
+      if (two) *reinterpret_cast<uint32_t*>(q + (6 - (n & 4))) = four ? u.y : u.w;
+      if (n & 1) q[lo] = (uint16_t)((four ? (two ? u.x : u.y) : two ? u.z : u.w) >> 16);
+    } else {   // a row inside a piece
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e >= lo && e < hi) q[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
     }
   }
   // The piece's e4m3 codes into a tensor of codes, which has V bytes where this one has 16.
