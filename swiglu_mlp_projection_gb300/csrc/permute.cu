@@ -695,8 +695,9 @@ unpermute_backward_few_kernel(const void* dy, const void* z, const int* position
         const Span16<E, RAGGED> o(p[b], bytes);
         if (p[b] < 0 || i >= o.n) continue;
         const int64_t at = o.base - o.shift + (int64_t)i * 16;
-        // (the tensor's last row may end inside 16 bytes)
-        if (!RAGGED || p[b] + 1 < rows) q[b] = load_once((const char*)z + at);
+        // (z may end inside the piece: its last row's, or of rows shorter than a
+        // piece one that has several)
+        if (!RAGGED || at + 16 <= rows * bytes) q[b] = load_once((const char*)z + at);
         else q[b] = load_inside<E>(z, at, rows * bytes);
       }
       Two g;

@@ -133,6 +133,20 @@ def test_unpermute_backward(cuda_lib, T, E, k, d, dropped, dtype):
     assert not bool(dw[rt.ids < 0].any())
 
 
+# rows shorter than 16 bytes, several to a piece: few tokens, and enough for the kernels that copy ahead
+NARROW = [(3, 4, 2, 1, 0), (1, 10, 10, 1, 0), (5, 8, 2, 3, 0.2), (9, 8, 3, 7, 0), (7, 4, 1, 5, 0.3), (4, 9, 9, 2, 0),
+          (50000, 8, 2, 1, 0.1), (50000, 16, 4, 3, 0), (50000, 4, 1, 7, 0.2)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,E,k,d,dropped", NARROW)
+def test_rows_shorter_than_a_piece(cuda_lib, T, E, k, d, dropped, dtype):
+    test_permute(cuda_lib, T, E, k, d, dropped, dtype)
+    test_unpermute(cuda_lib, T, E, k, d, dropped, dtype)
+    test_unpermute_backward(cuda_lib, T, E, k, d, dropped, dtype)
+    test_permute_fp8(cuda_lib, T, E, k, d, dropped)
+
+
 def test_gradients_against_differences(cuda_lib):
     T, E, k, d = 6, 5, 3, 20
     rt = routing(T, E, k, 7, 0.2)
