@@ -28,7 +28,8 @@
  *     surface at the caller's next synchronisation, as for any CUDA library.
  *   - Calls may come from several host threads, on one stream too: a call that
  *     uses the library's workspace enqueues its kernels without another such
- *     call's in between.  A workspace of the caller's serves one call at a time.
+ *     call's in between.  A workspace of the caller's serves one call at a time
+ *     and holds none of that call's tensors.
  *   - Argument validation is synchronous and enqueues nothing on failure.
  *   - The return value is a swiglu_status; swiglu_last_error_string() gives a
  *     human-readable detail for the calling thread's last failure.
@@ -261,7 +262,10 @@ SWIGLU_API size_t swiglu_fp8_workspace_bytes(int64_t M, int64_t d, int64_t d_ff,
  * swiglu_rms_norm_fp8, say): x8 e4m3 codes [M, d] and s_x their f32 row scales
  * [M]; row i stands for x8[i] * s_x[i].  The same codes and scales give the
  * bits that swiglu_up_fp8 gives.  A caller workspace of
- * swiglu_fp8_workspace_bytes is enough (it holds no codes here).  No
+ * swiglu_fp8_workspace_bytes is enough (its first bytes hold sums here, not
+ * codes).  An input in the workspace is refused (SWIGLU_ERR_INVALID_ARG):
+ * codes and scales that swiglu_up_fp8 left in one go on with another, or with
+ * that one's part from the first multiple of 256 bytes behind the scales.  No
  * counterpart in the pages.
  */
 SWIGLU_API int swiglu_up_fp8_rows(const void* x8, const float* s_x, const void* w8_gate,

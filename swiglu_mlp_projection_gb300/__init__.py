@@ -313,8 +313,8 @@ stands for codes[i] * scales[i] (``rms_norm_fp8`` and ``permute`` write them).""
 def swiglu_up_fp8(x, w, out=None, path="auto", workspace=None, stream=None):
     """h = silu(x @ W_gate) * (x @ W_up) with e4m3 weights ``w`` (an
     Fp8Weights) and x [M, d]: a bfloat16 tensor, quantized per row to e4m3
-    inside the call, or an Fp8Rows, whose codes are used as they are.  The
-    result [M, d_ff] is bfloat16."""
+    inside the call, or an Fp8Rows, whose codes are used as they are (and must
+    not lie in ``workspace``).  The result [M, d_ff] is bfloat16."""
     global _LIB
     torch = _TORCH or _torch()
     rows = isinstance(x, Fp8Rows)

@@ -1195,6 +1195,16 @@ int swiglu_up_fp8_rows(const void* x8, const float* s_x, const void* w8_gate, co
   if ((uintptr_t)s_x & 3u) return fail(SWIGLU_ERR_ALIGNMENT, "s_x must be 4-byte aligned");
   if (overlaps(h, (size_t)M * d_ff * 2, s_x, (size_t)M * 4))
     return fail(SWIGLU_ERR_INVALID_ARG, "h overlaps an input");
+  // (swiglu_up_fp8 leaves rows like these at the start of its workspace, where
+  // this call's counters and partial sums go)
+  const auto in_workspace = [&](const void* p, size_t n) {
+    return workspace && overlaps(p, n, workspace, workspace_bytes);
+  };
+  const size_t nw = (size_t)d * d_ff, ns = (size_t)d_ff * 4;
+  if (in_workspace(x8, (size_t)M * d) || in_workspace(s_x, (size_t)M * 4) ||
+      in_workspace(w8_gate, nw) || in_workspace(w8_up, nw) || in_workspace(s_gate, ns) ||
+      in_workspace(s_up, ns))
+    return fail(SWIGLU_ERR_INVALID_ARG, "an input overlaps the workspace");
   Call c{kOpUp, x8, w8_gate, w8_up, nullptr, h, M, d, d_ff, SWIGLU_BF16, path, workspace,
          workspace_bytes, (cudaStream_t)stream, kWeightsNK};
   c.fp8 = true;

@@ -30,6 +30,22 @@ def test_quantized_rows_give_the_same_bits(cuda_lib, M, d, d_ff, path):
     swg.check_device_status()
 
 
+@pytest.mark.parametrize("M,d,d_ff", [(7, 4096, 4096), (16, 896, 4864), (600, 2048, 1032)])
+def test_quantized_rows_where_the_up_projection_leaves_them(cuda_lib, M, d, d_ff):
+    """Codes and scales in the workspace go on with its part behind them; the whole of it is refused."""
+    w = swg.quantize_weights_fp8(randn(2, d, d_ff, scale=d ** -0.5), randn(3, d, d_ff, scale=d ** -0.5))
+    ws = torch.zeros(swg.fp8_workspace_bytes(M, d, d_ff), device=DEV, dtype=torch.uint8)
+    h = swg.swiglu_up_fp8(randn(1, M, d), w, workspace=ws)
+    at = (M * d + 255) // 256 * 256
+    end = at + (4 * M + 255) // 256 * 256
+    rows = swg.Fp8Rows(ws[:M * d].view(M, d), ws[at:at + 4 * M].view(torch.float32))
+    with pytest.raises(swg.SwiGLUError):
+        swg.swiglu_up_fp8(rows, w, workspace=ws)
+    for _ in range(2):
+        assert torch.equal(swg.swiglu_up_fp8(rows, w, workspace=ws[end:]), h)
+    swg.check_device_status()
+
+
 def test_quantized_rows_refused(cuda_lib):
     w = swg.quantize_weights_fp8(randn(2, 64, 72), randn(3, 64, 72))
     c, s = torch.zeros(4, 64, device=DEV, dtype=torch.uint8), torch.ones(4, device=DEV)

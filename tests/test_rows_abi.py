@@ -90,6 +90,15 @@ def test_refused(cuda_lib, fn, kw, status):
     assert cuda_lib.swiglu_last_error_string()
 
 
+@pytest.mark.parametrize("at", [A, 2 * A, 3 * A, 4 * A, 5 * A, 6 * A])
+def test_quantized_rows_refuse_an_input_in_the_workspace(cuda_lib, at):
+    """At the start of the workspace, where swiglu_up_fp8 leaves codes, and at its end."""
+    for ws, nws in ((at, 1 << 20), (at - (1 << 20), (1 << 20) + 1)):
+        assert cuda_lib.swiglu_up_fp8_rows(A, 2 * A, 3 * A, 4 * A, 5 * A, 6 * A, 7 * A, 4, 64, 72, 0, ws, nws,
+                                           None) == INVALID
+        assert b"workspace" in cuda_lib.swiglu_last_error_string()
+
+
 def test_workspace_query_refuses_invalid_sizes(cuda_lib):
     assert cuda_lib.swiglu_rms_norm_backward_workspace_bytes(-1, 64, 1) == 0
     assert cuda_lib.swiglu_rms_norm_backward_workspace_bytes(4, 64, 2) == 0
