@@ -497,7 +497,8 @@ SWIGLU_API int swiglu_rms_norm_fp8(const void* x, const void* residual, const vo
  * serves swiglu_rms_norm_fp8 too, where the quantization counts as the
  * identity.  workspace: as swiglu_up_ex, of
  * swiglu_rms_norm_backward_workspace_bytes(M, d, dtype), or NULL for the
- * library's own.  Errors as swiglu_rms_norm, _WORKSPACE, _OOM.
+ * library's own; it overlaps no input and no output.  Errors as
+ * swiglu_rms_norm, _WORKSPACE, _OOM.
  */
 SWIGLU_API int swiglu_rms_norm_backward(const void* dy, const void* s, const void* weight,
                                         const void* ds, void* dx, void* dweight, int64_t M,

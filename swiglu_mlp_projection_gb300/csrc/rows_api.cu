@@ -137,7 +137,9 @@ int swiglu_rms_norm_backward(const void* dy, const void* s, const void* weight, 
   if ((v = check_apart_or_same(out[0], in, 3)) != SWIGLU_OK ||
       (v = check_apart(out[0], in + 3, 2)) != SWIGLU_OK ||
       (v = check_apart(out[1], in, 5)) != SWIGLU_OK ||
-      (v = check_apart(out[1], out, 1)) != SWIGLU_OK)
+      (v = check_apart(out[1], out, 1)) != SWIGLU_OK ||
+      // (CTAs write their partial sums while others read)
+      (v = check_apart(in[4], in, 4)) != SWIGLU_OK)
     return v;
   int dev, num_sms;
   if ((v = api_current_device(&dev, &num_sms)) != SWIGLU_OK) return v;

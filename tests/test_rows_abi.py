@@ -99,6 +99,13 @@ def test_quantized_rows_refuse_an_input_in_the_workspace(cuda_lib, at):
         assert b"workspace" in cuda_lib.swiglu_last_error_string()
 
 
+@pytest.mark.parametrize("at", [A, 2 * A, 3 * A, 4 * A, 5 * A, 6 * A])
+def test_gradient_of_the_norm_refuses_a_tensor_in_the_workspace(cuda_lib, at):
+    for ws, nws in ((at, 1 << 20), (at - (1 << 20), (1 << 20) + 1)):
+        assert back(cuda_lib, ds=6 * A, ws=ws, nws=nws) == INVALID
+        assert b"workspace" in cuda_lib.swiglu_last_error_string()
+
+
 def test_workspace_query_refuses_invalid_sizes(cuda_lib):
     assert cuda_lib.swiglu_rms_norm_backward_workspace_bytes(-1, 64, 1) == 0
     assert cuda_lib.swiglu_rms_norm_backward_workspace_bytes(4, 64, 2) == 0
