@@ -472,8 +472,8 @@ SWIGLU_API size_t swiglu_experts_down_workspace_bytes(int64_t T, int64_t k, int6
  *   swiglu_up_fp8 quantizes x, from the f32 values: codes [M, d], scales [M]
  *   f32, y = codes * scales with scale = amax / 448, amax = max |y| of the row.
  *   A row of zeros (and one whose values before the division by the root stay
- *   below 2^-118) has scale 0; one with an infinity or NaN, scale NaN.  codes
- *   and scales overlap nothing.
+ *   below 2^-118) has scale 0; one that holds an infinity or NaN, or whose y
+ *   holds a NaN (a weight's), scale NaN.  codes and scales overlap nothing.
  */
 SWIGLU_API int swiglu_rms_norm(const void* x, const void* residual, const void* weight, void* y,
                                void* sum, int64_t M, int64_t d, float eps, int dtype,

@@ -49,7 +49,14 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// Largest of values that are not negative (their bits order like the values).
+// The larger of two; NaN if either is (fmaxf would drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Largest of values that are not negative, or max_nan's NaN (their bits order like
+// the values, and that NaN's, 0x7fffffff, come last).
 __device__ __forceinline__ float warp_max(float v) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
@@ -78,7 +85,7 @@ __device__ __forceinline__ void weigh(float2 (&t)[H], const float2 (&w)[H], floa
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     t[h] = mul2(t[h], w[h]);
-    if (FP8) m = fmaxf(m, fmaxf(fabsf(t[h].x), fabsf(t[h].y)));
+    if (FP8) m = max_nan(m, max_nan(fabsf(t[h].x), fabsf(t[h].y)));
   }
 }
 
@@ -107,7 +114,7 @@ template <bool FP8>
 __device__ __forceinline__ RowFactors row_factors(float q, float m, const NormArgs& a) {
   const float r = 1.0f / sqrtf(q / (float)a.d + a.eps);
   if (!FP8) return {r, 0.f};
-  const bool some = m >= kLeastAmax;
+  const bool some = !(m < kLeastAmax);   // (NaN gives NaN)
   return {some ? 448.0f / m : 0.f, (some ? m : 0.f) * r / 448.0f};
 }
 
@@ -289,7 +296,7 @@ struct Team {
       v.x += __shfl_xor_sync(~0u, v.x, o);
       if (SECOND == kNone) continue;
       const float u = __shfl_xor_sync(~0u, v.y, o);
-      v.y = SECOND == kMax ? fmaxf(v.y, u) : v.y + u;
+      v.y = SECOND == kMax ? max_nan(v.y, u) : v.y + u;
     }
     return v;
   }
@@ -311,7 +318,7 @@ struct Team {
     for (int i = 0; i < C * W; i += 32) {
       const float2 u = i + l < C * W ? red[stage][i + l] : make_float2(0.f, 0.f);
       v.x += u.x;
-      v.y = SECOND == kMax ? fmaxf(v.y, u.y) : v.y + u.y;
+      v.y = SECOND == kMax ? max_nan(v.y, u.y) : v.y + u.y;
     }
     return of_warp<SECOND>(v);
   }

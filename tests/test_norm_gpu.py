@@ -140,6 +140,25 @@ def test_rows_that_are_not_ordinary(cuda_lib, M, d):
     check_fp8(swg.Fp8Rows(f.codes[4:], f.scales[4:]), x[4:], None, w, 1e-6)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,d", [(1, 1), (3, 64), (300, 896), (300, 1031), (2, 4099), (200, 8192), (157, 3301),
+                                 (154, 9001), (153, 10000), (170, 13001), (3, 20003), (160, 32751)])
+def test_nan_of_the_weight(cuda_lib, M, d, dtype):
+    """amax = max |y| is NaN if one y is: the row's scale says so, wherever the NaN stands."""
+    x, r, w = inputs(M, d, dtype, F32, 95)
+    x[-1] = 0
+    for at in {0, d // 2, d - 1}:
+        v = w.clone()
+        v[at] = float("nan")
+        for rows in (swg.rms_norm_fp8(x, v), swg.rms_norm_fp8(x, v, residual=r)[0]):
+            assert bool(rows.scales.isnan().all())
+            assert bool(rows.codes.view(torch.float8_e4m3fn).float()[:, at].isnan().all())
+        y = swg.rms_norm(x, v)
+        assert bool(y[:, at].isnan().all()) and int(y.isnan().sum()) == M
+    rows = swg.rms_norm_fp8(x, w)
+    check_fp8(rows, x, None, w, 1e-6)
+
+
 def ref_backward(dy, s, w, ds, eps):
     """(dx, dweight, sizes of dx's terms, sizes of dweight's terms)."""
     dy, s, w = dy.to(D), s.to(D), w.to(D)
