@@ -576,7 +576,8 @@ norm_backward_kernel(const __grid_constant__ BackArgs a) {
   // t = s r:  dx = ds + r g - t r^2 mean(g s),  dweight += dy t
   const auto put = [&](int64_t row, int stage, float2 v) {
     const float r = rsqrtf(fmaf(v.x, inv_d, a.eps));
-    const float c = -r * r * (v.y * inv_d);
+    // (not r * r first, which leaves binary32 where eps is subnormal and s about 0)
+    const float c = -r * (v.y * inv_d * r);
     const float2 r2 = make_float2(r, r), c2 = make_float2(c, c);
 #pragma unroll
     for (int j = 0; j < P; ++j) {

@@ -227,6 +227,22 @@ def test_sizes_of_values(cuda_lib, M, d, dtype, scale, eps):
     check_backward(*swg.rms_norm_backward(dy, s, w, eps=eps), dy, s, w, None, eps)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,d", [(3, 64), (200, 897), (3, 4096), (300, 1000), (4, 20000), (5, 30001)])
+@pytest.mark.parametrize("eps", [2.0 ** -149, 1e-39, 2.0 ** -126, 1e-37])
+def test_smallest_eps(cuda_lib, M, d, dtype, eps):
+    """Rows of zeros, and rows whose squares are below binary32, have finite gradients: r is at most
+    2^74.5, and g r what dx then is.  (The squares that are lost would change r by less than 2^-28,
+    eps in binary32 by less than 2^-22.)"""
+    _, dy, w = inputs(M, d, dtype, F32, 97)
+    s = torch.zeros(M, d, device=DEV, dtype=dtype)
+    s[1] = 2.0 ** -90 * (1 + torch.arange(d, device=DEV) % 3)   # s^2 <= 9 * 2^-180
+    s[2:] = inputs(M, d, dtype, F32, 98)[0][2:]
+    y = swg.rms_norm(s, w, eps=eps)
+    assert bool(y.isfinite().all()) and not bool(y[0].any())
+    check_backward(*swg.rms_norm_backward(dy, s, w, eps=eps), dy, s, w, None, eps)
+
+
 def test_nothing_to_do(cuda_lib):
     for M, d in ((0, 64), (4, 0), (0, 0)):
         x, w = torch.empty(M, d, device=DEV, dtype=BF), torch.ones(d, device=DEV, dtype=BF)
