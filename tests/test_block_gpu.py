@@ -97,6 +97,64 @@ def test_block(cuda_lib, M, fp8, with_residual):
     swg.check_device_status()
 
 
+@pytest.mark.parametrize("M", [1, 16, 300])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_block_is_its_steps(cuda_lib, M, fp8, with_residual):
+    """The block gives the bits of norm, up and down called in turn, and each product is within
+    rounding of the 64-bit sums over the very operands that it multiplies, element by element.
+
+    A sum of K products, however ordered, and its scales are off by less than (K + 4) 2^-23 of the sum of
+    the products' sizes (twice the rounding of f32, for sums inside the tensor core); h = silu(g) u has
+    |silu'| <= 1.1, and its exponential and quotient less than 2^-18 of h; h and y are rounded to bf16.
+    """
+    d, d_ff = 896, 4864
+    x, r = randn(1, M, d), randn(2, M, d) if with_residual else None
+    nw = (1 + randn(3, d, scale=0.3).float()).to(BF)
+    wg, wu = randn(4, d, d_ff, scale=d ** -0.5), randn(5, d, d_ff, scale=d ** -0.5)
+    wd = randn(6, d_ff, d, scale=d_ff ** -0.5)
+
+    def rows64(codes, scales):
+        return codes.view(torch.float8_e4m3fn).to(D) * scales.to(D)[:, None]
+    if fp8:
+        up, down = swg.quantize_weights_fp8(wg, wu), swg.quantize_weight_fp8(wd)
+        wg, wu = rows64(up.w8_gate, up.s_gate).t(), rows64(up.w8_up, up.s_up).t()
+        wd = rows64(down.w8, down.s).t()
+        n = swg.rms_norm_fp8(x, nw, residual=r)
+    else:
+        up, down = (wg, wu), wd
+        n = swg.rms_norm(x, nw, residual=r)
+    n, s = (n, x) if r is None else n
+    h = swg.swiglu_up_fp8(n, up) if fp8 else swg.swiglu_up(n, wg, wu)
+    y = (swg.swiglu_down_fp8 if fp8 else swg.swiglu_down)(h, down, residual=s)
+    assert torch.equal(swg.swiglu_block(x, nw, up, down, residual=r), y)
+
+    n64, wg, wu, wd = (rows64(*n) if fp8 else n.to(D)), wg.to(D), wu.to(D), wd.to(D)
+    g, u = n64 @ wg, n64 @ wu
+    eg, eu = ((d + 4) * 2.0 ** -23 * (n64.abs() @ w.abs()) for w in (wg, wu))
+    a = g * torch.sigmoid(g)
+    tol = (2.0 ** -8 + 2.0 ** -18) * (a * u).abs() + 1.1 * eg * (u.abs() + eu) + a.abs() * eu
+    assert bool(((h.to(D) - a * u).abs() <= tol + 2.0 ** -133).all())
+    h64 = h.to(D)
+    if fp8:   # the codes and scales of h that the call leaves at the start of its workspace
+        need = cuda_lib.swiglu_down_fp8_workspace_bytes(M, d_ff, d, 0)
+        ws = torch.zeros(need, device=DEV, dtype=torch.uint8)
+        assert torch.equal(swg.swiglu_down_fp8(h, down, residual=s, workspace=ws), y)
+        at = (M * d_ff + 255) // 256 * 256
+        codes, scales = ws[:M * d_ff].view(M, d_ff), ws[at:at + 4 * M].view(torch.float32)
+        # (448 / amax, amax / 448 and the product with h are rounded to f32)
+        amax = h64.abs().amax(1)
+        assert bool(((scales.to(D) * 448 - amax).abs() <= 2.0 ** -24 * amax).all())
+        v = h64 * (448 / amax)[:, None]
+        err = (codes.view(torch.float8_e4m3fn).to(D) - v).abs()
+        assert bool((err <= v.abs() * (2.0 ** -4 + 2.0 ** -22) + 2.0 ** -10).all())
+        h64 = rows64(codes, scales)
+    y64 = s.to(D) + h64 @ wd
+    tol = 2.0 ** -8 * y64.abs() + (d_ff + 4) * 2.0 ** -23 * (h64.abs() @ wd.abs() + s.to(D).abs())
+    assert bool(((y.to(D) - y64).abs() <= tol * (1 + 2.0 ** -7)).all())
+    swg.check_device_status()
+
+
 def test_training_step_of_routed_experts(cuda_lib):
     """norm -> permute -> experts of one matrix each -> unpermute, and back: the gradients of
     input, norm weight and routing weights against autograd in 64 bits."""
