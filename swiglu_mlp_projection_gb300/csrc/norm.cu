@@ -189,10 +189,12 @@ norm_kernel(const __grid_constant__ NormArgs a) {
 constexpr int kPieces = 2;
 constexpr int team_threads(int w) { return 24 % w ? 32 * w : 768; }
 constexpr int team_rows(int w) { return team_threads(w) / 32 / w; }   // R
-// Stages of the copies, of `arrays` tensors each.  More is not better: the
-// gradient of 8192 x 4096 takes 44.3 us with two and 47.0 with three, 8192 x 4096
-// f32 80.8 and 84.7; only the lightest stages gain from a third (16384 x 256 9.2
-// and 8.8; the norm of 5001 x 897 f32 7.8 and 7.5).
+// Stages of the copies, of `arrays` tensors each.  More is not better: with 768
+// threads the gradient of 8192 x 4096 takes 44.3 us with two (147 KB) and 47.1 with
+// three (221 KB), 16384 x 896 22.5 and 23.0.  A third is for what has little under
+// way: 512 threads (4096 x 8192 48.0 with two, 47.6 with three; 8192 x 4096 f32 80.6
+// and 81.1), the gradient's rows of a warp (16384 x 512 14.2 and 14.1; x 256 8.4 and
+// 8.6), the norm's of four warps and less (5001 x 897 f32 7.55 and 7.45).
 constexpr int team_stages(int w, int arrays, int cluster) {
   if (cluster > 1) return w == 16 ? 4 : 3;
   return w == 16 || w <= (arrays == 3 ? 1 : 4) ? 3 : 2;
@@ -512,9 +514,9 @@ cudaError_t launch_rows(const NormArgs& a, int num_sms, cudaStream_t st) {
 //
 // A team's columns' sums of dweight stay in registers over all of its rows; each
 // CTA then writes one row of partial sums, and a second kernel adds those in a
-// fixed order.  Bound by memory but for its ends: 8192 x 4096 bf16 with ds 44.5 us
-// in a graph (6030 GB/s), of which the second kernel and the first rows' latency
-// take about 5; f32 80.7 us (6650 GB/s).  Without rows copied ahead it took 72 us,
+// fixed order.  Bound by memory but for its ends: 8192 x 4096 bf16 with ds 44.4 us
+// in a graph (6050 GB/s), of which the second kernel and the first rows' latency
+// take about 5; f32 80.6 us (6660 GB/s).  Without rows copied ahead it took 72 us,
 // with every CTA's own partial sums (456 of them) 63.6.
 
 struct BackArgs {
